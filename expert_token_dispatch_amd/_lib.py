@@ -55,6 +55,32 @@ class Saved(ctypes.Structure):
                 ("topk_ids", "topk_w", "offsets", "pair_row", "x_sorted", "gate", "up", "h", "y_sorted")]
 
 
+class PackedExperts(ctypes.Structure):
+    """moe_packed_experts: the local experts' weights in 4 bits (include/moe.h)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("gate_codes", "gate_scales", "up_codes", "up_scales", "down_codes", "down_scales")]
+
+
+class MuonDesc(ctypes.Structure):
+    """moe_muon_desc: a stack of matrices and how it is updated (include/moe.h)."""
+    _fields_ = [
+        ("count", ctypes.c_int32),
+        ("rows", ctypes.c_int32),
+        ("cols", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("steps", ctypes.c_int32),
+        ("coef_a", ctypes.c_float),
+        ("coef_b", ctypes.c_float),
+        ("coef_c", ctypes.c_float),
+        ("eps", ctypes.c_float),
+        ("momentum", ctypes.c_float),
+        ("nesterov", ctypes.c_int32),
+        ("lr", ctypes.c_float),
+        ("update_scale", ctypes.c_float),
+        ("weight_decay", ctypes.c_float),
+    ]
+
+
 def make_saved(t: dict) -> Saved:
     """t: a dict of device tensors under the moe_saved field names.  The struct
     keeps a reference to the dict, so the pointers stay valid while it lives."""
@@ -84,10 +110,31 @@ def make_desc(num_tokens: int, hidden: int, intermediate: int, num_experts: int,
                      num_experts if local_count is None else local_count, capacity_factor, dtype, weight_layout)
 
 
+def make_packed_experts(t: dict) -> PackedExperts:
+    """t: a dict of uint8 device tensors under the moe_packed_experts field names.  The
+    struct keeps a reference to the dict, so the pointers stay valid while it lives."""
+    v = PackedExperts(*[_p(t[n]) for n, _ in PackedExperts._fields_])
+    v._tensors = t
+    return v
+
+
+def make_muon_desc(count: int, rows: int, cols: int, dtype="bf16", steps: int = 5, momentum: float = 0.95,
+                   nesterov: bool = True, lr: float = 0.0, update_scale: float = 1.0, weight_decay: float = 0.0,
+                   eps: float = 1e-7, coefs=(0.0, 0.0, 0.0)) -> MuonDesc:
+    """coefs: (a, b, c) of a Newton-Schulz step; all zero for the usual ones."""
+    if isinstance(dtype, str):
+        dtype = {"bf16": MOE_BF16, "f32": MOE_F32}[dtype]
+    a, b, c = coefs
+    return MuonDesc(count, rows, cols, dtype, steps, a, b, c, eps, momentum, int(nesterov), lr, update_scale,
+                    weight_decay)
+
+
 _LIB = None
 _VP = ctypes.c_void_p
 _DP = ctypes.POINTER(LayerDesc)
 _OP = ctypes.c_void_p  # moe_route_opts*, NULL allowed
+_PP = ctypes.c_void_p  # moe_packed_experts*
+_MP = ctypes.POINTER(MuonDesc)
 
 
 def lib() -> ctypes.CDLL:
@@ -133,6 +180,15 @@ def lib() -> ctypes.CDLL:
             "moe_dispatch_backward": (st, [_DP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
             "moe_layer_backward": (st, [_DP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                         ctypes.c_size_t, _VP]),
+            "moe_pack_weights": (st, [ctypes.c_int32] * 5 + [_VP] * 4),
+            "moe_unpack_weights": (st, [ctypes.c_int32] * 5 + [_VP] * 4),
+            "moe_packed_workspace_size": (st, [_DP, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]),
+            "moe_grouped_ffn_packed": (st, [_DP, _VP, _VP, _PP, _VP, _VP, ctypes.c_size_t, _VP]),
+            "moe_layer_forward_packed": (st, [_DP, _OP, _VP, _VP, _VP, _PP, _VP, _VP, _VP, _VP, _VP, _VP,
+                                              ctypes.c_size_t, _VP]),
+            "moe_muon_workspace_size": (st, [_MP, ctypes.POINTER(ctypes.c_size_t)]),
+            "moe_orthogonalize": (st, [_MP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
+            "moe_muon_update": (st, [_MP, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -331,3 +387,86 @@ def moe_layer_backward(d, x, w_router, w_gate, w_up, w_down, saved, dy, dx, dw_r
     _check(lib().moe_layer_backward(ctypes.byref(d), _p(x), _p(w_router), _p(w_gate), _p(w_up), _p(w_down),
                                     _saved(saved), _p(dy), _p(dx), _p(dw_router), _p(db_router), _p(dw_gate),
                                     _p(dw_up), _p(dw_down), wp, wn, _s(stream)))
+
+
+# ---- expert weights in 4 bits ------------------------------------------------------------
+def _layout(weight_layout) -> int:
+    if isinstance(weight_layout, str):
+        return {"out_in": MOE_WEIGHTS_OUT_IN, "in_out": MOE_WEIGHTS_IN_OUT}[weight_layout]
+    return weight_layout
+
+
+def _stack_args(w, codes, scales, weight_layout):
+    """The call's sizes, from a weight stack [count, out, in] (or [count, in, out]) and its packed tensors."""
+    import torch
+    layout = _layout(weight_layout)
+    if w.dim() != 3 or w.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("a weight stack is a bfloat16 or float32 tensor of three dimensions")
+    count, out, in_ = w.shape if layout == MOE_WEIGHTS_OUT_IN else (w.shape[0], w.shape[2], w.shape[1])
+    for name, t, last in (("codes", codes, in_ // 2), ("scales", scales, in_ // 32)):
+        if t.dtype != torch.uint8 or tuple(t.shape) != (count, out, last):
+            raise ValueError(f"{name} of this stack is a uint8 tensor {(count, out, last)}")
+    return count, out, in_, MOE_BF16 if w.dtype == torch.bfloat16 else MOE_F32, layout
+
+
+def moe_pack_weights(w, codes, scales, weight_layout="out_in", stream=None) -> None:
+    """w [count, out, in] (or [count, in, out] for "in_out") into uint8 codes [count, out, in / 2] and
+    scales [count, out, in / 32]."""
+    _check(lib().moe_pack_weights(*_stack_args(w, codes, scales, weight_layout), _p(w), _p(codes), _p(scales),
+                                  _s(stream)))
+
+
+def moe_unpack_weights(codes, scales, w, weight_layout="out_in", stream=None) -> None:
+    _check(lib().moe_unpack_weights(*_stack_args(w, codes, scales, weight_layout), _p(codes), _p(scales), _p(w),
+                                    _s(stream)))
+
+
+def moe_packed_workspace_size(d: LayerDesc, stage: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_packed_workspace_size(ctypes.byref(d), stage, ctypes.byref(n)))
+    return n.value
+
+
+def _packed(v) -> Optional[int]:
+    return None if v is None else ctypes.addressof(v)
+
+
+def moe_grouped_ffn_packed(d, x_sorted, offsets, packed, y_sorted, ws=None, stream=None) -> None:
+    wp, wn = _ws(ws)
+    _check(lib().moe_grouped_ffn_packed(ctypes.byref(d), _p(x_sorted), _p(offsets), _packed(packed), _p(y_sorted),
+                                        wp, wn, _s(stream)))
+
+
+def moe_layer_forward_packed(d, opts, x, w_router, b_router, packed, y, ws, topk_ids_out=None, topk_w_out=None,
+                             counts_out=None, num_dropped_out=None, stream=None) -> None:
+    wp, wn = _ws(ws)
+    _check(lib().moe_layer_forward_packed(ctypes.byref(d), _opts(opts), _p(x), _p(w_router), _p(b_router),
+                                          _packed(packed), _p(y), _p(topk_ids_out), _p(topk_w_out), _p(counts_out),
+                                          _p(num_dropped_out), wp, wn, _s(stream)))
+
+
+# ---- training: the weight update -----------------------------------------------------------
+def moe_muon_workspace_size(m: MuonDesc) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_muon_workspace_size(ctypes.byref(m), ctypes.byref(n)))
+    return n.value
+
+
+def _muon_shapes(m, f32, **tensors):
+    import torch
+    for name, t in tensors.items():
+        want = torch.float32 if name in f32 or m.dtype == MOE_F32 else torch.bfloat16
+        if t is not None and (tuple(t.shape) != (m.count, m.rows, m.cols) or t.dtype != want):
+            raise ValueError(f"{name} of this update is a {want} tensor {(m.count, m.rows, m.cols)}")
+
+
+def moe_orthogonalize(m, g, o, ws, stream=None) -> None:
+    _muon_shapes(m, (), g=g, o=o)
+    wp, wn = _ws(ws)
+    _check(lib().moe_orthogonalize(ctypes.byref(m), _p(g), _p(o), wp, wn, _s(stream)))
+
+
+def moe_muon_update(m, grad, momentum, weight, ws, master=None, stream=None) -> None:
+    _muon_shapes(m, ("momentum", "master"), grad=grad, momentum=momentum, weight=weight, master=master)
+    wp, wn = _ws(ws)
+    _check(lib().moe_muon_update(ctypes.byref(m), _p(grad), _p(momentum), _p(master), _p(weight), wp, wn, _s(stream)))

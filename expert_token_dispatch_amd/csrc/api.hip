@@ -182,6 +182,26 @@ LayerBwdWs layer_bwd_layout(const moe_layer_desc* d, void* base) {
   return w;
 }
 
+// The packed layer: the layer's workspace with the packed feed-forward's scratch behind it.
+struct LayerPackedWs {
+  LayerWs w;
+  void* scratch;
+  size_t bytes;
+};
+
+LayerPackedWs layer_packed_layout(const moe_layer_desc* d, void* base) {
+  LayerPackedWs r{};
+  r.w = layer_layout(d, base);
+  r.scratch = base ? static_cast<char*>(base) + r.w.bytes : nullptr;
+  r.bytes = r.w.bytes + align_up(packed_ffn_scratch_bytes(d, max_pairs_of(d)), 256);
+  return r;
+}
+
+size_t packed_stage_bytes(const moe_layer_desc* d, int32_t stage) {
+  if (stage == MOE_STAGE_LAYER) return layer_packed_layout(d, nullptr).bytes;
+  return ffn_h_bytes(d) + align_up(packed_ffn_scratch_bytes(d, max_pairs_of(d)), 256);
+}
+
 size_t stage_bytes(const moe_layer_desc* d, int32_t stage) {
   switch (stage) {
     case MOE_STAGE_ROUTE:
@@ -222,14 +242,17 @@ size_t stage_bytes(const moe_layer_desc* d, int32_t stage) {
       return set_error(MOE_ERR_INVALID_ARG, "%s is not %d-byte aligned", #p, int(a));                       \
   } while (0)
 
-moe_status check_ws(const moe_layer_desc* d, int32_t stage, const void* ws, size_t ws_bytes) {
-  const size_t need = stage_bytes(d, stage);
+moe_status check_ws_bytes(size_t need, const void* ws, size_t ws_bytes) {
   if (need == 0) return MOE_OK;
   if (ws == nullptr || ws_bytes < need)
     return set_error(MOE_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given%s", need, ws_bytes,
                      ws == nullptr ? " (NULL)" : "");
   if (!aligned(ws, 256)) return set_error(MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   return MOE_OK;
+}
+
+moe_status check_ws(const moe_layer_desc* d, int32_t stage, const void* ws, size_t ws_bytes) {
+  return check_ws_bytes(stage_bytes(d, stage), ws, ws_bytes);
 }
 
 moe_status route_checks(const moe_layer_desc* d, const void* x, const void* w_router, const float* b_router,
@@ -288,6 +311,121 @@ moe_status combine_checks(const void* y_sorted, const int32_t* pair_row, const f
   REQUIRE_PTR(topk_w, 4);
   REQUIRE_PTR(y, 16);
   return MOE_OK;
+}
+
+moe_status packed_desc_checks(const moe_layer_desc* d) {
+  if (d->hidden % 32 != 0 || d->intermediate % 32 != 0)
+    return set_error(MOE_ERR_UNSUPPORTED, "packed experts: hidden and intermediate must be multiples of 32 (got %d, %d)",
+                     d->hidden, d->intermediate);
+  return MOE_OK;
+}
+
+moe_status packed_checks(const moe_packed_experts* p) {
+  if (p == nullptr) return set_error(MOE_ERR_INVALID_ARG, "packed is NULL");
+  REQUIRE_PTR(p->gate_codes, 16);
+  REQUIRE_PTR(p->gate_scales, 1);
+  REQUIRE_PTR(p->up_codes, 16);
+  REQUIRE_PTR(p->up_scales, 1);
+  REQUIRE_PTR(p->down_codes, 16);
+  REQUIRE_PTR(p->down_scales, 1);
+  return MOE_OK;
+}
+
+moe_status packed_ffn_checks(const void* x_sorted, const int32_t* offsets, const moe_packed_experts* p,
+                             const void* y_sorted) {
+  REQUIRE_PTR(x_sorted, 16);
+  REQUIRE_PTR(offsets, 4);
+  REQUIRE_PTR(y_sorted, 16);
+  return packed_checks(p);
+}
+
+moe_status pack_checks(int32_t count, int32_t out, int32_t in, int32_t dtype, int32_t layout, const void* w,
+                       const void* codes, const void* scales) {
+  if (count < 1) return set_error(MOE_ERR_INVALID_ARG, "count must be >= 1 (got %d)", count);
+  if (count > 65535) return set_error(MOE_ERR_UNSUPPORTED, "count above 65535 is not supported (got %d)", count);
+  if (out <= 0 || out % 8 != 0) return set_error(MOE_ERR_INVALID_ARG, "out must be a positive multiple of 8 (got %d)", out);
+  if (in <= 0 || in % 32 != 0) return set_error(MOE_ERR_INVALID_ARG, "in must be a positive multiple of 32 (got %d)", in);
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return set_error(MOE_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (layout != MOE_WEIGHTS_OUT_IN && layout != MOE_WEIGHTS_IN_OUT)
+    return set_error(MOE_ERR_INVALID_ARG, "unknown weight_layout %d", layout);
+  if ((out + 63) / 64 > 65535) return set_error(MOE_ERR_UNSUPPORTED, "out above %d is not supported", 65535 * 64);
+  REQUIRE_PTR(w, 16);
+  REQUIRE_PTR(codes, 16);
+  REQUIRE_PTR(scales, 1);
+  return MOE_OK;
+}
+
+// Largest |s (a + b s^2 + c s^4)| over s in [0, top]: at an end or where the derivative
+// a + 3 b s^2 + 5 c s^4 vanishes.
+double largest_image(double a, double b, double c, double top) {
+  auto f = [&](double s) { return fabs(s * (a + b * s * s + c * s * s * s * s)); };
+  double best = f(top);
+  const double disc = 9.0 * b * b - 20.0 * a * c;
+  double roots[2] = {-1.0, -1.0};  // values of s^2
+  if (c != 0.0) {
+    if (disc >= 0.0) {
+      roots[0] = (-3.0 * b + sqrt(disc)) / (10.0 * c);
+      roots[1] = (-3.0 * b - sqrt(disc)) / (10.0 * c);
+    }
+  } else if (b != 0.0) {
+    roots[0] = -a / (3.0 * b);
+  }
+  for (double r : roots)
+    if (r > 0.0 && r < top * top) best = std::max(best, f(sqrt(r)));
+  return best;
+}
+
+// What the update computes with: the descriptor's coefficients or the usual ones.
+struct MuonCoefs {
+  float a, b, c;
+};
+MuonCoefs muon_coefs(const moe_muon_desc* m) {
+  if (m->coef_a == 0.f && m->coef_b == 0.f && m->coef_c == 0.f) return {3.4445f, -4.7750f, 2.0315f};
+  return {m->coef_a, m->coef_b, m->coef_c};
+}
+
+moe_status muon_desc_checks(const moe_muon_desc* m) {
+  if (m == nullptr) return set_error(MOE_ERR_INVALID_ARG, "descriptor is NULL");
+  if (m->count < 1 || m->rows < 1 || m->cols < 1)
+    return set_error(MOE_ERR_INVALID_ARG, "count, rows and cols must be >= 1 (got %d, %d, %d)", m->count, m->rows, m->cols);
+  if (m->count > 65535) return set_error(MOE_ERR_UNSUPPORTED, "count above 65535 is not supported (got %d)", m->count);
+  if (m->dtype != MOE_F32 && m->dtype != MOE_BF16) return set_error(MOE_ERR_INVALID_ARG, "unknown dtype %d", m->dtype);
+  if (m->steps < 1 || m->steps > 10) return set_error(MOE_ERR_INVALID_ARG, "steps must be in [1, 10] (got %d)", m->steps);
+  if (!std::isfinite(m->coef_a) || !std::isfinite(m->coef_b) || !std::isfinite(m->coef_c))
+    return set_error(MOE_ERR_INVALID_ARG, "coefficients must be finite");
+  const MuonCoefs k = muon_coefs(m);
+  if (!(k.a > 0.f && k.a <= 4.f)) return set_error(MOE_ERR_INVALID_ARG, "coef_a must be in (0, 4] (got %g)", double(k.a));
+  // singular values start in [0, 1]; the float16 working range is sized for values up to 3
+  double top = 1.0;
+  for (int i = 0; i < m->steps; ++i) {
+    top = largest_image(k.a, k.b, k.c, top);
+    if (!(top <= 3.0))
+      return set_error(MOE_ERR_INVALID_ARG, "coefficients (%g, %g, %g) take a singular value past 3 in step %d",
+                       double(k.a), double(k.b), double(k.c), i + 1);
+    top = std::max(top, 1.0);
+  }
+  if (!(std::isfinite(m->eps) && m->eps >= 0.f)) return set_error(MOE_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!(m->momentum >= 0.f && m->momentum < 1.f))
+    return set_error(MOE_ERR_INVALID_ARG, "momentum must be in [0, 1) (got %g)", double(m->momentum));
+  if (m->nesterov != 0 && m->nesterov != 1)
+    return set_error(MOE_ERR_INVALID_ARG, "nesterov must be 0 or 1 (got %d)", m->nesterov);
+  if (!std::isfinite(m->lr) || !std::isfinite(m->update_scale) || !std::isfinite(m->weight_decay))
+    return set_error(MOE_ERR_INVALID_ARG, "lr, update_scale and weight_decay must be finite");
+  if (muon_matrix_bytes(m) >= (int64_t(1) << 32))
+    return set_error(MOE_ERR_UNSUPPORTED, "a matrix of %d x %d takes 4 GiB or more of workspace", m->rows, m->cols);
+  return MOE_OK;
+}
+
+MuonArgs muon_args(const moe_muon_desc* m, void* ws, void* stream) {
+  const MuonCoefs k = muon_coefs(m);
+  MuonArgs a{};
+  a.m = m;
+  a.ca = k.a;
+  a.cb = k.b;
+  a.cc = k.c;
+  a.ws = ws;
+  a.s = static_cast<hipStream_t>(stream);
+  return a;
 }
 
 moe_status saved_checks(const moe_saved* v) {
@@ -786,6 +924,119 @@ moe_status moe_layer_backward(const moe_layer_desc* d, const void* x, const void
   TRY(launch_route_backward(ra));
   DispatchBwdArgs da{d, w.dx_sorted, v.pair_row, v.topk_ids, w.dl, w_router, dx, s};
   return launch_dispatch_backward(da);
+}
+
+moe_status moe_pack_weights(int32_t count, int32_t out, int32_t in, int32_t dtype, int32_t weight_layout,
+                            const void* w, void* codes, void* scales, void* stream) {
+  CallScope scope;
+  TRY(pack_checks(count, out, in, dtype, weight_layout, w, codes, scales));
+  PackArgs a{count, out, in, dtype, weight_layout, const_cast<void*>(w), codes, scales, static_cast<hipStream_t>(stream)};
+  return launch_pack("pack_weights", a);
+}
+
+moe_status moe_unpack_weights(int32_t count, int32_t out, int32_t in, int32_t dtype, int32_t weight_layout,
+                              const void* codes, const void* scales, void* w, void* stream) {
+  CallScope scope;
+  TRY(pack_checks(count, out, in, dtype, weight_layout, w, codes, scales));
+  PackArgs a{count, out, in, dtype, weight_layout, w, const_cast<void*>(codes), const_cast<void*>(scales),
+             static_cast<hipStream_t>(stream)};
+  return launch_unpack("unpack_weights", a);
+}
+
+moe_status moe_packed_workspace_size(const moe_layer_desc* d, int32_t stage, size_t* bytes) {
+  TRY(check_desc(d));
+  TRY(packed_desc_checks(d));
+  if (bytes == nullptr) return set_error(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  if (stage != MOE_STAGE_FFN && stage != MOE_STAGE_LAYER)
+    return set_error(MOE_ERR_INVALID_ARG, "stage %d has no packed form", stage);
+  *bytes = packed_stage_bytes(d, stage);
+  return MOE_OK;
+}
+
+moe_status moe_grouped_ffn_packed(const moe_layer_desc* d, const void* x_sorted, const int32_t* offsets,
+                                  const moe_packed_experts* packed, void* y_sorted, void* ws, size_t ws_bytes,
+                                  void* stream) {
+  CallScope scope;
+  TRY(check_desc(d));
+  TRY(packed_desc_checks(d));
+  if (d->num_tokens == 0) return MOE_OK;
+  TRY(packed_ffn_checks(x_sorted, offsets, packed, y_sorted));
+  TRY(check_ws_bytes(packed_stage_bytes(d, MOE_STAGE_FFN), ws, ws_bytes));
+  PackedFfnArgs a{d, x_sorted, offsets, packed, y_sorted, ws, static_cast<char*>(ws) + ffn_h_bytes(d), max_pairs_of(d),
+                  static_cast<hipStream_t>(stream)};
+  return launch_packed_ffn(a);
+}
+
+moe_status moe_layer_forward_packed(const moe_layer_desc* d, const moe_route_opts* opts, const void* x,
+                                    const void* w_router, const float* b_router, const moe_packed_experts* packed,
+                                    void* y, int32_t* topk_ids_out, float* topk_w_out, int32_t* counts_out,
+                                    int64_t* num_dropped_out, void* ws, size_t ws_bytes, void* stream) {
+  CallScope scope;
+  TRY(check_desc(d));
+  TRY(packed_desc_checks(d));
+  if (d->num_tokens == 0) return MOE_OK;
+  TRY(check_ws_bytes(packed_stage_bytes(d, MOE_STAGE_LAYER), ws, ws_bytes));
+  const LayerPackedWs lp = layer_packed_layout(d, ws);
+  const LayerWs& w = lp.w;
+  int32_t* ids = topk_ids_out ? topk_ids_out : w.topk_ids;
+  float* tw = topk_w_out ? topk_w_out : w.topk_w;
+  int32_t* counts = counts_out ? counts_out : w.counts;
+  int64_t* dropped = num_dropped_out ? num_dropped_out : w.num_dropped;
+  const bool cap = capacity_of(d) >= 0;
+  TRY(route_checks(d, x, w_router, b_router, nullptr, nullptr, ids, tw, w.topk_logit));
+  TRY(dispatch_checks(d, x, ids, w.topk_logit, counts, w.offsets, w.sorted_pairs, w.pair_row, w.x_sorted, dropped));
+  TRY(packed_ffn_checks(w.x_sorted, w.offsets, packed, w.y_sorted));
+  TRY(combine_checks(w.y_sorted, w.pair_row, tw, y));
+  TRY(opts_checks(d, opts));
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const DispatchScratch scr = carve_dispatch_scratch(d, w.dispatch);
+  RouteArgs ra{d, x, w_router, b_router, nullptr, nullptr, ids, tw, cap ? w.topk_logit : nullptr,
+               static_cast<float*>(w.route), scr.blk_all, s};
+  apply_opts(ra, d, opts);
+  TRY(launch_route(ra));
+  DispatchArgs da{d, x, ids, w.topk_logit, counts, w.offsets, w.sorted_pairs, w.pair_row, w.x_sorted, dropped,
+                  scr, capacity_of(d), true, s};
+  TRY(launch_dispatch(da));
+  PackedFfnArgs fa{d, w.x_sorted, w.offsets, packed, w.y_sorted, w.h, lp.scratch, max_pairs_of(d), s};
+  TRY(launch_packed_ffn(fa));
+  CombineArgs ca{d, w.y_sorted, w.pair_row, tw, y, s};
+  return launch_combine(ca);
+}
+
+moe_status moe_muon_workspace_size(const moe_muon_desc* m, size_t* bytes) {
+  TRY(muon_desc_checks(m));
+  if (bytes == nullptr) return set_error(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = muon_workspace_bytes(m);
+  return MOE_OK;
+}
+
+moe_status moe_orthogonalize(const moe_muon_desc* m, const void* g, void* o, void* ws, size_t ws_bytes, void* stream) {
+  CallScope scope;
+  TRY(muon_desc_checks(m));
+  REQUIRE_PTR(g, 16);
+  REQUIRE_PTR(o, 16);
+  TRY(check_ws_bytes(muon_workspace_bytes(m), ws, ws_bytes));
+  MuonArgs a = muon_args(m, ws, stream);
+  a.grad = g;
+  a.out = o;
+  return launch_muon(a);
+}
+
+moe_status moe_muon_update(const moe_muon_desc* m, const void* grad, float* momentum, float* master, void* weight,
+                           void* ws, size_t ws_bytes, void* stream) {
+  CallScope scope;
+  TRY(muon_desc_checks(m));
+  REQUIRE_PTR(grad, 16);
+  REQUIRE_PTR(momentum, 16);
+  OPTIONAL_PTR(master, 16);
+  REQUIRE_PTR(weight, 16);
+  TRY(check_ws_bytes(muon_workspace_bytes(m), ws, ws_bytes));
+  MuonArgs a = muon_args(m, ws, stream);
+  a.grad = grad;
+  a.momentum = momentum;
+  a.master = master;
+  a.out = weight;
+  return launch_muon(a);
 }
 
 }  // extern "C"

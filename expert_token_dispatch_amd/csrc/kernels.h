@@ -113,6 +113,32 @@ bool skinny_ffn_fits(const moe_layer_desc* d, int64_t max_pairs);
 moe_status launch_skinny_ffn(const FfnArgs& a);
 moe_status launch_general_ffn(const FfnArgs& a);
 
+// ---- 4-bit expert weights (packed_weights.hip) -------------------------------
+struct PackArgs {
+  int count, out, in;
+  int dtype, layout;  // of w
+  void* w;
+  void* codes;
+  void* scales;
+  hipStream_t s;
+};
+moe_status launch_pack(const char* name, const PackArgs& a);    // w -> codes, scales
+moe_status launch_unpack(const char* name, const PackArgs& a);  // codes, scales -> w
+
+struct PackedFfnArgs {
+  const moe_layer_desc* d;
+  const void* x_sorted;
+  const int32_t* offsets;
+  const moe_packed_experts* p;
+  void* y_sorted;
+  void* h;        // [P_max, I]
+  void* scratch;  // packed_ffn_scratch_bytes
+  int64_t max_pairs;
+  hipStream_t s;
+};
+size_t packed_ffn_scratch_bytes(const moe_layer_desc* d, int64_t max_pairs);
+moe_status launch_packed_ffn(const PackedFfnArgs& a);
+
 struct CombineArgs {
   const moe_layer_desc* d;
   const void* y_sorted;
@@ -209,5 +235,21 @@ struct DispatchBwdArgs {
 moe_status launch_dispatch_backward(const DispatchBwdArgs& a);
 // Zero `bytes` (a multiple of 4) at a 16-byte aligned device pointer, by a kernel.
 moe_status launch_zero(const char* name, void* p, size_t bytes, hipStream_t s);
+
+
+// ---- the weight update (newton_schulz.hip) -----------------------------------
+struct MuonArgs {
+  const moe_muon_desc* m;
+  float ca, cb, cc;          // coefficients of a step
+  const void* grad;          // [count, rows, cols] dtype
+  float* momentum = nullptr; // NULL: orthogonalise grad itself
+  float* master = nullptr;
+  void* out;                 // the orthogonalised gradient, or with momentum the weight
+  void* ws;                  // muon_workspace_bytes
+  hipStream_t s;
+};
+int64_t muon_matrix_bytes(const moe_muon_desc* m);  // one matrix in the working type, sides rounded up
+size_t muon_workspace_bytes(const moe_muon_desc* m);
+moe_status launch_muon(const MuonArgs& a);
 
 }  // namespace moe

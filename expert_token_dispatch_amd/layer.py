@@ -114,6 +114,43 @@ class MoELayer:
         L.moe_selection_bias_update(self.desc, counts, bias, gamma)
         return bias
 
+    # ---- experts in 4 bits -----------------------------------------------------
+    def pack_experts(self) -> L.PackedExperts:
+        """The experts' weights as 4-bit codes with a scale per 32 inputs, in new tensors."""
+        d = self.desc
+        Lc, H, I = d.local_count, d.hidden, d.intermediate
+        t = {}
+        for name, w, out, in_ in (("gate", self.w_gate, I, H), ("up", self.w_up, I, H), ("down", self.w_down, H, I)):
+            codes, scales = t[name + "_codes"], t[name + "_scales"] = (
+                self._empty((Lc, out, in_ // 2), torch.uint8), self._empty((Lc, out, in_ // 32), torch.uint8))
+            L.moe_pack_weights(w, codes, scales, weight_layout=d.weight_layout)
+        return L.make_packed_experts(t)
+
+    def packed_workspace(self, stage: int) -> torch.Tensor:
+        key = ("packed", stage)
+        if key not in self._ws:
+            n = L.moe_packed_workspace_size(self.desc, stage)
+            self._ws[key] = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
+        return self._ws[key]
+
+    def grouped_ffn_packed(self, x_sorted, offsets, packed):
+        """grouped_ffn on the weights that `packed` (pack_experts) stands for."""
+        d = self.desc
+        y_sorted = self._empty((max(self.max_pairs, 1), d.hidden), x_sorted.dtype)
+        L.moe_grouped_ffn_packed(d, x_sorted, offsets, packed, y_sorted, ws=self.packed_workspace(L.MOE_STAGE_FFN))
+        return y_sorted
+
+    def forward_packed(self, x, packed, y=None, topk_ids_out=None, topk_w_out=None, counts_out=None,
+                       num_dropped_out=None, opts=None):
+        """forward on packed experts; the layer's own expert weights are not read."""
+        d = self.desc
+        if y is None:
+            y = self._empty((d.num_tokens, d.hidden), x.dtype)
+        L.moe_layer_forward_packed(d, opts, x, self.w_router, self.b_router, packed, y,
+                                   self.packed_workspace(L.MOE_STAGE_LAYER), topk_ids_out, topk_w_out, counts_out,
+                                   num_dropped_out)
+        return y
+
     def staged(self, x, logits_in=None, opts=None):
         """The four stage calls one after another; returns every intermediate."""
         r = self.route(x, logits_in=logits_in, want_logits=True, want_topk_logit=True, opts=opts)
@@ -191,3 +228,29 @@ class MoELayer:
                              ws=self.workspace(L.MOE_STAGE_ROUTE_BACKWARD))
         L.moe_dispatch_backward(d, dxs, t["pair_row"], t["topk_ids"], dl, self.w_router, g["dx"])
         return {**g, "dy_sorted": dys, "dl": dl, "dx_sorted": dxs}
+
+    # ---- the weight update -------------------------------------------------------
+    MUON_WEIGHTS = ("w_gate", "w_up", "w_down")
+
+    def muon_state(self, master: bool = True) -> dict:
+        """Momentum (zeros) of the expert weights and, for bf16 layers with `master`, float32 copies of them."""
+        names = self.MUON_WEIGHTS
+        st = {n: torch.zeros(getattr(self, n).shape, dtype=torch.float32, device=self.device) for n in names}
+        m = {n: getattr(self, n).float() for n in names} if master and self.dtype == "bf16" else {}
+        return {"momentum": st, "master": m}
+
+    def muon_update(self, grads: dict, state: dict, lr: float, momentum: float = 0.95, nesterov: bool = True,
+                    weight_decay: float = 0.0, update_scale: Optional[float] = None, steps: int = 5):
+        """One Muon step on the expert weights, in place, from backward()'s gradients and muon_state().
+        update_scale: factor of the orthogonalised update, by default 0.2 sqrt(longer side), which
+        gives its entries the size of an Adam step's."""
+        for n in self.MUON_WEIGHTS:
+            w = getattr(self, n)
+            scale = 0.2 * max(w.shape[1:]) ** 0.5 if update_scale is None else update_scale
+            m = L.make_muon_desc(*w.shape, dtype=self.dtype, steps=steps, momentum=momentum, nesterov=nesterov, lr=lr,
+                                 update_scale=scale, weight_decay=weight_decay)
+            size = L.moe_muon_workspace_size(m)
+            ws = self._ws.get("muon")
+            if ws is None or ws.numel() < size:  # one workspace for the three stacks, which follow each other
+                ws = self._ws["muon"] = torch.empty(size, dtype=torch.uint8, device=self.device)
+            L.moe_muon_update(m, grads["d" + n], state["momentum"][n], w, ws, master=state["master"].get(n))

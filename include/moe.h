@@ -325,6 +325,65 @@ moe_status moe_layer_forward_ex(const moe_layer_desc* d, const moe_route_opts* o
                                 void* stream);
 
 /* ======================================================================== */
+/* Expert weights in 4 bits.                                                 */
+/*                                                                           */
+/* A decode step is bound by streaming the expert weights, so a serving      */
+/* layer may hold them as 4-bit codes with a power-of-two scale per 32       */
+/* inputs (the OCP microscaling format MXFP4), 17/32 byte a weight:          */
+/*   codes   [L, out, in/2] bytes: e2m1 codes, the lower input in the low    */
+/*           half; code c is +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}, bit 3 the sign   */
+/*   scales  [L, out, in/32] bytes: byte b stands for 2^(b - 127), 255 for    */
+/*           NaN                                                             */
+/* always by output, whatever layout the weights they come from have.  A     */
+/* weight is value * 2^(b - 127), exact in bfloat16 and in float32 (one       */
+/* below 2^-126 in magnitude may be taken as zero).                           */
+/* ======================================================================== */
+
+/* Packs a stack of `count` matrices.  Per 32 inputs of one output the scale is
+ * 2^e, e = floor(log2 max|w|) - 2 held to [-127, 127]; every w / 2^e goes to the
+ * nearest code, ties to the even code, at most 6 in magnitude.  A group with a NaN
+ * or an infinity gets scale byte 255.
+ *   count >= 1 (at most 65535); out > 0, a multiple of 8; in > 0, a multiple of 32
+ *   w       device dtype, [count, out, in] (MOE_WEIGHTS_OUT_IN) or [count, in, out]
+ *   codes   device bytes out [count, out, in/2];  scales device bytes out [count, out, in/32] */
+moe_status moe_pack_weights(int32_t count, int32_t out, int32_t in, int32_t dtype, int32_t weight_layout,
+                            const void* w, void* codes, void* scales, void* stream);
+
+/* The values that codes and scales stand for, in the given type and layout.
+ * Arguments as moe_pack_weights; w is written. */
+moe_status moe_unpack_weights(int32_t count, int32_t out, int32_t in, int32_t dtype, int32_t weight_layout,
+                              const void* codes, const void* scales, void* w, void* stream);
+
+/* The local experts' packed weights, device pointers to bytes (codes 16-byte
+ * aligned).  desc->weight_layout does not matter to them. */
+typedef struct moe_packed_experts {
+  const void* gate_codes;  /* [L, I, H/2] */
+  const void* gate_scales; /* [L, I, H/32] */
+  const void* up_codes;    /* [L, I, H/2] */
+  const void* up_scales;   /* [L, I, H/32] */
+  const void* down_codes;  /* [L, H, I/2] */
+  const void* down_scales; /* [L, H, I/32] */
+} moe_packed_experts;
+
+/* Workspace bytes of the calls below: stage MOE_STAGE_FFN for
+ * moe_grouped_ffn_packed, MOE_STAGE_LAYER for moe_layer_forward_packed.
+ * MOE_ERR_UNSUPPORTED unless hidden and intermediate are multiples of 32. */
+moe_status moe_packed_workspace_size(const moe_layer_desc* d, int32_t stage, size_t* bytes);
+
+/* moe_grouped_ffn on packed experts: the same sums (float32) and roundings (h once,
+ * y once) over the weights that the codes stand for; x_sorted, y_sorted dtype.
+ * Errors as moe_grouped_ffn, and MOE_ERR_UNSUPPORTED as above. */
+moe_status moe_grouped_ffn_packed(const moe_layer_desc* d, const void* x_sorted, const int32_t* offsets,
+                                  const moe_packed_experts* packed, void* y_sorted, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+/* moe_layer_forward_ex on packed experts (the router stays in dtype). */
+moe_status moe_layer_forward_packed(const moe_layer_desc* d, const moe_route_opts* opts, const void* x,
+                                    const void* w_router, const float* b_router, const moe_packed_experts* packed,
+                                    void* y, int32_t* topk_ids_out, float* topk_w_out, int32_t* counts_out,
+                                    int64_t* num_dropped_out, void* ws, size_t ws_bytes, void* stream);
+
+/* ======================================================================== */
 /* Training: the backward pass.                                              */
 /*                                                                           */
 /* Transformers "Expert parallelism", section "Token dispatch": every rank   */
@@ -433,6 +492,72 @@ moe_status moe_layer_backward(const moe_layer_desc* d, const void* x, const void
                               const void* w_up, const void* w_down, const moe_saved* saved, const void* dy,
                               void* dx, void* dw_router, float* db_router, void* dw_gate, void* dw_up,
                               void* dw_down, void* ws, size_t ws_bytes, void* stream);
+
+/* ======================================================================== */
+/* Training: the weight update.                                              */
+/*                                                                           */
+/* The Muon update of a stack of matrices, such as an expert weight and its  */
+/* gradient from moe_layer_backward in either layout: momentum, then each    */
+/* matrix of the stack orthogonalised by Newton-Schulz steps, then the step  */
+/* on the weight.  With m the shorter side of a matrix U,                    */
+/*   X_0 = U / (|U|_F + eps)                                                 */
+/*   X_{i+1} = (a I + b A + c A^2) X_i,  A = X_i X_i^T  (m x m; for a tall    */
+/*   matrix A = X_i^T X_i on the right)                                      */
+/* which takes every singular value s of X to s (a + b s^2 + c s^4) and       */
+/* leaves the singular vectors.  A zero matrix stays zero.                    */
+/* ======================================================================== */
+
+/*   count, rows, cols  the stack [count, rows, cols], each >= 1 (count at most 65535)
+ *   dtype              moe_dtype of the gradient, the weight and moe_orthogonalize's result
+ *   steps              Newton-Schulz steps, 1..10
+ *   coef_a, b, c       coefficients of a step, 0 < a <= 4 (all three 0: 3.4445, -4.7750,
+ *                      2.0315).  Singular values start in [0, 1]; MOE_ERR_INVALID_ARG when a
+ *                      step could take one past 3
+ *   eps                added to the Frobenius norm, >= 0
+ *   momentum           mu in [0, 1);  nesterov: 0 or 1
+ *   lr, update_scale, weight_decay   finite factors of the step */
+typedef struct moe_muon_desc {
+  int32_t count;
+  int32_t rows;
+  int32_t cols;
+  int32_t dtype;
+  int32_t steps;
+  float coef_a;
+  float coef_b;
+  float coef_c;
+  float eps;
+  float momentum;
+  int32_t nesterov;
+  float lr;
+  float update_scale;
+  float weight_decay;
+} moe_muon_desc;
+
+/* Workspace bytes of the two calls below.  MOE_ERR_UNSUPPORTED when one matrix,
+ * its sides rounded up to multiples of 64, takes 4 GiB or more in the working type
+ * (2 bytes an element for MOE_BF16, 4 for MOE_F32). */
+moe_status moe_muon_workspace_size(const moe_muon_desc* m, size_t* bytes);
+
+/* o = the orthogonalised g, matrix by matrix; eps, steps and coefficients from m, the
+ * other fields are not used (but checked).  MOE_BF16: the products run on float16
+ * operands scaled by powers of two (X_0 as the sum of two) with float32 sums, the
+ * result is rounded once.  MOE_F32: float32 throughout.  o may be g.
+ *   g   device [count, rows, cols] dtype;  o  device [count, rows, cols] dtype out
+ *   ws  device workspace of moe_muon_workspace_size bytes */
+moe_status moe_orthogonalize(const moe_muon_desc* m, const void* g, void* o, void* ws, size_t ws_bytes, void* stream);
+
+/* One update step, in place:
+ *   M = mu M + grad;  U = grad + mu M (nesterov) or M;  O = orthogonalised U
+ *   W = W (1 - lr weight_decay) - lr update_scale O
+ * M, U and the step on W are float32.  With master weights W is `master` and weight
+ * receives it rounded; without (master NULL) W is `weight` itself, rounded once.
+ *   grad      device [count, rows, cols] dtype
+ *   momentum  device [count, rows, cols] float32, updated
+ *   master    device [count, rows, cols] float32, updated, or NULL
+ *   weight    device [count, rows, cols] dtype, updated
+ *   ws        device workspace of moe_muon_workspace_size bytes */
+moe_status moe_muon_update(const moe_muon_desc* m, const void* grad, float* momentum, float* master, void* weight,
+                           void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
