@@ -1,19 +1,24 @@
 // The packed experts' feed-forward for segments of a few rows (decode-sized batches).
 //
 // The product is bound by streaming the 4-bit weights, 17/32 byte each, so the work is
-// split over weight rows and, inside a block, over K.  A wave owns two streams of 16
+// split over weight rows and, where those are few, over K.  A wave owns two streams of 16
 // weight rows: the gate and the up rows of 16 output columns, or two neighbouring groups
 // of 16 output columns of the down product.  Of a block's four waves WK share one pair of
-// streams, each a K range of its own (summed in LDS in a fixed order), and 4 / WK work on
+// streams, each every WK-th step of K (summed in LDS in a fixed order), and 4 / WK work on
 // neighbouring columns.
 //
 // A step is 128 k: lane l reads 16 bytes (32 codes, one scale group) of row l % 16 at
 // k group l / 16, so a wave instruction reads 16 rows x 64 bytes.  The MFMA sums over k in
 // any order as long as both operands agree, so MFMA j of a step simply takes the lane's
 // codes 8j .. 8j+7 (k = 32 (l / 16) + 8 j ..) and the token row's elements at the same k.
-// The codes turn into bf16 with their scale applied by v_cvt_scalef32_pk_bf16_fp4, two a
-// time, exactly; a step is 16 of them and four MFMAs 16x16x32 per stream and 16 rows.
-// kBatch steps are loaded before the first is used; several waves a SIMD cover the rest.
+// The codes turn into bf16 with their scale applied by v_cvt_scalef32_pk_bf16_fp4, two at
+// a time, exactly; a step is 16 of them and four MFMAs 16x16x32 per stream and 16 rows.
+//
+// The weights of the next four steps are in flight in registers while a step is
+// multiplied.  One load brings a row's scales of four steps (lane group g holds step g's
+// four bytes, handed round by a lane permute).  The token rows go through LDS, a chunk of
+// four steps per wave at a time, double buffered: read straight from memory, 64 bytes a
+// lane and step, they would take the address units longer than the weights.
 #include <math.h>
 
 #include <algorithm>
@@ -24,9 +29,8 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256, kMaxRowBlocks = 4;
+constexpr int kThreads = 256;
 constexpr int kStep = 128;   // k of a step
-constexpr int kBatch = 4;    // steps loaded ahead
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
@@ -58,7 +62,15 @@ __device__ __forceinline__ int expert_of_slot(const int32_t* __restrict__ offset
   return -1;
 }
 
-template <int NMAT, int WK>
+// k of a chunk, and a row's bytes of it in LDS.  16-byte piece c of row r sits at piece
+// c ^ (r % 16), so the reads of 16 rows at one piece cover all banks.
+template <int WK>
+struct Chunk {
+  static constexpr int kAhead = WK == 4 ? 2 : 4;  // steps of a wave: a chunk's, and in flight
+  static constexpr int kSteps = WK * kAhead, kK = kSteps * kStep, kRowBytes = kK * 2, kPieces = kRowBytes / 16;
+};
+
+template <int NMAT, int WK, int NRB>
 __global__ __launch_bounds__(kThreads) void packed_gemm_kernel(const bf16_t* __restrict__ A,
                                                                const int32_t* __restrict__ offsets,
                                                                const uint8_t* __restrict__ q0,
@@ -66,8 +78,12 @@ __global__ __launch_bounds__(kThreads) void packed_gemm_kernel(const bf16_t* __r
                                                                const uint8_t* __restrict__ q1,
                                                                const uint8_t* __restrict__ s1, bf16_t* __restrict__ C,
                                                                int L, int N, int K) {
-  constexpr int WN = 4 / WK;
+  using Ch = Chunk<WK>;
+  constexpr int kAhead = Ch::kAhead;
+  constexpr int WN = 4 / WK, kRows = 16 * NRB;
   constexpr int kWaveCols = NMAT == 2 ? 16 : 32;
+  constexpr int kStage = kRows * Ch::kPieces / kThreads;  // 16-byte pieces of a chunk per thread
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int expert = __builtin_amdgcn_readfirstlane(expert_of_slot(offsets, L, blockIdx.y));
   if (expert < 0) return;
   const int seg0 = offsets[expert], seg_n = offsets[expert + 1] - seg0;
@@ -77,98 +93,157 @@ __global__ __launch_bounds__(kThreads) void packed_gemm_kernel(const bf16_t* __r
   const int lr = lane & 15, kg = lane >> 4;
   // rows past N repeat row N - 1 (never stored)
   const int r0 = min(col0 + lr, N - 1), r1 = NMAT == 2 ? r0 : min(col0 + 16 + lr, N - 1);
-  const size_t row0 = size_t(expert) * N + r0, row1 = size_t(expert) * N + r1;
-  const uint8_t* wq[2] = {q0 + row0 * (K / 2) + 16 * kg, (NMAT == 2 ? q1 : q0) + row1 * (K / 2) + 16 * kg};
-  const uint8_t* ws[2] = {s0 + row0 * (K / 32) + kg, (NMAT == 2 ? s1 : s0) + row1 * (K / 32) + kg};
-  // this wave's steps of K: the last one of all may be cut short (K is a multiple of 32)
-  const int steps = (K + kStep - 1) / kStep;
-  const int st0 = steps * wk / WK, st1 = steps * (wk + 1) / WK;
+  // codes by buffer loads over the expert's matrix: a byte offset per lane and stream, the
+  // step in the scalar offset; what lies behind the matrix reads as zero
+  const uint32_t qbytes = uint32_t(N) * uint32_t(K / 2);
+  const size_t eq = size_t(expert) * N * (K / 2), es = size_t(expert) * N * (K / 32);
+  const __amdgpu_buffer_rsrc_t rq[2] = {
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(q0 + eq), 0, qbytes, kRsrcFlags),
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>((NMAT == 2 ? q1 : q0) + eq), 0, qbytes, kRsrcFlags)};
+  const uint32_t vq[2] = {uint32_t(r0) * uint32_t(K / 2) + 16u * kg, uint32_t(r1) * uint32_t(K / 2) + 16u * kg};
+  const uint8_t* ws[2] = {s0 + es + size_t(r0) * (K / 32), (NMAT == 2 ? s1 : s0) + es + size_t(r1) * (K / 32)};
+  const int chunks = (K + Ch::kK - 1) / Ch::kK;
+  const int groups = K / 32;
 
-  __shared__ f32x4_t red[WK > 1 ? WN * (WK - 1) * 2 * kMaxRowBlocks * 64 : 1];
-
-  for (int m0 = 0; m0 < seg_n; m0 += 16 * kMaxRowBlocks) {
-    const int nrb = min(kMaxRowBlocks, (seg_n - m0 + 15) / 16);
-    const bf16_t* arow[kMaxRowBlocks];
+  // this wave's u-th step of chunk c is step c * kSteps + u * WK + wk of K.  Behind the last
+  // k of a row come the next row's codes: their scales are taken as 2^-127 and the token
+  // rows are zero there, so they add nothing.
+  u32x4_t w[kAhead][2];
+  uint32_t sc[2];
+  auto load_w = [&](int c, int u) {
+    const int st = c * Ch::kSteps + u * WK + wk;
+    if (st * kStep >= K) {  // no such step: zeros
+      w[u][0] = w[u][1] = u32x4_t{0, 0, 0, 0};
+      return;
+    }
 #pragma unroll
-    for (int rb = 0; rb < kMaxRowBlocks; ++rb)
-      arow[rb] = A + size_t(seg0 + min(m0 + rb * 16 + lr, seg_n - 1)) * K + 32 * kg;
-    f32x4_t acc[2][kMaxRowBlocks];
+    for (int m = 0; m < 2; ++m)
+      w[u][m] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rq[m], vq[m], uint32_t(st) * (kStep / 2), 0));
+  };
+  // lane group g: the four scale bytes of the wave's step g of the chunk
+  auto load_s = [&](int c) {
+    const int g0 = (c * Ch::kSteps + (kg % kAhead) * WK + wk) * (kStep / 32);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      uint32_t v = 0;
+      if (g0 + 4 <= groups) {
+        __builtin_memcpy(&v, ws[m] + g0, 4);
+      } else {
+        for (int i = 0; i < 3; ++i)
+          if (g0 + i < groups) v |= uint32_t(ws[m][g0 + i]) << (8 * i);
+      }
+      sc[m] = v;
+    }
+  };
+
+  // the lane's pieces of a token row: piece 16 s + (4 kg + j) ^ lr of row lr for MFMA j of step s
+  int aoff[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) aoff[j] = lr * Ch::kRowBytes + wk * 256 + (((4 * kg + j) ^ lr) * 16);
+  constexpr int kWpr = Ch::kPieces / 64;                      // waves per row of a chunk being staged
+  const int srow = wave / kWpr, spart = wave % kWpr;          // this wave stages rows srow, srow + 4 / kWpr, ..
+  const int spiece = spart * 64 + lane;
+
+  for (int m0 = 0; m0 < seg_n; m0 += kRows) {
+    const int n = min(kRows, seg_n - m0);
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<bf16_t*>(A + size_t(seg0 + m0) * K), 0, uint32_t(n) * uint32_t(K) * 2u, kRsrcFlags);
+    u32x4_t stage[kStage];
+    auto load_a = [&](int c) {
+      // lanes past the end of the row ask for what lies behind the buffer: zeros
+      const uint32_t vo = c * Ch::kK + spiece * 8 < K ? uint32_t(spiece) * 16u : 0xFFFFFFF0u;
+#pragma unroll
+      for (int i = 0; i < kStage; ++i) {
+        const int r = srow + i * (4 / kWpr);
+        if (r < n)
+          stage[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                     ra, vo, uint32_t(r) * uint32_t(K) * 2u + uint32_t(c) * Ch::kRowBytes, 0));
+      }
+    };
+    auto store_a = [&](int c) {
+      char* buf = lds + (c & 1) * kRows * Ch::kRowBytes;
+#pragma unroll
+      for (int i = 0; i < kStage; ++i) {
+        const int r = srow + i * (4 / kWpr);
+        if (r < n) *reinterpret_cast<u32x4_t*>(buf + r * Ch::kRowBytes + (spiece ^ (r & 15)) * 16) = stage[i];
+      }
+    };
+    f32x4_t acc[2][NRB];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int rb = 0; rb < kMaxRowBlocks; ++rb) acc[m][rb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int rb = 0; rb < NRB; ++rb) acc[m][rb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    for (int st = st0; st < st1; st += kBatch) {
-      u32x4_t w[2][kBatch];
-      uint32_t sb[2][kBatch];
-      u32x4_t a0[kBatch][4];
+    load_a(0);
+    load_s(0);
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int k0 = (st + u) * kStep;
-        // a lane's 32 k are inside K as a whole or outside; outside both operands are zero
-        const bool in = st + u < st1 && k0 + 32 * kg < K;
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          w[m][u] = in ? *reinterpret_cast<const u32x4_t*>(wq[m] + k0 / 2) : u32x4_t{0, 0, 0, 0};
-          sb[m][u] = in ? ws[m][k0 / 32] : 0u;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          a0[u][j] = in ? *reinterpret_cast<const u32x4_t*>(arow[0] + k0 + 8 * j) : u32x4_t{0, 0, 0, 0};
+    for (int u = 0; u < kAhead; ++u) load_w(0, u);
+    if (m0 > 0) __syncthreads();  // the LDS of the rows before is read out
+    store_a(0);
+    __syncthreads();
+    for (int c = 0; c < chunks; ++c) {
+      const char* buf = lds + (c & 1) * kRows * Ch::kRowBytes;
+      const bool more = c + 1 < chunks;
+      const uint32_t sc0 = sc[0], sc1 = sc[1];
+      if (more) {
+        load_a(c + 1);
+        load_s(c + 1);
       }
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (st + u < st1) {
-          const int k0 = (st + u) * kStep;
-          const bool in = k0 + 32 * kg < K;
-          const float f0 = __uint_as_float(sb[0][u] << 23), f1 = __uint_as_float(sb[1][u] << 23);
+      for (int u = 0; u < kAhead; ++u) {
+        // the scales of step u sit in lane group u, byte kg
+        const uint32_t b0 = uint32_t(__shfl(int(sc0), 16 * u + lr, 64)) >> (8 * kg);
+        const uint32_t b1 = uint32_t(__shfl(int(sc1), 16 * u + lr, 64)) >> (8 * kg);
+        const float f0 = __uint_as_float((b0 & 0xFFu) << 23), f1 = __uint_as_float((b1 & 0xFFu) << 23);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const bf16x8_t b0 = decode_frag(w[0][u][j], f0), b1 = decode_frag(w[1][u][j], f1);
+        for (int j = 0; j < 4; ++j) {
+          const bf16x8_t v0 = decode_frag(w[u][0][j], f0), v1 = decode_frag(w[u][1][j], f1);
+          // rows past n hold what the LDS held: they reach only outputs that are never stored
 #pragma unroll
-            for (int rb = 0; rb < kMaxRowBlocks; ++rb) {
-              if (rb < nrb) {
-                u32x4_t av = a0[u][j];
-                if (rb > 0) av = in ? *reinterpret_cast<const u32x4_t*>(arow[rb] + k0 + 8 * j) : u32x4_t{0, 0, 0, 0};
-                const bf16x8_t a = __builtin_bit_cast(bf16x8_t, av);
-                acc[0][rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b0, acc[0][rb], 0, 0, 0);
-                acc[1][rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b1, acc[1][rb], 0, 0, 0);
-              }
-            }
+          for (int rb = 0; rb < NRB; ++rb) {
+            const bf16x8_t a =
+                *reinterpret_cast<const bf16x8_t*>(buf + aoff[j] + rb * 16 * Ch::kRowBytes + u * WK * 256);
+            acc[0][rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, v0, acc[0][rb], 0, 0, 0);
+            acc[1][rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, v1, acc[1][rb], 0, 0, 0);
           }
         }
+        if (more) load_w(c + 1, u);
+        __builtin_amdgcn_sched_barrier(0);  // a step's reads stay in the step: registers
+      }
+      if (more) {
+        store_a(c + 1);
+        __syncthreads();
       }
     }
-    // the K ranges' sums, in the order of the ranges
+    // the waves' sums of one pair of streams, in the order of the waves
     if constexpr (WK > 1) {
-      f32x4_t* mine = red + wn * (WK - 1) * 2 * kMaxRowBlocks * 64;
-      if (m0 > 0) __syncthreads();
+      __syncthreads();
+      f32x4_t* mine = reinterpret_cast<f32x4_t*>(lds) + wn * (WK - 1) * 2 * NRB * 64;
       if (wk > 0) {
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int rb = 0; rb < kMaxRowBlocks; ++rb)
-            if (rb < nrb) mine[(((wk - 1) * 2 + m) * kMaxRowBlocks + rb) * 64 + lane] = acc[m][rb];
+          for (int rb = 0; rb < NRB; ++rb) mine[(((wk - 1) * 2 + m) * NRB + rb) * 64 + lane] = acc[m][rb];
       }
       __syncthreads();
       if (wk == 0) {
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int rb = 0; rb < kMaxRowBlocks; ++rb)
-            if (rb < nrb)
-              for (int k = 0; k < WK - 1; ++k) acc[m][rb] += mine[((k * 2 + m) * kMaxRowBlocks + rb) * 64 + lane];
+          for (int rb = 0; rb < NRB; ++rb)
+#pragma unroll
+            for (int k = 0; k < WK - 1; ++k) acc[m][rb] += mine[((k * 2 + m) * NRB + rb) * 64 + lane];
       }
     }
     // lane -> weight row (column of the output) lane & 15, register i -> token row 4 (lane / 16) + i
     if (wk == 0) {
 #pragma unroll
-      for (int rb = 0; rb < kMaxRowBlocks; ++rb) {
+      for (int rb = 0; rb < NRB; ++rb) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = m0 + rb * 16 + 4 * kg + i;
-          if (rb < nrb && r < seg_n) {
-            bf16_t* crow = C + size_t(seg0 + r) * N;
+          const int r = rb * 16 + 4 * kg + i;
+          if (r < n) {
+            bf16_t* crow = C + size_t(seg0 + m0 + r) * N;
             if (NMAT == 2) {
               if (col0 + lr < N) crow[col0 + lr] = f32_to_bf16(silu(acc[0][rb][i]) * acc[1][rb][i]);
             } else {
@@ -183,29 +258,52 @@ __global__ __launch_bounds__(kThreads) void packed_gemm_kernel(const bf16_t* __r
   }
 }
 
-template <int NMAT, int WK>
+template <int NMAT, int WK, int NRB>
 moe_status launch_wk(const char* name, const bf16_t* A, const int32_t* offsets, const void* q0, const void* s0,
                      const void* q1, const void* s1, bf16_t* C, int L, int N, int K, int64_t max_pairs, hipStream_t s) {
   constexpr int cols = (NMAT == 2 ? 16 : 32) * (4 / WK);
   const dim3 grid(unsigned((N + cols - 1) / cols), unsigned(std::min<int64_t>(L, max_pairs)));
-  MOE_LAUNCH(name, (packed_gemm_kernel<NMAT, WK>), grid, dim3(kThreads), 0, s, A, offsets,
-             static_cast<const uint8_t*>(q0), static_cast<const uint8_t*>(s0), static_cast<const uint8_t*>(q1),
-             static_cast<const uint8_t*>(s1), C, L, N, K);
+  auto kern = packed_gemm_kernel<NMAT, WK, NRB>;
+  constexpr int kBuf = 16 * NRB * Chunk<WK>::kRowBytes;
+  constexpr int kRed = 4 * 2 * NRB * 1024;  // an upper bound of the waves' sums
+  static_assert(kRed <= kBuf, "the sums fit in one buffer");
+  const int lds = K > Chunk<WK>::kK ? 2 * kBuf : kBuf;
+  if (lds > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, 2 * kBuf);
+    if (e != hipSuccess) return set_error(MOE_ERR_HIP, "%s: LDS attribute: %s", name, hipGetErrorString(e));
+  }
+  MOE_LAUNCH(name, kern, grid, dim3(kThreads), lds, s, A, offsets, static_cast<const uint8_t*>(q0),
+             static_cast<const uint8_t*>(s0), static_cast<const uint8_t*>(q1), static_cast<const uint8_t*>(s1), C, L, N,
+             K);
   return MOE_OK;
 }
 
-// Waves along K: four from eight steps of 128 on (two steps or more each), else two.
+// Waves along K: as many as it takes for two blocks a CU, given the experts that can have
+// rows, while every wave keeps two steps.
 template <int NMAT>
 moe_status launch(const char* name, const bf16_t* A, const int32_t* offsets, const void* q0, const void* s0,
                   const void* q1, const void* s1, bf16_t* C, int L, int N, int K, int64_t max_pairs, hipStream_t s) {
-  if (K >= 8 * kStep) return launch_wk<NMAT, 4>(name, A, offsets, q0, s0, q1, s1, C, L, N, K, max_pairs, s);
-  return launch_wk<NMAT, 2>(name, A, offsets, q0, s0, q1, s1, C, L, N, K, max_pairs, s);
+  constexpr int kCols = NMAT == 2 ? 64 : 128;
+  const int64_t blocks = (N + kCols - 1) / kCols * std::min<int64_t>(L, max_pairs);
+  const int steps = (K + kStep - 1) / kStep;
+  const bool many = max_pairs > 8 * int64_t(L);
+#define MOE_PACKED(WK_, NRB_) \
+  launch_wk<NMAT, WK_, NRB_>(name, A, offsets, q0, s0, q1, s1, C, L, N, K, max_pairs, s)
+  if (many) return MOE_PACKED(1, 2);
+  if (blocks < 256 && steps >= 8) return MOE_PACKED(4, 1);
+  if (blocks < 512 && steps >= 4) return MOE_PACKED(2, 1);
+  return MOE_PACKED(1, 1);
+#undef MOE_PACKED
 }
 
 }  // namespace
 
 bool packed_skinny_fits(const moe_layer_desc* d, int64_t max_pairs) {
-  return d->dtype == MOE_BF16 && max_pairs <= int64_t(32) * d->local_count;
+  // an expert's codes and 32 of its rows are addressed with 32-bit byte offsets
+  const int64_t H = d->hidden, I = d->intermediate;
+  return d->dtype == MOE_BF16 && max_pairs <= int64_t(32) * d->local_count && H * I / 2 < (int64_t(1) << 32) - 16 &&
+         std::max(H, I) * 64 < (int64_t(1) << 32) - 16;
 }
 
 moe_status launch_packed_skinny(const PackedFfnArgs& a) {
