@@ -7,10 +7,10 @@
 // Steps on the m x m side.  p(A_0), p(A_1), ... are polynomials of A_0: they commute and
 // are symmetric.  So a phase of several steps needs X only at its ends:
 //   A_0 = X X^T;  P_j = p(A_j),  Q_{j+1} = P_j Q_j,  A_{j+1} = P_j (P_j A_j);  X <- Q X.
-// P and Q are held without their multiples of I: P = a I + P', Q = q I + Q' with q = a^j,
-// so every product is one of P' or Q' plus multiples of matrices at hand, added in float32
-// (a I inside P would be rounded alike on the whole diagonal: 4% off for a matrix of rank
-// one, whose large singular value lives on the difference of a and the rest).
+// The m x m matrices are held as a float32 diagonal and the rest, zero on its diagonal: the
+// multiples of I that P and Q carry (a^3 = 41) stand beside large singular values' p of
+// 0.7, and rounding them with the rest would be rounding the difference.  With U = D_u + U'
+// a product is U V = U' V' + D_u V' + U' D_v + D_u D_v, the last three in the epilogue.
 // Every m x m product is symmetric: its upper triangle of tiles is computed and mirrored.
 // In units of m^3 multiply-adds (r the ratio of the sides) five single steps cost
 // 5 (3 r + 1), a phase of three and one of two 6 r + 14: the same at r = 1, two thirds
@@ -26,7 +26,7 @@
 // steps only X_0 is such an X.  Phases are at most three steps long, since rounding errors
 // of A grow by up to a^2 a step in the directions where A is small; they average out over
 // the shorter side (simulated error of the result, 0.16% of it the bfloat16 result's own:
-// 0.9% at 64, 0.4% at 128, 0.25% at 512, against 0.2% in single steps), so matrices with a
+// 0.7% at 64, 0.28% at 128, 0.2% at 512, against 0.18% in single steps), so matrices with a
 // shorter side of up to kSingleSteps take single steps, where the launches count more
 // than the products.  Float32 layers run on float32 operands in single steps (a phase
 // would double the error).
@@ -34,7 +34,7 @@
 
 #include <algorithm>
 
-#include "ffn_common.h"
+#include "big_tile.h"
 #include "kernels.h"
 
 namespace moe {
@@ -47,7 +47,7 @@ constexpr int kPad = 64;       // sides of the working matrices are multiples of
 constexpr int kThreads = 256;
 
 // Scales of the working values.  Singular values are at most 3 (the coefficients are
-// checked), so |X| <= 3, |A| <= 9, and |P'|, |Q'| <= a^3 <= 64 (up to a small factor): the
+// checked), so |X| <= 3, |A| <= 9, and |P|, |Q| <= a^3 <= 64 (up to a small factor): the
 // largest stored values are 3 * 2^14, 9 * 2^12 and 64 * 2^9, below float16's 65504.
 template <typename T> struct Scale;
 template <> struct Scale<f16_t> { static constexpr int x = 14, a = 12, q = 9; };
@@ -64,7 +64,7 @@ struct Plan {
   size_t x_bytes, q_bytes;      // one stack of X, of m x m matrices
   int nblk;                     // partial sums of squares per matrix
   bool single;                  // phases of one step (see the top of the file)
-  size_t o_part, o_x[4], o_q[5], bytes;
+  size_t o_part, o_x[4], o_q[5], o_d[5], bytes;
 };
 
 constexpr int kSingleSteps = 256;
@@ -99,7 +99,10 @@ Plan make_plan(const moe_muon_desc* m) {
   const bool split = m->dtype == MOE_BF16;
   const int xs = split ? (p.single ? 4 : 3) : 2;
   for (int i = 0; i < xs; ++i) p.o_x[i] = take(p.x_bytes);
-  for (int i = 0; i < (p.single ? 2 : 5); ++i) p.o_q[i] = take(p.q_bytes);
+  for (int i = 0; i < (p.single ? 2 : 5); ++i) {
+    p.o_q[i] = take(p.q_bytes);
+    p.o_d[i] = take(size_t(p.count) * p.mp * sizeof(float));
+  }
   p.bytes = o;
   return p;
 }
@@ -169,28 +172,47 @@ __global__ __launch_bounds__(kThreads) void start_kernel(const T* __restrict__ g
 }
 
 // ---- products ------------------------------------------------------------------------
-// C = alpha A B (+ beta D + beta2 D2) for every matrix of the stack.
+// An m x m matrix of the stack: the diagonal in float32, the rest (diagonal zero) scaled.
+template <typename W> struct Sym {
+  W* o;
+  float* d;
+};
+
+// One product for every matrix of the stack, sum = A B (+ A2 B2), and what is made of it.
 struct Product {
   const void* a;      // AK: k-major, element (m, k) at a[k * lda + m]; else m-major
   const void* b;      // BK: k-major, element (n, k) at b[k * ldb + n]; else n-major
-  const void* a2;     // second pair of operands, added (NULL: none)
+  const void* a2;     // the second pair of operands (NULL: none)
   const void* b2;
-  const void* d;      // added, elements where C's are (NULL: none)
-  const void* d2;
   void* c;
   void* c2;           // what C's rounding leaves (NULL: not kept)
-  size_t sa, sb, sc;  // elements from one matrix of the stack to the next 
+  size_t sa, sb, sc;  // elements from one matrix of the stack to the next
   int m, n, k, lda, ldb, ldc;
-  float alpha, beta, beta2;
-  int sym;            // C is symmetric: upper tiles only, mirrored
-  // the last product's epilogue: the result, or the step on the weight
+  float alpha;
+  // kGram, kSquare: C is symmetric, its upper tiles are formed and mirrored.  Off the diagonal
+  //   C_ij = alpha sum + (g0 + g1 du_i) V_ij + h1 dv_j U_ij   (kGram: alpha sum)
+  // on it, in float32, dc_i = alpha_d sum + k0 + k1 du_i + k2 du_i dv_i   (kGram: alpha_d sum)
+  const void* u;
+  const void* v;
+  const float* du;
+  const float* dv;
+  float* dc;
+  float g0, g1, h1, alpha_d, k0, k1, k2;
+  // kApply and the last product: C = alpha sum + beta d (x + x2), d by row, or by column
+  const void* x;
+  const void* x2;
+  const float* dq;
+  float beta;
+  int dq_col;
+  int mp;             // elements from one matrix's diagonal to the next
+  // the last product: the result, or the step on the weight
   void* out;
   float* master;
   int rows, cols;
   float keep, step;   // W = keep W - step C
 };
 
-enum OutKind { kInner = 0, kResult = 1, kUpdate = 2 };
+enum Kind { kGram = 0, kSquare = 1, kApply = 2, kResult = 3, kUpdate = 4 };
 
 template <typename W> struct Mma;
 template <> struct Mma<f16_t> {
@@ -263,16 +285,30 @@ struct OpTile {
   }
 };
 
+// Element (row, col) of the last product into the user's result or weight.
+template <typename T, int KIND>
+__device__ __forceinline__ void put_last(const Product& p, size_t z, int row, int col, float v) {
+  const size_t at = z * p.rows * p.cols + size_t(row) * p.cols + col;
+  T* o = static_cast<T*>(p.out) + at;
+  if constexpr (KIND == kUpdate) {
+    const float w = p.master != nullptr ? p.master[at] : Elem<T>::to_f32(*o);
+    v = w * p.keep - v * p.step;
+    if (p.master != nullptr) p.master[at] = v;
+  }
+  *o = Elem<T>::from_f32(v);
+}
+
 // 64 x 64 tiles, four waves 2 x 2, one MFMA 32x32 block each; the next k slice is in
 // registers while this one is multiplied.  Sides are multiples of 64, so no access needs
 // a bound but the last product's into the user's matrix.
-template <typename W, typename T, bool AK, bool BK, int OUT>
+template <typename W, typename T, bool AK, bool BK, int KIND>
 __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
   using TA = OpTile<W, AK>;
   using TB = OpTile<W, BK>;
   constexpr int kBK = TA::kBK;
+  constexpr bool kSym = KIND == kGram || KIND == kSquare;
   const int tm = blockIdx.y, tn = blockIdx.x;
-  if (p.sym && tn < tm) return;
+  if (kSym && tn < tm) return;
   const size_t z = blockIdx.z;
   __shared__ __attribute__((aligned(16))) W as[TA::kElems];
   __shared__ __attribute__((aligned(16))) W bs[TB::kElems];
@@ -309,41 +345,293 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
   }
   // lane -> column (lane & 31), register r -> row 8 (r / 4) + 4 (lane / 32) + r % 4
   const int col = tn * 64 + wn + (lane & 31);
+  const float* du = p.du + z * p.mp;
+  const float* dv = p.dv + z * p.mp;
+  const float* dq = p.dq + z * p.mp;
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
     const int row = tm * 64 + wm + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
     const size_t ci = z * p.sc + size_t(row) * p.ldc + col;
+    W* c = static_cast<W*>(p.c);
     float v = p.alpha * acc[r];
-    if (p.d2 != nullptr) v += p.beta2 * float(static_cast<const W*>(p.d2)[ci]);
-    if (p.d != nullptr) v += p.beta * float(static_cast<const W*>(p.d)[ci]);
-    if constexpr (OUT == kInner) {
-      const W h = W(v);
-      static_cast<W*>(p.c)[ci] = h;
-      if (p.c2 != nullptr) static_cast<W*>(p.c2)[ci] = W(v - float(h));
-      if (p.sym && tn != tm) static_cast<W*>(p.c)[z * p.sc + size_t(col) * p.ldc + row] = h;
-    } else if (row < p.rows && col < p.cols) {
-      const size_t at = z * p.rows * p.cols + size_t(row) * p.cols + col;
-      T* o = static_cast<T*>(p.out) + at;
-      if constexpr (OUT == kUpdate) {
-        const float w = p.master != nullptr ? p.master[at] : Elem<T>::to_f32(*o);
-        v = w * p.keep - v * p.step;
-        if (p.master != nullptr) p.master[at] = v;
+    if constexpr (kSym) {
+      if (row == col) {
+        float d = p.alpha_d * acc[r];
+        if constexpr (KIND == kSquare) d += p.k0 + (p.k1 + p.k2 * dv[row]) * du[row];
+        p.dc[z * p.mp + row] = d;
+        v = 0.f;
+      } else if constexpr (KIND == kSquare) {
+        v += (p.g0 + p.g1 * du[row]) * float(static_cast<const W*>(p.v)[ci]);
+        v += p.h1 * dv[col] * float(static_cast<const W*>(p.u)[ci]);
       }
-      *o = Elem<T>::from_f32(v);
+      c[ci] = W(v);
+      if (tn != tm) c[z * p.sc + size_t(col) * p.ldc + row] = W(v);
+    } else {
+      float x = float(static_cast<const W*>(p.x)[ci]);
+      if (p.x2 != nullptr) x += float(static_cast<const W*>(p.x2)[ci]);
+      v += p.beta * dq[p.dq_col ? col : row] * x;
+      if constexpr (KIND == kApply) {
+        const W h = W(v);
+        c[ci] = h;
+        if (p.c2 != nullptr) static_cast<W*>(p.c2)[ci] = W(v - float(h));
+      } else if (row < p.rows && col < p.cols) {
+        put_last<T, KIND>(p, z, row, col, v);
+      }
     }
   }
 }
 
-template <typename W, typename T, int OUT>
-moe_status launch_product(const char* name, const Product& p, bool ak, bool bk, int count, hipStream_t s) {
-  const dim3 grid(unsigned(p.n / 64), unsigned(p.m / 64), unsigned(count));
-  if (ak && bk) {
-    MOE_LAUNCH(name, (product_kernel<W, T, true, true, OUT>), grid, dim3(kThreads), 0, s, p);
-  } else if (bk) {
-    MOE_LAUNCH(name, (product_kernel<W, T, false, true, OUT>), grid, dim3(kThreads), 0, s, p);
-  } else {
-    MOE_LAUNCH(name, (product_kernel<W, T, false, false, OUT>), grid, dim3(kThreads), 0, s, p);
+// ---- the same on the large tile (float16, sides past kSingleSteps) ---------------------
+// 256 x 256 tiles of big_tile.h.  Its accumulators hold four neighbouring columns of one
+// row at a time, so the epilogue reads what it adds eight bytes a lane, turns the tile to
+// float16 in LDS and writes whole row pieces; a symmetric product's tile off the diagonal
+// is written a second time, its columns read back as rows by the transposing LDS reads.
+// Rows of the LDS tile are 32 bytes longer than the tile: the four rows that such a read
+// takes from lie in different banks.
+//
+// Blocks that run at once on an XCD get consecutive tile numbers; those run over (matrix,
+// group of four n-tiles, m-tile, n-tile in group), a symmetric product's over m <= n.
+namespace nsbig {
+
+using big::BK;
+using big::BM;
+using big::BNE;
+constexpr int kGroup = 4;
+constexpr int kRS = BNE * 2 + 32;
+constexpr size_t kLds = big::kLoopLdsMax > size_t(BM) * kRS ? big::kLoopLdsMax : size_t(BM) * kRS;
+
+__host__ __device__ inline int sym_tiles(int t) { return t * (t + 1) / 2; }
+
+// tile number -> (m-tile, n-tile)
+template <bool SYM>
+__device__ __forceinline__ void tile_at(int t, int MT, int NT, int& tm, int& tn) {
+  int g = 0;
+  for (;; ++g) {  // at most NT / 4 groups
+    const int w = min(kGroup, NT - g * kGroup);
+    // a symmetric group's n-tiles 4g .. 4g + w - 1 have 4g + 1, .., 4g + w m-tiles
+    const int n = SYM ? w * g * kGroup + sym_tiles(w) : MT * w;
+    if (t < n || (g + 1) * kGroup >= NT) {
+      if (!SYM || t < w * g * kGroup) {
+        tm = t / w;
+        tn = g * kGroup + t % w;
+      } else {
+        t -= w * g * kGroup;
+        int r = 0;
+        while (t >= w - r) t -= w - r++;  // rows of the triangle: w, w - 1, .. tiles
+        tm = g * kGroup + r;
+        tn = tm + t;
+      }
+      return;
+    }
+    t -= n;
   }
+}
+
+__device__ __forceinline__ void unpack4(uint2 w, float* f) {
+  typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+  const h4 v = __builtin_bit_cast(h4, w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = float(v[i]);
+}
+__device__ __forceinline__ uint2 pack4(const float* f) {
+  typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(uint2, h4{f16_t(f[0]), f16_t(f[1]), f16_t(f[2]), f16_t(f[3])});
+}
+
+template <int NW, bool AKM, bool BKN, int KIND>
+__global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, int per, int total) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  using S = big::Shape<false, NW>;
+  constexpr int NB = S::NB, kThr = NW * 64;
+  constexpr bool kSym = KIND == kGram || KIND == kSquare;
+  const int xcd = blockIdx.x % big::kXcds, loc = blockIdx.x / big::kXcds;
+  const int t = xcd * per + loc;
+  if (loc >= per || t >= total) return;
+  const int MT = (p.m + BM - 1) / BM, NT = (p.n + BNE - 1) / BNE;
+  const int each = kSym ? sym_tiles(NT) : MT * NT;
+  const size_t z = t / each;
+  int tm, tn;
+  tile_at<kSym>(t % each, MT, NT, tm, tn);
+  const int row0 = tm * BM, n0 = tn * BNE;
+
+  big::Operands op;
+  op.A = static_cast<const uint16_t*>(p.a) + z * p.sa;
+  op.A2 = static_cast<const uint16_t*>(p.a2 != nullptr ? p.a2 : p.a) + z * p.sa;
+  op.a_rows = AKM ? p.k : p.m;
+  op.lda = p.lda;
+  op.Bg = static_cast<const uint16_t*>(p.b) + z * p.sb;
+  op.Bu = static_cast<const uint16_t*>(p.b2 != nullptr ? p.b2 : p.b) + z * p.sb;
+  op.b_rows = BKN ? p.k : p.n;
+  op.ldb = p.ldb;
+  const int nk = p.k / BK;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int wm = S::wm(wave), wn = S::wn(wave), fr = lane & 31, g4 = lane >> 5;
+  const float* du = p.du + z * p.mp;
+  const float* dv = p.dv + z * p.mp;
+  const float* dq = p.dq + z * p.mp;
+
+  const auto epi = [&](f32x16_t (&acc)[4][NB]) {
+    MOE_LGKMCNT0();
+    block_barrier();  // every wave is done reading the last stage
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int rt = wm * 128 + i * 32 + fr, row = row0 + rt;
+      const bool rok = row < p.m;
+      const float dr = !rok ? 0.f : (KIND == kSquare ? du[row] : (!kSym && !p.dq_col ? dq[row] : 0.f));
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int cl = wn * NB * 32 + j * 32 + 8 * q + 4 * g4, col = n0 + cl;
+          const bool ok = rok && col < p.n;  // sides are multiples of 64: four columns at once
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = p.alpha * acc[i][j][4 * q + e];
+          if (ok) {
+            const size_t ci = z * p.sc + size_t(row) * p.ldc + col;
+            if constexpr (KIND == kSquare) {
+              float fu[4], fv[4];
+              unpack4(*reinterpret_cast<const uint2*>(static_cast<const f16_t*>(p.u) + ci), fu);
+              unpack4(*reinterpret_cast<const uint2*>(static_cast<const f16_t*>(p.v) + ci), fv);
+              const f32x4_t dc4 = *reinterpret_cast<const f32x4_t*>(dv + col);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] += (p.g0 + p.g1 * dr) * fv[e] + p.h1 * dc4[e] * fu[e];
+            }
+            if constexpr (kSym) {
+              if (unsigned(row - col) < 4u) {
+                const int e = row - col;
+                float d = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (k == e) {
+                    d = p.alpha_d * acc[i][j][4 * q + k];
+                    v[k] = 0.f;
+                  }
+                if constexpr (KIND == kSquare) d += p.k0 + (p.k1 + p.k2 * dv[row]) * dr;
+                p.dc[z * p.mp + row] = d;
+              }
+            } else {
+              float fx[4];
+              unpack4(*reinterpret_cast<const uint2*>(static_cast<const f16_t*>(p.x) + ci), fx);
+              if (p.x2 != nullptr) {
+                float f2[4];
+                unpack4(*reinterpret_cast<const uint2*>(static_cast<const f16_t*>(p.x2) + ci), f2);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) fx[e] += f2[e];
+              }
+              f32x4_t d4 = {dr, dr, dr, dr};
+              if (p.dq_col) d4 = *reinterpret_cast<const f32x4_t*>(dq + col);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] += p.beta * d4[e] * fx[e];
+            }
+            if constexpr (KIND == kUpdate) {
+              if (row < p.rows) {
+                const size_t at = z * p.rows * p.cols + size_t(row) * p.cols + col;
+                if (p.cols % 4 == 0) {
+                  if (col < p.cols) {
+                    uint2* o = reinterpret_cast<uint2*>(static_cast<bf16_t*>(p.out) + at);
+                    f32x4_t w;
+                    if (p.master != nullptr) {
+                      w = *reinterpret_cast<const f32x4_t*>(p.master + at);
+                    } else {
+                      const uint2 b = *o;
+                      w = f32x4_t{__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xFFFF0000u),
+                                  __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xFFFF0000u)};
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = w[e] * p.keep - v[e] * p.step;
+                    if (p.master != nullptr) *reinterpret_cast<f32x4_t*>(p.master + at) = w;
+                    *o = make_uint2(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]));
+                  }
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    if (col + e < p.cols) put_last<bf16_t, KIND>(p, z, row, col + e, v[e]);
+                }
+              }
+            }
+          }
+          if constexpr (KIND == kResult) {
+            *reinterpret_cast<uint2*>(lds + rt * kRS + cl * 2) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+          } else if constexpr (KIND != kUpdate) {
+            *reinterpret_cast<uint2*>(lds + rt * kRS + cl * 2) = pack4(v);
+          }
+        }
+      }
+    }
+    if constexpr (KIND == kUpdate) return;
+    MOE_LGKMCNT0();
+    block_barrier();
+    constexpr int kPieces = BNE / 8;
+    if constexpr (KIND == kResult) {
+      const int rows = p.rows - row0, cols = p.cols - n0;
+      bf16_t* o = static_cast<bf16_t*>(p.out) + z * p.rows * p.cols + size_t(row0) * p.cols + n0;
+#pragma unroll
+      for (int k = 0; k < BM * kPieces / kThr; ++k) {
+        const int id = tid + k * kThr, r = id / kPieces, c = (id % kPieces) * 8;
+        if (r >= rows || c >= cols) continue;
+        const char* src = lds + r * kRS + c * 2;
+        if (p.cols % 8 == 0) {
+          *reinterpret_cast<u32x4_t*>(o + size_t(r) * p.cols + c) = *reinterpret_cast<const u32x4_t*>(src);
+        } else {
+          for (int e = 0; e < 8 && c + e < cols; ++e)
+            o[size_t(r) * p.cols + c + e] = reinterpret_cast<const bf16_t*>(src)[e];
+        }
+      }
+    } else {
+      f16_t* c = static_cast<f16_t*>(p.c) + z * p.sc;
+#pragma unroll
+      for (int k = 0; k < BM * kPieces / kThr; ++k) {
+        const int id = tid + k * kThr, r = id / kPieces, cc = (id % kPieces) * 8;
+        if (row0 + r < p.m && n0 + cc < p.n)
+          *reinterpret_cast<u32x4_t*>(c + size_t(row0 + r) * p.ldc + n0 + cc) =
+              *reinterpret_cast<const u32x4_t*>(lds + r * kRS + cc * 2);
+      }
+      if (kSym && tm != tn) {
+        // 16 columns x 32 rows a wave and turn: lane group G has rows 8 G .. of them, lane i
+        // of a group column i
+        const int G = lane >> 4, il = lane & 15;
+#pragma unroll
+        for (int k = 0; k < (BM / 32) * (BNE / 16) / NW; ++k) {
+          const int u = wave + k * NW, r0 = (u % (BM / 32)) * 32 + 8 * G, c0 = (u / (BM / 32)) * 16;
+          const char* src = lds + (r0 + (il >> 2)) * kRS + (c0 + 4 * (il & 3)) * 2;
+          const bf16x8_t v = read_kn_frag2(src, src + 4 * kRS);
+          if (n0 + c0 + il < p.n && row0 + r0 < p.m)
+            *reinterpret_cast<u32x4_t*>(c + size_t(n0 + c0 + il) * p.ldc + row0 + r0) = __builtin_bit_cast(u32x4_t, v);
+        }
+      }
+    }
+  };
+  big::tile_loop<1, false, NW, BKN, AKM, big::F16, true>(op, p.n, nk, row0, n0, 0, p.a2 != nullptr ? 2 * nk : nk, lds, epi);
+}
+
+template <int NW, bool AKM, bool BKN, int KIND>
+moe_status launch_nw(const char* name, const Product& p, int count, hipStream_t s) {
+  auto kern = tile_kernel<NW, AKM, BKN, KIND>;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, int(kLds));
+  if (e != hipSuccess) return set_error(MOE_ERR_HIP, "%s: LDS attribute: %s", name, hipGetErrorString(e));
+  const int MT = (p.m + BM - 1) / BM, NT = (p.n + BNE - 1) / BNE;
+  const int64_t total = int64_t(count) * (KIND == kGram || KIND == kSquare ? sym_tiles(NT) : MT * NT);
+  const int per = int((total + big::kXcds - 1) / big::kXcds);
+  MOE_LAUNCH(name, kern, dim3(unsigned(per * big::kXcds)), dim3(NW * 64), kLds, s, p, per, int(total));
+  return MOE_OK;
+}
+
+template <bool AKM, bool BKN, int KIND>
+moe_status launch(const char* name, const Product& p, int count, hipStream_t s) {
+  return launch_nw<8, AKM, BKN, KIND>(name, p, count, s);
+}
+
+}  // namespace nsbig
+
+template <typename W, typename T, bool AK, bool BK, int KIND>
+moe_status launch_product(const char* name, const Product& p, bool large, int count, hipStream_t s) {
+  if constexpr (sizeof(W) == 2) {
+    if (large) return nsbig::launch<AK, BK, KIND>(name, p, count, s);
+  }
+  MOE_LAUNCH(name, (product_kernel<W, T, AK, BK, KIND>), dim3(unsigned(p.n / 64), unsigned(p.m / 64), unsigned(count)),
+             dim3(kThreads), 0, s, p);
   return MOE_OK;
 }
 
@@ -361,7 +649,9 @@ struct Run {
   static constexpr bool kSplit = sizeof(W) == 2;  // X_0 as the sum of two
 
   W* x(int i) const { return reinterpret_cast<W*>(base + p.o_x[i]); }
-  W* q(int i) const { return reinterpret_cast<W*>(base + p.o_q[i]); }
+  Sym<W> q(int i) const {
+    return {reinterpret_cast<W*>(base + p.o_q[i]), reinterpret_cast<float*>(base + p.o_d[i])};
+  }
 
   moe_status start() const {
     const int64_t n = int64_t(p.rows) * p.cols;
@@ -387,41 +677,48 @@ struct Run {
   }
 
   // A = X X^T (or X^T X)
-  moe_status gram(const W* x, W* out) const {
+  moe_status gram(const W* x, Sym<W> out) const {
     Product g{};
     g.a = g.b = x;
-    g.c = out;
+    g.c = out.o;
+    g.dc = out.d;
     g.sa = g.sb = size_t(p.rp) * p.cp;
     g.sc = size_t(p.mp) * p.mp;
-    g.m = g.n = g.ldc = p.mp;
+    g.m = g.n = g.ldc = g.mp = p.mp;
     g.k = p.tall ? p.rp : p.cp;
     g.lda = g.ldb = p.cp;
     g.alpha = ldexpf(1.f, Scale<W>::a - 2 * Scale<W>::x);
-    g.sym = 1;
-    return launch_product<W, T, kInner>("ns_gram", g, p.tall, p.tall, p.count, a.s);
+    g.alpha_d = ldexpf(1.f, -2 * Scale<W>::x);
+    if (p.tall) return launch_product<W, T, true, true, kGram>("ns_gram", g, !p.single, p.count, a.s);
+    return launch_product<W, T, false, false, kGram>("ns_gram", g, !p.single, p.count, a.s);
   }
 
-  // out = alpha u v + beta d (+ beta2 d2), all m x m, symmetric and commuting
-  moe_status square(const char* name, const W* u, const W* v, W* out, float alpha, const W* d, float beta,
-                    const W* d2 = nullptr, float beta2 = 0.f) const {
+  // out = k0 I + k1 u + k2 u v; scales 2^su, 2^sv, 2^so of the stored parts.  All commute; k1
+  // needs u = v.
+  moe_status square(const char* name, Sym<W> u, int su, Sym<W> v, int sv, Sym<W> out, int so, float k0, float k1,
+                    float k2) const {
     Product g{};
-    g.a = u;
-    g.b = v;  // symmetric: its columns are its rows
-    g.d = d;
-    g.d2 = d2;
-    g.c = out;
+    g.a = g.u = u.o;
+    g.b = g.v = v.o;  // symmetric: its columns are its rows
+    g.du = u.d;
+    g.dv = v.d;
+    g.c = out.o;
+    g.dc = out.d;
     g.sa = g.sb = g.sc = size_t(p.mp) * p.mp;
-    g.m = g.n = g.k = g.lda = g.ldb = g.ldc = p.mp;
-    g.alpha = alpha;
-    g.beta = beta;
-    g.beta2 = beta2;
-    g.sym = 1;
-    return launch_product<W, T, kInner>(name, g, false, false, p.count, a.s);
+    g.m = g.n = g.k = g.lda = g.ldb = g.ldc = g.mp = p.mp;
+    g.alpha = ldexpf(k2, so - su - sv);
+    g.g0 = ldexpf(k1, so - sv);
+    g.g1 = ldexpf(k2, so - sv);
+    g.h1 = ldexpf(k2, so - su);
+    g.alpha_d = ldexpf(k2, -su - sv);
+    g.k0 = k0;
+    g.k1 = k1;
+    g.k2 = k2;
+    return launch_product<W, T, false, false, kSquare>(name, g, !p.single, p.count, a.s);
   }
 
-  // (q0 I + q) X (or X (q0 I + q)), X = x + x2; to `out` (+ out2), or into the user's
-  // result when out is NULL
-  moe_status apply(float q0, const W* q, const W* x, const W* x2, W* out, W* out2) const {
+  // q X (or X q), X = x + x2; to `out` (+ out2), or into the user's result when out is NULL
+  moe_status apply(Sym<W> q, const W* x, const W* x2, W* out, W* out2) const {
     Product g{};
     const size_t sq = size_t(p.mp) * p.mp, sx = size_t(p.rp) * p.cp;
     // the low halves first, while the sums are small
@@ -430,15 +727,15 @@ struct Run {
     if (p.tall) {
       g.a = first;
       g.a2 = second;
-      g.b = q;
-      g.b2 = q;
+      g.b = q.o;
+      g.b2 = q.o;
       g.sa = sx;
       g.sb = sq;
       g.lda = p.cp;
       g.ldb = p.mp;
     } else {
-      g.a = q;
-      g.a2 = second != nullptr ? q : nullptr;
+      g.a = q.o;
+      g.a2 = second != nullptr ? q.o : nullptr;
       g.b = first;
       g.b2 = second;
       g.sa = sq;
@@ -449,59 +746,62 @@ struct Run {
     g.sc = sx;
     g.m = p.rp;
     g.n = g.ldc = p.cp;
-    g.k = p.mp;
-    g.d = x;
-    g.d2 = x2;
-    const bool bk = !p.tall;
+    g.k = g.mp = p.mp;
+    g.x = x;
+    g.x2 = x2;
+    g.dq = q.d;
+    g.dq_col = p.tall;
     if (out != nullptr) {
-      g.beta = g.beta2 = q0;
       g.c = out;
       g.c2 = out2;
       g.alpha = ldexpf(1.f, -Scale<W>::q);
-      return launch_product<W, T, kInner>("ns_apply", g, false, bk, p.count, a.s);
+      g.beta = 1.f;
+      return launch_apply<kApply>("ns_apply", g);
     }
     g.alpha = ldexpf(1.f, -Scale<W>::q - Scale<W>::x);
-    g.beta = g.beta2 = ldexpf(q0, -Scale<W>::x);
+    g.beta = ldexpf(1.f, -Scale<W>::x);
     g.out = a.out;
     g.rows = p.rows;
     g.cols = p.cols;
-    if (a.momentum == nullptr) return launch_product<W, T, kResult>("ns_apply_result", g, false, bk, p.count, a.s);
+    if (a.momentum == nullptr) return launch_apply<kResult>("ns_apply_result", g);
     g.master = a.master;
     g.keep = 1.f - a.m->lr * a.m->weight_decay;
     g.step = a.m->lr * a.m->update_scale;
-    return launch_product<W, T, kUpdate>("muon_apply", g, false, bk, p.count, a.s);
+    return launch_apply<kUpdate>("muon_apply", g);
+  }
+
+  template <int KIND>
+  moe_status launch_apply(const char* name, const Product& g) const {
+    if (p.tall) return launch_product<W, T, false, false, KIND>(name, g, !p.single, p.count, a.s);
+    return launch_product<W, T, false, true, KIND>(name, g, !p.single, p.count, a.s);
   }
 
   moe_status run() const {
     TRY_NS(start());
-    const float iq = ldexpf(1.f, -Scale<W>::q);
+    constexpr int sa = Scale<W>::a, sq = Scale<W>::q;
     int cur = 0, done = 0;  // X in x(cur), its low half, if it has one, in x(cur + 2)
     bool split = kSplit;
     while (done < a.m->steps) {
       const int len = std::min(a.m->steps - done, p.single ? 1 : (done == 0 ? 3 : 2));
-      // A in q(0); P, Q and two for what is being formed in the others
-      W* A = q(0);
-      W* Q = q(1);
-      float q0 = a.ca;
-      TRY_NS(gram(x(cur), A));
+      // A in 0; Q in 1, P in 2 (Q and what it becomes in 1 and 3), and T = P A in 4
+      int Q = 1;
+      TRY_NS(gram(x(cur), q(0)));
       for (int k = 0; k < len; ++k) {
-        W* P = k == 0 ? Q : q(2);
-        TRY_NS(square("ns_poly", A, A, P, ldexpf(a.cc, Scale<W>::q - 2 * Scale<W>::a), A,
-                      ldexpf(a.cb, Scale<W>::q - Scale<W>::a)));
+        const int P = k == 0 ? Q : 2;
+        TRY_NS(square("ns_poly", q(0), sa, q(0), sa, q(P), sq, a.ca, a.cb, a.cc));
         if (k + 1 < len) {
-          TRY_NS(square("ns_next", P, A, q(4), iq, A, a.ca));
-          TRY_NS(square("ns_next", P, q(4), A, iq, q(4), a.ca));
+          TRY_NS(square("ns_next", q(P), sq, q(0), sa, q(4), sa, 0.f, 0.f, 1.f));
+          TRY_NS(square("ns_next", q(P), sq, q(4), sa, q(0), sa, 0.f, 0.f, 1.f));
         }
         if (k > 0) {
-          W* N = Q == q(1) ? q(3) : q(1);
-          TRY_NS(square("ns_join", P, Q, N, iq, Q, a.ca, P, q0));
+          const int N = Q == 1 ? 3 : 1;
+          TRY_NS(square("ns_join", q(P), sq, q(Q), sq, q(N), sq, 0.f, 0.f, 1.f));
           Q = N;
-          q0 *= a.ca;
         }
       }
       done += len;
       const bool last = done == a.m->steps, keep = kSplit && p.single && done == 1;
-      TRY_NS(apply(q0, Q, x(cur), split ? x(cur + 2) : nullptr, last ? nullptr : x(cur ^ 1), keep ? x((cur ^ 1) + 2) : nullptr));
+      TRY_NS(apply(q(Q), x(cur), split ? x(cur + 2) : nullptr, last ? nullptr : x(cur ^ 1), keep ? x((cur ^ 1) + 2) : nullptr));
       cur ^= 1;
       split = keep;
     }

@@ -61,7 +61,8 @@ def assert_near(got, ref, dtype, what=""):
 
 
 SHAPES = [(1, 1, 1), (3, 2, 7), (2, 9, 3), (2, 64, 64), (1, 65, 63), (4, 100, 260), (2, 260, 100), (1, 300, 290),
-          (2, 257, 700), (2, 700, 257), (1, 128, 2048), (1, 640, 640)]
+          (2, 257, 700), (2, 700, 257), (1, 128, 2048), (1, 640, 640),
+          (1, 1090, 1300), (1, 1300, 1090), (9, 264, 520)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
