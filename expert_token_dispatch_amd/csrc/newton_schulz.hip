@@ -111,21 +111,56 @@ Plan make_plan(const moe_muon_desc* m) {
 // Per matrix the sum of squares of U in double (a gradient's squares leave float32's range
 // long before its values do), by blocks in a fixed order.  MOM: the momentum is updated
 // on the way.  Bound by HBM.
+template <typename T> struct alignas(16) Vec8 {
+  T e[8];
+};
+
+// Eight elements of a row of `cols` from column c: in one piece where rows are whole pieces
+// (vec), else one by one; zeros past the end.
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int c, int cols, bool vec, float* f) {
+  if (vec && c < cols) {
+    const Vec8<T> v = *reinterpret_cast<const Vec8<T>*>(row + c);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = Elem<T>::to_f32(v.e[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = c + k < cols ? Elem<T>::to_f32(row[c + k]) : 0.f;
+  }
+}
+
+// The stack is walked as runs of eight elements of the whole matrix (n is rows * cols: rows
+// do not matter here).
 template <typename T, bool MOM>
 __global__ __launch_bounds__(kThreads) void norm_kernel(const T* __restrict__ g, float* __restrict__ mom, float mu,
                                                         int nesterov, int64_t n, double* __restrict__ part) {
   const size_t z = blockIdx.y;
   const T* gz = g + z * n;
   float* mz = MOM ? mom + z * n : nullptr;
+  const bool vec = n % 8 == 0;  // every matrix starts on a whole piece
   double s = 0.0;
-  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < n; i += int64_t(gridDim.x) * kThreads) {
-    float u = Elem<T>::to_f32(gz[i]);
+  for (int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 8; i < n; i += int64_t(gridDim.x) * kThreads * 8) {
+    float u[8], m[8];
+    const int left = int(n - i < 8 ? n - i : 8);
+    load8(gz + i, 0, left, vec, u);
     if constexpr (MOM) {
-      const float v = mu * mz[i] + u;
-      mz[i] = v;
-      u = nesterov ? u + mu * v : v;
+      load8(mz + i, 0, left, vec, m);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        m[k] = mu * m[k] + u[k];
+        u[k] = nesterov ? u[k] + mu * m[k] : m[k];
+      }
+      if (vec) {
+        reinterpret_cast<uint4*>(mz + i)[0] = pack16(m, float{});
+        reinterpret_cast<uint4*>(mz + i)[1] = pack16(m + 4, float{});
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < left) mz[i + k] = m[k];
+      }
     }
-    s += double(u) * double(u);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += double(u[k]) * double(u[k]);
   }
   for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
   __shared__ double w[kThreads / 64];
@@ -135,7 +170,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(const T* __restrict__ g,
 }
 
 // X_0 = U / (|U| + eps), scaled, into the padded working matrices (hi, and lo with what
-// hi's rounding left); the padding is zero.
+// hi's rounding left); the padding is zero.  Runs of eight elements of a padded row.
 template <typename T, typename W, bool MOM>
 __global__ __launch_bounds__(kThreads) void start_kernel(const T* __restrict__ g, const float* __restrict__ mom, float mu,
                                                          int nesterov, int rows, int cols, int rp, int cp,
@@ -143,31 +178,40 @@ __global__ __launch_bounds__(kThreads) void start_kernel(const T* __restrict__ g
                                                          W* __restrict__ hi, W* __restrict__ lo) {
   const size_t z = blockIdx.y;
   __shared__ double total;
-  if (threadIdx.x == 0) {
+  if (threadIdx.x < 64) {
     double s = 0.0;
-    for (int i = 0; i < nblk; ++i) s += part[z * nblk + i];
-    total = s;
+    for (int i = threadIdx.x; i < nblk; i += 64) s += part[z * nblk + i];
+    for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
+    if (threadIdx.x == 0) total = s;
   }
   __syncthreads();
   const double norm = sqrt(total) + double(eps);
   const double inv = norm > 0.0 ? double(1 << Scale<W>::x) / norm : (norm == 0.0 ? 0.0 : norm);
-  const T* gz = g + z * rows * cols;
-  const float* mz = MOM ? mom + z * rows * cols : nullptr;
-  W* hz = hi + z * rp * cp;
-  W* lz = lo == nullptr ? nullptr : lo + z * rp * cp;
-  const int64_t n = int64_t(rp) * cp;
-  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < n; i += int64_t(gridDim.x) * kThreads) {
-    const int r = int(i / cp), c = int(i % cp);
-    float x = 0.f;
+  const size_t n = size_t(rows) * cols, np = size_t(rp) * cp;
+  const bool vec = cols % 8 == 0;
+  const int pieces = cp / 8;
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < int64_t(np / 8);
+       i += int64_t(gridDim.x) * kThreads) {
+    const int r = int(i / pieces), c = int(i % pieces) * 8;
+    float u[8] = {};
     if (r < rows && c < cols) {
-      const int64_t at = int64_t(r) * cols + c;
-      float u = Elem<T>::to_f32(gz[at]);
-      if constexpr (MOM) u = nesterov ? u + mu * mz[at] : mz[at];
-      x = float(double(u) * inv);
+      load8(g + z * n + size_t(r) * cols, c, cols, vec, u);
+      if constexpr (MOM) {
+        float m[8];
+        load8(mom + z * n + size_t(r) * cols, c, cols, vec, m);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[k] = nesterov ? u[k] + mu * m[k] : m[k];
+      }
     }
-    const W h = W(x);
-    hz[i] = h;
-    if (lz != nullptr) lz[i] = W(x - float(h));
+    Vec8<W> h, l;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float x = float(double(u[k]) * inv);
+      h.e[k] = W(x);
+      l.e[k] = W(x - float(h.e[k]));
+    }
+    *reinterpret_cast<Vec8<W>*>(hi + z * np + i * 8) = h;
+    if (lo != nullptr) *reinterpret_cast<Vec8<W>*>(lo + z * np + i * 8) = l;
   }
 }
 
@@ -473,87 +517,106 @@ __global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, int per, int t
   const auto epi = [&](f32x16_t (&acc)[4][NB]) {
     MOE_LGKMCNT0();
     block_barrier();  // every wave is done reading the last stage
+    // what the epilogue adds, by buffer loads: rows past the matrix read as zero, so no load
+    // hangs on a branch and many are in flight
+    const auto rsrc = [&](const void* x) {
+      return __builtin_amdgcn_make_buffer_rsrc(const_cast<f16_t*>(static_cast<const f16_t*>(x) + z * p.sc), 0,
+                                               uint32_t(p.m) * uint32_t(p.ldc) * 2u, kRsrcFlags);
+    };
+    const __amdgpu_buffer_rsrc_t r0 = rsrc(KIND == kSquare ? p.v : p.x);
+    const __amdgpu_buffer_rsrc_t r1 = rsrc(KIND == kSquare ? p.u : (p.x2 != nullptr ? p.x2 : p.x));
+    const float second = KIND == kSquare || p.x2 != nullptr ? 1.f : 0.f;
+    f32x4_t dc4[NB][4];
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int col = min(n0 + wn * NB * 32 + j * 32 + 8 * q + 4 * g4, p.n - 4);
+        dc4[j][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        if constexpr (KIND == kSquare) dc4[j][q] = *reinterpret_cast<const f32x4_t*>(dv + col);
+        if constexpr (!kSym)
+          if (p.dq_col) dc4[j][q] = *reinterpret_cast<const f32x4_t*>(dq + col);
+      }
+    // a row block at a time: its loads take whole lines of 32 rows, piece after piece
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int rt = wm * 128 + i * 32 + fr, row = row0 + rt;
-      const bool rok = row < p.m;
-      const float dr = !rok ? 0.f : (KIND == kSquare ? du[row] : (!kSym && !p.dq_col ? dq[row] : 0.f));
+      const int rowc = min(row, p.m - 1);
+      const float dri = KIND == kSquare ? du[rowc] : (!kSym && !p.dq_col ? dq[rowc] : 0.f);
+      uint2 l0[NB][4], l1[NB][4];
+      if constexpr (KIND != kGram) {
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int col = n0 + wn * NB * 32 + j * 32 + 8 * q + 4 * g4;
+            const uint32_t off = (uint32_t(row) * uint32_t(p.ldc) + uint32_t(col)) * 2u;
+            l0[j][q] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r0, off, 0, 0));
+            l1[j][q] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r1, off, 0, 0));
+          }
+      }
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int cl = wn * NB * 32 + j * 32 + 8 * q + 4 * g4, col = n0 + cl;
-          const bool ok = rok && col < p.n;  // sides are multiples of 64: four columns at once
           float v[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = p.alpha * acc[i][j][4 * q + e];
-          if (ok) {
-            const size_t ci = z * p.sc + size_t(row) * p.ldc + col;
-            if constexpr (KIND == kSquare) {
-              float fu[4], fv[4];
-              unpack4(*reinterpret_cast<const uint2*>(static_cast<const f16_t*>(p.u) + ci), fu);
-              unpack4(*reinterpret_cast<const uint2*>(static_cast<const f16_t*>(p.v) + ci), fv);
-              const f32x4_t dc4 = *reinterpret_cast<const f32x4_t*>(dv + col);
+          if constexpr (KIND != kGram) {
+            float f0[4], f1[4];
+            unpack4(l0[j][q], f0);
+            unpack4(l1[j][q], f1);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] += (p.g0 + p.g1 * dr) * fv[e] + p.h1 * dc4[e] * fu[e];
-            }
-            if constexpr (kSym) {
-              if (unsigned(row - col) < 4u) {
-                const int e = row - col;
-                float d = 0.f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  if (k == e) {
-                    d = p.alpha_d * acc[i][j][4 * q + k];
-                    v[k] = 0.f;
-                  }
-                if constexpr (KIND == kSquare) d += p.k0 + (p.k1 + p.k2 * dv[row]) * dr;
-                p.dc[z * p.mp + row] = d;
-              }
-            } else {
-              float fx[4];
-              unpack4(*reinterpret_cast<const uint2*>(static_cast<const f16_t*>(p.x) + ci), fx);
-              if (p.x2 != nullptr) {
-                float f2[4];
-                unpack4(*reinterpret_cast<const uint2*>(static_cast<const f16_t*>(p.x2) + ci), f2);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) fx[e] += f2[e];
-              }
-              f32x4_t d4 = {dr, dr, dr, dr};
-              if (p.dq_col) d4 = *reinterpret_cast<const f32x4_t*>(dq + col);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] += p.beta * d4[e] * fx[e];
-            }
-            if constexpr (KIND == kUpdate) {
-              if (row < p.rows) {
-                const size_t at = z * p.rows * p.cols + size_t(row) * p.cols + col;
-                if (p.cols % 4 == 0) {
-                  if (col < p.cols) {
-                    uint2* o = reinterpret_cast<uint2*>(static_cast<bf16_t*>(p.out) + at);
-                    f32x4_t w;
-                    if (p.master != nullptr) {
-                      w = *reinterpret_cast<const f32x4_t*>(p.master + at);
-                    } else {
-                      const uint2 b = *o;
-                      w = f32x4_t{__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xFFFF0000u),
-                                  __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xFFFF0000u)};
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = w[e] * p.keep - v[e] * p.step;
-                    if (p.master != nullptr) *reinterpret_cast<f32x4_t*>(p.master + at) = w;
-                    *o = make_uint2(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]));
-                  }
-                } else {
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    if (col + e < p.cols) put_last<bf16_t, KIND>(p, z, row, col + e, v[e]);
-                }
-              }
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (KIND == kSquare)
+                v[e] += (p.g0 + p.g1 * dri) * f0[e] + p.h1 * dc4[j][q][e] * f1[e];
+              else
+                v[e] += p.beta * (p.dq_col ? dc4[j][q][e] : dri) * (f0[e] + second * f1[e]);
             }
           }
-          if constexpr (KIND == kResult) {
+          if constexpr (kSym) {
+            if (tm == tn && unsigned(row - col) < 4u && row < p.m) {
+              const int e = row - col;
+              float d = 0.f;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (k == e) {
+                  d = p.alpha_d * acc[i][j][4 * q + k];
+                  v[k] = 0.f;
+                }
+              if constexpr (KIND == kSquare) d += p.k0 + (p.k1 + p.k2 * dv[row]) * dri;
+              p.dc[z * p.mp + row] = d;
+            }
+          }
+          if constexpr (KIND == kUpdate) {
+            if (row < p.rows) {
+              const size_t at = z * p.rows * p.cols + size_t(row) * p.cols + col;
+              if (p.cols % 4 == 0) {
+                if (col < p.cols) {
+                  uint2* o = reinterpret_cast<uint2*>(static_cast<bf16_t*>(p.out) + at);
+                  f32x4_t w;
+                  if (p.master != nullptr) {
+                    w = *reinterpret_cast<const f32x4_t*>(p.master + at);
+                  } else {
+                    const uint2 b = *o;
+                    w = f32x4_t{__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xFFFF0000u),
+                                __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xFFFF0000u)};
+                  }
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) w[e] = w[e] * p.keep - v[e] * p.step;
+                  if (p.master != nullptr) *reinterpret_cast<f32x4_t*>(p.master + at) = w;
+                  *o = make_uint2(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]));
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (col + e < p.cols) put_last<bf16_t, KIND>(p, z, row, col + e, v[e]);
+              }
+            }
+          } else if constexpr (KIND == kResult) {
             *reinterpret_cast<uint2*>(lds + rt * kRS + cl * 2) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-          } else if constexpr (KIND != kUpdate) {
+          } else {
             *reinterpret_cast<uint2*>(lds + rt * kRS + cl * 2) = pack4(v);
           }
         }
