@@ -64,7 +64,7 @@ struct Plan {
   size_t x_bytes, q_bytes;      // one stack of X, of m x m matrices
   int nblk;                     // partial sums of squares per matrix
   bool single;                  // phases of one step (see the top of the file)
-  size_t o_part, o_x[4], o_q[5], o_d[5], bytes;
+  size_t o_part, o_x[4], o_t[3], o_q[5], o_d[5], bytes;
 };
 
 constexpr int kSingleSteps = 256;
@@ -99,6 +99,10 @@ Plan make_plan(const moe_muon_desc* m) {
   const bool split = m->dtype == MOE_BF16;
   const int xs = split ? (p.single ? 4 : 3) : 2;
   for (int i = 0; i < xs; ++i) p.o_x[i] = take(p.x_bytes);
+  // the large tile takes its operands along K, so X is kept transposed too: both X, and for a
+  // wide matrix the low half of X_0
+  if (!p.single)
+    for (int i = 0; i < (p.tall ? 2 : 3); ++i) p.o_t[i] = take(p.x_bytes);
   for (int i = 0; i < (p.single ? 2 : 5); ++i) {
     p.o_q[i] = take(p.q_bytes);
     p.o_d[i] = take(size_t(p.count) * p.mp * sizeof(float));
@@ -215,6 +219,77 @@ __global__ __launch_bounds__(kThreads) void start_kernel(const T* __restrict__ g
   }
 }
 
+// The same for the large tile, which also wants X transposed [cp, rp] (thi; tlo if given): a
+// block turns a tile of 64 x 64 in LDS.  Rows of the LDS tile are 33 words, so reading down a
+// column passes over the banks.
+template <typename T, bool MOM>
+__global__ __launch_bounds__(kThreads) void start_both_kernel(const T* __restrict__ g, const float* __restrict__ mom,
+                                                              float mu, int nesterov, int rows, int cols, int rp, int cp,
+                                                              const double* __restrict__ part, int nblk, float eps,
+                                                              f16_t* __restrict__ hi, f16_t* __restrict__ lo,
+                                                              f16_t* __restrict__ thi, f16_t* __restrict__ tlo) {
+  constexpr int kLd = 66;
+  __shared__ f16_t th[64 * kLd], tl[64 * kLd];
+  __shared__ double total;
+  const size_t z = blockIdx.z;
+  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
+  const size_t n = size_t(rows) * cols, np = size_t(rp) * cp;
+  const bool vec = cols % 8 == 0;
+  float u[2][8] = {};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = r0 + 32 * h + threadIdx.x / 8, c = c0 + threadIdx.x % 8 * 8;
+    if (r < rows && c < cols) {
+      load8(g + z * n + size_t(r) * cols, c, cols, vec, u[h]);
+      if constexpr (MOM) {
+        float m[8];
+        load8(mom + z * n + size_t(r) * cols, c, cols, vec, m);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[h][k] = nesterov ? u[h][k] + mu * m[k] : m[k];
+      }
+    }
+  }
+  if (threadIdx.x < 64) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < nblk; i += 64) s += part[z * nblk + i];
+    for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
+    if (threadIdx.x == 0) total = s;
+  }
+  __syncthreads();
+  const double norm = sqrt(total) + double(eps);
+  const double inv = norm > 0.0 ? double(1 << Scale<f16_t>::x) / norm : (norm == 0.0 ? 0.0 : norm);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = 32 * h + threadIdx.x / 8, c = threadIdx.x % 8 * 8;
+    Vec8<f16_t> vh, vl;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float x = float(double(u[h][k]) * inv);
+      vh.e[k] = f16_t(x);
+      vl.e[k] = f16_t(x - float(vh.e[k]));
+      th[r * kLd + c + k] = vh.e[k];
+      tl[r * kLd + c + k] = vl.e[k];
+    }
+    const size_t at = z * np + size_t(r0 + r) * cp + c0 + c;
+    *reinterpret_cast<Vec8<f16_t>*>(hi + at) = vh;
+    *reinterpret_cast<Vec8<f16_t>*>(lo + at) = vl;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = 32 * h + threadIdx.x / 8, r = threadIdx.x % 8 * 8;
+    Vec8<f16_t> vh, vl;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      vh.e[k] = th[(r + k) * kLd + c];
+      vl.e[k] = tl[(r + k) * kLd + c];
+    }
+    const size_t at = z * np + size_t(c0 + c) * rp + r0 + r;
+    *reinterpret_cast<Vec8<f16_t>*>(thi + at) = vh;
+    if (tlo != nullptr) *reinterpret_cast<Vec8<f16_t>*>(tlo + at) = vl;
+  }
+}
+
 // ---- products ------------------------------------------------------------------------
 // An m x m matrix of the stack: the diagonal in float32, the rest (diagonal zero) scaled.
 template <typename W> struct Sym {
@@ -229,7 +304,9 @@ struct Product {
   const void* a2;     // the second pair of operands (NULL: none)
   const void* b2;
   void* c;
-  void* c2;           // what C's rounding leaves (NULL: not kept)
+  void* c2;           // what C's rounding leaves (small tiles only; NULL: not kept)
+  void* ct;           // C transposed (large tiles only; NULL: not kept)
+  int ldct;
   size_t sa, sb, sc;  // elements from one matrix of the stack to the next
   int m, n, k, lda, ldb, ldc;
   float alpha;
@@ -426,7 +503,9 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
 }
 
 // ---- the same on the large tile (float16, sides past kSingleSteps) ---------------------
-// 256 x 256 tiles of big_tile.h.  Its accumulators hold four neighbouring columns of one
+// 256 x 256 tiles of big_tile.h, both operands contiguous along K: X is kept in both layouts
+// (with one operand the other way round, through the transposing LDS reads, a step of 64 k
+// took 2.25 us against 1.69, with both 3.1).  The accumulators hold four neighbouring columns of one
 // row at a time, so the epilogue reads what it adds eight bytes a lane, turns the tile to
 // float16 in LDS and writes whole row pieces; a symmetric product's tile off the diagonal
 // is written a second time, its columns read back as rows by the transposing LDS reads.
@@ -482,7 +561,7 @@ __device__ __forceinline__ uint2 pack4(const float* f) {
   return __builtin_bit_cast(uint2, h4{f16_t(f[0]), f16_t(f[1]), f16_t(f[2]), f16_t(f[3])});
 }
 
-template <int NW, bool AKM, bool BKN, int KIND>
+template <int NW, int KIND>
 __global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, int per, int total) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   using S = big::Shape<false, NW>;
@@ -501,11 +580,11 @@ __global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, int per, int t
   big::Operands op;
   op.A = static_cast<const uint16_t*>(p.a) + z * p.sa;
   op.A2 = static_cast<const uint16_t*>(p.a2 != nullptr ? p.a2 : p.a) + z * p.sa;
-  op.a_rows = AKM ? p.k : p.m;
+  op.a_rows = p.m;
   op.lda = p.lda;
   op.Bg = static_cast<const uint16_t*>(p.b) + z * p.sb;
   op.Bu = static_cast<const uint16_t*>(p.b2 != nullptr ? p.b2 : p.b) + z * p.sb;
-  op.b_rows = BKN ? p.k : p.n;
+  op.b_rows = p.n;
   op.ldb = p.ldb;
   const int nk = p.k / BK;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
@@ -650,9 +729,11 @@ __global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, int per, int t
           *reinterpret_cast<u32x4_t*>(c + size_t(row0 + r) * p.ldc + n0 + cc) =
               *reinterpret_cast<const u32x4_t*>(lds + r * kRS + cc * 2);
       }
-      if (kSym && tm != tn) {
+      if (kSym ? tm != tn : p.ct != nullptr) {
         // 16 columns x 32 rows a wave and turn: lane group G has rows 8 G .. of them, lane i
         // of a group column i
+        f16_t* ct = kSym ? c : static_cast<f16_t*>(p.ct) + z * p.sc;
+        const int ldct = kSym ? p.ldc : p.ldct;
         const int G = lane >> 4, il = lane & 15;
 #pragma unroll
         for (int k = 0; k < (BM / 32) * (BNE / 16) / NW; ++k) {
@@ -660,17 +741,17 @@ __global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, int per, int t
           const char* src = lds + (r0 + (il >> 2)) * kRS + (c0 + 4 * (il & 3)) * 2;
           const bf16x8_t v = read_kn_frag2(src, src + 4 * kRS);
           if (n0 + c0 + il < p.n && row0 + r0 < p.m)
-            *reinterpret_cast<u32x4_t*>(c + size_t(n0 + c0 + il) * p.ldc + row0 + r0) = __builtin_bit_cast(u32x4_t, v);
+            *reinterpret_cast<u32x4_t*>(ct + size_t(n0 + c0 + il) * ldct + row0 + r0) = __builtin_bit_cast(u32x4_t, v);
         }
       }
     }
   };
-  big::tile_loop<1, false, NW, BKN, AKM, big::F16, true>(op, p.n, nk, row0, n0, 0, p.a2 != nullptr ? 2 * nk : nk, lds, epi);
+  big::tile_loop<1, false, NW, false, false, big::F16, true>(op, p.n, nk, row0, n0, 0, p.a2 != nullptr ? 2 * nk : nk, lds, epi);
 }
 
-template <int NW, bool AKM, bool BKN, int KIND>
+template <int NW, int KIND>
 moe_status launch_nw(const char* name, const Product& p, int count, hipStream_t s) {
-  auto kern = tile_kernel<NW, AKM, BKN, KIND>;
+  auto kern = tile_kernel<NW, KIND>;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, int(kLds));
   if (e != hipSuccess) return set_error(MOE_ERR_HIP, "%s: LDS attribute: %s", name, hipGetErrorString(e));
@@ -681,17 +762,17 @@ moe_status launch_nw(const char* name, const Product& p, int count, hipStream_t 
   return MOE_OK;
 }
 
-template <bool AKM, bool BKN, int KIND>
+template <int KIND>
 moe_status launch(const char* name, const Product& p, int count, hipStream_t s) {
-  return launch_nw<8, AKM, BKN, KIND>(name, p, count, s);
+  return launch_nw<8, KIND>(name, p, count, s);
 }
 
 }  // namespace nsbig
 
 template <typename W, typename T, bool AK, bool BK, int KIND>
 moe_status launch_product(const char* name, const Product& p, bool large, int count, hipStream_t s) {
-  if constexpr (sizeof(W) == 2) {
-    if (large) return nsbig::launch<AK, BK, KIND>(name, p, count, s);
+  if constexpr (sizeof(W) == 2 && !AK && !BK) {
+    if (large) return nsbig::launch<KIND>(name, p, count, s);
   }
   MOE_LAUNCH(name, (product_kernel<W, T, AK, BK, KIND>), dim3(unsigned(p.n / 64), unsigned(p.m / 64), unsigned(count)),
              dim3(kThreads), 0, s, p);
@@ -712,6 +793,7 @@ struct Run {
   static constexpr bool kSplit = sizeof(W) == 2;  // X_0 as the sum of two
 
   W* x(int i) const { return reinterpret_cast<W*>(base + p.o_x[i]); }
+  W* xt(int i) const { return reinterpret_cast<W*>(base + p.o_t[i]); }
   Sym<W> q(int i) const {
     return {reinterpret_cast<W*>(base + p.o_q[i]), reinterpret_cast<float*>(base + p.o_d[i])};
   }
@@ -725,34 +807,54 @@ struct Run {
     const int64_t np = int64_t(p.rp) * p.cp;
     const dim3 gs(unsigned(std::min<int64_t>(1024, (np + 2047) / 2048)), unsigned(p.count));
     W* lo = kSplit ? x(2) : nullptr;
-    if (a.momentum != nullptr) {
+    const bool mom = a.momentum != nullptr;
+    if (mom) {
       MOE_LAUNCH("muon_momentum", (norm_kernel<T, true>), gn, dim3(kThreads), 0, a.s, g, a.momentum, m->momentum,
                  m->nesterov, n, part);
-      MOE_LAUNCH("muon_start", (start_kernel<T, W, true>), gs, dim3(kThreads), 0, a.s, g, a.momentum, m->momentum,
-                 m->nesterov, p.rows, p.cols, p.rp, p.cp, part, p.nblk, m->eps, x(0), lo);
     } else {
       MOE_LAUNCH("orth_norm", (norm_kernel<T, false>), gn, dim3(kThreads), 0, a.s, g, static_cast<float*>(nullptr), 0.f,
                  0, n, part);
+    }
+    if constexpr (kSplit) {
+      if (!p.single) {
+        const dim3 gb(unsigned(p.cp / 64), unsigned(p.rp / 64), unsigned(p.count));
+        W* tlo = p.tall ? nullptr : xt(2);
+        if (mom) {
+          MOE_LAUNCH("muon_start", (start_both_kernel<T, true>), gb, dim3(kThreads), 0, a.s, g, a.momentum, m->momentum,
+                     m->nesterov, p.rows, p.cols, p.rp, p.cp, part, p.nblk, m->eps, x(0), lo, xt(0), tlo);
+        } else {
+          MOE_LAUNCH("orth_start", (start_both_kernel<T, false>), gb, dim3(kThreads), 0, a.s, g,
+                     static_cast<const float*>(nullptr), 0.f, 0, p.rows, p.cols, p.rp, p.cp, part, p.nblk, m->eps, x(0),
+                     lo, xt(0), tlo);
+        }
+        return MOE_OK;
+      }
+    }
+    if (mom) {
+      MOE_LAUNCH("muon_start", (start_kernel<T, W, true>), gs, dim3(kThreads), 0, a.s, g, a.momentum, m->momentum,
+                 m->nesterov, p.rows, p.cols, p.rp, p.cp, part, p.nblk, m->eps, x(0), lo);
+    } else {
       MOE_LAUNCH("orth_start", (start_kernel<T, W, false>), gs, dim3(kThreads), 0, a.s, g,
                  static_cast<const float*>(nullptr), 0.f, 0, p.rows, p.cols, p.rp, p.cp, part, p.nblk, m->eps, x(0), lo);
     }
     return MOE_OK;
   }
 
-  // A = X X^T (or X^T X)
-  moe_status gram(const W* x, Sym<W> out) const {
+  // A = X X^T (or X^T X), X in x(i)
+  moe_status gram(int i, Sym<W> out) const {
     Product g{};
-    g.a = g.b = x;
+    const bool turned = !p.single && p.tall;  // the rows of the transposed X
+    g.a = g.b = turned ? xt(i) : x(i);
     g.c = out.o;
     g.dc = out.d;
     g.sa = g.sb = size_t(p.rp) * p.cp;
     g.sc = size_t(p.mp) * p.mp;
     g.m = g.n = g.ldc = g.mp = p.mp;
     g.k = p.tall ? p.rp : p.cp;
-    g.lda = g.ldb = p.cp;
+    g.lda = g.ldb = turned ? p.rp : p.cp;
     g.alpha = ldexpf(1.f, Scale<W>::a - 2 * Scale<W>::x);
     g.alpha_d = ldexpf(1.f, -2 * Scale<W>::x);
-    if (p.tall) return launch_product<W, T, true, true, kGram>("ns_gram", g, !p.single, p.count, a.s);
+    if (p.tall && !turned) return launch_product<W, T, true, true, kGram>("ns_gram", g, false, p.count, a.s);
     return launch_product<W, T, false, false, kGram>("ns_gram", g, !p.single, p.count, a.s);
   }
 
@@ -780,13 +882,18 @@ struct Run {
     return launch_product<W, T, false, false, kSquare>(name, g, !p.single, p.count, a.s);
   }
 
-  // q X (or X q), X = x + x2; to `out` (+ out2), or into the user's result when out is NULL
-  moe_status apply(Sym<W> q, const W* x, const W* x2, W* out, W* out2) const {
+  // q X (or X q) for X in x(i), with its low half if `split`; into x(to), with its low half if
+  // `keep`, or into the user's result (to < 0)
+  moe_status apply(Sym<W> q, int i, bool split, int to, bool keep) const {
     Product g{};
     const size_t sq = size_t(p.mp) * p.mp, sx = size_t(p.rp) * p.cp;
+    const W* hi = x(i);
+    const W* lo = split ? x(i + 2) : nullptr;
     // the low halves first, while the sums are small
-    const W* first = x2 != nullptr ? x2 : x;
-    const W* second = x2 != nullptr ? x : nullptr;
+    const bool turned = !p.single && !p.tall;
+    const W* h = turned ? xt(i) : hi;
+    const W* first = split ? (turned ? xt(2) : lo) : h;
+    const W* second = split ? h : nullptr;
     if (p.tall) {
       g.a = first;
       g.a2 = second;
@@ -804,19 +911,23 @@ struct Run {
       g.sa = sq;
       g.sb = sx;
       g.lda = p.mp;
-      g.ldb = p.cp;
+      g.ldb = turned ? p.rp : p.cp;
     }
     g.sc = sx;
     g.m = p.rp;
     g.n = g.ldc = p.cp;
     g.k = g.mp = p.mp;
-    g.x = x;
-    g.x2 = x2;
+    g.x = hi;
+    g.x2 = lo;
     g.dq = q.d;
     g.dq_col = p.tall;
-    if (out != nullptr) {
-      g.c = out;
-      g.c2 = out2;
+    if (to >= 0) {
+      g.c = x(to);
+      if (keep) g.c2 = x(to + 2);
+      if (!p.single) {
+        g.ct = xt(to);
+        g.ldct = p.rp;
+      }
       g.alpha = ldexpf(1.f, -Scale<W>::q);
       g.beta = 1.f;
       return launch_apply<kApply>("ns_apply", g);
@@ -835,7 +946,7 @@ struct Run {
 
   template <int KIND>
   moe_status launch_apply(const char* name, const Product& g) const {
-    if (p.tall) return launch_product<W, T, false, false, KIND>(name, g, !p.single, p.count, a.s);
+    if (p.tall || !p.single) return launch_product<W, T, false, false, KIND>(name, g, !p.single, p.count, a.s);
     return launch_product<W, T, false, true, KIND>(name, g, !p.single, p.count, a.s);
   }
 
@@ -848,7 +959,7 @@ struct Run {
       const int len = std::min(a.m->steps - done, p.single ? 1 : (done == 0 ? 3 : 2));
       // A in 0; Q in 1, P in 2 (Q and what it becomes in 1 and 3), and T = P A in 4
       int Q = 1;
-      TRY_NS(gram(x(cur), q(0)));
+      TRY_NS(gram(cur, q(0)));
       for (int k = 0; k < len; ++k) {
         const int P = k == 0 ? Q : 2;
         TRY_NS(square("ns_poly", q(0), sa, q(0), sa, q(P), sq, a.ca, a.cb, a.cc));
@@ -864,7 +975,7 @@ struct Run {
       }
       done += len;
       const bool last = done == a.m->steps, keep = kSplit && p.single && done == 1;
-      TRY_NS(apply(q(Q), x(cur), split ? x(cur + 2) : nullptr, last ? nullptr : x(cur ^ 1), keep ? x((cur ^ 1) + 2) : nullptr));
+      TRY_NS(apply(q(Q), cur, split, last ? -1 : cur ^ 1, keep));
       cur ^= 1;
       split = keep;
     }
