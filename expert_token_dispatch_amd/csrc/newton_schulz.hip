@@ -7,10 +7,10 @@
 // Steps on the m x m side.  p(A_0), p(A_1), ... are polynomials of A_0: they commute and
 // are symmetric.  So a phase of several steps needs X only at its ends:
 //   A_0 = X X^T;  P_j = p(A_j),  Q_{j+1} = P_j Q_j,  A_{j+1} = P_j (P_j A_j);  X <- Q X.
-// The m x m matrices are held as a float32 diagonal and the rest, zero on its diagonal: the
-// multiples of I that P and Q carry (a^3 = 41) stand beside large singular values' p of
-// 0.7, and rounding them with the rest would be rounding the difference.  With U = D_u + U'
-// a product is U V = U' V' + D_u V' + U' D_v + D_u D_v, the last three in the epilogue.
+// P and Q are held as a float32 diagonal and the rest, zero on its diagonal: the multiples
+// of I that they carry (a, a^2, a^3 = 41) stand beside values of p of 0.7 for the large
+// singular values, and rounding them with the rest would be rounding the difference.  With
+// P = D_p + P' a product is P T = P' T + D_p T, and D_p T is added in the epilogue.
 // Every m x m product is symmetric: its upper triangle of tiles is computed and mirrored.
 // In units of m^3 multiply-adds (r the ratio of the sides) five single steps cost
 // 5 (3 r + 1), a phase of three and one of two 6 r + 14: the same at r = 1, two thirds
@@ -291,7 +291,7 @@ __global__ __launch_bounds__(kThreads) void start_both_kernel(const T* __restric
 }
 
 // ---- products ------------------------------------------------------------------------
-// An m x m matrix of the stack: the diagonal in float32, the rest (diagonal zero) scaled.
+// An m x m matrix of the stack, scaled; P and Q with the diagonal in float32 and zero in o.
 template <typename W> struct Sym {
   W* o;
   float* d;
@@ -310,15 +310,18 @@ struct Product {
   size_t sa, sb, sc;  // elements from one matrix of the stack to the next
   int m, n, k, lda, ldb, ldc;
   float alpha;
-  // kGram, kSquare: C is symmetric, its upper tiles are formed and mirrored.  Off the diagonal
-  //   C_ij = alpha sum + (g0 + g1 du_i) V_ij + h1 dv_j U_ij   (kGram: alpha sum)
-  // on it, in float32, dc_i = alpha_d sum + k0 + k1 du_i + k2 du_i dv_i   (kGram: alpha_d sum)
+  // kGram .. kJoin: C is symmetric, its upper tiles are formed and mirrored.
+  //   kGram  C = alpha sum
+  //   kPoly  C = alpha sum + g V, with k0 I
+  //   kNext  C = alpha sum + g D_u V
+  //   kJoin  C = alpha sum + g D_u V + h U D_v, with D_u D_v
+  // kPoly and kJoin put the diagonal into dc (times unit) and leave C's zero.
   const void* u;
   const void* v;
   const float* du;
   const float* dv;
   float* dc;
-  float g0, g1, h1, alpha_d, k0, k1, k2;
+  float g, h, k0, unit;
   // kApply and the last product: C = alpha sum + beta d (x + x2), d by row, or by column
   const void* x;
   const void* x2;
@@ -333,7 +336,7 @@ struct Product {
   float keep, step;   // W = keep W - step C
 };
 
-enum Kind { kGram = 0, kSquare = 1, kApply = 2, kResult = 3, kUpdate = 4 };
+enum Kind { kGram = 0, kPoly = 1, kNext = 2, kJoin = 3, kApply = 4, kResult = 5, kUpdate = 6 };
 
 template <typename W> struct Mma;
 template <> struct Mma<f16_t> {
@@ -427,7 +430,7 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
   using TA = OpTile<W, AK>;
   using TB = OpTile<W, BK>;
   constexpr int kBK = TA::kBK;
-  constexpr bool kSym = KIND == kGram || KIND == kSquare;
+  constexpr bool kSym = KIND <= kJoin;
   const int tm = blockIdx.y, tn = blockIdx.x;
   if (kSym && tn < tm) return;
   const size_t z = blockIdx.z;
@@ -476,14 +479,12 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
     W* c = static_cast<W*>(p.c);
     float v = p.alpha * acc[r];
     if constexpr (kSym) {
-      if (row == col) {
-        float d = p.alpha_d * acc[r];
-        if constexpr (KIND == kSquare) d += p.k0 + (p.k1 + p.k2 * dv[row]) * du[row];
-        p.dc[z * p.mp + row] = d;
+      if constexpr (KIND == kPoly) v += p.g * float(static_cast<const W*>(p.v)[ci]);
+      if constexpr (KIND == kNext || KIND == kJoin) v += p.g * du[row] * float(static_cast<const W*>(p.v)[ci]);
+      if constexpr (KIND == kJoin) v += p.h * dv[col] * float(static_cast<const W*>(p.u)[ci]);
+      if ((KIND == kPoly || KIND == kJoin) && row == col) {
+        p.dc[z * p.mp + row] = v * p.unit + (KIND == kPoly ? p.k0 : du[row] * dv[row]);
         v = 0.f;
-      } else if constexpr (KIND == kSquare) {
-        v += (p.g0 + p.g1 * du[row]) * float(static_cast<const W*>(p.v)[ci]);
-        v += p.h1 * dv[col] * float(static_cast<const W*>(p.u)[ci]);
       }
       c[ci] = W(v);
       if (tn != tm) c[z * p.sc + size_t(col) * p.ldc + row] = W(v);
@@ -566,7 +567,7 @@ __global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, int per, int t
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   using S = big::Shape<false, NW>;
   constexpr int NB = S::NB, kThr = NW * 64;
-  constexpr bool kSym = KIND == kGram || KIND == kSquare;
+  constexpr bool kSym = KIND <= kJoin;
   const int xcd = blockIdx.x % big::kXcds, loc = blockIdx.x / big::kXcds;
   const int t = xcd * per + loc;
   if (loc >= per || t >= total) return;
@@ -602,9 +603,9 @@ __global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, int per, int t
       return __builtin_amdgcn_make_buffer_rsrc(const_cast<f16_t*>(static_cast<const f16_t*>(x) + z * p.sc), 0,
                                                uint32_t(p.m) * uint32_t(p.ldc) * 2u, kRsrcFlags);
     };
-    const __amdgpu_buffer_rsrc_t r0 = rsrc(KIND == kSquare ? p.v : p.x);
-    const __amdgpu_buffer_rsrc_t r1 = rsrc(KIND == kSquare ? p.u : (p.x2 != nullptr ? p.x2 : p.x));
-    const float second = KIND == kSquare || p.x2 != nullptr ? 1.f : 0.f;
+    const __amdgpu_buffer_rsrc_t r0 = rsrc(kSym ? p.v : p.x);
+    const __amdgpu_buffer_rsrc_t r1 = rsrc(kSym ? p.u : p.x2);
+    const bool two = KIND == kJoin || (KIND == kApply && p.x2 != nullptr);
     f32x4_t dc4[NB][4];
 #pragma unroll
     for (int j = 0; j < NB; ++j)
@@ -612,7 +613,7 @@ __global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, int per, int t
       for (int q = 0; q < 4; ++q) {
         const int col = min(n0 + wn * NB * 32 + j * 32 + 8 * q + 4 * g4, p.n - 4);
         dc4[j][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        if constexpr (KIND == kSquare) dc4[j][q] = *reinterpret_cast<const f32x4_t*>(dv + col);
+        if constexpr (KIND == kJoin) dc4[j][q] = *reinterpret_cast<const f32x4_t*>(dv + col);
         if constexpr (!kSym)
           if (p.dq_col) dc4[j][q] = *reinterpret_cast<const f32x4_t*>(dq + col);
       }
@@ -621,7 +622,7 @@ __global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, int per, int t
     for (int i = 0; i < 4; ++i) {
       const int rt = wm * 128 + i * 32 + fr, row = row0 + rt;
       const int rowc = min(row, p.m - 1);
-      const float dri = KIND == kSquare ? du[rowc] : (!kSym && !p.dq_col ? dq[rowc] : 0.f);
+      const float dri = KIND == kNext || KIND == kJoin ? du[rowc] : (!kSym && !p.dq_col ? dq[rowc] : 0.f);
       uint2 l0[NB][4], l1[NB][4];
       if constexpr (KIND != kGram) {
 #pragma unroll
@@ -631,7 +632,8 @@ __global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, int per, int t
             const int col = n0 + wn * NB * 32 + j * 32 + 8 * q + 4 * g4;
             const uint32_t off = (uint32_t(row) * uint32_t(p.ldc) + uint32_t(col)) * 2u;
             l0[j][q] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r0, off, 0, 0));
-            l1[j][q] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r1, off, 0, 0));
+            l1[j][q] = make_uint2(0u, 0u);
+            if (two) l1[j][q] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r1, off, 0, 0));
           }
       }
 #pragma unroll
@@ -648,24 +650,23 @@ __global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, int per, int t
             unpack4(l1[j][q], f1);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              if constexpr (KIND == kSquare)
-                v[e] += (p.g0 + p.g1 * dri) * f0[e] + p.h1 * dc4[j][q][e] * f1[e];
-              else
-                v[e] += p.beta * (p.dq_col ? dc4[j][q][e] : dri) * (f0[e] + second * f1[e]);
+              if constexpr (KIND == kPoly) v[e] += p.g * f0[e];
+              if constexpr (KIND == kNext) v[e] += p.g * dri * f0[e];
+              if constexpr (KIND == kJoin) v[e] += p.g * dri * f0[e] + p.h * dc4[j][q][e] * f1[e];
+              if constexpr (!kSym) v[e] += p.beta * (p.dq_col ? dc4[j][q][e] : dri) * (f0[e] + f1[e]);
             }
           }
-          if constexpr (kSym) {
+          if constexpr (KIND == kPoly || KIND == kJoin) {
             if (tm == tn && unsigned(row - col) < 4u && row < p.m) {
               const int e = row - col;
               float d = 0.f;
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 if (k == e) {
-                  d = p.alpha_d * acc[i][j][4 * q + k];
+                  d = v[k];
                   v[k] = 0.f;
                 }
-              if constexpr (KIND == kSquare) d += p.k0 + (p.k1 + p.k2 * dv[row]) * dri;
-              p.dc[z * p.mp + row] = d;
+              p.dc[z * p.mp + row] = d * p.unit + (KIND == kPoly ? p.k0 : dri * dv[row]);
             }
           }
           if constexpr (KIND == kUpdate) {
@@ -756,7 +757,7 @@ moe_status launch_nw(const char* name, const Product& p, int count, hipStream_t 
                                            hipFuncAttributeMaxDynamicSharedMemorySize, int(kLds));
   if (e != hipSuccess) return set_error(MOE_ERR_HIP, "%s: LDS attribute: %s", name, hipGetErrorString(e));
   const int MT = (p.m + BM - 1) / BM, NT = (p.n + BNE - 1) / BNE;
-  const int64_t total = int64_t(count) * (KIND == kGram || KIND == kSquare ? sym_tiles(NT) : MT * NT);
+  const int64_t total = int64_t(count) * (KIND <= kJoin ? sym_tiles(NT) : MT * NT);
   const int per = int((total + big::kXcds - 1) / big::kXcds);
   MOE_LAUNCH(name, kern, dim3(unsigned(per * big::kXcds)), dim3(NW * 64), kLds, s, p, per, int(total));
   return MOE_OK;
@@ -846,22 +847,20 @@ struct Run {
     const bool turned = !p.single && p.tall;  // the rows of the transposed X
     g.a = g.b = turned ? xt(i) : x(i);
     g.c = out.o;
-    g.dc = out.d;
     g.sa = g.sb = size_t(p.rp) * p.cp;
     g.sc = size_t(p.mp) * p.mp;
     g.m = g.n = g.ldc = g.mp = p.mp;
     g.k = p.tall ? p.rp : p.cp;
     g.lda = g.ldb = turned ? p.rp : p.cp;
     g.alpha = ldexpf(1.f, Scale<W>::a - 2 * Scale<W>::x);
-    g.alpha_d = ldexpf(1.f, -2 * Scale<W>::x);
     if (p.tall && !turned) return launch_product<W, T, true, true, kGram>("ns_gram", g, false, p.count, a.s);
     return launch_product<W, T, false, false, kGram>("ns_gram", g, !p.single, p.count, a.s);
   }
 
-  // out = k0 I + k1 u + k2 u v; scales 2^su, 2^sv, 2^so of the stored parts.  All commute; k1
-  // needs u = v.
-  moe_status square(const char* name, Sym<W> u, int su, Sym<W> v, int sv, Sym<W> out, int so, float k0, float k1,
-                    float k2) const {
+  // m x m products of commuting symmetric matrices, their scales 2^su, 2^sv, 2^so
+  template <int KIND>
+  moe_status square(const char* name, Sym<W> u, int su, Sym<W> v, int sv, Sym<W> out, int so, float factor = 1.f,
+                    float linear = 1.f, float k0 = 0.f) const {
     Product g{};
     g.a = g.u = u.o;
     g.b = g.v = v.o;  // symmetric: its columns are its rows
@@ -871,15 +870,12 @@ struct Run {
     g.dc = out.d;
     g.sa = g.sb = g.sc = size_t(p.mp) * p.mp;
     g.m = g.n = g.k = g.lda = g.ldb = g.ldc = g.mp = p.mp;
-    g.alpha = ldexpf(k2, so - su - sv);
-    g.g0 = ldexpf(k1, so - sv);
-    g.g1 = ldexpf(k2, so - sv);
-    g.h1 = ldexpf(k2, so - su);
-    g.alpha_d = ldexpf(k2, -su - sv);
+    g.alpha = ldexpf(factor, so - su - sv);
+    g.g = ldexpf(linear, so - sv);
+    g.h = ldexpf(1.f, so - su);
     g.k0 = k0;
-    g.k1 = k1;
-    g.k2 = k2;
-    return launch_product<W, T, false, false, kSquare>(name, g, !p.single, p.count, a.s);
+    g.unit = ldexpf(1.f, -so);
+    return launch_product<W, T, false, false, KIND>(name, g, !p.single, p.count, a.s);
   }
 
   // q X (or X q) for X in x(i), with its low half if `split`; into x(to), with its low half if
@@ -962,14 +958,14 @@ struct Run {
       TRY_NS(gram(cur, q(0)));
       for (int k = 0; k < len; ++k) {
         const int P = k == 0 ? Q : 2;
-        TRY_NS(square("ns_poly", q(0), sa, q(0), sa, q(P), sq, a.ca, a.cb, a.cc));
+        TRY_NS(square<kPoly>("ns_poly", q(0), sa, q(0), sa, q(P), sq, a.cc, a.cb, a.ca));
         if (k + 1 < len) {
-          TRY_NS(square("ns_next", q(P), sq, q(0), sa, q(4), sa, 0.f, 0.f, 1.f));
-          TRY_NS(square("ns_next", q(P), sq, q(4), sa, q(0), sa, 0.f, 0.f, 1.f));
+          TRY_NS(square<kNext>("ns_next", q(P), sq, q(0), sa, q(4), sa));
+          TRY_NS(square<kNext>("ns_next", q(P), sq, q(4), sa, q(0), sa));
         }
         if (k > 0) {
           const int N = Q == 1 ? 3 : 1;
-          TRY_NS(square("ns_join", q(P), sq, q(Q), sq, q(N), sq, 0.f, 0.f, 1.f));
+          TRY_NS(square<kJoin>("ns_join", q(P), sq, q(Q), sq, q(N), sq));
           Q = N;
         }
       }
