@@ -411,6 +411,9 @@ moe_status muon_desc_checks(const moe_muon_desc* m) {
     return set_error(MOE_ERR_INVALID_ARG, "nesterov must be 0 or 1 (got %d)", m->nesterov);
   if (!std::isfinite(m->lr) || !std::isfinite(m->update_scale) || !std::isfinite(m->weight_decay))
     return set_error(MOE_ERR_INVALID_ARG, "lr, update_scale and weight_decay must be finite");
+  if (m->rows > 65535 * 64 || m->cols > 65535 * 64)
+    return set_error(MOE_ERR_UNSUPPORTED, "rows and cols above %d are not supported (got %d, %d)", 65535 * 64, m->rows,
+                     m->cols);
   if (muon_matrix_bytes(m) >= (int64_t(1) << 32))
     return set_error(MOE_ERR_UNSUPPORTED, "a matrix of %d x %d takes 4 GiB or more of workspace", m->rows, m->cols);
   return MOE_OK;

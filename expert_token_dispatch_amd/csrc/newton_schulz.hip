@@ -64,7 +64,7 @@ struct Plan {
   size_t x_bytes, q_bytes;      // one stack of X, of m x m matrices
   int nblk;                     // partial sums of squares per matrix
   bool single;                  // phases of one step (see the top of the file)
-  size_t o_part, o_x[4], o_t[3], o_q[5], o_d[5], bytes;
+  size_t o_part, o_x[4], o_t[4], o_q[5], o_d[5], bytes;
 };
 
 constexpr int kSingleSteps = 256;
@@ -95,14 +95,13 @@ Plan make_plan(const moe_muon_desc* m) {
   };
   p.o_part = take(size_t(p.count) * p.nblk * sizeof(double));
   p.single = m->dtype == MOE_F32 || std::min(m->rows, m->cols) <= kSingleSteps;
-  // X and the X after it, then (float16) the low halves of X_0 and, in single steps, X_1
-  const bool split = m->dtype == MOE_BF16;
-  const int xs = split ? (p.single ? 4 : 3) : 2;
-  for (int i = 0; i < xs; ++i) p.o_x[i] = take(p.x_bytes);
-  // the large tile takes its operands along K, so X is kept transposed too: both X, and for a
-  // wide matrix the low half of X_0
-  if (!p.single)
-    for (int i = 0; i < (p.tall ? 2 : 3); ++i) p.o_t[i] = take(p.x_bytes);
+  // X and the X after it, as they are and transposed, and their low halves: of X_0, in single
+  // steps of X_1 too
+  for (int i = 0; i < 4; ++i) {
+    const bool used = i < 2 || (m->dtype == MOE_BF16 && (i == 2 || p.single));
+    p.o_x[i] = take(used ? p.x_bytes : 0);
+    p.o_t[i] = take(used ? p.x_bytes : 0);
+  }
   for (int i = 0; i < (p.single ? 2 : 5); ++i) {
     p.o_q[i] = take(p.q_bytes);
     p.o_d[i] = take(size_t(p.count) * p.mp * sizeof(float));
@@ -173,63 +172,20 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(const T* __restrict__ g,
   if (threadIdx.x == 0) part[z * gridDim.x + blockIdx.x] = (w[0] + w[1]) + (w[2] + w[3]);
 }
 
-// X_0 = U / (|U| + eps), scaled, into the padded working matrices (hi, and lo with what
-// hi's rounding left); the padding is zero.  Runs of eight elements of a padded row.
+// X_0 = U / (|U| + eps), scaled, into the padded working matrices: X [rp, cp] and, since the
+// products take every operand along K, X transposed [cp, rp].  lo and tlo (each may be NULL)
+// receive what the rounding of hi left.  The padding is zero.  A block turns a tile of
+// 64 x 64 in LDS, whose rows are an odd number of words, so reading down a column passes over
+// the banks.
 template <typename T, typename W, bool MOM>
 __global__ __launch_bounds__(kThreads) void start_kernel(const T* __restrict__ g, const float* __restrict__ mom, float mu,
                                                          int nesterov, int rows, int cols, int rp, int cp,
                                                          const double* __restrict__ part, int nblk, float eps,
-                                                         W* __restrict__ hi, W* __restrict__ lo) {
-  const size_t z = blockIdx.y;
-  __shared__ double total;
-  if (threadIdx.x < 64) {
-    double s = 0.0;
-    for (int i = threadIdx.x; i < nblk; i += 64) s += part[z * nblk + i];
-    for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
-    if (threadIdx.x == 0) total = s;
-  }
-  __syncthreads();
-  const double norm = sqrt(total) + double(eps);
-  const double inv = norm > 0.0 ? double(1 << Scale<W>::x) / norm : (norm == 0.0 ? 0.0 : norm);
-  const size_t n = size_t(rows) * cols, np = size_t(rp) * cp;
-  const bool vec = cols % 8 == 0;
-  const int pieces = cp / 8;
-  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < int64_t(np / 8);
-       i += int64_t(gridDim.x) * kThreads) {
-    const int r = int(i / pieces), c = int(i % pieces) * 8;
-    float u[8] = {};
-    if (r < rows && c < cols) {
-      load8(g + z * n + size_t(r) * cols, c, cols, vec, u);
-      if constexpr (MOM) {
-        float m[8];
-        load8(mom + z * n + size_t(r) * cols, c, cols, vec, m);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) u[k] = nesterov ? u[k] + mu * m[k] : m[k];
-      }
-    }
-    Vec8<W> h, l;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float x = float(double(u[k]) * inv);
-      h.e[k] = W(x);
-      l.e[k] = W(x - float(h.e[k]));
-    }
-    *reinterpret_cast<Vec8<W>*>(hi + z * np + i * 8) = h;
-    if (lo != nullptr) *reinterpret_cast<Vec8<W>*>(lo + z * np + i * 8) = l;
-  }
-}
-
-// The same for the large tile, which also wants X transposed [cp, rp] (thi; tlo if given): a
-// block turns a tile of 64 x 64 in LDS.  Rows of the LDS tile are 33 words, so reading down a
-// column passes over the banks.
-template <typename T, bool MOM>
-__global__ __launch_bounds__(kThreads) void start_both_kernel(const T* __restrict__ g, const float* __restrict__ mom,
-                                                              float mu, int nesterov, int rows, int cols, int rp, int cp,
-                                                              const double* __restrict__ part, int nblk, float eps,
-                                                              f16_t* __restrict__ hi, f16_t* __restrict__ lo,
-                                                              f16_t* __restrict__ thi, f16_t* __restrict__ tlo) {
-  constexpr int kLd = 66;
-  __shared__ f16_t th[64 * kLd], tl[64 * kLd];
+                                                         W* __restrict__ hi, W* __restrict__ lo, W* __restrict__ thi,
+                                                         W* __restrict__ tlo) {
+  constexpr bool kSplit = sizeof(W) == 2;
+  constexpr int kLd = kSplit ? 66 : 65;
+  __shared__ W th[64 * kLd], tl[kSplit ? 64 * kLd : 1];
   __shared__ double total;
   const size_t z = blockIdx.z;
   const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
@@ -257,36 +213,36 @@ __global__ __launch_bounds__(kThreads) void start_both_kernel(const T* __restric
   }
   __syncthreads();
   const double norm = sqrt(total) + double(eps);
-  const double inv = norm > 0.0 ? double(1 << Scale<f16_t>::x) / norm : (norm == 0.0 ? 0.0 : norm);
+  const double inv = norm > 0.0 ? double(1 << Scale<W>::x) / norm : (norm == 0.0 ? 0.0 : norm);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int r = 32 * h + threadIdx.x / 8, c = threadIdx.x % 8 * 8;
-    Vec8<f16_t> vh, vl;
+    Vec8<W> vh, vl;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float x = float(double(u[h][k]) * inv);
-      vh.e[k] = f16_t(x);
-      vl.e[k] = f16_t(x - float(vh.e[k]));
+      vh.e[k] = W(x);
+      vl.e[k] = W(x - float(vh.e[k]));
       th[r * kLd + c + k] = vh.e[k];
-      tl[r * kLd + c + k] = vl.e[k];
+      if constexpr (kSplit) tl[r * kLd + c + k] = vl.e[k];
     }
     const size_t at = z * np + size_t(r0 + r) * cp + c0 + c;
-    *reinterpret_cast<Vec8<f16_t>*>(hi + at) = vh;
-    *reinterpret_cast<Vec8<f16_t>*>(lo + at) = vl;
+    *reinterpret_cast<Vec8<W>*>(hi + at) = vh;
+    if (kSplit && lo != nullptr) *reinterpret_cast<Vec8<W>*>(lo + at) = vl;
   }
   __syncthreads();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int c = 32 * h + threadIdx.x / 8, r = threadIdx.x % 8 * 8;
-    Vec8<f16_t> vh, vl;
+    Vec8<W> vh, vl;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       vh.e[k] = th[(r + k) * kLd + c];
-      vl.e[k] = tl[(r + k) * kLd + c];
+      if constexpr (kSplit) vl.e[k] = tl[(r + k) * kLd + c];
     }
     const size_t at = z * np + size_t(c0 + c) * rp + r0 + r;
-    *reinterpret_cast<Vec8<f16_t>*>(thi + at) = vh;
-    if (tlo != nullptr) *reinterpret_cast<Vec8<f16_t>*>(tlo + at) = vl;
+    *reinterpret_cast<Vec8<W>*>(thi + at) = vh;
+    if (kSplit && tlo != nullptr) *reinterpret_cast<Vec8<W>*>(tlo + at) = vl;
   }
 }
 
@@ -299,13 +255,14 @@ template <typename W> struct Sym {
 
 // One product for every matrix of the stack, sum = A B (+ A2 B2), and what is made of it.
 struct Product {
-  const void* a;      // AK: k-major, element (m, k) at a[k * lda + m]; else m-major
-  const void* b;      // BK: k-major, element (n, k) at b[k * ldb + n]; else n-major
+  const void* a;      // element (m, k) at a[m * lda + k]
+  const void* b;      // element (n, k) at b[n * ldb + k]
   const void* a2;     // the second pair of operands (NULL: none)
   const void* b2;
   void* c;
-  void* c2;           // what C's rounding leaves (small tiles only; NULL: not kept)
-  void* ct;           // C transposed (large tiles only; NULL: not kept)
+  void* ct;           // C transposed (kApply)
+  void* c2;           // what C's rounding leaves, and that transposed (kApply on small tiles; or NULL)
+  void* ct2;
   int ldct;
   size_t sa, sb, sc;  // elements from one matrix of the stack to the next
   int m, n, k, lda, ldb, ldc;
@@ -338,74 +295,23 @@ struct Product {
 
 enum Kind { kGram = 0, kPoly = 1, kNext = 2, kJoin = 3, kApply = 4, kResult = 5, kUpdate = 6 };
 
+// Eight k values of 32 rows of each operand: one MFMA 32x32x16, or eight 32x32x2.
 template <typename W> struct Mma;
 template <> struct Mma<f16_t> {
   static constexpr int kVec = 1;  // 16-byte vectors of a lane's 8 k values
-  __device__ static void mma(const uint4* a, const uint4* b, f32x16_t& c) {
+  __device__ static void mma(const u32x4_t* a, const u32x4_t* b, f32x16_t& c) {
     c = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a[0]), __builtin_bit_cast(f16x8_t, b[0]), c,
                                                0, 0, 0);
   }
 };
 template <> struct Mma<float> {
   static constexpr int kVec = 2;
-  __device__ static void mma(const uint4* a, const uint4* b, f32x16_t& c) {
+  __device__ static void mma(const u32x4_t* a, const u32x4_t* b, f32x16_t& c) {
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[v].x), __uint_as_float(b[v].x), c, 0, 0, 0);
-      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[v].y), __uint_as_float(b[v].y), c, 0, 0, 0);
-      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[v].z), __uint_as_float(b[v].z), c, 0, 0, 0);
-      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[v].w), __uint_as_float(b[v].w), c, 0, 0, 0);
-    }
-  }
-};
-
-// One operand's LDS tile: 64 rows (m or n) by kBK k values, m-major as [64][kBK + pad],
-// k-major as [kBK][64 + pad].  128 bytes of k either way.
-template <typename W, bool KM>
-struct OpTile {
-  static constexpr int kBK = 128 / int(sizeof(W));
-  static constexpr int kEpv = 16 / int(sizeof(W));
-  static constexpr int kRows = KM ? kBK : 64;
-  static constexpr int kCols = KM ? 64 : kBK;
-  static constexpr int kLd = kCols + kEpv;  // rows padded by 16 bytes
-  static constexpr int kChunks = kRows * kCols / kEpv / kThreads;
-  static constexpr int kElems = kRows * kLd;
-
-  // the 16-byte pieces of this thread, from the tile's first row (m-major) or column
-  __device__ static void load(const W* p, int ld, uint4 (&r)[kChunks]) {
+    for (int v = 0; v < 2; ++v)
 #pragma unroll
-    for (int j = 0; j < kChunks; ++j) {
-      const int c = threadIdx.x + j * kThreads;
-      r[j] = *reinterpret_cast<const uint4*>(p + size_t(c / (kCols / kEpv)) * ld + (c % (kCols / kEpv)) * kEpv);
-    }
-  }
-  __device__ static void store(W* t, const uint4 (&r)[kChunks]) {
-#pragma unroll
-    for (int j = 0; j < kChunks; ++j) {
-      const int c = threadIdx.x + j * kThreads;
-      *reinterpret_cast<uint4*>(t + (c / (kCols / kEpv)) * kLd + (c % (kCols / kEpv)) * kEpv) = r[j];
-    }
-  }
-  // row base + (lane & 31), k values kc + 8 (lane / 32) .. +7
-  __device__ static void frag(const W* t, int base, int kc, uint4* f) {
-    const int lane = threadIdx.x & 63;
-    if constexpr (!KM) {
-      const uint4* p = reinterpret_cast<const uint4*>(t + (base + (lane & 31)) * kLd + kc + 8 * (lane >> 5));
-#pragma unroll
-      for (int v = 0; v < Mma<W>::kVec; ++v) f[v] = p[v];
-    } else if constexpr (sizeof(W) == 2) {
-      const int G = lane >> 4, i = lane & 15;
-      const W* p = t + (kc + 8 * (G >> 1) + (i >> 2)) * kLd + base + 16 * (G & 1) + 4 * (i & 3);
-      f[0] = __builtin_bit_cast(uint4, read_kn_frag2(reinterpret_cast<const char*>(p),
-                                                     reinterpret_cast<const char*>(p + 4 * kLd)));
-    } else {
-      const W* p = t + (kc + 8 * (lane >> 5)) * kLd + base + (lane & 31);
-      uint32_t w[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(p[k * kLd]);
-      f[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      f[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
+      for (int k = 0; k < 4; ++k)
+        c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[v][k]), __uint_as_float(b[v][k]), c, 0, 0, 0);
   }
 };
 
@@ -422,91 +328,156 @@ __device__ __forceinline__ void put_last(const Product& p, size_t z, int row, in
   *o = Elem<T>::from_f32(v);
 }
 
-// 64 x 64 tiles, four waves 2 x 2, one MFMA 32x32 block each; the next k slice is in
-// registers while this one is multiplied.  Sides are multiples of 64, so no access needs
-// a bound but the last product's into the user's matrix.
-template <typename W, typename T, bool AK, bool BK, int KIND>
-__global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
-  using TA = OpTile<W, AK>;
-  using TB = OpTile<W, BK>;
-  constexpr int kBK = TA::kBK;
+// Tiles of BT x BT (64 or 128), four waves 2 x 2.  A stage is 128 bytes of k of the tile's A
+// and B rows, filled by direct global->LDS loads (1 KB: eight rows) kSlots - 1 stages ahead,
+// one barrier a stage.  16-byte piece c of row r sits at piece c ^ (r / 2 % 8), so the reads
+// of 16 rows at one piece cover all banks.
+template <int BT>
+struct Ring {
+  static constexpr int kStage = 2 * BT * 128, kSlots = BT == 64 ? 4 : 3;
+  static constexpr int kPerWave = kStage / 1024 / 4, kLds = kSlots * kStage;
+};
+
+template <typename W, typename T, int BT, int KIND>
+__device__ __forceinline__ void product_body(const Product& p, char* lds) {
+  using R = Ring<BT>;
   constexpr bool kSym = KIND <= kJoin;
+  constexpr int MI = BT / 64, kBytes = int(sizeof(W));
   const int tm = blockIdx.y, tn = blockIdx.x;
   if (kSym && tn < tm) return;
   const size_t z = blockIdx.z;
-  __shared__ __attribute__((aligned(16))) W as[TA::kElems];
-  __shared__ __attribute__((aligned(16))) W bs[TB::kElems];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-  f32x16_t acc;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wm = (wave >> 1) * (BT / 2), wn = (wave & 1) * (BT / 2);
+  // waves 0 and 1 load A rows, 2 and 3 B rows; rows past the matrix repeat its last one
+  const bool is_a = wave < 2;
+  const int ld = is_a ? p.lda : p.ldb, rows = is_a ? p.m : p.n;
+  const size_t off = z * (is_a ? p.sa : p.sb);
+  const uint32_t bytes = uint32_t(rows) * uint32_t(ld) * kBytes;
+  const W* first = static_cast<const W*>(is_a ? p.a : p.b) + off;
+  const W* second = p.a2 != nullptr ? static_cast<const W*>(is_a ? p.a2 : p.b2) + off : first;
+  const __amdgpu_buffer_rsrc_t r0 = __builtin_amdgcn_make_buffer_rsrc(const_cast<W*>(first), 0, bytes, kRsrcFlags);
+  const __amdgpu_buffer_rsrc_t r1 = __builtin_amdgcn_make_buffer_rsrc(const_cast<W*>(second), 0, bytes, kRsrcFlags);
+  uint32_t vo[R::kPerWave];
 #pragma unroll
-  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
-  const size_t ka = AK ? size_t(p.lda) : 1, kb = BK ? size_t(p.ldb) : 1;
-  const size_t a0 = z * p.sa + (AK ? size_t(tm) * 64 : size_t(tm) * 64 * p.lda);
-  const size_t b0 = z * p.sb + (BK ? size_t(tn) * 64 : size_t(tn) * 64 * p.ldb);
-  const int slices = p.k / kBK, total = p.a2 != nullptr ? 2 * slices : slices;
-  uint4 ra[TA::kChunks], rb[TB::kChunks];
-  auto fetch = [&](int s) {
-    const bool second = s >= slices;
-    const size_t k0 = size_t(second ? s - slices : s) * kBK;
-    TA::load(static_cast<const W*>(second ? p.a2 : p.a) + a0 + k0 * ka, p.lda, ra);
-    TB::load(static_cast<const W*>(second ? p.b2 : p.b) + b0 + k0 * kb, p.ldb, rb);
+  for (int j = 0; j < R::kPerWave; ++j) {
+    const int r = (wave & 1) * (BT / 2) + 8 * j + (lane >> 3);  // row of the operand's part of the stage
+    const int row = min((is_a ? tm : tn) * BT + r, rows - 1);
+    vo[j] = uint32_t(row) * uint32_t(ld) * kBytes + uint32_t(((lane & 7) ^ ((r >> 1) & 7)) * 16);
+  }
+  const int slices = p.k * kBytes / 128, total = p.a2 != nullptr ? 2 * slices : slices;
+  auto issue = [&](int s) {  // stage min(s, total - 1) into its slot
+    const int st = min(s, total - 1);
+    char* slot = lds + (s % R::kSlots) * R::kStage + R::kPerWave * wave * 1024;
+    const uint32_t ko = uint32_t(st >= slices ? st - slices : st) * 128u;
+#pragma unroll
+    for (int j = 0; j < R::kPerWave; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(st >= slices ? r1 : r0, (lds_ptr_t)(slot + j * 1024), 16, vo[j], ko, 0, 0);
   };
-  fetch(0);
-  for (int s = 0; s < total; ++s) {
-    __syncthreads();
-    TA::store(as, ra);
-    TB::store(bs, rb);
-    __syncthreads();
-    if (s + 1 < total) fetch(s + 1);
+  f32x16_t acc[MI][MI];
 #pragma unroll
-    for (int kc = 0; kc < kBK; kc += 16) {
-      uint4 fa[Mma<W>::kVec], fb[Mma<W>::kVec];
-      TA::frag(as, wm, kc, fa);
-      TB::frag(bs, wn, kc, fb);
-      Mma<W>::mma(fa, fb, acc);
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < MI; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  int ao[MI], bo[MI], sw = ((lane & 31) >> 1) & 7;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    ao[i] = (wm + i * 32 + (lane & 31)) * 128;
+    bo[i] = (BT + wn + i * 32 + (lane & 31)) * 128;
+  }
+  constexpr int kVec = Mma<W>::kVec;
+  for (int s = 0; s < R::kSlots - 1; ++s) issue(s);
+  for (int s = 0; s < total; ++s) {
+    MOE_VMCNT(R::kPerWave * (R::kSlots - 2));  // this wave's loads of stage s have landed
+    MOE_LGKMCNT0();                            // and its reads of stage s - 1
+    block_barrier();                           // every wave's have
+    issue(s + R::kSlots - 1);                  // into the slot stage s - 1 used
+    const char* st = lds + (s % R::kSlots) * R::kStage;
+#pragma unroll
+    for (int kc = 0; kc < 8 / (2 * kVec); ++kc) {
+      u32x4_t fa[MI][kVec], fb[MI][kVec];
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) {
+        const int c = (((2 * kc + (lane >> 5)) * kVec + v) ^ sw) * 16;
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+          fa[i][v] = *reinterpret_cast<const u32x4_t*>(st + ao[i] + c);
+          fb[i][v] = *reinterpret_cast<const u32x4_t*>(st + bo[i] + c);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < MI; ++j) Mma<W>::mma(fa[i], fb[j], acc[i][j]);
     }
   }
+  MOE_VMCNT(0);  // the ring's last (repeated) loads land before the block ends
   // lane -> column (lane & 31), register r -> row 8 (r / 4) + 4 (lane / 32) + r % 4
-  const int col = tn * 64 + wn + (lane & 31);
   const float* du = p.du + z * p.mp;
   const float* dv = p.dv + z * p.mp;
   const float* dq = p.dq + z * p.mp;
+  W* c = static_cast<W*>(p.c);
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int row = tm * 64 + wm + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-    const size_t ci = z * p.sc + size_t(row) * p.ldc + col;
-    W* c = static_cast<W*>(p.c);
-    float v = p.alpha * acc[r];
-    if constexpr (kSym) {
-      if constexpr (KIND == kPoly) v += p.g * float(static_cast<const W*>(p.v)[ci]);
-      if constexpr (KIND == kNext || KIND == kJoin) v += p.g * du[row] * float(static_cast<const W*>(p.v)[ci]);
-      if constexpr (KIND == kJoin) v += p.h * dv[col] * float(static_cast<const W*>(p.u)[ci]);
-      if ((KIND == kPoly || KIND == kJoin) && row == col) {
-        p.dc[z * p.mp + row] = v * p.unit + (KIND == kPoly ? p.k0 : du[row] * dv[row]);
-        v = 0.f;
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < MI; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int col = tn * BT + wn + j * 32 + (lane & 31);
+        const int row = tm * BT + wm + i * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        if (BT > kPad && (row >= p.m || col >= p.n)) continue;
+        const size_t ci = z * p.sc + size_t(row) * p.ldc + col;
+        float v = p.alpha * acc[i][j][r];
+        if constexpr (kSym) {
+          if constexpr (KIND == kPoly) v += p.g * float(static_cast<const W*>(p.v)[ci]);
+          if constexpr (KIND == kNext || KIND == kJoin) v += p.g * du[row] * float(static_cast<const W*>(p.v)[ci]);
+          if constexpr (KIND == kJoin) v += p.h * dv[col] * float(static_cast<const W*>(p.u)[ci]);
+          if ((KIND == kPoly || KIND == kJoin) && row == col) {
+            p.dc[z * p.mp + row] = v * p.unit + (KIND == kPoly ? p.k0 : du[row] * dv[row]);
+            v = 0.f;
+          }
+          c[ci] = W(v);
+          if (tn != tm) c[z * p.sc + size_t(col) * p.ldc + row] = W(v);
+        } else {
+          float x = float(static_cast<const W*>(p.x)[ci]);
+          if (p.x2 != nullptr) x += float(static_cast<const W*>(p.x2)[ci]);
+          v += p.beta * dq[p.dq_col ? col : row] * x;
+          if constexpr (KIND == kApply) {
+            const W h = W(v), l = W(v - float(h));
+            const size_t ti = z * p.sc + size_t(col) * p.ldct + row;
+            c[ci] = h;
+            static_cast<W*>(p.ct)[ti] = h;
+            if (p.c2 != nullptr) static_cast<W*>(p.c2)[ci] = l;
+            if (p.ct2 != nullptr) static_cast<W*>(p.ct2)[ti] = l;
+          } else if (row < p.rows && col < p.cols) {
+            put_last<T, KIND>(p, z, row, col, v);
+          }
+        }
       }
-      c[ci] = W(v);
-      if (tn != tm) c[z * p.sc + size_t(col) * p.ldc + row] = W(v);
-    } else {
-      float x = float(static_cast<const W*>(p.x)[ci]);
-      if (p.x2 != nullptr) x += float(static_cast<const W*>(p.x2)[ci]);
-      v += p.beta * dq[p.dq_col ? col : row] * x;
-      if constexpr (KIND == kApply) {
-        const W h = W(v);
-        c[ci] = h;
-        if (p.c2 != nullptr) static_cast<W*>(p.c2)[ci] = W(v - float(h));
-      } else if (row < p.rows && col < p.cols) {
-        put_last<T, KIND>(p, z, row, col, v);
-      }
-    }
-  }
+}
+
+template <typename W, typename T, int BT, int KIND>
+__global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  product_body<W, T, BT, KIND>(p, lds);
+}
+
+template <typename W, typename T, int BT, int KIND>
+moe_status launch_ring(const char* name, const Product& p, int count, hipStream_t s) {
+  auto kern = product_kernel<W, T, BT, KIND>;
+  constexpr int lds = Ring<BT>::kLds;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e != hipSuccess) return set_error(MOE_ERR_HIP, "%s: LDS attribute: %s", name, hipGetErrorString(e));
+  MOE_LAUNCH(name, kern, dim3(unsigned((p.n + BT - 1) / BT), unsigned((p.m + BT - 1) / BT), unsigned(count)),
+             dim3(kThreads), lds, s, p);
+  return MOE_OK;
 }
 
 // ---- the same on the large tile (float16, sides past kSingleSteps) ---------------------
-// 256 x 256 tiles of big_tile.h, both operands contiguous along K: X is kept in both layouts
-// (with one operand the other way round, through the transposing LDS reads, a step of 64 k
-// took 2.25 us against 1.69, with both 3.1).  The accumulators hold four neighbouring columns of one
+// 256 x 256 tiles of big_tile.h, both operands along K (with one of them the other way round,
+// through the transposing LDS reads, a step of 64 k took 2.25 us against 1.69, with both 3.1).  The accumulators hold four neighbouring columns of one
 // row at a time, so the epilogue reads what it adds eight bytes a lane, turns the tile to
 // float16 in LDS and writes whole row pieces; a symmetric product's tile off the diagonal
 // is written a second time, its columns read back as rows by the transposing LDS reads.
@@ -763,21 +734,26 @@ moe_status launch_nw(const char* name, const Product& p, int count, hipStream_t 
   return MOE_OK;
 }
 
+// Four waves from 64 steps of k on, eight below, as for the grouped products (muon_wide's
+// shape, K = 4096 and 14336: four are 2.7% faster; orth_many's, K = 768: 6% slower).
 template <int KIND>
 moe_status launch(const char* name, const Product& p, int count, hipStream_t s) {
+  if (p.k / BK >= 64) return launch_nw<4, KIND>(name, p, count, s);
   return launch_nw<8, KIND>(name, p, count, s);
 }
 
 }  // namespace nsbig
 
-template <typename W, typename T, bool AK, bool BK, int KIND>
+// The large tile takes float16 matrices past kSingleSteps; of the small ones the 128 x 128
+// where they fill the CUs twice.
+template <typename W, typename T, int KIND>
 moe_status launch_product(const char* name, const Product& p, bool large, int count, hipStream_t s) {
-  if constexpr (sizeof(W) == 2 && !AK && !BK) {
+  if constexpr (sizeof(W) == 2) {
     if (large) return nsbig::launch<KIND>(name, p, count, s);
   }
-  MOE_LAUNCH(name, (product_kernel<W, T, AK, BK, KIND>), dim3(unsigned(p.n / 64), unsigned(p.m / 64), unsigned(count)),
-             dim3(kThreads), 0, s, p);
-  return MOE_OK;
+  const int64_t t = int64_t((p.m + 127) / 128) * ((p.n + 127) / 128) * count;
+  if ((KIND <= kJoin ? t / 2 : t) >= 512) return launch_ring<W, T, 128, KIND>(name, p, count, s);
+  return launch_ring<W, T, 64, KIND>(name, p, count, s);
 }
 
 #define TRY_NS(expr)                       \
@@ -805,9 +781,11 @@ struct Run {
     const T* g = static_cast<const T*>(a.grad);
     double* part = reinterpret_cast<double*>(base + p.o_part);
     const dim3 gn(unsigned(p.nblk), unsigned(p.count));
-    const int64_t np = int64_t(p.rp) * p.cp;
-    const dim3 gs(unsigned(std::min<int64_t>(1024, (np + 2047) / 2048)), unsigned(p.count));
+    const dim3 gs(unsigned(p.cp / 64), unsigned(p.rp / 64), unsigned(p.count));
+    // the low half where the first application takes it as an operand, and in the X layout
+    // for its epilogue
     W* lo = kSplit ? x(2) : nullptr;
+    W* tlo = kSplit && !p.tall ? xt(2) : nullptr;
     const bool mom = a.momentum != nullptr;
     if (mom) {
       MOE_LAUNCH("muon_momentum", (norm_kernel<T, true>), gn, dim3(kThreads), 0, a.s, g, a.momentum, m->momentum,
@@ -816,27 +794,13 @@ struct Run {
       MOE_LAUNCH("orth_norm", (norm_kernel<T, false>), gn, dim3(kThreads), 0, a.s, g, static_cast<float*>(nullptr), 0.f,
                  0, n, part);
     }
-    if constexpr (kSplit) {
-      if (!p.single) {
-        const dim3 gb(unsigned(p.cp / 64), unsigned(p.rp / 64), unsigned(p.count));
-        W* tlo = p.tall ? nullptr : xt(2);
-        if (mom) {
-          MOE_LAUNCH("muon_start", (start_both_kernel<T, true>), gb, dim3(kThreads), 0, a.s, g, a.momentum, m->momentum,
-                     m->nesterov, p.rows, p.cols, p.rp, p.cp, part, p.nblk, m->eps, x(0), lo, xt(0), tlo);
-        } else {
-          MOE_LAUNCH("orth_start", (start_both_kernel<T, false>), gb, dim3(kThreads), 0, a.s, g,
-                     static_cast<const float*>(nullptr), 0.f, 0, p.rows, p.cols, p.rp, p.cp, part, p.nblk, m->eps, x(0),
-                     lo, xt(0), tlo);
-        }
-        return MOE_OK;
-      }
-    }
     if (mom) {
       MOE_LAUNCH("muon_start", (start_kernel<T, W, true>), gs, dim3(kThreads), 0, a.s, g, a.momentum, m->momentum,
-                 m->nesterov, p.rows, p.cols, p.rp, p.cp, part, p.nblk, m->eps, x(0), lo);
+                 m->nesterov, p.rows, p.cols, p.rp, p.cp, part, p.nblk, m->eps, x(0), lo, xt(0), tlo);
     } else {
       MOE_LAUNCH("orth_start", (start_kernel<T, W, false>), gs, dim3(kThreads), 0, a.s, g,
-                 static_cast<const float*>(nullptr), 0.f, 0, p.rows, p.cols, p.rp, p.cp, part, p.nblk, m->eps, x(0), lo);
+                 static_cast<const float*>(nullptr), 0.f, 0, p.rows, p.cols, p.rp, p.cp, part, p.nblk, m->eps, x(0), lo,
+                 xt(0), tlo);
     }
     return MOE_OK;
   }
@@ -844,17 +808,15 @@ struct Run {
   // A = X X^T (or X^T X), X in x(i)
   moe_status gram(int i, Sym<W> out) const {
     Product g{};
-    const bool turned = !p.single && p.tall;  // the rows of the transposed X
-    g.a = g.b = turned ? xt(i) : x(i);
+    g.a = g.b = p.tall ? xt(i) : x(i);
     g.c = out.o;
     g.sa = g.sb = size_t(p.rp) * p.cp;
     g.sc = size_t(p.mp) * p.mp;
     g.m = g.n = g.ldc = g.mp = p.mp;
     g.k = p.tall ? p.rp : p.cp;
-    g.lda = g.ldb = turned ? p.rp : p.cp;
+    g.lda = g.ldb = g.k;
     g.alpha = ldexpf(1.f, Scale<W>::a - 2 * Scale<W>::x);
-    if (p.tall && !turned) return launch_product<W, T, true, true, kGram>("ns_gram", g, false, p.count, a.s);
-    return launch_product<W, T, false, false, kGram>("ns_gram", g, !p.single, p.count, a.s);
+    return launch_product<W, T, kGram>("ns_gram", g, !p.single, p.count, a.s);
   }
 
   // m x m products of commuting symmetric matrices, their scales 2^su, 2^sv, 2^so
@@ -875,7 +837,7 @@ struct Run {
     g.h = ldexpf(1.f, so - su);
     g.k0 = k0;
     g.unit = ldexpf(1.f, -so);
-    return launch_product<W, T, false, false, KIND>(name, g, !p.single, p.count, a.s);
+    return launch_product<W, T, KIND>(name, g, !p.single, p.count, a.s);
   }
 
   // q X (or X q) for X in x(i), with its low half if `split`; into x(to), with its low half if
@@ -886,10 +848,8 @@ struct Run {
     const W* hi = x(i);
     const W* lo = split ? x(i + 2) : nullptr;
     // the low halves first, while the sums are small
-    const bool turned = !p.single && !p.tall;
-    const W* h = turned ? xt(i) : hi;
-    const W* first = split ? (turned ? xt(2) : lo) : h;
-    const W* second = split ? h : nullptr;
+    const W* first = p.tall ? (split ? lo : hi) : (split ? xt(i + 2) : xt(i));
+    const W* second = !split ? nullptr : (p.tall ? hi : xt(i));
     if (p.tall) {
       g.a = first;
       g.a2 = second;
@@ -907,7 +867,7 @@ struct Run {
       g.sa = sq;
       g.sb = sx;
       g.lda = p.mp;
-      g.ldb = turned ? p.rp : p.cp;
+      g.ldb = p.rp;
     }
     g.sc = sx;
     g.m = p.rp;
@@ -919,31 +879,26 @@ struct Run {
     g.dq_col = p.tall;
     if (to >= 0) {
       g.c = x(to);
-      if (keep) g.c2 = x(to + 2);
-      if (!p.single) {
-        g.ct = xt(to);
-        g.ldct = p.rp;
+      g.ct = xt(to);
+      g.ldct = p.rp;
+      if (keep) {
+        g.c2 = x(to + 2);
+        g.ct2 = p.tall ? nullptr : xt(to + 2);
       }
       g.alpha = ldexpf(1.f, -Scale<W>::q);
       g.beta = 1.f;
-      return launch_apply<kApply>("ns_apply", g);
+      return launch_product<W, T, kApply>("ns_apply", g, !p.single, p.count, a.s);
     }
     g.alpha = ldexpf(1.f, -Scale<W>::q - Scale<W>::x);
     g.beta = ldexpf(1.f, -Scale<W>::x);
     g.out = a.out;
     g.rows = p.rows;
     g.cols = p.cols;
-    if (a.momentum == nullptr) return launch_apply<kResult>("ns_apply_result", g);
+    if (a.momentum == nullptr) return launch_product<W, T, kResult>("ns_apply_result", g, !p.single, p.count, a.s);
     g.master = a.master;
     g.keep = 1.f - a.m->lr * a.m->weight_decay;
     g.step = a.m->lr * a.m->update_scale;
-    return launch_apply<kUpdate>("muon_apply", g);
-  }
-
-  template <int KIND>
-  moe_status launch_apply(const char* name, const Product& g) const {
-    if (p.tall || !p.single) return launch_product<W, T, false, false, KIND>(name, g, !p.single, p.count, a.s);
-    return launch_product<W, T, false, true, KIND>(name, g, !p.single, p.count, a.s);
+    return launch_product<W, T, kUpdate>("muon_apply", g, !p.single, p.count, a.s);
   }
 
   moe_status run() const {

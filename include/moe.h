@@ -507,7 +507,8 @@ moe_status moe_layer_backward(const moe_layer_desc* d, const void* x, const void
 /* leaves the singular vectors.  A zero matrix stays zero.                    */
 /* ======================================================================== */
 
-/*   count, rows, cols  the stack [count, rows, cols], each >= 1 (count at most 65535)
+/*   count, rows, cols  the stack [count, rows, cols], each >= 1 (count at most 65535, rows and
+ *                      cols at most 4194240)
  *   dtype              moe_dtype of the gradient, the weight and moe_orthogonalize's result
  *   steps              Newton-Schulz steps, 1..10
  *   coef_a, b, c       coefficients of a step, 0 < a <= 4 (all three 0: 3.4445, -4.7750,

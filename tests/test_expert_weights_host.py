@@ -106,6 +106,7 @@ MUON_BAD = [
     (dict(coefs=(1.0, 9.0, -9.0)), "INVALID_ARG"),       # both ends fine, past 3 between them
     (dict(coefs=(float("nan"), 0.0, 0.0)), "INVALID_ARG"),
     (dict(rows=65536, cols=32768), "UNSUPPORTED"),       # 4 GiB in float16
+    (dict(rows=4194241, cols=1), "UNSUPPORTED"),
 ]
 
 
