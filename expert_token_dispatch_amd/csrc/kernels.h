@@ -141,6 +141,9 @@ moe_status launch_packed_ffn(const PackedFfnArgs& a);
 // its kernel for a few rows per expert (packed_skinny.hip), which needs no scratch
 bool packed_skinny_fits(const moe_layer_desc* d, int64_t max_pairs);
 moe_status launch_packed_skinny(const PackedFfnArgs& a);
+// and for more (packed_gemm.hip), without scratch too
+bool packed_gemm_fits(const moe_layer_desc* d, int64_t max_pairs);
+moe_status launch_packed_gemm(const PackedFfnArgs& a);
 
 struct CombineArgs {
   const moe_layer_desc* d;

@@ -1,0 +1,305 @@
+// The packed experts' feed-forward for segments past a few rows, on the 4-bit weights as
+// they are.
+//
+// A block of four waves owns 128 token rows by 256 weight rows of one expert (gate/up: 128
+// gate rows and the same up rows), a wave all the token rows by 64 weight rows: 4 x 2 MFMA
+// 32x32 accumulators, 32-row blocks past the segment's end left out.  Two blocks share a
+// CU, so that one's epilogue runs beside the other's products.
+//
+// A step is 64 k.  Token rows (128 bytes a step) and codes (32 bytes a step) come by direct
+// global->LDS loads into three slots, two steps ahead.  A lane takes 16 bytes of codes, 32 k
+// under one scale, for its weight row; they become four fragments in registers
+// (v_cvt_scalef32_pk_bf16_fp4, eight a fragment pair, beside eight MFMAs).  The MFMA sums
+// over k in any order: fragment c of lane half g is k = 32 g + 8 c .. of the step in both
+// operands.  The scale bytes come straight to registers, two steps (four bytes) a load.
+//
+// In LDS 16-byte piece c of token row r sits at piece c ^ (r / 2 % 8), piece c of weight row
+// r at c ^ (r / 8 % 2): the reads of 16 rows at one piece cover all banks.
+#include <math.h>
+
+#include <algorithm>
+
+#include "big_tile.h"
+#include "kernels.h"
+#include "packed.h"
+
+namespace moe {
+namespace {
+namespace pk {
+
+constexpr int BM = 128, BNR = 256, BK = 64, kThreads = 256, kSlots = 3;
+constexpr int kStageA = BM * 128, kStageB = BNR * 32, kStage = kStageA + kStageB;  // 16 + 8 KB
+constexpr int kGroup = 4;  // n-tiles per group of the tile order
+constexpr int kXcds = 8;
+
+template <int NMAT>
+struct Shape {
+  static constexpr int kCols = BNR / NMAT;         // output columns
+  static constexpr int kRS = kCols * 2 + 16;       // a row of the output tile in LDS
+  static constexpr int kLds = kSlots * kStage > BM * kRS ? kSlots * kStage : BM * kRS;
+};
+
+// Tile t of the local experts' tiles, numbered over (expert, group of n-tiles, m-tile, n-tile
+// in group); every wave finds it for itself, 64 experts at a time.  Returns the total.
+struct Tile {
+  int expert, row0, rows, n;
+};
+__device__ __forceinline__ int tiles_of(const int32_t* __restrict__ offsets, int L, int NT, int e, int& first) {
+  first = offsets[min(e, L)];
+  const int n = e < L ? offsets[e + 1] - first : 0;
+  return (n + BM - 1) / BM * NT;
+}
+__device__ __forceinline__ int total_tiles(const int32_t* __restrict__ offsets, int L, int NT) {
+  int sum = 0, first;
+  for (int e = threadIdx.x & 63; e < L; e += 64) sum += tiles_of(offsets, L, NT, e, first);
+  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
+  return sum;
+}
+__device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offsets, int L, int NT, int t) {
+  const int lane = threadIdx.x & 63;
+  Tile r{-1, 0, 0, 0};
+  for (int base = 0; base < L; base += 64) {
+    int first;
+    const int mine = tiles_of(offsets, L, NT, base + lane, first);
+    int incl = mine;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(incl, d, 64);
+      if (lane >= d) incl += o;
+    }
+    const uint64_t past = __ballot(incl > t);
+    if (past) {
+      const int l = __ffsll((unsigned long long)past) - 1;
+      r.expert = base + l;
+      t -= __shfl(incl - mine, l, 64);
+      const int seg0 = __shfl(first, l, 64), mt = __shfl(mine, l, 64) / NT;
+      const int seg1 = offsets[r.expert + 1];
+      const int g = min(t / (mt * kGroup), (NT - 1) / kGroup);
+      t -= g * mt * kGroup;
+      const int w = min(kGroup, NT - g * kGroup);
+      r.row0 = seg0 + t / w * BM;
+      r.rows = min(BM, seg1 - r.row0);
+      r.n = g * kGroup + t % w;
+      return r;
+    }
+    t -= __shfl(incl, 63, 64);
+  }
+  return r;
+}
+
+template <int NMAT>
+__device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t* __restrict__ offsets,
+                                     const uint8_t* __restrict__ q0, const uint8_t* __restrict__ s0,
+                                     const uint8_t* __restrict__ q1, const uint8_t* __restrict__ s1,
+                                     bf16_t* __restrict__ C, int L, int N, int K, char* lds) {
+  using S = Shape<NMAT>;
+  const int NT = (N + S::kCols - 1) / S::kCols;
+  const int total = __builtin_amdgcn_readfirstlane(total_tiles(offsets, L, NT));
+  const int per = (total + kXcds - 1) / kXcds;
+  const int xcd = blockIdx.x % kXcds, loc = blockIdx.x / kXcds, t = xcd * per + loc;
+  if (loc >= per || t >= total) return;
+  const Tile tile = find_tile(offsets, L, NT, t);
+  const int expert = __builtin_amdgcn_readfirstlane(tile.expert);
+  const int row0 = __builtin_amdgcn_readfirstlane(tile.row0), rows = __builtin_amdgcn_readfirstlane(tile.rows);
+  const int n0 = __builtin_amdgcn_readfirstlane(tile.n) * S::kCols;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int half = lane >> 5, fr = lane & 31;
+
+  // ---- loads.  Token rows: this wave's 32 (four loads of eight rows); past the segment
+  // they repeat its last row.  Codes: its 64 stage rows (two loads of 32); gate/up: waves 0
+  // and 1 gate rows, 2 and 3 up rows.  Rows past N repeat row N - 1.  Neither reaches an
+  // output that is stored.
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<bf16_t*>(A + size_t(row0) * K), 0, uint32_t(rows) * uint32_t(K) * 2u, kRsrcFlags);
+  const size_t eq = size_t(expert) * N * (K / 2), es = size_t(expert) * N * (K / 32);
+  const bool second = NMAT == 2 && wave >= 2;
+  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>((second ? q1 : q0) + eq), 0,
+                                                                      uint32_t(N) * uint32_t(K / 2), kRsrcFlags);
+  uint32_t va[4], vb[2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = wave * 32 + 8 * j + (lane >> 3);
+    va[j] = uint32_t(min(r, rows - 1)) * uint32_t(K) * 2u + uint32_t(((lane & 7) ^ ((r >> 1) & 7)) * 16);
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int r = wave * 64 + 32 * j + (lane >> 1);  // stage row
+    const int row = min(n0 + (NMAT == 2 ? r % 128 : r), N - 1);
+    vb[j] = uint32_t(row) * uint32_t(K / 2) + uint32_t(((lane & 1) ^ ((r >> 3) & 1)) * 16);
+  }
+  const int steps = (K + BK - 1) / BK;
+  // K is a multiple of 32: the last step may be half a one; its token pieces past K read as
+  // zero (an address behind the buffer), its codes may be whatever follows
+  const bool cut = (K & 32) != 0;
+  auto issue = [&](int s) {  // step min(s, steps - 1) into slot s
+    const int st = min(s, steps - 1);
+    char* slot = lds + (s % kSlots) * kStage;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = (lane & 7) ^ (((wave * 32 + 8 * j + (lane >> 3)) >> 1) & 7);
+      const uint32_t vo = cut && st == steps - 1 && c >= 4 ? 0xFFFFFFF0u : va[j];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(slot + (4 * wave + j) * 1024), 16, vo, uint32_t(st) * 128u, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(slot + kStageA + (2 * wave + j) * 1024), 16, vb[j],
+                                               uint32_t(st) * 32u, 0, 0);
+  };
+
+  // ---- this lane's weight rows: stage row of block j, and its scales.  Four bytes are two
+  // steps; where a row's bytes are no whole words the loads are unaligned, and at its end short.
+  const uint8_t* sp[2];
+  int br[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    br[j] = NMAT == 2 ? j * 128 + wave * 32 + fr : wave * 64 + j * 32 + fr;
+    const int row = min(n0 + (NMAT == 2 ? wave * 32 + fr : br[j]), N - 1);
+    sp[j] = (NMAT == 2 && j == 1 ? s1 : s0) + es + size_t(row) * (K / 32);
+  }
+  const int groups = K / 32;
+  auto load_s = [&](int s, uint32_t (&v)[2]) {  // the scales of steps s and s + 1, s even
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      v[j] = 0;
+      if (2 * s + 4 <= groups) {
+        __builtin_memcpy(&v[j], sp[j] + 2 * s, 4);
+      } else {
+        for (int i = 0; i < 3; ++i)
+          if (2 * s + i < groups) v[j] |= uint32_t(sp[j][2 * s + i]) << (8 * i);
+      }
+    }
+  };
+
+  f32x16_t acc[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  const int sw = (fr >> 1) & 7;
+  const int blocks = (rows + 31) / 32;
+  uint32_t sc[2], sn[2];
+  load_s(0, sc);
+  issue(0);
+  issue(1);
+  for (int s = 0; s < steps; ++s) {
+    // the step's loads have landed: at most the next step's six are left (and any scales,
+    // which only makes the wait longer)
+    MOE_VMCNT(6);
+    MOE_LGKMCNT0();
+    block_barrier();
+    issue(s + 2);
+    if ((s & 1) == 0) load_s(s + 2 < steps ? s + 2 : 0, sn);
+    const char* st = lds + (s % kSlots) * kStage;
+    u32x4_t w[2];
+    float f[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      w[j] = *reinterpret_cast<const u32x4_t*>(st + kStageA + br[j] * 32 + ((half ^ ((br[j] >> 3) & 1)) * 16));
+      f[j] = __uint_as_float(((sc[j] >> (16 * (s & 1) + 8 * half)) & 0xFFu) << 23);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const bf16x8_t b0 = decode_frag(w[0][c], f[0]), b1 = decode_frag(w[1][c], f[1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i < blocks) {
+          const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(st + (i * 32 + fr) * 128 + (((4 * half + c) ^ sw) * 16));
+          acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b0, a, acc[i][0], 0, 0, 0);
+          acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b1, a, acc[i][1], 0, 0, 0);
+        }
+      }
+    }
+    if (s & 1) {
+      sc[0] = sn[0];
+      sc[1] = sn[1];
+    }
+  }
+  MOE_VMCNT(0);  // the last (repeated) loads land before the LDS is used again
+  MOE_LGKMCNT0();
+  block_barrier();
+
+  // ---- epilogue: the products were (weight rows) x (token rows), so lane l holds token row
+  // l % 32 and register 4q + u column 8q + 4 (l / 32) + u; the tile goes through LDS and
+  // out in whole row pieces
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i < blocks) {
+#pragma unroll
+      for (int j = 0; j < 2 / NMAT; ++j) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            v[u] = NMAT == 2 ? silu(acc[i][0][4 * q + u]) * acc[i][1][4 * q + u] : acc[i][j][4 * q + u];
+          const int cl = (NMAT == 2 ? wave * 32 : wave * 64 + j * 32) + 8 * q + 4 * half;
+          *reinterpret_cast<uint2*>(lds + (i * 32 + fr) * S::kRS + cl * 2) =
+              make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        }
+      }
+    }
+  }
+  MOE_LGKMCNT0();
+  block_barrier();
+  constexpr int kPieces = S::kCols / 8;
+#pragma unroll
+  for (int u = 0; u < BM * kPieces / kThreads; ++u) {
+    const int id = tid + kThreads * u, r = id / kPieces, c = id % kPieces * 8;
+    // N is a multiple of 8: a piece is inside or outside as a whole
+    if (r < rows && n0 + c < N)
+      *reinterpret_cast<u32x4_t*>(C + size_t(row0 + r) * N + n0 + c) =
+          *reinterpret_cast<const u32x4_t*>(lds + r * S::kRS + c * 2);
+  }
+}
+
+template <int NMAT>
+__global__ __launch_bounds__(kThreads, 2) void kernel(const bf16_t* __restrict__ A, const int32_t* __restrict__ offsets,
+                                                      const uint8_t* __restrict__ q0, const uint8_t* __restrict__ s0,
+                                                      const uint8_t* __restrict__ q1, const uint8_t* __restrict__ s1,
+                                                      bf16_t* __restrict__ C, int L, int N, int K) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  body<NMAT>(A, offsets, q0, s0, q1, s1, C, L, N, K, lds);
+}
+
+template <int NMAT>
+moe_status launch(const char* name, const bf16_t* A, const int32_t* offsets, const void* q0, const void* s0,
+                  const void* q1, const void* s1, bf16_t* C, int L, int N, int K, int64_t max_pairs, hipStream_t s) {
+  using S = Shape<NMAT>;
+  auto kern = kernel<NMAT>;
+  const hipError_t e =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
+  if (e != hipSuccess) return set_error(MOE_ERR_HIP, "%s: LDS attribute: %s", name, hipGetErrorString(e));
+  // at most this many tiles: every expert with rows may end in a partly filled one
+  const int64_t m = max_pairs / BM + std::min<int64_t>(L, max_pairs);
+  const int64_t tiles = m * ((N + S::kCols - 1) / S::kCols);
+  const int64_t per = (tiles + kXcds - 1) / kXcds;
+  MOE_LAUNCH(name, kern, dim3(unsigned(per * kXcds)), dim3(kThreads), S::kLds, s, A, offsets,
+             static_cast<const uint8_t*>(q0), static_cast<const uint8_t*>(s0), static_cast<const uint8_t*>(q1),
+             static_cast<const uint8_t*>(s1), C, L, N, K);
+  return MOE_OK;
+}
+
+}  // namespace pk
+}  // namespace
+
+bool packed_gemm_fits(const moe_layer_desc* d, int64_t max_pairs) {
+  // an expert's codes and 128 token rows are addressed with 32-bit byte offsets, tiles counted in an int
+  const int64_t H = d->hidden, I = d->intermediate;
+  return d->dtype == MOE_BF16 && H * I / 2 < (int64_t(1) << 32) - 16 && std::max(H, I) * 256 < (int64_t(1) << 32) - 16 &&
+         (max_pairs / pk::BM + d->local_count) * ((std::max(H, I) + 127) / 128) < (int64_t(1) << 30);
+}
+
+moe_status launch_packed_gemm(const PackedFfnArgs& a) {
+  const moe_layer_desc* d = a.d;
+  const int L = d->local_count, H = d->hidden, I = d->intermediate;
+  const moe_packed_experts& p = *a.p;
+  bf16_t* h = static_cast<bf16_t*>(a.h);
+  const moe_status st = pk::launch<2>("ffn_gate_up", static_cast<const bf16_t*>(a.x_sorted), a.offsets, p.gate_codes,
+                                      p.gate_scales, p.up_codes, p.up_scales, h, L, I, H, a.max_pairs, a.s);
+  if (st != MOE_OK) return st;
+  return pk::launch<1>("ffn_down", h, a.offsets, p.down_codes, p.down_scales, p.down_codes, p.down_scales,
+                       static_cast<bf16_t*>(a.y_sorted), L, H, I, a.max_pairs, a.s);
+}
+
+}  // namespace moe

@@ -25,24 +25,13 @@
 
 #include "ffn_common.h"
 #include "kernels.h"
+#include "packed.h"
 
 namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kStep = 128;   // k of a step
-
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-
-// eight codes -> eight bf16, times the scale
-__device__ __forceinline__ bf16x8_t decode_frag(uint32_t w, float s) {
-  u32x4_t r;
-  r[0] = __builtin_bit_cast(uint32_t, (bf16x2_t)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
-  r[1] = __builtin_bit_cast(uint32_t, (bf16x2_t)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
-  r[2] = __builtin_bit_cast(uint32_t, (bf16x2_t)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
-  r[3] = __builtin_bit_cast(uint32_t, (bf16x2_t)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
-  return __builtin_bit_cast(bf16x8_t, r);
-}
 
 // The `slot`-th expert that has rows (slots are at most the rows, experts may be many and
 // mostly empty), or -1.  Every wave finds it for itself.

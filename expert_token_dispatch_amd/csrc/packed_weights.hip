@@ -246,13 +246,14 @@ size_t stack_bytes(const moe_layer_desc* d) {
 }  // namespace
 
 size_t packed_ffn_scratch_bytes(const moe_layer_desc* d, int64_t max_pairs) {
-  if (packed_skinny_fits(d, max_pairs)) return 0;
+  if (packed_skinny_fits(d, max_pairs) || packed_gemm_fits(d, max_pairs)) return 0;
   return 3 * stack_bytes(d) + align_up(ffn_scratch_bytes(d, max_pairs), 256);
 }
 
 moe_status launch_packed_ffn(const PackedFfnArgs& a) {
   if (a.max_pairs <= 0) return MOE_OK;
   if (packed_skinny_fits(a.d, a.max_pairs)) return launch_packed_skinny(a);
+  if (packed_gemm_fits(a.d, a.max_pairs)) return launch_packed_gemm(a);
   const moe_layer_desc* d = a.d;
   const int L = d->local_count, H = d->hidden, I = d->intermediate;
   char* base = static_cast<char*>(a.scratch);

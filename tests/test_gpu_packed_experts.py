@@ -123,6 +123,11 @@ FFN = [
     (256, 320, (300, 0, 200), "bf16"),
     (256, 320, (700, 90), "bf16"),
     (4096, 64, (1, 1), "bf16"),
+    (96, 160, (70, 40), "bf16"),
+    (352, 96, (150,), "bf16"),
+    (96, 1184, (130, 0, 300), "bf16"),
+    (64, 32, tuple(33 + i % 5 for i in range(70)), "bf16"),
+    (2880, 352, (128, 0, 257), "bf16"),
     (96, 64, (0, 9, 40), "f32"),
     (512, 256, (1, 64, 0), "f32"),
 ]
