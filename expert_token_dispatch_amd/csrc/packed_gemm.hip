@@ -183,10 +183,10 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
   load_s(0, sc);
   issue(0);
   issue(1);
-  // full: all four row blocks, without a branch among the products, whose operands for the
-  // next chunk are then read and decoded between them
-  const auto run = [&](auto full_t) {
-    constexpr bool full = decltype(full_t)::value;
+  // by the tile's row blocks, so that no branch stands among the products: the operands for
+  // the next chunk are read and decoded between them
+  const auto run = [&](auto blocks_t) {
+    constexpr int MB = decltype(blocks_t)::value;
     for (int s = 0; s < steps; ++s) {
       // the step's loads have landed: at most the next step's six are left (and any scales,
       // which only makes the wait longer)
@@ -206,49 +206,34 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
       const auto frag_a = [&](int i, int c) {
         return *reinterpret_cast<const bf16x8_t*>(st + (i * 32 + fr) * 128 + (((4 * half + c) ^ sw) * 16));
       };
-      if constexpr (full) {
-        bf16x8_t fa[2][4], fb[2][2];
+      bf16x8_t fa[2][MB], fb[2][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) fa[0][i] = frag_a(i, 0);
+      for (int i = 0; i < MB; ++i) fa[0][i] = frag_a(i, 0);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) fb[0][j] = decode_frag(w[j][0], f[j]);
+      for (int j = 0; j < 2; ++j) fb[0][j] = decode_frag(w[j][0], f[j]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c < 3) {
+      for (int c = 0; c < 4; ++c) {
+        if (c < 3) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) fa[(c + 1) & 1][i] = frag_a(i, c + 1);
+          for (int i = 0; i < MB; ++i) fa[(c + 1) & 1][i] = frag_a(i, c + 1);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) fb[(c + 1) & 1][j] = decode_frag(w[j][c + 1], f[j]);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[c & 1][j], fa[c & 1][i], acc[i][j], 0, 0, 0);
-          if (c < 3) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-              __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-              __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
-              __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            }
-          }
-          __builtin_amdgcn_sched_barrier(0);
+          for (int j = 0; j < 2; ++j) fb[(c + 1) & 1][j] = decode_frag(w[j][c + 1], f[j]);
         }
-      } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const bf16x8_t b0 = decode_frag(w[0][c], f[0]), b1 = decode_frag(w[1][c], f[1]);
+        for (int i = 0; i < MB; ++i)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (i < blocks) {
-              const bf16x8_t a = frag_a(i, c);
-              acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b0, a, acc[i][0], 0, 0, 0);
-              acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b1, a, acc[i][1], 0, 0, 0);
-            }
+          for (int j = 0; j < 2; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[c & 1][j], fa[c & 1][i], acc[i][j], 0, 0, 0);
+        if (c < 3) {
+#pragma unroll
+          for (int i = 0; i < MB; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 8 / MB, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
           }
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
       if (s & 1) {
         sc[0] = sn[0];
@@ -256,7 +241,12 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
       }
     }
   };
-  if (blocks == 4) run(std::true_type{}); else run(std::false_type{});
+  switch (blocks) {
+    case 1: run(std::integral_constant<int, 1>{}); break;
+    case 2: run(std::integral_constant<int, 2>{}); break;
+    case 3: run(std::integral_constant<int, 3>{}); break;
+    default: run(std::integral_constant<int, 4>{});
+  }
   MOE_VMCNT(0);  // the last (repeated) loads land before the LDS is used again
   MOE_LGKMCNT0();
   block_barrier();
