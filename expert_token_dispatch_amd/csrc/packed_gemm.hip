@@ -4,7 +4,8 @@
 // A block of four waves owns 128 token rows by 256 weight rows of one expert (gate/up: 128
 // gate rows and the same up rows), a wave all the token rows by 64 weight rows: 4 x 2 MFMA
 // 32x32 accumulators, 32-row blocks past the segment's end left out.  Two blocks share a
-// CU, so that one's epilogue runs beside the other's products.
+// CU, so that one's epilogue runs beside the other's products.  Where those tiles are too
+// few for the card, a tile has 128 weight rows, and three or four blocks share a CU.
 //
 // A step is 64 k.  Token rows (128 bytes a step) and codes (32 bytes a step) come by direct
 // global->LDS loads into three slots, two steps ahead.  A lane takes 16 bytes of codes, 32 k
@@ -28,16 +29,28 @@ namespace moe {
 namespace {
 namespace pk {
 
-constexpr int BM = 128, BNR = 256, BK = 64, kThreads = 256, kSlots = 3;
-constexpr int kStageA = BM * 128, kStageB = BNR * 32, kStage = kStageA + kStageB;  // 16 + 8 KB
+constexpr int BM = 128, BK = 64, kThreads = 256;
 constexpr int kGroup = 4;  // n-tiles per group of the tile order
 constexpr int kXcds = 8;
 
-template <int NMAT>
+// BNR: weight rows of a tile, 256 or 128
+template <int NMAT, int BNR>
 struct Shape {
-  static constexpr int kCols = BNR / NMAT;         // output columns
-  static constexpr int kRS = kCols * 2 + 16;       // a row of the output tile in LDS
+  static constexpr int NJ = BNR / 128;               // 32-row weight blocks of a wave
+  static constexpr int kSlots = BNR == 256 ? 3 : 2;
+  static constexpr int kLdB = BNR / 128;             // 1 KB loads of codes per wave and step
+  static constexpr int kLoads = 4 + kLdB;
+  static constexpr int kStageA = BM * 128, kStage = kStageA + BNR * 32;
+  static constexpr int kCols = BNR / NMAT;           // output columns
+  static constexpr int kRS = kCols * 2 + 16;         // a row of the output tile in LDS
   static constexpr int kLds = kSlots * kStage > BM * kRS ? kSlots * kStage : BM * kRS;
+  // gate/up: stage rows 0 .. kCols - 1 are gate rows, the others up rows.  Row l of a wave's
+  // block j; with one block a wave holds 16 gate rows and the up rows beside them.
+  __device__ static int stage_row(int wave, int j, int l) {
+    if (NMAT == 1) return wave * 32 * NJ + j * 32 + l;
+    if (NJ == 2) return j * kCols + wave * 32 + l;
+    return (l >> 4) * kCols + wave * 16 + (l & 15);
+  }
 };
 
 // Tile t of the local experts' tiles, numbered over (expert, group of n-tiles, m-tile, n-tile
@@ -87,12 +100,13 @@ __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offsets, i
   return r;
 }
 
-template <int NMAT>
+template <int NMAT, int BNR>
 __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t* __restrict__ offsets,
                                      const uint8_t* __restrict__ q0, const uint8_t* __restrict__ s0,
                                      const uint8_t* __restrict__ q1, const uint8_t* __restrict__ s1,
                                      bf16_t* __restrict__ C, int L, int N, int K, char* lds) {
-  using S = Shape<NMAT>;
+  using S = Shape<NMAT, BNR>;
+  constexpr int NJ = S::NJ, kSlots = S::kSlots, kStage = S::kStage, kStageA = S::kStageA;
   const int NT = (N + S::kCols - 1) / S::kCols;
   const int total = __builtin_amdgcn_readfirstlane(total_tiles(offsets, L, NT));
   const int per = (total + kXcds - 1) / kXcds;
@@ -106,8 +120,8 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
   const int half = lane >> 5, fr = lane & 31;
 
   // ---- loads.  Token rows: this wave's 32 (four loads of eight rows); past the segment
-  // they repeat its last row.  Codes: its 64 stage rows (two loads of 32); gate/up: waves 0
-  // and 1 gate rows, 2 and 3 up rows.  Rows past N repeat row N - 1.  Neither reaches an
+  // they repeat its last row.  Codes: its quarter of the stage rows, 32 a load; gate/up:
+  // waves 0 and 1 gate rows, 2 and 3 up rows.  Rows past N repeat row N - 1.  Neither reaches an
   // output that is stored.
   const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<bf16_t*>(A + size_t(row0) * K), 0, uint32_t(rows) * uint32_t(K) * 2u, kRsrcFlags);
@@ -115,16 +129,16 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
   const bool second = NMAT == 2 && wave >= 2;
   const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>((second ? q1 : q0) + eq), 0,
                                                                       uint32_t(N) * uint32_t(K / 2), kRsrcFlags);
-  uint32_t va[4], vb[2];
+  uint32_t va[4], vb[S::kLdB];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int r = wave * 32 + 8 * j + (lane >> 3);
     va[j] = uint32_t(min(r, rows - 1)) * uint32_t(K) * 2u + uint32_t(((lane & 7) ^ ((r >> 1) & 7)) * 16);
   }
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int r = wave * 64 + 32 * j + (lane >> 1);  // stage row
-    const int row = min(n0 + (NMAT == 2 ? r % 128 : r), N - 1);
+  for (int j = 0; j < S::kLdB; ++j) {
+    const int r = wave * (BNR / 4) + 32 * j + (lane >> 1);  // stage row
+    const int row = min(n0 + r % S::kCols, N - 1);
     vb[j] = uint32_t(row) * uint32_t(K / 2) + uint32_t(((lane & 1) ^ ((r >> 3) & 1)) * 16);
   }
   const int steps = (K + BK - 1) / BK;
@@ -141,25 +155,25 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(slot + (4 * wave + j) * 1024), 16, vo, uint32_t(st) * 128u, 0, 0);
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(slot + kStageA + (2 * wave + j) * 1024), 16, vb[j],
+    for (int j = 0; j < S::kLdB; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(slot + kStageA + (S::kLdB * wave + j) * 1024), 16, vb[j],
                                                uint32_t(st) * 32u, 0, 0);
   };
 
   // ---- this lane's weight rows: stage row of block j, and its scales.  Four bytes are two
   // steps; where a row's bytes are no whole words the loads are unaligned, and at its end short.
-  const uint8_t* sp[2];
-  int br[2];
+  const uint8_t* sp[NJ];
+  int br[NJ];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    br[j] = NMAT == 2 ? j * 128 + wave * 32 + fr : wave * 64 + j * 32 + fr;
-    const int row = min(n0 + (NMAT == 2 ? wave * 32 + fr : br[j]), N - 1);
-    sp[j] = (NMAT == 2 && j == 1 ? s1 : s0) + es + size_t(row) * (K / 32);
+  for (int j = 0; j < NJ; ++j) {
+    br[j] = S::stage_row(wave, j, fr);
+    const int row = min(n0 + br[j] % S::kCols, N - 1);
+    sp[j] = (NMAT == 2 && br[j] >= S::kCols ? s1 : s0) + es + size_t(row) * (K / 32);
   }
   const int groups = K / 32;
-  auto load_s = [&](int s, uint32_t (&v)[2]) {  // the scales of steps s and s + 1, s even
+  auto load_s = [&](int s, uint32_t (&v)[NJ]) {  // the scales of steps s and s + 1, s even
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < NJ; ++j) {
       v[j] = 0;
       if (2 * s + 4 <= groups) {
         __builtin_memcpy(&v[j], sp[j] + 2 * s, 4);
@@ -170,74 +184,74 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
     }
   };
 
-  f32x16_t acc[4][2];
+  f32x16_t acc[4][NJ];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   const int sw = (fr >> 1) & 7;
   const int blocks = (rows + 31) / 32;
-  uint32_t sc[2], sn[2];
+  uint32_t sc[NJ], sn[NJ];
   load_s(0, sc);
-  issue(0);
-  issue(1);
+#pragma unroll
+  for (int s = 0; s < kSlots - 1; ++s) issue(s);
   // by the tile's row blocks, so that no branch stands among the products: the operands for
   // the next chunk are read and decoded between them
   const auto run = [&](auto blocks_t) {
     constexpr int MB = decltype(blocks_t)::value;
     for (int s = 0; s < steps; ++s) {
-      // the step's loads have landed: at most the next step's six are left (and any scales,
-      // which only makes the wait longer)
-      MOE_VMCNT(6);
+      // the step's loads have landed: at most the later steps' are left (and any scales, which
+      // only makes the wait longer)
+      MOE_VMCNT(S::kLoads * (kSlots - 2));
       MOE_LGKMCNT0();
       block_barrier();
-      issue(s + 2);
+      issue(s + kSlots - 1);
       if ((s & 1) == 0) load_s(s + 2 < steps ? s + 2 : 0, sn);
       const char* st = lds + (s % kSlots) * kStage;
-      u32x4_t w[2];
-      float f[2];
+      u32x4_t w[NJ];
+      float f[NJ];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < NJ; ++j) {
         w[j] = *reinterpret_cast<const u32x4_t*>(st + kStageA + br[j] * 32 + ((half ^ ((br[j] >> 3) & 1)) * 16));
         f[j] = __uint_as_float(((sc[j] >> (16 * (s & 1) + 8 * half)) & 0xFFu) << 23);
       }
       const auto frag_a = [&](int i, int c) {
         return *reinterpret_cast<const bf16x8_t*>(st + (i * 32 + fr) * 128 + (((4 * half + c) ^ sw) * 16));
       };
-      bf16x8_t fa[2][MB], fb[2][2];
+      bf16x8_t fa[2][MB], fb[2][NJ];
 #pragma unroll
       for (int i = 0; i < MB; ++i) fa[0][i] = frag_a(i, 0);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) fb[0][j] = decode_frag(w[j][0], f[j]);
+      for (int j = 0; j < NJ; ++j) fb[0][j] = decode_frag(w[j][0], f[j]);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         if (c < 3) {
 #pragma unroll
           for (int i = 0; i < MB; ++i) fa[(c + 1) & 1][i] = frag_a(i, c + 1);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) fb[(c + 1) & 1][j] = decode_frag(w[j][c + 1], f[j]);
+          for (int j = 0; j < NJ; ++j) fb[(c + 1) & 1][j] = decode_frag(w[j][c + 1], f[j]);
         }
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < NJ; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[c & 1][j], fa[c & 1][i], acc[i][j], 0, 0, 0);
         if (c < 3) {
 #pragma unroll
           for (int i = 0; i < MB; ++i) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, 8 / MB, 0);
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 4 * NJ / MB, 0);
+            if constexpr (NJ == 2) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
           }
         }
         __builtin_amdgcn_sched_barrier(0);
       }
       if (s & 1) {
-        sc[0] = sn[0];
-        sc[1] = sn[1];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) sc[j] = sn[j];
       }
     }
   };
@@ -258,14 +272,20 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
   for (int i = 0; i < 4; ++i) {
     if (i < blocks) {
 #pragma unroll
-      for (int j = 0; j < 2 / NMAT; ++j) {
+      for (int j = 0; j < (NMAT == 2 ? 1 : NJ); ++j) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < (NMAT == 2 && NJ == 1 ? 2 : 4); ++q) {
           float v[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            v[u] = NMAT == 2 ? silu(acc[i][0][4 * q + u]) * acc[i][1][4 * q + u] : acc[i][j][4 * q + u];
-          const int cl = (NMAT == 2 ? wave * 32 : wave * 64 + j * 32) + 8 * q + 4 * half;
+          for (int u = 0; u < 4; ++u) {
+            if constexpr (NMAT == 1)
+              v[u] = acc[i][j][4 * q + u];
+            else if constexpr (NJ == 2)
+              v[u] = silu(acc[i][0][4 * q + u]) * acc[i][1][4 * q + u];
+            else  // gate rows are the block's first 16, two q
+              v[u] = silu(acc[i][0][4 * q + u]) * acc[i][0][4 * (q + 2) + u];
+          }
+          const int cl = wave * (S::kCols / 4) + j * 32 + 8 * q + 4 * half;
           *reinterpret_cast<uint2*>(lds + (i * 32 + fr) * S::kRS + cl * 2) =
               make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
         }
@@ -285,20 +305,20 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
   }
 }
 
-template <int NMAT>
+template <int NMAT, int BNR>
 __global__ __launch_bounds__(kThreads, 2) void kernel(const bf16_t* __restrict__ A, const int32_t* __restrict__ offsets,
                                                       const uint8_t* __restrict__ q0, const uint8_t* __restrict__ s0,
                                                       const uint8_t* __restrict__ q1, const uint8_t* __restrict__ s1,
                                                       bf16_t* __restrict__ C, int L, int N, int K) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  body<NMAT>(A, offsets, q0, s0, q1, s1, C, L, N, K, lds);
+  body<NMAT, BNR>(A, offsets, q0, s0, q1, s1, C, L, N, K, lds);
 }
 
-template <int NMAT>
-moe_status launch(const char* name, const bf16_t* A, const int32_t* offsets, const void* q0, const void* s0,
-                  const void* q1, const void* s1, bf16_t* C, int L, int N, int K, int64_t max_pairs, hipStream_t s) {
-  using S = Shape<NMAT>;
-  auto kern = kernel<NMAT>;
+template <int NMAT, int BNR>
+moe_status launch_bnr(const char* name, const bf16_t* A, const int32_t* offsets, const void* q0, const void* s0,
+                      const void* q1, const void* s1, bf16_t* C, int L, int N, int K, int64_t max_pairs, hipStream_t s) {
+  using S = Shape<NMAT, BNR>;
+  auto kern = kernel<NMAT, BNR>;
   const hipError_t e =
       hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
   if (e != hipSuccess) return set_error(MOE_ERR_HIP, "%s: LDS attribute: %s", name, hipGetErrorString(e));
@@ -312,6 +332,16 @@ moe_status launch(const char* name, const bf16_t* A, const int32_t* offsets, con
   return MOE_OK;
 }
 
+// 256 weight rows a tile where that gives every CU four tiles, else 128
+template <int NMAT>
+moe_status launch(const char* name, const bf16_t* A, const int32_t* offsets, const void* q0, const void* s0,
+                  const void* q1, const void* s1, bf16_t* C, int L, int N, int K, int64_t max_pairs, hipStream_t s) {
+  const int64_t m = max_pairs / BM + std::min<int64_t>(L, max_pairs) / 2;
+  if (m * ((N + 256 / NMAT - 1) / (256 / NMAT)) >= 1024)
+    return launch_bnr<NMAT, 256>(name, A, offsets, q0, s0, q1, s1, C, L, N, K, max_pairs, s);
+  return launch_bnr<NMAT, 128>(name, A, offsets, q0, s0, q1, s1, C, L, N, K, max_pairs, s);
+}
+
 }  // namespace pk
 }  // namespace
 
@@ -319,7 +349,7 @@ bool packed_gemm_fits(const moe_layer_desc* d, int64_t max_pairs) {
   // an expert's codes and 128 token rows are addressed with 32-bit byte offsets, tiles counted in an int
   const int64_t H = d->hidden, I = d->intermediate;
   return d->dtype == MOE_BF16 && H * I / 2 < (int64_t(1) << 32) - 16 && std::max(H, I) * 256 < (int64_t(1) << 32) - 16 &&
-         (max_pairs / pk::BM + d->local_count) * ((std::max(H, I) + 127) / 128) < (int64_t(1) << 30);
+         (max_pairs / pk::BM + d->local_count) * ((std::max(H, I) + 63) / 64) < (int64_t(1) << 30);
 }
 
 moe_status launch_packed_gemm(const PackedFfnArgs& a) {
