@@ -53,49 +53,67 @@ struct Shape {
   }
 };
 
-// Tile t of the local experts' tiles, numbered over (expert, group of n-tiles, m-tile, n-tile
-// in group); every wave finds it for itself, 64 experts at a time.  Returns the total.
+// Tiles of the local experts are numbered one of two ways; every wave finds its own, 64
+// experts at a time.
+//   In order (many tiles): over (expert, group of n-tiles, m-tile, n-tile in group), each XCD
+//   a range, so that the blocks which run at once on an XCD share weight and token rows in L2.
+//   By size (a few tiles a CU): full m-tiles of all experts, then the segments' tails of more
+//   than half a tile, then the others, over (expert, m-tile, n-tile), dealt out singly: the
+//   short ones fill the gaps at the end.
 struct Tile {
   int expert, row0, rows, n;
 };
-__device__ __forceinline__ int tiles_of(const int32_t* __restrict__ offsets, int L, int NT, int e, int& first) {
+
+// m-tiles of expert e in size class c (-1: all), and its first row of that class
+__device__ __forceinline__ int m_tiles(const int32_t* __restrict__ offsets, int L, int e, int c, int& first) {
   first = offsets[min(e, L)];
-  const int n = e < L ? offsets[e + 1] - first : 0;
-  return (n + BM - 1) / BM * NT;
+  const int n = e < L ? offsets[e + 1] - first : 0, full = n / BM, tail = n % BM;
+  if (c < 0) return full + (tail > 0);
+  if (c == 0) return full;
+  first += full * BM;
+  return c == 1 ? tail > BM / 2 : tail > 0 && tail <= BM / 2;
 }
+
 __device__ __forceinline__ int total_tiles(const int32_t* __restrict__ offsets, int L, int NT) {
   int sum = 0, first;
-  for (int e = threadIdx.x & 63; e < L; e += 64) sum += tiles_of(offsets, L, NT, e, first);
+  for (int e = threadIdx.x & 63; e < L; e += 64) sum += m_tiles(offsets, L, e, -1, first) * NT;
   for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
   return sum;
 }
-__device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offsets, int L, int NT, int t) {
+
+__device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offsets, int L, int NT, int t, bool by_size) {
   const int lane = threadIdx.x & 63;
   Tile r{-1, 0, 0, 0};
-  for (int base = 0; base < L; base += 64) {
-    int first;
-    const int mine = tiles_of(offsets, L, NT, base + lane, first);
-    int incl = mine;
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(incl, d, 64);
-      if (lane >= d) incl += o;
+  for (int c = by_size ? 0 : -1; c < 3; ++c) {
+    for (int base = 0; base < L; base += 64) {
+      int first;
+      const int mt = m_tiles(offsets, L, base + lane, c, first), mine = mt * NT;
+      int incl = mine;
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(incl, d, 64);
+        if (lane >= d) incl += o;
+      }
+      const uint64_t past = __ballot(incl > t);
+      if (past) {
+        const int l = __ffsll((unsigned long long)past) - 1;
+        r.expert = base + l;
+        t -= __shfl(incl - mine, l, 64);
+        const int row = __shfl(first, l, 64), m = __shfl(mt, l, 64), end = offsets[r.expert + 1];
+        if (by_size) {
+          r.row0 = row + t / NT * BM;
+          r.n = t % NT;
+        } else {
+          const int g = min(t / (m * kGroup), (NT - 1) / kGroup);
+          t -= g * m * kGroup;
+          const int w = min(kGroup, NT - g * kGroup);
+          r.row0 = row + t / w * BM;
+          r.n = g * kGroup + t % w;
+        }
+        r.rows = min(BM, end - r.row0);
+        return r;
+      }
+      t -= __shfl(incl, 63, 64);
     }
-    const uint64_t past = __ballot(incl > t);
-    if (past) {
-      const int l = __ffsll((unsigned long long)past) - 1;
-      r.expert = base + l;
-      t -= __shfl(incl - mine, l, 64);
-      const int seg0 = __shfl(first, l, 64), mt = __shfl(mine, l, 64) / NT;
-      const int seg1 = offsets[r.expert + 1];
-      const int g = min(t / (mt * kGroup), (NT - 1) / kGroup);
-      t -= g * mt * kGroup;
-      const int w = min(kGroup, NT - g * kGroup);
-      r.row0 = seg0 + t / w * BM;
-      r.rows = min(BM, seg1 - r.row0);
-      r.n = g * kGroup + t % w;
-      return r;
-    }
-    t -= __shfl(incl, 63, 64);
   }
   return r;
 }
@@ -109,18 +127,20 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
   constexpr int NJ = S::NJ, kSlots = S::kSlots, kStage = S::kStage, kStageA = S::kStageA;
   const int NT = (N + S::kCols - 1) / S::kCols;
   const int total = __builtin_amdgcn_readfirstlane(total_tiles(offsets, L, NT));
+  constexpr bool by_size = BNR == 128;  // the tiles that are taken where there are few
   const int per = (total + kXcds - 1) / kXcds;
-  const int xcd = blockIdx.x % kXcds, loc = blockIdx.x / kXcds, t = xcd * per + loc;
-  if (loc >= per || t >= total) return;
-  const Tile tile = find_tile(offsets, L, NT, t);
+  const int xcd = blockIdx.x % kXcds, loc = blockIdx.x / kXcds, t = by_size ? int(blockIdx.x) : xcd * per + loc;
+  if ((!by_size && loc >= per) || t >= total) return;
+  const Tile tile = find_tile(offsets, L, NT, t, by_size);
   const int expert = __builtin_amdgcn_readfirstlane(tile.expert);
   const int row0 = __builtin_amdgcn_readfirstlane(tile.row0), rows = __builtin_amdgcn_readfirstlane(tile.rows);
   const int n0 = __builtin_amdgcn_readfirstlane(tile.n) * S::kCols;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int half = lane >> 5, fr = lane & 31;
+  const int blocks = (rows + 31) / 32;  // 32-row blocks that have rows
 
-  // ---- loads.  Token rows: this wave's 32 (four loads of eight rows); past the segment
-  // they repeat its last row.  Codes: its quarter of the stage rows, 32 a load; gate/up:
+  // ---- loads.  Token rows: this wave's 32 (four loads of eight rows), if the segment has
+  // any of them; past its end they repeat its last row.  Codes: its quarter of the stage rows, 32 a load; gate/up:
   // waves 0 and 1 gate rows, 2 and 3 up rows.  Rows past N repeat row N - 1.  Neither reaches an
   // output that is stored.
   const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
@@ -148,11 +168,14 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
   auto issue = [&](int s) {  // step min(s, steps - 1) into slot s
     const int st = min(s, steps - 1);
     char* slot = lds + (s % kSlots) * kStage;
+    if (wave < blocks) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = (lane & 7) ^ (((wave * 32 + 8 * j + (lane >> 3)) >> 1) & 7);
-      const uint32_t vo = cut && st == steps - 1 && c >= 4 ? 0xFFFFFFF0u : va[j];
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(slot + (4 * wave + j) * 1024), 16, vo, uint32_t(st) * 128u, 0, 0);
+      for (int j = 0; j < 4; ++j) {
+        const int c = (lane & 7) ^ (((wave * 32 + 8 * j + (lane >> 3)) >> 1) & 7);
+        const uint32_t vo = cut && st == steps - 1 && c >= 4 ? 0xFFFFFFF0u : va[j];
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(slot + (4 * wave + j) * 1024), 16, vo,
+                                                 uint32_t(st) * 128u, 0, 0);
+      }
     }
 #pragma unroll
     for (int j = 0; j < S::kLdB; ++j)
@@ -192,7 +215,6 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   const int sw = (fr >> 1) & 7;
-  const int blocks = (rows + 31) / 32;
   uint32_t sc[NJ], sn[NJ];
   load_s(0, sc);
 #pragma unroll
@@ -204,11 +226,15 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
     for (int s = 0; s < steps; ++s) {
       // the step's loads have landed: at most the later steps' are left (and any scales, which
       // only makes the wait longer)
-      MOE_VMCNT(S::kLoads * (kSlots - 2));
+      if (wave < blocks) MOE_VMCNT(S::kLoads * (kSlots - 2));
+      else MOE_VMCNT(S::kLdB * (kSlots - 2));
       MOE_LGKMCNT0();
       block_barrier();
-      issue(s + kSlots - 1);
+      // the scales first: loads return in order, and behind the refill they would make the
+      // wave wait for it
       if ((s & 1) == 0) load_s(s + 2 < steps ? s + 2 : 0, sn);
+      asm volatile("" ::: "memory");
+      issue(s + kSlots - 1);
       const char* st = lds + (s % kSlots) * kStage;
       u32x4_t w[NJ];
       float f[NJ];

@@ -128,6 +128,8 @@ FFN = [
     (96, 1184, (130, 0, 300), "bf16"),
     (64, 32, tuple(33 + i % 5 for i in range(70)), "bf16"),
     (2880, 352, (128, 0, 257), "bf16"),
+    (64, 2080, (8000, 0, 101), "bf16"),
+    (4096, 64, (127, 8000), "bf16"),
     (96, 64, (0, 9, 40), "f32"),
     (512, 256, (1, 64, 0), "f32"),
 ]
