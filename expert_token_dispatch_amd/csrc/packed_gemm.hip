@@ -5,7 +5,7 @@
 // gate rows and the same up rows), a wave all the token rows by 64 weight rows: 4 x 2 MFMA
 // 32x32 accumulators, 32-row blocks past the segment's end left out.  Two blocks share a
 // CU, so that one's epilogue runs beside the other's products.  Where those tiles are too
-// few for the card, a tile has 128 weight rows, and three or four blocks share a CU.
+// few for the card, a tile has 128 weight rows.
 //
 // A step is 64 k.  Token rows (128 bytes a step) and codes (32 bytes a step) come by direct
 // global->LDS loads into three slots, two steps ahead.  A lane takes 16 bytes of codes, 32 k
@@ -37,7 +37,7 @@ constexpr int kXcds = 8;
 template <int NMAT, int BNR>
 struct Shape {
   static constexpr int NJ = BNR / 128;               // 32-row weight blocks of a wave
-  static constexpr int kSlots = BNR == 256 ? 3 : 2;
+  static constexpr int kSlots = 3;
   static constexpr int kLdB = BNR / 128;             // 1 KB loads of codes per wave and step
   static constexpr int kLoads = 4 + kLdB;
   static constexpr int kStageA = BM * 128, kStage = kStageA + BNR * 32;
@@ -55,9 +55,9 @@ struct Shape {
 
 // Tiles of the local experts are numbered one of two ways; every wave finds its own, 64
 // experts at a time.
-//   In order (many tiles): over (expert, group of n-tiles, m-tile, n-tile in group), each XCD
+//   In order (many): over (expert, group of n-tiles, m-tile, n-tile in group), each XCD
 //   a range, so that the blocks which run at once on an XCD share weight and token rows in L2.
-//   By size (a few tiles a CU): full m-tiles of all experts, then the segments' tails of more
+//   By size (few tiles): full m-tiles of all experts, then the segments' tails of more
 //   than half a tile, then the others, over (expert, m-tile, n-tile), dealt out singly: the
 //   short ones fill the gaps at the end.
 struct Tile {
@@ -122,12 +122,11 @@ template <int NMAT, int BNR>
 __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t* __restrict__ offsets,
                                      const uint8_t* __restrict__ q0, const uint8_t* __restrict__ s0,
                                      const uint8_t* __restrict__ q1, const uint8_t* __restrict__ s1,
-                                     bf16_t* __restrict__ C, int L, int N, int K, char* lds) {
+                                     bf16_t* __restrict__ C, int L, int N, int K, bool by_size, char* lds) {
   using S = Shape<NMAT, BNR>;
   constexpr int NJ = S::NJ, kSlots = S::kSlots, kStage = S::kStage, kStageA = S::kStageA;
   const int NT = (N + S::kCols - 1) / S::kCols;
   const int total = __builtin_amdgcn_readfirstlane(total_tiles(offsets, L, NT));
-  constexpr bool by_size = BNR == 128;  // the tiles that are taken where there are few
   const int per = (total + kXcds - 1) / kXcds;
   const int xcd = blockIdx.x % kXcds, loc = blockIdx.x / kXcds, t = by_size ? int(blockIdx.x) : xcd * per + loc;
   if ((!by_size && loc >= per) || t >= total) return;
@@ -139,8 +138,8 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
   const int half = lane >> 5, fr = lane & 31;
   const int blocks = (rows + 31) / 32;  // 32-row blocks that have rows
 
-  // ---- loads.  Token rows: this wave's 32 (four loads of eight rows), if the segment has
-  // any of them; past its end they repeat its last row.  Codes: its quarter of the stage rows, 32 a load; gate/up:
+  // ---- loads.  Token rows: this wave's 32 (four loads of eight rows); past the segment
+  // they repeat its last row.  Codes: its quarter of the stage rows, 32 a load; gate/up:
   // waves 0 and 1 gate rows, 2 and 3 up rows.  Rows past N repeat row N - 1.  Neither reaches an
   // output that is stored.
   const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
@@ -168,14 +167,12 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
   auto issue = [&](int s) {  // step min(s, steps - 1) into slot s
     const int st = min(s, steps - 1);
     char* slot = lds + (s % kSlots) * kStage;
-    if (wave < blocks) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = (lane & 7) ^ (((wave * 32 + 8 * j + (lane >> 3)) >> 1) & 7);
-        const uint32_t vo = cut && st == steps - 1 && c >= 4 ? 0xFFFFFFF0u : va[j];
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(slot + (4 * wave + j) * 1024), 16, vo,
-                                                 uint32_t(st) * 128u, 0, 0);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const int c = (lane & 7) ^ (((wave * 32 + 8 * j + (lane >> 3)) >> 1) & 7);
+      const uint32_t vo = cut && st == steps - 1 && c >= 4 ? 0xFFFFFFF0u : va[j];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(slot + (4 * wave + j) * 1024), 16, vo,
+                                               uint32_t(st) * 128u, 0, 0);
     }
 #pragma unroll
     for (int j = 0; j < S::kLdB; ++j)
@@ -226,8 +223,7 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
     for (int s = 0; s < steps; ++s) {
       // the step's loads have landed: at most the later steps' are left (and any scales, which
       // only makes the wait longer)
-      if (wave < blocks) MOE_VMCNT(S::kLoads * (kSlots - 2));
-      else MOE_VMCNT(S::kLdB * (kSlots - 2));
+      MOE_VMCNT(S::kLoads * (kSlots - 2));
       MOE_LGKMCNT0();
       block_barrier();
       // the scales first: loads return in order, and behind the refill they would make the
@@ -335,14 +331,15 @@ template <int NMAT, int BNR>
 __global__ __launch_bounds__(kThreads, 2) void kernel(const bf16_t* __restrict__ A, const int32_t* __restrict__ offsets,
                                                       const uint8_t* __restrict__ q0, const uint8_t* __restrict__ s0,
                                                       const uint8_t* __restrict__ q1, const uint8_t* __restrict__ s1,
-                                                      bf16_t* __restrict__ C, int L, int N, int K) {
+                                                      bf16_t* __restrict__ C, int L, int N, int K, int by_size) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  body<NMAT, BNR>(A, offsets, q0, s0, q1, s1, C, L, N, K, lds);
+  body<NMAT, BNR>(A, offsets, q0, s0, q1, s1, C, L, N, K, by_size != 0, lds);
 }
 
 template <int NMAT, int BNR>
 moe_status launch_bnr(const char* name, const bf16_t* A, const int32_t* offsets, const void* q0, const void* s0,
-                      const void* q1, const void* s1, bf16_t* C, int L, int N, int K, int64_t max_pairs, hipStream_t s) {
+                      const void* q1, const void* s1, bf16_t* C, int L, int N, int K, int64_t max_pairs, bool by_size,
+                      hipStream_t s) {
   using S = Shape<NMAT, BNR>;
   auto kern = kernel<NMAT, BNR>;
   const hipError_t e =
@@ -354,18 +351,21 @@ moe_status launch_bnr(const char* name, const bf16_t* A, const int32_t* offsets,
   const int64_t per = (tiles + kXcds - 1) / kXcds;
   MOE_LAUNCH(name, kern, dim3(unsigned(per * kXcds)), dim3(kThreads), S::kLds, s, A, offsets,
              static_cast<const uint8_t*>(q0), static_cast<const uint8_t*>(s0), static_cast<const uint8_t*>(q1),
-             static_cast<const uint8_t*>(s1), C, L, N, K);
+             static_cast<const uint8_t*>(s1), C, L, N, K, by_size ? 1 : 0);
   return MOE_OK;
 }
 
-// 256 weight rows a tile where that gives every CU four tiles, else 128
+// Tiles of 256 weight rows, 128 where those would not give every CU one; by size while a CU
+// gets fewer than four, in order from there (a prefill of 16384 pairs on 8 experts: in order
+// -2%; 2047 pairs on 16 experts of very different load: by size -6%).
 template <int NMAT>
 moe_status launch(const char* name, const bf16_t* A, const int32_t* offsets, const void* q0, const void* s0,
                   const void* q1, const void* s1, bf16_t* C, int L, int N, int K, int64_t max_pairs, hipStream_t s) {
   const int64_t m = max_pairs / BM + std::min<int64_t>(L, max_pairs) / 2;
-  if (m * ((N + 256 / NMAT - 1) / (256 / NMAT)) >= 1024)
-    return launch_bnr<NMAT, 256>(name, A, offsets, q0, s0, q1, s1, C, L, N, K, max_pairs, s);
-  return launch_bnr<NMAT, 128>(name, A, offsets, q0, s0, q1, s1, C, L, N, K, max_pairs, s);
+  const int64_t tiles = m * ((N + 256 / NMAT - 1) / (256 / NMAT));
+  if (tiles >= 256)
+    return launch_bnr<NMAT, 256>(name, A, offsets, q0, s0, q1, s1, C, L, N, K, max_pairs, tiles < 1024, s);
+  return launch_bnr<NMAT, 128>(name, A, offsets, q0, s0, q1, s1, C, L, N, K, max_pairs, true, s);
 }
 
 }  // namespace pk

@@ -34,17 +34,21 @@ constexpr int kThreads = 256;
 constexpr int kStep = 128;   // k of a step
 
 // The `slot`-th expert that has rows (slots are at most the rows, experts may be many and
-// mostly empty), or -1.  Every wave finds it for itself.
-__device__ __forceinline__ int expert_of_slot(const int32_t* __restrict__ offsets, int L, int slot) {
+// mostly empty) and its segment, or -1.  Every wave finds it for itself.
+__device__ __forceinline__ int expert_of_slot(const int32_t* __restrict__ offsets, int L, int slot, int& seg0,
+                                              int& seg_n) {
   const int lane = threadIdx.x & 63;
   for (int base = 0; base < L; base += 64) {
     const int e = base + lane;
-    const bool has = e < L && offsets[e + 1] > offsets[e];
-    const uint64_t m = __ballot(has);
+    const int o0 = offsets[min(e, L)], o1 = offsets[min(e + 1, L)];
+    const uint64_t m = __ballot(o1 > o0);
     const int n = __popcll(m);
     if (slot < n) {
-      const uint64_t hit = __ballot(has && __popcll(m & lanemask_lt()) == slot);
-      return base + __ffsll((unsigned long long)hit) - 1;
+      const uint64_t hit = __ballot(o1 > o0 && __popcll(m & lanemask_lt()) == slot);
+      const int l = __ffsll((unsigned long long)hit) - 1;
+      seg0 = __builtin_amdgcn_readlane(o0, l);
+      seg_n = __builtin_amdgcn_readlane(o1, l) - seg0;
+      return base + l;
     }
     slot -= n;
   }
@@ -73,9 +77,9 @@ __global__ __launch_bounds__(kThreads) void packed_gemm_kernel(const bf16_t* __r
   constexpr int kWaveCols = NMAT == 2 ? 16 : 32;
   constexpr int kStage = kRows * Ch::kPieces / kThreads;  // 16-byte pieces of a chunk per thread
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  const int expert = __builtin_amdgcn_readfirstlane(expert_of_slot(offsets, L, blockIdx.y));
+  int seg0 = 0, seg_n = 0;
+  const int expert = __builtin_amdgcn_readfirstlane(expert_of_slot(offsets, L, blockIdx.y, seg0, seg_n));
   if (expert < 0) return;
-  const int seg0 = offsets[expert], seg_n = offsets[expert + 1] - seg0;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wk = wave % WK, wn = wave / WK;
   const int col0 = (blockIdx.x * WN + wn) * kWaveCols;  // first output column of this wave

@@ -100,9 +100,8 @@ __global__ __launch_bounds__(kThreads) void pack_rows_kernel(const T* __restrict
 }
 
 template <typename T>
-__global__ __launch_bounds__(kThreads) void unpack_rows_kernel(const uint32_t* __restrict__ codes,
-                                                               const uint8_t* __restrict__ scales, T* __restrict__ w,
-                                                               int64_t units) {
+__device__ __forceinline__ void unpack_rows(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                                            T* __restrict__ w, int64_t units) {
   const int64_t step = int64_t(gridDim.x) * kThreads;
   for (int64_t u = int64_t(blockIdx.x) * kThreads + threadIdx.x; u < units; u += step) {
     __attribute__((aligned(16))) T o[8];
@@ -111,6 +110,13 @@ __global__ __launch_bounds__(kThreads) void unpack_rows_kernel(const uint32_t* _
     for (int i = 0; i < int(sizeof(o) / 16); ++i)
       reinterpret_cast<uint4*>(w + u * 8)[i] = reinterpret_cast<const uint4*>(o)[i];
   }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void unpack_rows_kernel(const uint32_t* __restrict__ codes,
+                                                               const uint8_t* __restrict__ scales, T* __restrict__ w,
+                                                               int64_t units) {
+  unpack_rows(codes, scales, w, units);
 }
 
 // Weights stored [in, out]: a block turns a tile of kTI inputs x kTO outputs round in
@@ -192,6 +198,18 @@ __global__ __launch_bounds__(kThreads) void unpack_cols_kernel(const uint32_t* _
   }
 }
 
+// Three stacks stored [out, in] in one launch (y: which).
+struct Unpack3 {
+  const uint32_t* codes[3];
+  const uint8_t* scales[3];
+  void* w[3];
+};
+template <typename T>
+__global__ __launch_bounds__(kThreads) void unpack3_rows_kernel(Unpack3 a, int64_t units) {
+  const int i = blockIdx.y;
+  unpack_rows(a.codes[i], a.scales[i], static_cast<T*>(a.w[i]), units);
+}
+
 unsigned row_blocks(int64_t units) {
   const int64_t b = (units + kThreads - 1) / kThreads;
   return unsigned(b < 16384 ? b : 16384);
@@ -236,9 +254,10 @@ moe_status launch_unpack(const char* name, const PackArgs& a) {
 }
 
 // ---- the experts' feed-forward on packed weights -------------------------------------
-// Rows enough to be bound by the products: the three stacks are unpacked into the
-// workspace and the products run on them.  The unpacked stacks hold the same values
-// as the codes, so nothing is rounded on the way.
+// bf16 layers read the codes in the products (packed_skinny.hip, packed_gemm.hip).  For
+// float32 layers, and bf16 experts too large for those kernels' 32-bit offsets, the three
+// stacks are unpacked into the workspace and the products run on them: the unpacked
+// stacks hold the same values as the codes, so nothing is rounded on the way.
 namespace {
 size_t stack_bytes(const moe_layer_desc* d) {
   return align_up(size_t(d->local_count) * d->hidden * d->intermediate * dtype_bytes(d->dtype), 256);
@@ -255,18 +274,23 @@ moe_status launch_packed_ffn(const PackedFfnArgs& a) {
   if (packed_skinny_fits(a.d, a.max_pairs)) return launch_packed_skinny(a);
   if (packed_gemm_fits(a.d, a.max_pairs)) return launch_packed_gemm(a);
   const moe_layer_desc* d = a.d;
-  const int L = d->local_count, H = d->hidden, I = d->intermediate;
   char* base = static_cast<char*>(a.scratch);
   void* w[3];
   for (int i = 0; i < 3; ++i) w[i] = base + size_t(i) * stack_bytes(d);
   const moe_packed_experts& p = *a.p;
+  Unpack3 u{};
   const void* codes[3] = {p.gate_codes, p.up_codes, p.down_codes};
   const void* scales[3] = {p.gate_scales, p.up_scales, p.down_scales};
   for (int i = 0; i < 3; ++i) {
-    PackArgs u{L, i == 2 ? H : I, i == 2 ? I : H, d->dtype, MOE_WEIGHTS_OUT_IN, w[i], const_cast<void*>(codes[i]),
-               const_cast<void*>(scales[i]), a.s};
-    const moe_status st = launch_unpack("ffn_unpack", u);
-    if (st != MOE_OK) return st;
+    u.codes[i] = static_cast<const uint32_t*>(codes[i]);
+    u.scales[i] = static_cast<const uint8_t*>(scales[i]);
+    u.w[i] = w[i];
+  }
+  const int64_t units = int64_t(d->local_count) * d->hidden * d->intermediate / 8;
+  if (d->dtype == MOE_BF16) {
+    MOE_LAUNCH("ffn_unpack", unpack3_rows_kernel<bf16_t>, dim3(row_blocks(units), 3), dim3(kThreads), 0, a.s, u, units);
+  } else {
+    MOE_LAUNCH("ffn_unpack", unpack3_rows_kernel<float>, dim3(row_blocks(units), 3), dim3(kThreads), 0, a.s, u, units);
   }
   moe_layer_desc dl = *d;
   dl.weight_layout = MOE_WEIGHTS_OUT_IN;  // the unpacked stacks' layout, whatever the layer's own
