@@ -331,24 +331,28 @@ __device__ __forceinline__ void put_last(const Product& p, size_t z, int row, in
 // Tiles of BT x BT (64 or 128), four waves 2 x 2.  A stage is 128 bytes of k of the tile's A
 // and B rows, filled by direct global->LDS loads (1 KB: eight rows) kSlots - 1 stages ahead,
 // one barrier a stage.  16-byte piece c of row r sits at piece c ^ (r / 2 % 8), so the reads
-// of 16 rows at one piece cover all banks.
-template <int BT>
+// of 16 rows at one piece cover all banks.  KS > 1 (64 x 64 tiles, too few for the card): KS
+// groups of four waves take a range of K each, with a ring of its own; their sums are added
+// in the order of the ranges, a share of the registers by each group.
+template <int BT, int KS>
 struct Ring {
-  static constexpr int kStage = 2 * BT * 128, kSlots = BT == 64 ? 4 : 3;
-  static constexpr int kPerWave = kStage / 1024 / 4, kLds = kSlots * kStage;
+  static constexpr int kStage = 2 * BT * 128, kSlots = BT == 128 ? 3 : (KS == 4 ? 2 : (KS == 2 ? 3 : 4));
+  static constexpr int kPerWave = kStage / 1024 / 4, kLds = KS * kSlots * kStage;
 };
 
-template <typename W, typename T, int BT, int KIND>
-__device__ __forceinline__ void product_body(const Product& p, char* lds) {
-  using R = Ring<BT>;
+template <typename W, typename T, int BT, int KS, int KIND>
+__device__ __forceinline__ void product_body(const Product& p, char* lds0) {
+  using R = Ring<BT, KS>;
   constexpr bool kSym = KIND <= kJoin;
   constexpr int MI = BT / 64, kBytes = int(sizeof(W));
   const int tm = blockIdx.y, tn = blockIdx.x;
   if (kSym && tn < tm) return;
   const size_t z = blockIdx.z;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3), lane = threadIdx.x & 63;
+  const int group = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
   const int wm = (wave >> 1) * (BT / 2), wn = (wave & 1) * (BT / 2);
-  // waves 0 and 1 load A rows, 2 and 3 B rows; rows past the matrix repeat its last one
+  char* lds = lds0 + group * R::kSlots * R::kStage;
+  // of a group, waves 0 and 1 load A rows, 2 and 3 B rows; rows past the matrix repeat its last one
   const bool is_a = wave < 2;
   const int ld = is_a ? p.lda : p.ldb, rows = is_a ? p.m : p.n;
   const size_t off = z * (is_a ? p.sa : p.sb);
@@ -365,8 +369,10 @@ __device__ __forceinline__ void product_body(const Product& p, char* lds) {
     vo[j] = uint32_t(row) * uint32_t(ld) * kBytes + uint32_t(((lane & 7) ^ ((r >> 1) & 7)) * 16);
   }
   const int slices = p.k * kBytes / 128, total = p.a2 != nullptr ? 2 * slices : slices;
-  auto issue = [&](int s) {  // stage min(s, total - 1) into its slot
-    const int st = min(s, total - 1);
+  const int turns = (total + KS - 1) / KS;            // this group's stages: mine from `from` on
+  const int from = group * turns, mine = min(turns, total - from);
+  auto issue = [&](int s) {  // the group's stage s, or the last one there is, into its slot
+    const int st = min(from + s, total - 1);
     char* slot = lds + (s % R::kSlots) * R::kStage + R::kPerWave * wave * 1024;
     const uint32_t ko = uint32_t(st >= slices ? st - slices : st) * 128u;
 #pragma unroll
@@ -388,11 +394,12 @@ __device__ __forceinline__ void product_body(const Product& p, char* lds) {
   }
   constexpr int kVec = Mma<W>::kVec;
   for (int s = 0; s < R::kSlots - 1; ++s) issue(s);
-  for (int s = 0; s < total; ++s) {
+  for (int s = 0; s < turns; ++s) {
     MOE_VMCNT(R::kPerWave * (R::kSlots - 2));  // this wave's loads of stage s have landed
     MOE_LGKMCNT0();                            // and its reads of stage s - 1
     block_barrier();                           // every wave's have
     issue(s + R::kSlots - 1);                  // into the slot stage s - 1 used
+    if (KS > 1 && s >= mine) continue;         // the last range may be short
     const char* st = lds + (s % R::kSlots) * R::kStage;
 #pragma unroll
     for (int kc = 0; kc < 8 / (2 * kVec); ++kc) {
@@ -412,7 +419,23 @@ __device__ __forceinline__ void product_body(const Product& p, char* lds) {
         for (int j = 0; j < MI; ++j) Mma<W>::mma(fa[i], fb[j], acc[i][j]);
     }
   }
-  MOE_VMCNT(0);  // the ring's last (repeated) loads land before the block ends
+  MOE_VMCNT(0);  // the ring's last (repeated) loads land before the LDS is used again, or the block ends
+  constexpr int kRegs = 16 / KS;  // of each accumulator, this thread's share of the epilogue
+  if constexpr (KS > 1) {
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(lds0);
+    const int t = threadIdx.x & 255;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) sums[(group * 16 + r) * 256 + t] = acc[0][0][r];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kRegs; ++r) {
+      float v = 0.f;
+#pragma unroll
+      for (int g = 0; g < KS; ++g) v += sums[(g * 16 + group * kRegs + r) * 256 + t];
+      acc[0][0][r] = v;
+    }
+  }
   // lane -> column (lane & 31), register r -> row 8 (r / 4) + 4 (lane / 32) + r % 4
   const float* du = p.du + z * p.mp;
   const float* dv = p.dv + z * p.mp;
@@ -423,9 +446,10 @@ __device__ __forceinline__ void product_body(const Product& p, char* lds) {
 #pragma unroll
     for (int j = 0; j < MI; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
+      for (int r = 0; r < kRegs; ++r) {
+        const int reg = group * kRegs + r;
         const int col = tn * BT + wn + j * 32 + (lane & 31);
-        const int row = tm * BT + wm + i * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        const int row = tm * BT + wm + i * 32 + 8 * (reg >> 2) + 4 * (lane >> 5) + (reg & 3);
         if (BT > kPad && (row >= p.m || col >= p.n)) continue;
         const size_t ci = z * p.sc + size_t(row) * p.ldc + col;
         float v = p.alpha * acc[i][j][r];
@@ -457,21 +481,22 @@ __device__ __forceinline__ void product_body(const Product& p, char* lds) {
       }
 }
 
-template <typename W, typename T, int BT, int KIND>
-__global__ __launch_bounds__(kThreads) void product_kernel(Product p) {
+template <typename W, typename T, int BT, int KS, int KIND>
+__global__ __launch_bounds__(kThreads * KS) void product_kernel(Product p) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  product_body<W, T, BT, KIND>(p, lds);
+  product_body<W, T, BT, KS, KIND>(p, lds);
 }
 
-template <typename W, typename T, int BT, int KIND>
+template <typename W, typename T, int BT, int KS, int KIND>
 moe_status launch_ring(const char* name, const Product& p, int count, hipStream_t s) {
-  auto kern = product_kernel<W, T, BT, KIND>;
-  constexpr int lds = Ring<BT>::kLds;
+  auto kern = product_kernel<W, T, BT, KS, KIND>;
+  constexpr int lds = Ring<BT, KS>::kLds;
+  static_assert(KS == 1 || KS * 16 * 256 * 4 <= lds, "the groups' sums fit");
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return set_error(MOE_ERR_HIP, "%s: LDS attribute: %s", name, hipGetErrorString(e));
   MOE_LAUNCH(name, kern, dim3(unsigned((p.n + BT - 1) / BT), unsigned((p.m + BT - 1) / BT), unsigned(count)),
-             dim3(kThreads), lds, s, p);
+             dim3(kThreads * KS), lds, s, p);
   return MOE_OK;
 }
 
@@ -744,16 +769,23 @@ moe_status launch(const char* name, const Product& p, int count, hipStream_t s) 
 
 }  // namespace nsbig
 
-// The large tile takes float16 matrices past kSingleSteps; of the small ones the 128 x 128
-// where they fill the CUs twice.
+// The large tile takes float16 matrices past kSingleSteps.  Of the small ones the 128 x 128
+// where they fill the CUs twice, else 64 x 64, K split over groups of waves where those do
+// not fill them once, or twice, and every group has two stages.
 template <typename W, typename T, int KIND>
 moe_status launch_product(const char* name, const Product& p, bool large, int count, hipStream_t s) {
   if constexpr (sizeof(W) == 2) {
     if (large) return nsbig::launch<KIND>(name, p, count, s);
   }
-  const int64_t t = int64_t((p.m + 127) / 128) * ((p.n + 127) / 128) * count;
-  if ((KIND <= kJoin ? t / 2 : t) >= 512) return launch_ring<W, T, 128, KIND>(name, p, count, s);
-  return launch_ring<W, T, 64, KIND>(name, p, count, s);
+  const auto tiles = [&](int bt) {
+    const int64_t m = (p.m + bt - 1) / bt, n = (p.n + bt - 1) / bt;
+    return (KIND <= kJoin ? m * (m + 1) / 2 : m * n) * count;
+  };
+  if (tiles(128) >= 512) return launch_ring<W, T, 128, 1, KIND>(name, p, count, s);
+  const int stages = p.k * int(sizeof(W)) / 128 * (p.a2 != nullptr ? 2 : 1);
+  if (tiles(64) <= 256 && stages >= 8) return launch_ring<W, T, 64, 4, KIND>(name, p, count, s);
+  if (tiles(64) <= 512 && stages >= 4) return launch_ring<W, T, 64, 2, KIND>(name, p, count, s);
+  return launch_ring<W, T, 64, 1, KIND>(name, p, count, s);
 }
 
 #define TRY_NS(expr)                       \
