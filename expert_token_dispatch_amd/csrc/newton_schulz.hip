@@ -769,18 +769,21 @@ moe_status launch(const char* name, const Product& p, int count, hipStream_t s) 
 
 }  // namespace nsbig
 
-// The large tile takes float16 matrices past kSingleSteps.  Of the small ones the 128 x 128
-// where they fill the CUs twice, else 64 x 64, K split over groups of waves where those do
-// not fill them once, or twice, and every group has two stages.
+// The large tile takes float16 matrices past kSingleSteps, from kLargeTiles tiles on (one
+// matrix of 600 x 1500, 6 and 18 tiles: 536 us on it, 171 on the small ones; 16 of 512 x 512,
+// 48 and 64 tiles: the same; 8 of 1000 x 1000, 80 and 128: 649 against 1050).  Of the small
+// tiles the 128 x 128 where they fill the CUs twice, else 64 x 64, K split over groups of
+// waves where those do not fill them once, or twice, and every group has two stages.
+constexpr int kLargeTiles = 48;
 template <typename W, typename T, int KIND>
 moe_status launch_product(const char* name, const Product& p, bool large, int count, hipStream_t s) {
-  if constexpr (sizeof(W) == 2) {
-    if (large) return nsbig::launch<KIND>(name, p, count, s);
-  }
   const auto tiles = [&](int bt) {
     const int64_t m = (p.m + bt - 1) / bt, n = (p.n + bt - 1) / bt;
     return (KIND <= kJoin ? m * (m + 1) / 2 : m * n) * count;
   };
+  if constexpr (sizeof(W) == 2) {
+    if (large && tiles(256) >= kLargeTiles) return nsbig::launch<KIND>(name, p, count, s);
+  }
   if (tiles(128) >= 512) return launch_ring<W, T, 128, 1, KIND>(name, p, count, s);
   const int stages = p.k * int(sizeof(W)) / 128 * (p.a2 != nullptr ? 2 : 1);
   if (tiles(64) <= 256 && stages >= 8) return launch_ring<W, T, 64, 4, KIND>(name, p, count, s);
