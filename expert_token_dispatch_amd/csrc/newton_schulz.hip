@@ -315,42 +315,213 @@ template <> struct Mma<float> {
   }
 };
 
-// Element (row, col) of the last product into the user's result or weight.
-template <typename T, int KIND>
-__device__ __forceinline__ void put_last(const Product& p, size_t z, int row, int col, float v) {
-  const size_t at = z * p.rows * p.cols + size_t(row) * p.cols + col;
-  T* o = static_cast<T*>(p.out) + at;
-  if constexpr (KIND == kUpdate) {
-    const float w = p.master != nullptr ? p.master[at] : Elem<T>::to_f32(*o);
-    v = w * p.keep - v * p.step;
-    if (p.master != nullptr) p.master[at] = v;
-  }
-  *o = Elem<T>::from_f32(v);
+// ---- epilogues.  The products are formed as (B rows) x (A rows), so lane l holds row l % 32
+// of a 32x32 block and register 4q + u its column 8q + 4 (l / 32) + u: four neighbouring
+// columns at a time.  Sides of the working matrices are multiples of 64, so four columns, or
+// eight, are inside a matrix or outside as a whole.
+template <typename W> struct alignas(4 * sizeof(W)) Vec4 {
+  W e[4];
+};
+template <typename W>
+__device__ __forceinline__ void load4(const void* base, size_t at, float* f) {
+  const Vec4<W> v = *reinterpret_cast<const Vec4<W>*>(static_cast<const W*>(base) + at);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f[k] = float(v.e[k]);
 }
 
-// Tiles of BT x BT (64 or 128), four waves 2 x 2.  A stage is 128 bytes of k of the tile's A
-// and B rows, filled by direct global->LDS loads (1 KB: eight rows) kSlots - 1 stages ahead,
-// one barrier a stage.  16-byte piece c of row r sits at piece c ^ (r / 2 % 8), so the reads
-// of 16 rows at one piece cover all banks.  KS > 1 (64 x 64 tiles, too few for the card): KS
-// groups of four waves take a range of K each, with a ring of its own; their sums are added
-// in the order of the ranges, a share of the registers by each group.
-template <int BT, int KS>
-struct Ring {
-  static constexpr int kStage = 2 * BT * 128, kSlots = BT == 128 ? 3 : (KS == 4 ? 2 : (KS == 2 ? 3 : 4));
-  static constexpr int kPerWave = kStage / 1024 / 4, kLds = KS * kSlots * kStage;
+// Four columns of the last product into the user's result or weight.
+template <typename T, int KIND>
+__device__ __forceinline__ void put_last(const Product& p, size_t z, int row, int col, const float* v) {
+  if (row >= p.rows) return;
+  const size_t at = z * p.rows * p.cols + size_t(row) * p.cols + col;
+  T* o = static_cast<T*>(p.out) + at;
+  if (p.cols % 4 == 0) {
+    if (col >= p.cols) return;
+    float w[4];
+    if constexpr (KIND == kUpdate) {
+      if (p.master != nullptr) {
+        load4<float>(p.master, at, w);
+      } else {
+        const Vec4<T> b = *reinterpret_cast<const Vec4<T>*>(o);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = Elem<T>::to_f32(b.e[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = w[k] * p.keep - v[k] * p.step;
+      if (p.master != nullptr) *reinterpret_cast<Vec4<float>*>(p.master + at) = Vec4<float>{w[0], w[1], w[2], w[3]};
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = v[k];
+    }
+    Vec4<T> r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r.e[k] = Elem<T>::from_f32(w[k]);
+    *reinterpret_cast<Vec4<T>*>(o) = r;
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (col + k >= p.cols) break;
+    float w = v[k];
+    if constexpr (KIND == kUpdate) {
+      w = (p.master != nullptr ? p.master[at + k] : Elem<T>::to_f32(o[k])) * p.keep - w * p.step;
+      if (p.master != nullptr) p.master[at + k] = w;
+    }
+    o[k] = Elem<T>::from_f32(w);
+  }
+}
+
+// A tile of R x C in LDS, rows of RS bytes, into c at (row0, n0) of an m x n matrix, by
+// 16-byte pieces; threads t of N.
+template <typename W, int R, int C, int RS, int N>
+__device__ __forceinline__ void store_tile(const char* lds, W* c, int ldc, int m, int n, int row0, int n0, int t) {
+  constexpr int kEl = 16 / int(sizeof(W)), kPieces = C / kEl;
+#pragma unroll
+  for (int k = 0; k < (R * kPieces + N - 1) / N; ++k) {
+    const int id = t + k * N, r = id / kPieces, e = (id % kPieces) * kEl;
+    if (R * kPieces % N != 0 && id >= R * kPieces) break;
+    if (row0 + r < m && n0 + e < n)
+      *reinterpret_cast<u32x4_t*>(c + size_t(row0 + r) * ldc + n0 + e) =
+          *reinterpret_cast<const u32x4_t*>(lds + r * RS + e * int(sizeof(W)));
+  }
+}
+
+// The same tile transposed: its columns as rows n0 + .. of an n x m matrix.  float16: by the
+// transposing LDS reads, 16 columns x 32 rows a wave and turn (lane group G rows 8 G .., lane i
+// of a group column i).  float32: 16 columns x 16 rows, four rows a lane.  RS is chosen so that
+// a read's rows lie in different banks.
+template <typename W, int R, int C, int RS, int N>
+__device__ __forceinline__ void store_tile_turned(const char* lds, W* c, int ldc, int m, int n, int row0, int n0, int t) {
+  const int lane = t & 63, G = lane >> 4, il = lane & 15;
+  constexpr int kRows = sizeof(W) == 2 ? 32 : 16, kTurns = (R / kRows) * (C / 16);
+#pragma unroll
+  for (int k = 0; k < (kTurns + N / 64 - 1) / (N / 64); ++k) {
+    const int u = (t >> 6) + k * (N / 64);
+    if (kTurns % (N / 64) != 0 && u >= kTurns) break;
+    const int r0 = (u % (R / kRows)) * kRows + G * (kRows / 4), c0 = (u / (R / kRows)) * 16;
+    u32x4_t v;
+    if constexpr (sizeof(W) == 2) {
+      const char* src = lds + (r0 + (il >> 2)) * RS + (c0 + 4 * (il & 3)) * 2;
+      v = __builtin_bit_cast(u32x4_t, read_kn_frag2(src, src + 4 * RS));
+    } else {
+      const char* src = lds + r0 * RS + (c0 + il) * 4;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const uint32_t*>(src + e * RS);
+    }
+    if (n0 + c0 + il < n && row0 + r0 < m) *reinterpret_cast<u32x4_t*>(c + size_t(n0 + c0 + il) * ldc + row0 + r0) = v;
+  }
+}
+
+// ---- which tile a block forms.  Blocks that run at once on an XCD get consecutive tile
+// numbers, so that its L2 holds the rows they share; the numbers run over (matrix, group of
+// four n-tiles, m-tile, n-tile in the group), a symmetric product's over m <= n.
+constexpr int kGroup = 4;
+
+__host__ __device__ inline int sym_tiles(int t) { return t * (t + 1) / 2; }
+
+// t / d by the high half of t * (2^64 / d + 1), exact below 2^31.  The compiler's division
+// takes a block some hundred dependent instructions before its first load.
+struct Divisor {
+  uint64_t m;  // 0: d is 1
+  Divisor() = default;
+  explicit Divisor(int d) : m(d == 1 ? 0 : ~uint64_t(0) / uint64_t(d) + 1) {}
+  __device__ __forceinline__ int operator()(int t) const { return m == 0 ? t : int(__umul64hi(uint64_t(t), m)); }
 };
 
-template <typename W, typename T, int BT, int KS, int KIND>
-__device__ __forceinline__ void product_body(const Product& p, char* lds0) {
-  using R = Ring<BT, KS>;
+// t / w, w = 1, 2, 3 or 4
+__device__ __forceinline__ int over_group(int t, int w) {
+  return w == 3 ? int(__umulhi(unsigned(t), 0xAAAAAAABu) >> 1) : t >> (w >> 1);
+}
+
+struct TileMap {
+  int MT, NT;  // m-tiles and n-tiles of a matrix
+  int each;    // tiles of a matrix
+  int per;     // tiles of an XCD
+  int total;
+  Divisor by_each, by_group;
+  unsigned blocks() const { return unsigned(per) * big::kXcds; }
+};
+
+template <bool SYM>
+TileMap tile_map(int m, int n, int bm, int bn, int count) {
+  TileMap t;
+  t.MT = (m + bm - 1) / bm;
+  t.NT = (n + bn - 1) / bn;
+  t.each = SYM ? sym_tiles(t.NT) : t.MT * t.NT;
+  t.total = count * t.each;
+  t.per = (t.total + big::kXcds - 1) / big::kXcds;
+  t.by_each = Divisor(t.each);
+  t.by_group = Divisor(t.MT * kGroup);
+  return t;
+}
+
+// this block's matrix and tile; false: it has none
+template <bool SYM>
+__device__ __forceinline__ bool tile_of_block(const TileMap& map, size_t& z, int& tm, int& tn) {
+  int t = int(blockIdx.x % big::kXcds) * map.per + int(blockIdx.x / big::kXcds);
+  if (t >= map.total) return false;
+  const int matrix = map.by_each(t);
+  z = matrix;
+  t -= matrix * map.each;
+  if constexpr (SYM) {
+    for (int g = 0;; ++g) {
+      // the group's n-tiles 4g .. 4g + w - 1 have 4g + 1, .., 4g + w m-tiles
+      const int w = min(kGroup, map.NT - g * kGroup), n = w * g * kGroup + sym_tiles(w);
+      if (t >= n) {
+        t -= n;
+        continue;
+      }
+      if (t < w * g * kGroup) {
+        tm = over_group(t, w);
+        tn = g * kGroup + t - tm * w;
+      } else {
+        t -= w * g * kGroup;
+        int r = 0;
+        while (t >= w - r) t -= w - r++;  // rows of the triangle: w, w - 1, .. tiles
+        tm = g * kGroup + r;
+        tn = tm + t;
+      }
+      return true;
+    }
+  } else {
+    const int g = map.by_group(t), w = min(kGroup, map.NT - g * kGroup);
+    t -= g * map.MT * kGroup;
+    tm = over_group(t, w);
+    tn = g * kGroup + t - tm * w;
+    return true;
+  }
+}
+
+// Tiles of 64 x 64, four waves 2 x 2 of 32 x 32.  A stage is 128 bytes of k of the tile's A
+// and B rows, filled by direct global->LDS loads (1 KB: eight rows) kSlots - 1 stages ahead,
+// one barrier a stage.  16-byte piece c of row r sits at piece c ^ (r / 2 % 8), so the reads
+// of 16 rows at one piece cover all banks.  KS > 1 (too few tiles for the card): KS groups of
+// four waves take a range of K each, with a ring of its own; their sums are added in the order
+// of the ranges, a share of the registers by each group.
+//
+// What bounds it: in float32 the MFMAs (32 matrices of 1024 x 1024, five steps: 5.6 ms, 126
+// TFLOP/s).  Their stages are long, so two slots do, and five blocks a CU hide one another's
+// barriers and epilogues: three and four slots took 9% longer, 128 x 128 tiles 10%.
+template <typename W, int KS>
+struct Ring {
+  static constexpr int kStage = 2 * kPad * 128, kSlots = sizeof(W) == 4 || KS == 4 ? 2 : (KS == 2 ? 3 : 4);
+  static constexpr int kRow = kPad * int(sizeof(W)) + (sizeof(W) == 2 ? 32 : 16);  // of the tile in LDS
+  static constexpr int kPerWave = kStage / 1024 / 4, kLds = KS * kSlots * kStage;
+  static_assert(kPad * kRow <= kLds, "the tile fits");
+  static_assert(KS == 1 || KS * 16 * 256 * 4 <= kLds, "the groups' sums fit");
+};
+
+template <typename W, typename T, int KS, int KIND>
+__device__ __forceinline__ void product_body(const Product& p, const TileMap& map, char* lds0) {
+  using R = Ring<W, KS>;
   constexpr bool kSym = KIND <= kJoin;
-  constexpr int MI = BT / 64, kBytes = int(sizeof(W));
-  const int tm = blockIdx.y, tn = blockIdx.x;
-  if (kSym && tn < tm) return;
-  const size_t z = blockIdx.z;
+  constexpr int kBytes = int(sizeof(W));
+  size_t z;
+  int tm, tn;
+  if (!tile_of_block<kSym>(map, z, tm, tn)) return;
   const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3), lane = threadIdx.x & 63;
   const int group = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
-  const int wm = (wave >> 1) * (BT / 2), wn = (wave & 1) * (BT / 2);
+  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
   char* lds = lds0 + group * R::kSlots * R::kStage;
   // of a group, waves 0 and 1 load A rows, 2 and 3 B rows; rows past the matrix repeat its last one
   const bool is_a = wave < 2;
@@ -364,8 +535,8 @@ __device__ __forceinline__ void product_body(const Product& p, char* lds0) {
   uint32_t vo[R::kPerWave];
 #pragma unroll
   for (int j = 0; j < R::kPerWave; ++j) {
-    const int r = (wave & 1) * (BT / 2) + 8 * j + (lane >> 3);  // row of the operand's part of the stage
-    const int row = min((is_a ? tm : tn) * BT + r, rows - 1);
+    const int r = (wave & 1) * 32 + 8 * j + (lane >> 3);  // row of the operand's part of the stage
+    const int row = min((is_a ? tm : tn) * kPad + r, rows - 1);
     vo[j] = uint32_t(row) * uint32_t(ld) * kBytes + uint32_t(((lane & 7) ^ ((r >> 1) & 7)) * 16);
   }
   const int slices = p.k * kBytes / 128, total = p.a2 != nullptr ? 2 * slices : slices;
@@ -379,19 +550,10 @@ __device__ __forceinline__ void product_body(const Product& p, char* lds0) {
     for (int j = 0; j < R::kPerWave; ++j)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(st >= slices ? r1 : r0, (lds_ptr_t)(slot + j * 1024), 16, vo[j], ko, 0, 0);
   };
-  f32x16_t acc[MI][MI];
+  f32x16_t acc;
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int j = 0; j < MI; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  int ao[MI], bo[MI], sw = ((lane & 31) >> 1) & 7;
-#pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    ao[i] = (wm + i * 32 + (lane & 31)) * 128;
-    bo[i] = (BT + wn + i * 32 + (lane & 31)) * 128;
-  }
+  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
+  const int sw = ((lane & 31) >> 1) & 7, ao = (wm + (lane & 31)) * 128, bo = (kPad + wn + (lane & 31)) * 128;
   constexpr int kVec = Mma<W>::kVec;
   for (int s = 0; s < R::kSlots - 1; ++s) issue(s);
   for (int s = 0; s < turns; ++s) {
@@ -403,20 +565,14 @@ __device__ __forceinline__ void product_body(const Product& p, char* lds0) {
     const char* st = lds + (s % R::kSlots) * R::kStage;
 #pragma unroll
     for (int kc = 0; kc < 8 / (2 * kVec); ++kc) {
-      u32x4_t fa[MI][kVec], fb[MI][kVec];
+      u32x4_t fa[kVec], fb[kVec];
 #pragma unroll
       for (int v = 0; v < kVec; ++v) {
         const int c = (((2 * kc + (lane >> 5)) * kVec + v) ^ sw) * 16;
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          fa[i][v] = *reinterpret_cast<const u32x4_t*>(st + ao[i] + c);
-          fb[i][v] = *reinterpret_cast<const u32x4_t*>(st + bo[i] + c);
-        }
+        fa[v] = *reinterpret_cast<const u32x4_t*>(st + ao + c);
+        fb[v] = *reinterpret_cast<const u32x4_t*>(st + bo + c);
       }
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < MI; ++j) Mma<W>::mma(fa[i], fb[j], acc[i][j]);
+      Mma<W>::mma(fb, fa, acc);
     }
   }
   MOE_VMCNT(0);  // the ring's last (repeated) loads land before the LDS is used again, or the block ends
@@ -426,77 +582,119 @@ __device__ __forceinline__ void product_body(const Product& p, char* lds0) {
     float* sums = reinterpret_cast<float*>(lds0);
     const int t = threadIdx.x & 255;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) sums[(group * 16 + r) * 256 + t] = acc[0][0][r];
+    for (int r = 0; r < 16; ++r) sums[(group * 16 + r) * 256 + t] = acc[r];
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < kRegs; ++r) {
       float v = 0.f;
 #pragma unroll
       for (int g = 0; g < KS; ++g) v += sums[(g * 16 + group * kRegs + r) * 256 + t];
-      acc[0][0][r] = v;
+      acc[r] = v;
     }
   }
-  // lane -> column (lane & 31), register r -> row 8 (r / 4) + 4 (lane / 32) + r % 4
+  __syncthreads();  // the LDS is read out
+  const int row0 = tm * kPad, n0 = tn * kPad;
+  constexpr int RS = R::kRow;
   const float* du = p.du + z * p.mp;
   const float* dv = p.dv + z * p.mp;
   const float* dq = p.dq + z * p.mp;
-  W* c = static_cast<W*>(p.c);
+  f32x4_t low[kRegs / 4];
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
+  for (int qq = 0; qq < kRegs / 4; ++qq) {
+    const int rt = wm + (lane & 31), ct = wn + 8 * (group * (kRegs / 4) + qq) + 4 * (lane >> 5);
+    const int row = row0 + rt, col = n0 + ct;
+    const size_t ci = z * p.sc + size_t(row) * p.ldc + col;
+    float v[4], f[4];
 #pragma unroll
-    for (int j = 0; j < MI; ++j)
+    for (int e = 0; e < 4; ++e) v[e] = p.alpha * acc[4 * qq + e];
+    if constexpr (kSym) {
+      if constexpr (KIND != kGram) {
+        load4<W>(p.v, ci, f);
+        const float by = KIND == kPoly ? p.g : p.g * du[row];
 #pragma unroll
-      for (int r = 0; r < kRegs; ++r) {
-        const int reg = group * kRegs + r;
-        const int col = tn * BT + wn + j * 32 + (lane & 31);
-        const int row = tm * BT + wm + i * 32 + 8 * (reg >> 2) + 4 * (lane >> 5) + (reg & 3);
-        if (BT > kPad && (row >= p.m || col >= p.n)) continue;
-        const size_t ci = z * p.sc + size_t(row) * p.ldc + col;
-        float v = p.alpha * acc[i][j][r];
-        if constexpr (kSym) {
-          if constexpr (KIND == kPoly) v += p.g * float(static_cast<const W*>(p.v)[ci]);
-          if constexpr (KIND == kNext || KIND == kJoin) v += p.g * du[row] * float(static_cast<const W*>(p.v)[ci]);
-          if constexpr (KIND == kJoin) v += p.h * dv[col] * float(static_cast<const W*>(p.u)[ci]);
-          if ((KIND == kPoly || KIND == kJoin) && row == col) {
-            p.dc[z * p.mp + row] = v * p.unit + (KIND == kPoly ? p.k0 : du[row] * dv[row]);
-            v = 0.f;
-          }
-          c[ci] = W(v);
-          if (tn != tm) c[z * p.sc + size_t(col) * p.ldc + row] = W(v);
-        } else {
-          float x = float(static_cast<const W*>(p.x)[ci]);
-          if (p.x2 != nullptr) x += float(static_cast<const W*>(p.x2)[ci]);
-          v += p.beta * dq[p.dq_col ? col : row] * x;
-          if constexpr (KIND == kApply) {
-            const W h = W(v), l = W(v - float(h));
-            const size_t ti = z * p.sc + size_t(col) * p.ldct + row;
-            c[ci] = h;
-            static_cast<W*>(p.ct)[ti] = h;
-            if (p.c2 != nullptr) static_cast<W*>(p.c2)[ci] = l;
-            if (p.ct2 != nullptr) static_cast<W*>(p.ct2)[ti] = l;
-          } else if (row < p.rows && col < p.cols) {
-            put_last<T, KIND>(p, z, row, col, v);
-          }
-        }
+        for (int e = 0; e < 4; ++e) v[e] += by * f[e];
       }
+      if constexpr (KIND == kJoin) {
+        load4<W>(p.u, ci, f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += p.h * dv[col + e] * f[e];
+      }
+      if constexpr (KIND == kPoly || KIND == kJoin) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (row == col + e) {
+            p.dc[z * p.mp + row] = v[e] * p.unit + (KIND == kPoly ? p.k0 : du[row] * dv[row]);
+            v[e] = 0.f;
+          }
+      }
+    } else {
+      load4<W>(p.x, ci, f);
+      if (p.x2 != nullptr) {
+        float f2[4];
+        load4<W>(p.x2, ci, f2);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] += f2[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += p.beta * dq[p.dq_col ? col + e : row] * f[e];
+    }
+    if constexpr (KIND == kResult || KIND == kUpdate) {
+      put_last<T, KIND>(p, z, row, col, v);
+    } else {
+      Vec4<W> h;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        h.e[e] = W(v[e]);
+        if constexpr (KIND == kApply && kBytes == 2) low[qq][e] = v[e] - float(h.e[e]);
+      }
+      *reinterpret_cast<Vec4<W>*>(lds0 + rt * RS + ct * kBytes) = h;
+    }
+  }
+  if constexpr (KIND != kResult && KIND != kUpdate) {
+    constexpr int kAll = kThreads * KS;
+    __syncthreads();
+    W* c = static_cast<W*>(p.c) + z * p.sc;
+    store_tile<W, kPad, kPad, RS, kAll>(lds0, c, p.ldc, p.m, p.n, row0, n0, threadIdx.x);
+    if (kSym && tm != tn)
+      store_tile_turned<W, kPad, kPad, RS, kAll>(lds0, c, p.ldc, p.m, p.n, row0, n0, threadIdx.x);
+    if constexpr (KIND == kApply) {
+      store_tile_turned<W, kPad, kPad, RS, kAll>(lds0, static_cast<W*>(p.ct) + z * p.sc, p.ldct, p.m, p.n, row0, n0,
+                                             threadIdx.x);
+      if (kBytes == 2 && p.c2 != nullptr) {  // the low halves, through the same tile
+        __syncthreads();
+#pragma unroll
+        for (int qq = 0; qq < kRegs / 4; ++qq) {
+          const int rt = wm + (lane & 31), ct = wn + 8 * (group * (kRegs / 4) + qq) + 4 * (lane >> 5);
+          Vec4<W> l;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) l.e[e] = W(low[qq][e]);
+          *reinterpret_cast<Vec4<W>*>(lds0 + rt * RS + ct * kBytes) = l;
+        }
+        __syncthreads();
+        store_tile<W, kPad, kPad, RS, kAll>(lds0, static_cast<W*>(p.c2) + z * p.sc, p.ldc, p.m, p.n, row0, n0, threadIdx.x);
+        if (p.ct2 != nullptr)
+          store_tile_turned<W, kPad, kPad, RS, kAll>(lds0, static_cast<W*>(p.ct2) + z * p.sc, p.ldct, p.m, p.n, row0, n0,
+                                                 threadIdx.x);
+      }
+    }
+  }
 }
 
-template <typename W, typename T, int BT, int KS, int KIND>
-__global__ __launch_bounds__(kThreads * KS) void product_kernel(Product p) {
+template <typename W, typename T, int KS, int KIND>
+__global__ __launch_bounds__(kThreads * KS) void product_kernel(Product p, TileMap map) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  product_body<W, T, BT, KS, KIND>(p, lds);
+  product_body<W, T, KS, KIND>(p, map, lds);
 }
 
-template <typename W, typename T, int BT, int KS, int KIND>
+template <typename W, typename T, int KS, int KIND>
 moe_status launch_ring(const char* name, const Product& p, int count, hipStream_t s) {
-  auto kern = product_kernel<W, T, BT, KS, KIND>;
-  constexpr int lds = Ring<BT, KS>::kLds;
-  static_assert(KS == 1 || KS * 16 * 256 * 4 <= lds, "the groups' sums fit");
+  auto kern = product_kernel<W, T, KS, KIND>;
+  constexpr int lds = Ring<W, KS>::kLds;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return set_error(MOE_ERR_HIP, "%s: LDS attribute: %s", name, hipGetErrorString(e));
-  MOE_LAUNCH(name, kern, dim3(unsigned((p.n + BT - 1) / BT), unsigned((p.m + BT - 1) / BT), unsigned(count)),
-             dim3(kThreads * KS), lds, s, p);
+  const TileMap map = tile_map<KIND <= kJoin>(p.m, p.n, kPad, kPad, count);
+  MOE_LAUNCH(name, kern, dim3(map.blocks()), dim3(kThreads * KS), lds, s, p, map);
   return MOE_OK;
 }
 
@@ -508,44 +706,13 @@ moe_status launch_ring(const char* name, const Product& p, int count, hipStream_
 // is written a second time, its columns read back as rows by the transposing LDS reads.
 // Rows of the LDS tile are 32 bytes longer than the tile: the four rows that such a read
 // takes from lie in different banks.
-//
-// Blocks that run at once on an XCD get consecutive tile numbers; those run over (matrix,
-// group of four n-tiles, m-tile, n-tile in group), a symmetric product's over m <= n.
 namespace nsbig {
 
 using big::BK;
 using big::BM;
 using big::BNE;
-constexpr int kGroup = 4;
 constexpr int kRS = BNE * 2 + 32;
 constexpr size_t kLds = big::kLoopLdsMax > size_t(BM) * kRS ? big::kLoopLdsMax : size_t(BM) * kRS;
-
-__host__ __device__ inline int sym_tiles(int t) { return t * (t + 1) / 2; }
-
-// tile number -> (m-tile, n-tile)
-template <bool SYM>
-__device__ __forceinline__ void tile_at(int t, int MT, int NT, int& tm, int& tn) {
-  int g = 0;
-  for (;; ++g) {  // at most NT / 4 groups
-    const int w = min(kGroup, NT - g * kGroup);
-    // a symmetric group's n-tiles 4g .. 4g + w - 1 have 4g + 1, .., 4g + w m-tiles
-    const int n = SYM ? w * g * kGroup + sym_tiles(w) : MT * w;
-    if (t < n || (g + 1) * kGroup >= NT) {
-      if (!SYM || t < w * g * kGroup) {
-        tm = t / w;
-        tn = g * kGroup + t % w;
-      } else {
-        t -= w * g * kGroup;
-        int r = 0;
-        while (t >= w - r) t -= w - r++;  // rows of the triangle: w, w - 1, .. tiles
-        tm = g * kGroup + r;
-        tn = tm + t;
-      }
-      return;
-    }
-    t -= n;
-  }
-}
 
 __device__ __forceinline__ void unpack4(uint2 w, float* f) {
   typedef _Float16 h4 __attribute__((ext_vector_type(4)));
@@ -559,19 +726,14 @@ __device__ __forceinline__ uint2 pack4(const float* f) {
 }
 
 template <int NW, int KIND>
-__global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, int per, int total) {
+__global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, TileMap map) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   using S = big::Shape<false, NW>;
   constexpr int NB = S::NB, kThr = NW * 64;
   constexpr bool kSym = KIND <= kJoin;
-  const int xcd = blockIdx.x % big::kXcds, loc = blockIdx.x / big::kXcds;
-  const int t = xcd * per + loc;
-  if (loc >= per || t >= total) return;
-  const int MT = (p.m + BM - 1) / BM, NT = (p.n + BNE - 1) / BNE;
-  const int each = kSym ? sym_tiles(NT) : MT * NT;
-  const size_t z = t / each;
+  size_t z;
   int tm, tn;
-  tile_at<kSym>(t % each, MT, NT, tm, tn);
+  if (!tile_of_block<kSym>(map, z, tm, tn)) return;
   const int row0 = tm * BM, n0 = tn * BNE;
 
   big::Operands op;
@@ -666,30 +828,7 @@ __global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, int per, int t
             }
           }
           if constexpr (KIND == kUpdate) {
-            if (row < p.rows) {
-              const size_t at = z * p.rows * p.cols + size_t(row) * p.cols + col;
-              if (p.cols % 4 == 0) {
-                if (col < p.cols) {
-                  uint2* o = reinterpret_cast<uint2*>(static_cast<bf16_t*>(p.out) + at);
-                  f32x4_t w;
-                  if (p.master != nullptr) {
-                    w = *reinterpret_cast<const f32x4_t*>(p.master + at);
-                  } else {
-                    const uint2 b = *o;
-                    w = f32x4_t{__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xFFFF0000u),
-                                __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xFFFF0000u)};
-                  }
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) w[e] = w[e] * p.keep - v[e] * p.step;
-                  if (p.master != nullptr) *reinterpret_cast<f32x4_t*>(p.master + at) = w;
-                  *o = make_uint2(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]));
-                }
-              } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (col + e < p.cols) put_last<bf16_t, KIND>(p, z, row, col + e, v[e]);
-              }
-            }
+            put_last<bf16_t, KIND>(p, z, row, col, v);
           } else if constexpr (KIND == kResult) {
             *reinterpret_cast<uint2*>(lds + rt * kRS + cl * 2) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
           } else {
@@ -719,28 +858,10 @@ __global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, int per, int t
       }
     } else {
       f16_t* c = static_cast<f16_t*>(p.c) + z * p.sc;
-#pragma unroll
-      for (int k = 0; k < BM * kPieces / kThr; ++k) {
-        const int id = tid + k * kThr, r = id / kPieces, cc = (id % kPieces) * 8;
-        if (row0 + r < p.m && n0 + cc < p.n)
-          *reinterpret_cast<u32x4_t*>(c + size_t(row0 + r) * p.ldc + n0 + cc) =
-              *reinterpret_cast<const u32x4_t*>(lds + r * kRS + cc * 2);
-      }
-      if (kSym ? tm != tn : p.ct != nullptr) {
-        // 16 columns x 32 rows a wave and turn: lane group G has rows 8 G .. of them, lane i
-        // of a group column i
-        f16_t* ct = kSym ? c : static_cast<f16_t*>(p.ct) + z * p.sc;
-        const int ldct = kSym ? p.ldc : p.ldct;
-        const int G = lane >> 4, il = lane & 15;
-#pragma unroll
-        for (int k = 0; k < (BM / 32) * (BNE / 16) / NW; ++k) {
-          const int u = wave + k * NW, r0 = (u % (BM / 32)) * 32 + 8 * G, c0 = (u / (BM / 32)) * 16;
-          const char* src = lds + (r0 + (il >> 2)) * kRS + (c0 + 4 * (il & 3)) * 2;
-          const bf16x8_t v = read_kn_frag2(src, src + 4 * kRS);
-          if (n0 + c0 + il < p.n && row0 + r0 < p.m)
-            *reinterpret_cast<u32x4_t*>(ct + size_t(n0 + c0 + il) * ldct + row0 + r0) = __builtin_bit_cast(u32x4_t, v);
-        }
-      }
+      store_tile<f16_t, BM, BNE, kRS, kThr>(lds, c, p.ldc, p.m, p.n, row0, n0, tid);
+      if (kSym ? tm != tn : p.ct != nullptr)
+        store_tile_turned<f16_t, BM, BNE, kRS, kThr>(lds, kSym ? c : static_cast<f16_t*>(p.ct) + z * p.sc,
+                                                     kSym ? p.ldc : p.ldct, p.m, p.n, row0, n0, tid);
     }
   };
   big::tile_loop<1, false, NW, false, false, big::F16, true>(op, p.n, nk, row0, n0, 0, p.a2 != nullptr ? 2 * nk : nk, lds, epi);
@@ -752,10 +873,8 @@ moe_status launch_nw(const char* name, const Product& p, int count, hipStream_t 
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, int(kLds));
   if (e != hipSuccess) return set_error(MOE_ERR_HIP, "%s: LDS attribute: %s", name, hipGetErrorString(e));
-  const int MT = (p.m + BM - 1) / BM, NT = (p.n + BNE - 1) / BNE;
-  const int64_t total = int64_t(count) * (KIND <= kJoin ? sym_tiles(NT) : MT * NT);
-  const int per = int((total + big::kXcds - 1) / big::kXcds);
-  MOE_LAUNCH(name, kern, dim3(unsigned(per * big::kXcds)), dim3(NW * 64), kLds, s, p, per, int(total));
+  const TileMap map = tile_map<KIND <= kJoin>(p.m, p.n, BM, BNE, count);
+  MOE_LAUNCH(name, kern, dim3(map.blocks()), dim3(NW * 64), kLds, s, p, map);
   return MOE_OK;
 }
 
@@ -784,11 +903,10 @@ moe_status launch_product(const char* name, const Product& p, bool large, int co
   if constexpr (sizeof(W) == 2) {
     if (large && tiles(256) >= kLargeTiles) return nsbig::launch<KIND>(name, p, count, s);
   }
-  if (tiles(128) >= 512) return launch_ring<W, T, 128, 1, KIND>(name, p, count, s);
   const int stages = p.k * int(sizeof(W)) / 128 * (p.a2 != nullptr ? 2 : 1);
-  if (tiles(64) <= 256 && stages >= 8) return launch_ring<W, T, 64, 4, KIND>(name, p, count, s);
-  if (tiles(64) <= 512 && stages >= 4) return launch_ring<W, T, 64, 2, KIND>(name, p, count, s);
-  return launch_ring<W, T, 64, 1, KIND>(name, p, count, s);
+  if (tiles(64) <= 256 && stages >= 8) return launch_ring<W, T, 4, KIND>(name, p, count, s);
+  if (tiles(64) <= 512 && stages >= 4) return launch_ring<W, T, 2, KIND>(name, p, count, s);
+  return launch_ring<W, T, 1, KIND>(name, p, count, s);
 }
 
 #define TRY_NS(expr)                       \
