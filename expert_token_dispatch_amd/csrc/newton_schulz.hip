@@ -27,8 +27,10 @@
 // of A grow by up to a^2 a step in the directions where A is small; they average out over
 // the shorter side (simulated error of the result, 0.16% of it the bfloat16 result's own:
 // 0.7% at 64, 0.28% at 128, 0.2% at 512, against 0.18% in single steps), so matrices with a
-// shorter side of up to kSingleSteps take single steps, where the launches count more
-// than the products.  Float32 layers run on float32 operands in single steps (a phase
+// shorter side of up to 128 take single steps, and up to 256 those that are less than twice
+// as long: there a phase has no fewer products to do (128 matrices of 256 x 256: 331 us in
+// phases, 295 in single steps; 32 of 256 x 1024: 228 and 259; 256 of 256 x 512: 712 and
+// 1094).  Float32 layers run on float32 operands in single steps (a phase
 // would double the error).
 #include <math.h>
 
@@ -67,7 +69,10 @@ struct Plan {
   size_t o_part, o_x[4], o_t[4], o_q[5], o_d[5], bytes;
 };
 
-constexpr int kSingleSteps = 256;
+bool single_steps(int rows, int cols) {
+  const int shorter = std::min(rows, cols), longer = std::max(rows, cols);
+  return shorter <= 128 || (shorter <= 256 && longer < 2 * shorter);
+}
 
 // elements of a matrix that one block of the norm kernel adds up
 constexpr int64_t kNormElems = 16384;
@@ -94,7 +99,7 @@ Plan make_plan(const moe_muon_desc* m) {
     return r;
   };
   p.o_part = take(size_t(p.count) * p.nblk * sizeof(double));
-  p.single = m->dtype == MOE_F32 || std::min(m->rows, m->cols) <= kSingleSteps;
+  p.single = m->dtype == MOE_F32 || single_steps(m->rows, m->cols);
   // X and the X after it, as they are and transposed, and their low halves: of X_0, in single
   // steps of X_1 too
   for (int i = 0; i < 4; ++i) {
@@ -698,10 +703,10 @@ moe_status launch_ring(const char* name, const Product& p, int count, hipStream_
   return MOE_OK;
 }
 
-// ---- the same on the large tile (float16, sides past kSingleSteps) ---------------------
+// ---- the same on the large tile (float16) ----------------------------------------------
 // 256 x 256 tiles of big_tile.h, both operands along K (with one of them the other way round,
-// through the transposing LDS reads, a step of 64 k took 2.25 us against 1.69, with both 3.1).  The accumulators hold four neighbouring columns of one
-// row at a time, so the epilogue reads what it adds eight bytes a lane, turns the tile to
+// through the transposing LDS reads, a step of 64 k took 2.25 us against 1.69, with both 3.1).
+// The accumulators hold four neighbouring columns of one row at a time, so the epilogue reads what it adds eight bytes a lane, turns the tile to
 // float16 in LDS and writes whole row pieces; a symmetric product's tile off the diagonal
 // is written a second time, its columns read back as rows by the transposing LDS reads.
 // Rows of the LDS tile are 32 bytes longer than the tile: the four rows that such a read
@@ -878,8 +883,8 @@ moe_status launch_nw(const char* name, const Product& p, int count, hipStream_t 
   return MOE_OK;
 }
 
-// Four waves from 64 steps of k on, eight below, as for the grouped products (muon_wide's
-// shape, K = 4096 and 14336: four are 2.7% faster; orth_many's, K = 768: 6% slower).
+// Four waves from 64 steps of k on, eight below, as for the grouped products (K = 4096 and
+// 14336: four are 2.7% faster; K = 768: 6% slower).
 template <int KIND>
 moe_status launch(const char* name, const Product& p, int count, hipStream_t s) {
   if (p.k / BK >= 64) return launch_nw<4, KIND>(name, p, count, s);
@@ -888,20 +893,21 @@ moe_status launch(const char* name, const Product& p, int count, hipStream_t s) 
 
 }  // namespace nsbig
 
-// The large tile takes float16 matrices past kSingleSteps, from kLargeTiles tiles on (one
-// matrix of 600 x 1500, 6 and 18 tiles: 536 us on it, 171 on the small ones; 16 of 512 x 512,
-// 48 and 64 tiles: the same; 8 of 1000 x 1000, 80 and 128: 649 against 1050).  Of the small
-// tiles the 128 x 128 where they fill the CUs twice, else 64 x 64, K split over groups of
-// waves where those do not fill them once, or twice, and every group has two stages.
-constexpr int kLargeTiles = 48;
+// float16 phases: large tiles or small ones.  A round of large tiles on 256 CUs takes as long
+// as some 1800 small ones (fitted to 18 stacks timed on both: 2 matrices of 2000 x 2000, 1056
+// and 2048 small tiles a product, 943 us on large tiles and 844 on small ones; 4 of them 1073
+// and 1555; 128 of 300 x 300, two rounds that are mostly padding, 782 and 528).
+// Small tiles too few for the CUs split K over groups of waves: four while there is a CU for
+// each tile, two while there are two tiles, and every group has two stages.
+constexpr int kRound = 1800;
 template <typename W, typename T, int KIND>
-moe_status launch_product(const char* name, const Product& p, bool large, int count, hipStream_t s) {
+moe_status launch_product(const char* name, const Product& p, bool phases, int count, hipStream_t s) {
   const auto tiles = [&](int bt) {
     const int64_t m = (p.m + bt - 1) / bt, n = (p.n + bt - 1) / bt;
     return (KIND <= kJoin ? m * (m + 1) / 2 : m * n) * count;
   };
   if constexpr (sizeof(W) == 2) {
-    if (large && tiles(256) >= kLargeTiles) return nsbig::launch<KIND>(name, p, count, s);
+    if (phases && tiles(64) >= kRound * ((tiles(256) + 255) / 256)) return nsbig::launch<KIND>(name, p, count, s);
   }
   const int stages = p.k * int(sizeof(W)) / 128 * (p.a2 != nullptr ? 2 : 1);
   if (tiles(64) <= 256 && stages >= 8) return launch_ring<W, T, 4, KIND>(name, p, count, s);

@@ -212,6 +212,54 @@ def test_muon_update(shape, dtype, master, nesterov, decay):
             assert torch.equal(weight, mast.to(TYPES[dtype]))
 
 
+def newton_schulz_f64(u, steps=5, coefs=USUAL, eps=1e-7):
+    """The formula on float64 matrices of the GPU, for sides that are slow on the CPU."""
+    a, b, c = coefs
+    x = u / (u.norm() + eps)
+    for _ in range(steps):
+        g = torch.mm(x, x.t().contiguous()) if x.shape[0] <= x.shape[1] else torch.mm(x.t().contiguous(), x)
+        p = b * g + c * torch.mm(g, g)
+        x = a * x + (torch.mm(p, x) if x.shape[0] <= x.shape[1] else torch.mm(x, p))
+    return x
+
+
+# stacks that fill the card: products of many tiles in one launch, odd sides, long K
+@pytest.mark.parametrize("shape", [(14, 990, 1010), (16, 1010, 996), (16, 950, 4100), (1, 4100, 4100), (2, 2100, 4100),
+                                   (40, 200, 1000), (130, 300, 290), (200, 70, 65), (33, 250, 130)])
+def test_stacks_that_fill_the_card(shape):
+    say(f"[muon] stack {shape}")
+    gen = torch.Generator(device="cuda").manual_seed(sum(shape))
+    L, R, C = shape
+    r = max(1, min(R, C) // 16)
+    strong = torch.stack([torch.mm(torch.randn((R, r), device="cuda", generator=gen),
+                                   torch.randn((r, C), device="cuda", generator=gen)) for _ in range(L)])
+    g = (1e-3 * (strong / math.sqrt(r) + 0.25 * torch.randn(shape, device="cuda", generator=gen))).bfloat16()
+    o = orthogonalize(g, "bf16")
+    lr, scale, decay = (float(np.float32(v)) for v in (2e-3, 0.2 * math.sqrt(max(R, C)), 0.1))
+    m = etd.make_muon_desc(*shape, momentum=0.95, nesterov=False, lr=lr, update_scale=scale, weight_decay=decay)
+    ws = torch.full((etd.moe_muon_workspace_size(m),), 255, dtype=torch.uint8, device="cuda")
+    w0 = torch.randn(shape, device="cuda", generator=gen) / math.sqrt(C)
+    mast, weight, mom = w0.clone(), w0.bfloat16(), torch.zeros(shape, device="cuda")
+    etd.moe_muon_update(m, g, mom, weight, ws, master=mast)
+    alone = w0.bfloat16()
+    etd.moe_muon_update(m, g, torch.zeros(shape, device="cuda"), alone, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(mom, g.float())                    # of a momentum that was zero
+    assert torch.equal(weight, mast.bfloat16())
+    for z in sorted({0, L // 2, L - 1}):
+        ref = newton_schulz_f64(g[z].double())
+        n = float(ref.norm())
+        err = float((o[z].double() - ref).norm()) / n
+        say(f"[muon]   matrix {z} error {err:.2e}")
+        assert err <= TOL["bf16"]
+        want = w0[z].double() * (1.0 - lr * decay) - lr * scale * ref
+        slack = lr * scale * TOL["bf16"] * n + 3 * 2.0 ** -24 * float(want.norm())
+        assert float((mast[z].double() - want).norm()) <= slack
+        # without a master the weight is rounded before and after, half a step each
+        slack += 2 * 2.0 ** -8 * float(w0[z].norm() + lr * scale * n)
+        assert float((alone[z].double() - want).norm()) <= slack
+
+
 def test_zero_gradient_only_decays_the_weight():
     shape = (2, 40, 72)
     w = torch.randn(shape, device="cuda")
