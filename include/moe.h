@@ -1,6 +1,8 @@
 /*
- * moe.h -- C ABI of libmoe: the forward pass of one mixture-of-experts layer
- * on one GPU's share of the experts, for AMD Instinct MI355X (gfx950).
+ * moe.h -- C ABI of libmoe: the forward and backward pass of one
+ * mixture-of-experts layer on one GPU's share of the experts, the update of
+ * its expert weights and the forward on expert weights in 4 bits, for AMD
+ * Instinct MI355X (gfx950).
  *
  * The layer follows the four steps named on the Ultralytics glossary page
  * "Expert Parallelism", section "How tokens move between GPUs": route every
