@@ -350,3 +350,75 @@ def test_train_update_pack_and_serve(layout):
     plain = layer.forward(x)
     a, b = np_of(served).astype(np.float64), np_of(plain).astype(np.float64)
     assert np.linalg.norm(a - b) <= 2 * 2.0 ** -7 * np.linalg.norm(b)   # each: h and y rounded once
+
+
+@pytest.mark.parametrize("shape", [(14, 990, 1010), (4, 300, 290), (5, 60, 200)])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_a_gradient_that_is_not_finite_spoils_its_own_matrix_only(shape, bad):
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    g = (1e-3 * torch.randn(shape, device="cuda", generator=gen)).bfloat16()
+    w0 = torch.randn(shape, device="cuda", generator=gen)
+    m = etd.make_muon_desc(*shape, lr=1e-2)
+    ws = torch.full((etd.moe_muon_workspace_size(m),), 255, dtype=torch.uint8, device="cuda")
+
+    def step(grad):
+        mast, w, mom = w0.clone(), w0.bfloat16(), torch.zeros(shape, device="cuda")
+        etd.moe_muon_update(m, grad, mom, w, ws, master=mast)
+        return mast, w, mom
+
+    ref = step(g)
+    broken = g.clone()
+    broken[2, shape[1] - 1, 1] = bad
+    got = step(broken)
+    torch.cuda.synchronize()
+    others = [z for z in range(shape[0]) if z != 2]
+    for a, b in zip(got, ref):
+        assert torch.equal(a[others], b[others])
+    assert not torch.isfinite(got[0][2]).any()
+
+
+def test_two_updates_at_once_on_two_streams():
+    shapes = [(6, 520, 600), (14, 990, 1010)]
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    sets = []
+    for s in shapes:
+        m = etd.make_muon_desc(*s, lr=1e-2)
+        sets.append((m, (1e-3 * torch.randn(s, device="cuda", generator=gen)).bfloat16(),
+                     torch.randn(s, device="cuda", generator=gen)))
+
+    def run(m, g, w0, stream):
+        ws = torch.empty(etd.moe_muon_workspace_size(m), dtype=torch.uint8, device="cuda")
+        mast, w, mom = w0.clone(), w0.bfloat16(), torch.zeros_like(w0)
+        torch.cuda.synchronize()
+        return mast, lambda: etd.moe_muon_update(m, g, mom, w, ws, master=mast, stream=stream)
+
+    want = []
+    for s in sets:
+        mast, call = run(*s, None)
+        for _ in range(3):
+            call()
+        want.append(mast)
+    streams = [torch.cuda.Stream() for _ in sets]
+    pairs = [run(*s, st) for s, st in zip(sets, streams)]
+    for _ in range(3):
+        for _, call in pairs:
+            call()
+    torch.cuda.synchronize()
+    for (mast, _), ref in zip(pairs, want):
+        assert torch.equal(mast, ref)
+
+
+def test_a_stack_of_more_than_2_to_31_elements():
+    shape = (2100, 1024, 1024)
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    g = torch.randn(shape, device="cuda", generator=gen, dtype=torch.bfloat16)
+    w = torch.zeros(shape, device="cuda", dtype=torch.bfloat16)
+    mom = torch.zeros(shape, device="cuda")
+    m = etd.make_muon_desc(*shape, momentum=0.5, nesterov=False, lr=1.0, update_scale=-1.0)
+    ws = torch.empty(etd.moe_muon_workspace_size(m), dtype=torch.uint8, device="cuda")
+    etd.moe_muon_update(m, g, mom, w, ws)       # from zero weights: W is the orthogonalised gradient
+    torch.cuda.synchronize()
+    for z in (0, 1050, 2047, 2048, 2099):
+        assert torch.equal(mom[z], g[z].float())
+        ref = newton_schulz_f64(g[z].double())
+        assert float((w[z].double() - ref).norm() / ref.norm()) <= TOL["bf16"]

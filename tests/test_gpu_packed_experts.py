@@ -242,3 +242,95 @@ def test_packed_layer_in_a_graph_and_on_another_stream(name):
         assert torch.equal(y_g, ref), f"replay {r}"
         assert torch.equal(layer.forward_packed(x, packed), ref)
         torch.cuda.synchronize()
+
+
+def ffn_packed(x, rows, stacks, dtype="bf16", y=None):
+    """y of the packed feed-forward on segments of `rows`; stacks: {name: (codes, scales)}."""
+    H, I = x.shape[1], stacks["gate"][0].shape[1]
+    packed = etd.make_packed_experts({f"{n}_{k}": s[i] for n, s in stacks.items() for i, k in ((0, "codes"), (1, "scales"))})
+    d = etd.make_desc(x.shape[0], H, I, len(rows), 1, dtype=dtype)
+    ws = torch.full((etd.moe_packed_workspace_size(d, etd.MOE_STAGE_FFN),), 255, dtype=torch.uint8, device="cuda")
+    off = torch.from_numpy(np.r_[0, np.cumsum(rows)].astype(np.int32)).cuda()
+    y = torch.full_like(x, 3.0) if y is None else y
+    etd.moe_grouped_ffn_packed(d, x, off, packed, y, ws=ws)
+    torch.cuda.synchronize()
+    return y
+
+
+# few rows, few rows with K split over waves, tiles of 128 weight rows, of 256, float32
+NAN_GROUPS = [(96, 160, (3, 0, 2), "bf16"), (1088, 1056, (1, 2), "bf16"), (320, 288, (70, 9, 140), "bf16"),
+              (288, 4128, (260, 900, 130), "bf16"), (96, 64, (9, 0, 40), "f32")]
+
+
+@pytest.mark.parametrize("H,I,rows,dtype", NAN_GROUPS)
+def test_a_nan_group_reaches_only_the_outputs_that_it_weighs(H, I, rows, dtype):
+    say(f"[packed ffn] NaN groups H={H} I={I} rows={rows} {dtype}")
+    rng = np.random.default_rng(7)
+    L, P = len(rows), sum(rows)
+    x = torch.from_numpy(rng.standard_normal((P, H)).astype(np.float32)).to(TYPES[dtype]).cuda()
+    clean = {n: packed_stack(rng, L, N, K)[:2] for n, N, K in (("gate", I, H), ("up", I, H), ("down", H, I))}
+    ref = ffn_packed(x, rows, clean, dtype)
+    assert torch.isfinite(ref).all()
+    last = slice(P - rows[-1], P)
+    for o in (0, 17, H - 1):                      # a down row: one column of its expert's rows
+        s = clean["down"][1].clone()
+        s[L - 1, o, (o * 5) % (I // 32)] = 255
+        y = ffn_packed(x, rows, {**clean, "down": (clean["down"][0], s)}, dtype)
+        assert torch.isnan(y[last, o]).all()
+        y[last, o] = ref[last, o]
+        assert torch.equal(y, ref)
+    for name, i in (("gate", 0), ("up", I - 1)):  # an entry of h: every output of its expert's rows
+        s = clean[name][1].clone()
+        s[0, i, (H // 32) - 1] = 255
+        y = ffn_packed(x, rows, {**clean, name: (clean[name][0], s)}, dtype)
+        assert torch.isnan(y[:rows[0]]).all() and torch.equal(y[rows[0]:], ref[rows[0]:])
+
+
+@pytest.mark.parametrize("H,I,L,P,dtype", [(64, 96, 5, 20, "bf16"), (64, 96, 2, 500, "bf16"), (96, 2048, 4, 9000, "bf16"),
+                                           (64, 96, 3, 40, "f32")])
+def test_segments_without_rows_write_nothing(H, I, L, P, dtype):
+    rng = np.random.default_rng(8)
+    stacks = {n: packed_stack(rng, L, N, K)[:2] for n, N, K in (("gate", I, H), ("up", I, H), ("down", H, I))}
+    y = ffn_packed(torch.randn((P, H), device="cuda").to(TYPES[dtype]), [0] * L, stacks, dtype)
+    assert torch.all(y == 3.0)
+
+
+@pytest.mark.parametrize("hot", [0, 19, 39])
+def test_one_expert_with_all_the_rows_of_a_decode_step(hot):
+    rng = np.random.default_rng(9)
+    H, I, L, n = 256, 160, 40, 333                # 333 rows on 40 experts: the kernel for few rows
+    rows = [n if e == hot else 0 for e in range(L)]
+    full = {k: packed_stack(rng, L, N, K) for k, N, K in (("gate", I, H), ("up", I, H), ("down", H, I))}
+    x = torch.from_numpy(rng.standard_normal((n, H)).astype(np.float32)).bfloat16()
+    y = ffn_packed(x.cuda(), rows, {k: v[:2] for k, v in full.items()})
+    ref, bound = ffn_reference(x.double().numpy(), [full[k][2][hot] for k in ("gate", "up", "down")], "bf16")
+    assert (np.abs(np_of(y).astype(np.float64) - ref) <= bound).all()
+
+
+def test_zero_capacity_gives_a_zero_packed_layer():
+    s = synth.spec("skewed_capacity", T=1000, H=64, I=64, E=8, k=2, L=8, capacity_factor=0.001)
+    layer, x = layer_of(synth.make_layer(s))
+    dropped = torch.empty((1,), dtype=torch.int64, device="cuda")
+    y = layer.forward_packed(x, layer.pack_experts(), y=torch.full_like(x, 3.0), num_dropped_out=dropped)
+    torch.cuda.synchronize()
+    assert int(dropped) == s.T * s.k and torch.all(y == 0)
+
+
+def test_stacks_past_4_gib_are_reached():
+    """The last expert of a stack whose codes lie past 32-bit offsets, in both kernels."""
+    H, I, L = 4096, 8192, 300                     # 5.03 GB of codes a stack; one tensor serves all three
+    codes = torch.zeros((L, I, H // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.full((L, I, H // 32), 127, dtype=torch.uint8, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    codes[-1] = torch.randint(0, 256, codes[-1].shape, dtype=torch.uint8, device="cuda", generator=gen)
+    scales[-1] = 120 + torch.randint(0, 3, scales[-1].shape, dtype=torch.uint8, device="cuda", generator=gen)
+    stacks = {"gate": (codes, scales), "up": (codes, scales),
+              "down": (codes.view(L, H, I // 2), scales.view(L, H, I // 32))}
+    for n, spare in ((3, 0), (200, 64 * L)):      # spare rows: more than 32 an expert
+        x = torch.randn((n + spare, H), device="cuda", generator=gen).bfloat16()
+        y = ffn_packed(x, [0] * (L - 1) + [n], stacks)
+        alone = ffn_packed(x, [n], {k: (c[-1:].clone(), s[-1:].clone()) for k, (c, s) in stacks.items()})
+        assert torch.all(y[n:] == 3.0) and float(y[:n].float().abs().max()) > 0
+        # tiles and waves along K may differ between the two calls: the sums' order, not the values
+        a, b = y[:n].double(), alone[:n].double()
+        assert float((a - b).norm() / b.norm()) <= 2.0 ** -7
