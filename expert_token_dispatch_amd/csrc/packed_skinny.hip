@@ -57,21 +57,57 @@ __device__ __forceinline__ int expert_of_slot(const int32_t* __restrict__ offset
 
 // k of a chunk, and a row's bytes of it in LDS.  16-byte piece c of row r sits at piece
 // c ^ (r % 16), so the reads of 16 rows at one piece cover all banks.
-template <int WK>
+template <typename T, int WK>
 struct Chunk {
-  static constexpr int kAhead = WK == 4 ? 2 : 4;  // steps of a wave: a chunk's, and in flight
-  static constexpr int kSteps = WK * kAhead, kK = kSteps * kStep, kRowBytes = kK * 2, kPieces = kRowBytes / 16;
+  // steps of a wave: a chunk's, and in flight
+  static constexpr int kAhead = (WK == 4 ? 2 : 4) * 2 / int(sizeof(T));
+  static constexpr int kSteps = WK * kAhead, kK = kSteps * kStep;
+  static constexpr int kRowBytes = kK * int(sizeof(T)), kPieces = kRowBytes / 16;
+  static constexpr int kStepBytes = kStep * int(sizeof(T)), kLanePieces = kStepBytes / 64;  // of a row's step, a lane's
 };
 
-template <int NMAT, int WK, int NRB>
-__global__ __launch_bounds__(kThreads) void packed_gemm_kernel(const bf16_t* __restrict__ A,
+// Eight codes under one scale times a token row's elements at their k, for every 16 rows:
+// piece(rb, i) is the lane's i-th 16-byte piece of the eight.
+template <int NRB, typename P>
+__device__ __forceinline__ void multiply(bf16_t, const uint32_t (&w)[2], const float (&f)[2], const P& piece,
+                                         f32x4_t (&acc)[2][NRB]) {
+  const bf16x8_t v0 = decode_frag(w[0], f[0]), v1 = decode_frag(w[1], f[1]);
+#pragma unroll
+  for (int rb = 0; rb < NRB; ++rb) {
+    const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(piece(rb, 0));
+    acc[0][rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, v0, acc[0][rb], 0, 0, 0);
+    acc[1][rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, v1, acc[1][rb], 0, 0, 0);
+  }
+}
+template <int NRB, typename P>
+__device__ __forceinline__ void multiply(float, const uint32_t (&w)[2], const float (&f)[2], const P& piece,
+                                         f32x4_t (&acc)[2][NRB]) {
+  float v[2][8];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) decode_f32(w[m], f[m], v[m]);
+#pragma unroll
+  for (int rb = 0; rb < NRB; ++rb) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f32x4_t a = *reinterpret_cast<const f32x4_t*>(piece(rb, i));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[0][rb] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], v[0][4 * i + e], acc[0][rb], 0, 0, 0);
+        acc[1][rb] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], v[1][4 * i + e], acc[1][rb], 0, 0, 0);
+      }
+    }
+  }
+}
+
+template <typename T, int NMAT, int WK, int NRB>
+__global__ __launch_bounds__(kThreads) void packed_gemm_kernel(const T* __restrict__ A,
                                                                const int32_t* __restrict__ offsets,
                                                                const uint8_t* __restrict__ q0,
                                                                const uint8_t* __restrict__ s0,
                                                                const uint8_t* __restrict__ q1,
-                                                               const uint8_t* __restrict__ s1, bf16_t* __restrict__ C,
+                                                               const uint8_t* __restrict__ s1, T* __restrict__ C,
                                                                int L, int N, int K) {
-  using Ch = Chunk<WK>;
+  using Ch = Chunk<T, WK>;
   constexpr int kAhead = Ch::kAhead;
   constexpr int WN = 4 / WK, kRows = 16 * NRB;
   constexpr int kWaveCols = NMAT == 2 ? 16 : 32;
@@ -129,10 +165,12 @@ __global__ __launch_bounds__(kThreads) void packed_gemm_kernel(const bf16_t* __r
     }
   };
 
-  // the lane's pieces of a token row: piece 16 s + (4 kg + j) ^ lr of row lr for MFMA j of step s
-  int aoff[4];
+  // the lane's pieces of a token row's step: a quarter of it from piece kLanePieces kg on, turned by lr
+  constexpr int kPer = Ch::kLanePieces / 4;  // pieces of eight elements
+  int aoff[Ch::kLanePieces];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) aoff[j] = lr * Ch::kRowBytes + wk * 256 + (((4 * kg + j) ^ lr) * 16);
+  for (int j = 0; j < Ch::kLanePieces; ++j)
+    aoff[j] = lr * Ch::kRowBytes + wk * Ch::kStepBytes + (((Ch::kLanePieces * kg + j) ^ lr) * 16);
   constexpr int kWpr = Ch::kPieces / 64;                      // waves per row of a chunk being staged
   const int srow = wave / kWpr, spart = wave % kWpr;          // this wave stages rows srow, srow + 4 / kWpr, ..
   const int spiece = spart * 64 + lane;
@@ -140,17 +178,17 @@ __global__ __launch_bounds__(kThreads) void packed_gemm_kernel(const bf16_t* __r
   for (int m0 = 0; m0 < seg_n; m0 += kRows) {
     const int n = min(kRows, seg_n - m0);
     const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<bf16_t*>(A + size_t(seg0 + m0) * K), 0, uint32_t(n) * uint32_t(K) * 2u, kRsrcFlags);
+        const_cast<T*>(A + size_t(seg0 + m0) * K), 0, uint32_t(n) * uint32_t(K) * uint32_t(sizeof(T)), kRsrcFlags);
     u32x4_t stage[kStage];
     auto load_a = [&](int c) {
       // lanes past the end of the row ask for what lies behind the buffer: zeros
-      const uint32_t vo = c * Ch::kK + spiece * 8 < K ? uint32_t(spiece) * 16u : 0xFFFFFFF0u;
+      const uint32_t vo = c * Ch::kK + spiece * (16 / int(sizeof(T))) < K ? uint32_t(spiece) * 16u : 0xFFFFFFF0u;
 #pragma unroll
       for (int i = 0; i < kStage; ++i) {
         const int r = srow + i * (4 / kWpr);
         if (r < n)
           stage[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                                     ra, vo, uint32_t(r) * uint32_t(K) * 2u + uint32_t(c) * Ch::kRowBytes, 0));
+                                                     ra, vo, uint32_t(r) * uint32_t(K) * uint32_t(sizeof(T)) + uint32_t(c) * Ch::kRowBytes, 0));
       }
     };
     auto store_a = [&](int c) {
@@ -187,18 +225,14 @@ __global__ __launch_bounds__(kThreads) void packed_gemm_kernel(const bf16_t* __r
         // the scales of step u sit in lane group u, byte kg
         const uint32_t b0 = uint32_t(__shfl(int(sc0), 16 * u + lr, 64)) >> (8 * kg);
         const uint32_t b1 = uint32_t(__shfl(int(sc1), 16 * u + lr, 64)) >> (8 * kg);
-        const float f0 = __uint_as_float((b0 & 0xFFu) << 23), f1 = __uint_as_float((b1 & 0xFFu) << 23);
+        const float f[2] = {__uint_as_float((b0 & 0xFFu) << 23), __uint_as_float((b1 & 0xFFu) << 23)};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const bf16x8_t v0 = decode_frag(w[u][0][j], f0), v1 = decode_frag(w[u][1][j], f1);
           // rows past n hold what the LDS held: they reach only outputs that are never stored
-#pragma unroll
-          for (int rb = 0; rb < NRB; ++rb) {
-            const bf16x8_t a =
-                *reinterpret_cast<const bf16x8_t*>(buf + aoff[j] + rb * 16 * Ch::kRowBytes + u * WK * 256);
-            acc[0][rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, v0, acc[0][rb], 0, 0, 0);
-            acc[1][rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, v1, acc[1][rb], 0, 0, 0);
-          }
+          const uint32_t codes[2] = {w[u][0][j], w[u][1][j]};
+          multiply<NRB>(T{}, codes, f, [&](int rb, int i) {
+            return buf + aoff[j * kPer + i] + rb * 16 * Ch::kRowBytes + u * WK * Ch::kStepBytes;
+          }, acc);
         }
         if (more) load_w(c + 1, u);
         __builtin_amdgcn_sched_barrier(0);  // a step's reads stay in the step: registers
@@ -236,13 +270,13 @@ __global__ __launch_bounds__(kThreads) void packed_gemm_kernel(const bf16_t* __r
         for (int i = 0; i < 4; ++i) {
           const int r = rb * 16 + 4 * kg + i;
           if (r < n) {
-            bf16_t* crow = C + size_t(seg0 + m0 + r) * N;
+            T* crow = C + size_t(seg0 + m0 + r) * N;
             if (NMAT == 2) {
-              if (col0 + lr < N) crow[col0 + lr] = f32_to_bf16(silu(acc[0][rb][i]) * acc[1][rb][i]);
+              if (col0 + lr < N) crow[col0 + lr] = Elem<T>::from_f32(silu(acc[0][rb][i]) * acc[1][rb][i]);
             } else {
 #pragma unroll
               for (int s = 0; s < 2; ++s)
-                if (col0 + 16 * s + lr < N) crow[col0 + 16 * s + lr] = f32_to_bf16(acc[s][rb][i]);
+                if (col0 + 16 * s + lr < N) crow[col0 + 16 * s + lr] = Elem<T>::from_f32(acc[s][rb][i]);
             }
           }
         }
@@ -251,16 +285,16 @@ __global__ __launch_bounds__(kThreads) void packed_gemm_kernel(const bf16_t* __r
   }
 }
 
-template <int NMAT, int WK, int NRB>
-moe_status launch_wk(const char* name, const bf16_t* A, const int32_t* offsets, const void* q0, const void* s0,
-                     const void* q1, const void* s1, bf16_t* C, int L, int N, int K, int64_t max_pairs, hipStream_t s) {
+template <typename T, int NMAT, int WK, int NRB>
+moe_status launch_wk(const char* name, const T* A, const int32_t* offsets, const void* q0, const void* s0,
+                     const void* q1, const void* s1, T* C, int L, int N, int K, int64_t max_pairs, hipStream_t s) {
   constexpr int cols = (NMAT == 2 ? 16 : 32) * (4 / WK);
   const dim3 grid(unsigned((N + cols - 1) / cols), unsigned(std::min<int64_t>(L, max_pairs)));
-  auto kern = packed_gemm_kernel<NMAT, WK, NRB>;
-  constexpr int kBuf = 16 * NRB * Chunk<WK>::kRowBytes;
+  auto kern = packed_gemm_kernel<T, NMAT, WK, NRB>;
+  constexpr int kBuf = 16 * NRB * Chunk<T, WK>::kRowBytes;
   constexpr int kRed = 4 * 2 * NRB * 1024;  // an upper bound of the waves' sums
   static_assert(kRed <= kBuf, "the sums fit in one buffer");
-  const int lds = K > Chunk<WK>::kK ? 2 * kBuf : kBuf;
+  const int lds = K > Chunk<T, WK>::kK ? 2 * kBuf : kBuf;
   if (lds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, 2 * kBuf);
@@ -274,15 +308,15 @@ moe_status launch_wk(const char* name, const bf16_t* A, const int32_t* offsets, 
 
 // Waves along K: as many as it takes for two blocks a CU, given the experts that can have
 // rows, while every wave keeps two steps.
-template <int NMAT>
-moe_status launch(const char* name, const bf16_t* A, const int32_t* offsets, const void* q0, const void* s0,
-                  const void* q1, const void* s1, bf16_t* C, int L, int N, int K, int64_t max_pairs, hipStream_t s) {
+template <typename T, int NMAT>
+moe_status launch(const char* name, const T* A, const int32_t* offsets, const void* q0, const void* s0,
+                  const void* q1, const void* s1, T* C, int L, int N, int K, int64_t max_pairs, hipStream_t s) {
   constexpr int kCols = NMAT == 2 ? 64 : 128;
   const int64_t blocks = (N + kCols - 1) / kCols * std::min<int64_t>(L, max_pairs);
   const int steps = (K + kStep - 1) / kStep;
   const bool many = max_pairs > 8 * int64_t(L);
 #define MOE_PACKED(WK_, NRB_) \
-  launch_wk<NMAT, WK_, NRB_>(name, A, offsets, q0, s0, q1, s1, C, L, N, K, max_pairs, s)
+  launch_wk<T, NMAT, WK_, NRB_>(name, A, offsets, q0, s0, q1, s1, C, L, N, K, max_pairs, s)
   if (many) return MOE_PACKED(1, 2);
   if (blocks < 256 && steps >= 8) return MOE_PACKED(4, 1);
   if (blocks < 512 && steps >= 4) return MOE_PACKED(2, 1);
@@ -295,20 +329,27 @@ moe_status launch(const char* name, const bf16_t* A, const int32_t* offsets, con
 bool packed_skinny_fits(const moe_layer_desc* d, int64_t max_pairs) {
   // an expert's codes and 32 of its rows are addressed with 32-bit byte offsets
   const int64_t H = d->hidden, I = d->intermediate;
-  return d->dtype == MOE_BF16 && max_pairs <= int64_t(32) * d->local_count && H * I / 2 < (int64_t(1) << 32) - 16 &&
-         std::max(H, I) * 64 < (int64_t(1) << 32) - 16;
+  return max_pairs <= int64_t(32) * d->local_count && H * I / 2 < (int64_t(1) << 32) - 16 &&
+         std::max(H, I) * 32 * int64_t(dtype_bytes(d->dtype)) < (int64_t(1) << 32) - 16;
 }
 
-moe_status launch_packed_skinny(const PackedFfnArgs& a) {
+namespace {
+template <typename T>
+moe_status run(const PackedFfnArgs& a) {
   const moe_layer_desc* d = a.d;
   const int L = d->local_count, H = d->hidden, I = d->intermediate;
   const moe_packed_experts& p = *a.p;
-  bf16_t* h = static_cast<bf16_t*>(a.h);
-  const moe_status st = launch<2>("ffn_gate_up", static_cast<const bf16_t*>(a.x_sorted), a.offsets, p.gate_codes,
-                                  p.gate_scales, p.up_codes, p.up_scales, h, L, I, H, a.max_pairs, a.s);
+  T* h = static_cast<T*>(a.h);
+  const moe_status st = launch<T, 2>("ffn_gate_up", static_cast<const T*>(a.x_sorted), a.offsets, p.gate_codes,
+                                     p.gate_scales, p.up_codes, p.up_scales, h, L, I, H, a.max_pairs, a.s);
   if (st != MOE_OK) return st;
-  return launch<1>("ffn_down", h, a.offsets, p.down_codes, p.down_scales, p.down_codes, p.down_scales,
-                   static_cast<bf16_t*>(a.y_sorted), L, H, I, a.max_pairs, a.s);
+  return launch<T, 1>("ffn_down", h, a.offsets, p.down_codes, p.down_scales, p.down_codes, p.down_scales,
+                      static_cast<T*>(a.y_sorted), L, H, I, a.max_pairs, a.s);
+}
+}  // namespace
+
+moe_status launch_packed_skinny(const PackedFfnArgs& a) {
+  return a.d->dtype == MOE_BF16 ? run<bf16_t>(a) : run<float>(a);
 }
 
 }  // namespace moe

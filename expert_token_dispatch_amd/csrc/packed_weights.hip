@@ -20,6 +20,7 @@
 
 #include "common.h"
 #include "kernels.h"
+#include "packed.h"
 
 namespace moe {
 namespace {
@@ -60,27 +61,10 @@ __device__ __forceinline__ uint32_t encode8(const float* f, uint32_t byte) {
 }
 
 __device__ __forceinline__ void decode8(uint32_t w, uint32_t byte, bf16_t* o) {
-  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-  const float s = __uint_as_float(byte << 23);
-  uint32_t* p = reinterpret_cast<uint32_t*>(o);
-  p[0] = __builtin_bit_cast(uint32_t, (b2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
-  p[1] = __builtin_bit_cast(uint32_t, (b2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
-  p[2] = __builtin_bit_cast(uint32_t, (b2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
-  p[3] = __builtin_bit_cast(uint32_t, (b2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
+  *reinterpret_cast<bf16x8_t*>(o) = decode_frag(w, __uint_as_float(byte << 23));
 }
 __device__ __forceinline__ void decode8(uint32_t w, uint32_t byte, float* o) {
-  typedef float f2 __attribute__((ext_vector_type(2)));
-  const float s = __uint_as_float(byte << 23);
-  f2 v[4];
-  v[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 0);
-  v[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 1);
-  v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 2);
-  v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 3);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    o[2 * i] = v[i].x;
-    o[2 * i + 1] = v[i].y;
-  }
+  decode_f32(w, __uint_as_float(byte << 23), o);
 }
 
 // Weights stored [out, in]: the stack is one run of units of eight weights, a lane
@@ -254,8 +238,8 @@ moe_status launch_unpack(const char* name, const PackArgs& a) {
 }
 
 // ---- the experts' feed-forward on packed weights -------------------------------------
-// bf16 layers read the codes in the products (packed_skinny.hip, packed_gemm.hip).  For
-// float32 layers, and bf16 experts too large for those kernels' 32-bit offsets, the three
+// The products read the codes themselves (packed_skinny.hip for both types, packed_gemm.hip
+// for bf16).  For more float32 rows, and experts too large for those kernels' 32-bit offsets, the three
 // stacks are unpacked into the workspace and the products run on them: the unpacked
 // stacks hold the same values as the codes, so nothing is rounded on the way.
 namespace {

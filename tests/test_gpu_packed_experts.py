@@ -334,3 +334,26 @@ def test_stacks_past_4_gib_are_reached():
         # tiles and waves along K may differ between the two calls: the sums' order, not the values
         a, b = y[:n].double(), alone[:n].double()
         assert float((a - b).norm() / b.norm()) <= 2.0 ** -7
+
+
+# one step of K or several, K cut inside a step, waves along K 1, 2 and 4, 16 or 32 rows a pass
+F32_ROWS = [(32, 32, (1,)), (32, 96, (0, 5, 16)), (288, 160, (17, 0, 3, 40)), (512, 1056, (1, 1)), (2080, 544, (2, 0, 9)),
+            (1024, 2048, (1,)), (160, 1312, (31, 33, 32)), (96, 64, (1, 0, 0, 0, 90, 2)), (544, 96, (7,) * 70)]
+
+
+@pytest.mark.parametrize("H,I,rows", F32_ROWS)
+def test_float32_rows_on_packed_experts(H, I, rows):
+    say(f"[packed ffn] float32 H={H} I={I} rows={rows}")
+    rng = np.random.default_rng(H + I)
+    L, P, spare = len(rows), sum(rows), 3
+    full = {k: packed_stack(rng, L, N, K) for k, N, K in (("gate", I, H), ("up", I, H), ("down", H, I))}
+    x = torch.from_numpy(rng.standard_normal((P + spare, H)).astype(np.float32))
+    y = ffn_packed(x.cuda(), rows, {k: v[:2] for k, v in full.items()}, "f32")
+    assert torch.all(y[P:] == 3.0)
+    got, off = np_of(y).astype(np.float64), np.r_[0, np.cumsum(rows)]
+    for e in range(L):
+        r = slice(off[e], off[e + 1])
+        if rows[e]:
+            ref, bound = ffn_reference(x[r].double().numpy(), [full[k][2][e] for k in ("gate", "up", "down")], "f32")
+            over = np.abs(got[r] - ref) / bound
+            assert over.max() <= 1.0, f"expert {e}: {over.max()} of the bound"
