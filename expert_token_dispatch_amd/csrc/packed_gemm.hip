@@ -7,15 +7,19 @@
 // CU, so that one's epilogue runs beside the other's products.  Where those tiles are too
 // few for the card, a tile has 128 weight rows.
 //
-// A step is 64 k.  Token rows (128 bytes a step) and codes (32 bytes a step) come by direct
-// global->LDS loads into three slots, two steps ahead.  A lane takes 16 bytes of codes, 32 k
+// A step is 64 k.  Token rows (128 bytes a step) come by direct global->LDS loads into three
+// slots, two steps ahead.  Codes (32 bytes a step) too, or, where rows begin at multiples of
+// 64 bytes, two steps at a time into two slots, one stage ahead: half as many loads, each of
+// which fetches its lines anew (SP, steps of a stage of codes.  H 4096, I 14336, 8 experts:
+// 512 rows 329 us with one, 299 with two, 16384 rows 4885 and 4809; H = I = 2880, whose rows
+// of 1440 bytes put every other piece of 64 across a boundary, 2047 rows: 189 and 194).  A lane takes 16 bytes of codes, 32 k
 // under one scale, for its weight row; they become four fragments in registers
 // (v_cvt_scalef32_pk_bf16_fp4, eight a fragment pair, beside eight MFMAs).  The MFMA sums
 // over k in any order: fragment c of lane half g is k = 32 g + 8 c .. of the step in both
 // operands.  The scale bytes come straight to registers, two steps (four bytes) a load.
 //
 // In LDS 16-byte piece c of token row r sits at piece c ^ (r / 2 % 8), piece c of weight row
-// r at c ^ (r / 8 % 2): the reads of 16 rows at one piece cover all banks.
+// r at c ^ (r / 8 % 2), of two steps' four at c ^ (r / 4 % 4): the reads of 16 rows at one piece cover all banks.
 #include <math.h>
 
 #include <algorithm>
@@ -33,19 +37,19 @@ constexpr int BM = 128, BK = 64, kThreads = 256;
 constexpr int kGroup = 4;  // n-tiles per group of the tile order
 constexpr int kXcds = 8;
 
-// BNR: weight rows of a tile, 256 or 128
-template <int NMAT, int BNR>
+// BNR: weight rows of a tile, 256 or 128; SP: steps of a stage of codes, 1 or 2
+template <int NMAT, int BNR, int SP>
 struct Shape {
   static constexpr int NJ = BNR / 128;               // 32-row weight blocks of a wave
-  static constexpr int kSlots = 3;
-  static constexpr int kLdB = BNR / 128;             // 1 KB loads of codes per wave and step
-  static constexpr int kLoads = 4 + kLdB;
-  static constexpr int kStageA = BM * 128, kStage = kStageA + BNR * 32;
+  static constexpr int kSlotsA = 3, kSlotsB = SP == 1 ? 3 : 2;
+  static constexpr int kLdA = 4, kLdB = BNR * SP / 128;  // 1 KB loads per wave and stage: token rows, codes
+  static constexpr int kStageA = BM * 128, kStageB = BNR * 32 * SP, kRing = kSlotsA * kStageA + kSlotsB * kStageB;
   static constexpr int kCols = BNR / NMAT;           // output columns
   static constexpr int kRS = kCols * 2 + 16;         // a row of the output tile in LDS
-  static constexpr int kLds = kSlots * kStage > BM * kRS ? kSlots * kStage : BM * kRS;
+  static constexpr int kLds = kRing > BM * kRS ? kRing : BM * kRS;
   // gate/up: stage rows 0 .. kCols - 1 are gate rows, the others up rows.  Row l of a wave's
   // block j; with one block a wave holds 16 gate rows and the up rows beside them.
+  __device__ static int turn(int r) { return SP == 1 ? (r >> 3) & 1 : (r >> 2) & 3; }  // of weight row r's pieces
   __device__ static int stage_row(int wave, int j, int l) {
     if (NMAT == 1) return wave * 32 * NJ + j * 32 + l;
     if (NJ == 2) return j * kCols + wave * 32 + l;
@@ -118,13 +122,14 @@ __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offsets, i
   return r;
 }
 
-template <int NMAT, int BNR>
+template <int NMAT, int BNR, int SP>
 __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t* __restrict__ offsets,
                                      const uint8_t* __restrict__ q0, const uint8_t* __restrict__ s0,
                                      const uint8_t* __restrict__ q1, const uint8_t* __restrict__ s1,
                                      bf16_t* __restrict__ C, int L, int N, int K, bool by_size, char* lds) {
-  using S = Shape<NMAT, BNR>;
-  constexpr int NJ = S::NJ, kSlots = S::kSlots, kStage = S::kStage, kStageA = S::kStageA;
+  using S = Shape<NMAT, BNR, SP>;
+  constexpr int NJ = S::NJ;
+  char* const lds_b = lds + S::kSlotsA * S::kStageA;
   const int NT = (N + S::kCols - 1) / S::kCols;
   const int total = __builtin_amdgcn_readfirstlane(total_tiles(offsets, L, NT));
   const int per = (total + kXcds - 1) / kXcds;
@@ -139,7 +144,7 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
   const int blocks = (rows + 31) / 32;  // 32-row blocks that have rows
 
   // ---- loads.  Token rows: this wave's 32 (four loads of eight rows); past the segment
-  // they repeat its last row.  Codes: its quarter of the stage rows, 32 a load; gate/up:
+  // they repeat its last row.  Codes: its quarter of the stage rows, 32 / SP a load; gate/up:
   // waves 0 and 1 gate rows, 2 and 3 up rows.  Rows past N repeat row N - 1.  Neither reaches an
   // output that is stored.
   const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
@@ -156,17 +161,17 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
   }
 #pragma unroll
   for (int j = 0; j < S::kLdB; ++j) {
-    const int r = wave * (BNR / 4) + 32 * j + (lane >> 1);  // stage row
+    const int r = wave * (BNR / 4) + 32 / SP * j + lane / (2 * SP);  // stage row
     const int row = min(n0 + r % S::kCols, N - 1);
-    vb[j] = uint32_t(row) * uint32_t(K / 2) + uint32_t(((lane & 1) ^ ((r >> 3) & 1)) * 16);
+    vb[j] = uint32_t(row) * uint32_t(K / 2) + uint32_t(((lane & (2 * SP - 1)) ^ S::turn(r)) * 16);
   }
   const int steps = (K + BK - 1) / BK;
   // K is a multiple of 32: the last step may be half a one; its token pieces past K read as
   // zero (an address behind the buffer), its codes may be whatever follows
   const bool cut = (K & 32) != 0;
-  auto issue = [&](int s) {  // step min(s, steps - 1) into slot s
+  auto issue_a = [&](int s) {  // step min(s, steps - 1) into slot s
     const int st = min(s, steps - 1);
-    char* slot = lds + (s % kSlots) * kStage;
+    char* slot = lds + (s % S::kSlotsA) * S::kStageA;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int c = (lane & 7) ^ (((wave * 32 + 8 * j + (lane >> 3)) >> 1) & 7);
@@ -174,10 +179,14 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(slot + (4 * wave + j) * 1024), 16, vo,
                                                uint32_t(st) * 128u, 0, 0);
     }
+  };
+  auto issue_b = [&](int stage) {  // steps SP stage .., or the last stage there is
+    const int st = min(stage, (steps - 1) / SP);
+    char* slot = lds_b + (stage % S::kSlotsB) * S::kStageB;
 #pragma unroll
     for (int j = 0; j < S::kLdB; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(slot + kStageA + (S::kLdB * wave + j) * 1024), 16, vb[j],
-                                               uint32_t(st) * 32u, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(slot + (S::kLdB * wave + j) * 1024), 16, vb[j],
+                                               uint32_t(st) * (32u * SP), 0, 0);
   };
 
   // ---- this lane's weight rows: stage row of block j, and its scales.  Four bytes are two
@@ -214,29 +223,44 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
   const int sw = (fr >> 1) & 7;
   uint32_t sc[NJ], sn[NJ];
   load_s(0, sc);
-#pragma unroll
-  for (int s = 0; s < kSlots - 1; ++s) issue(s);
+  issue_a(0);
+  issue_b(0);
+  issue_a(1);
+  if (SP == 1) issue_b(1);
   // by the tile's row blocks, so that no branch stands among the products: the operands for
   // the next chunk are read and decoded between them
   const auto run = [&](auto blocks_t) {
     constexpr int MB = decltype(blocks_t)::value;
     for (int s = 0; s < steps; ++s) {
-      // the step's loads have landed: at most the later steps' are left (and any scales, which
-      // only makes the wait longer)
-      MOE_VMCNT(S::kLoads * (kSlots - 2));
+      // the step's loads have landed: behind them only the next step's token rows were issued,
+      // and the codes that the last step asked for (and any scales, which only makes the
+      // wait longer)
+      if ((s & 1) == 0) {
+        MOE_VMCNT(S::kLdA + (SP == 1 ? S::kLdB : 0));
+      } else {
+        MOE_VMCNT(S::kLdA + S::kLdB);
+      }
       MOE_LGKMCNT0();
       block_barrier();
       // the scales first: loads return in order, and behind the refill they would make the
       // wave wait for it
-      if ((s & 1) == 0) load_s(s + 2 < steps ? s + 2 : 0, sn);
-      asm volatile("" ::: "memory");
-      issue(s + kSlots - 1);
-      const char* st = lds + (s % kSlots) * kStage;
+      if ((s & 1) == 0) {
+        load_s(s + 2 < steps ? s + 2 : 0, sn);
+        asm volatile("" ::: "memory");
+      }
+      issue_a(s + 2);
+      if (SP == 1)
+        issue_b(s + 2);
+      else if ((s & 1) == 0)
+        issue_b(s / 2 + 1);
+      const char* st = lds + (s % S::kSlotsA) * S::kStageA;
+      const char* stb = lds_b + (s / SP % S::kSlotsB) * S::kStageB;
+      const int first = s % SP * 2;  // of the lane's pieces of the stage
       u32x4_t w[NJ];
       float f[NJ];
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        w[j] = *reinterpret_cast<const u32x4_t*>(st + kStageA + br[j] * 32 + ((half ^ ((br[j] >> 3) & 1)) * 16));
+        w[j] = *reinterpret_cast<const u32x4_t*>(stb + br[j] * 32 * SP + (((first + half) ^ S::turn(br[j])) * 16));
         f[j] = __uint_as_float(((sc[j] >> (16 * (s & 1) + 8 * half)) & 0xFFu) << 23);
       }
       const auto frag_a = [&](int i, int c) {
@@ -327,21 +351,21 @@ __device__ __forceinline__ void body(const bf16_t* __restrict__ A, const int32_t
   }
 }
 
-template <int NMAT, int BNR>
+template <int NMAT, int BNR, int SP>
 __global__ __launch_bounds__(kThreads, 2) void kernel(const bf16_t* __restrict__ A, const int32_t* __restrict__ offsets,
                                                       const uint8_t* __restrict__ q0, const uint8_t* __restrict__ s0,
                                                       const uint8_t* __restrict__ q1, const uint8_t* __restrict__ s1,
                                                       bf16_t* __restrict__ C, int L, int N, int K, int by_size) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  body<NMAT, BNR>(A, offsets, q0, s0, q1, s1, C, L, N, K, by_size != 0, lds);
+  body<NMAT, BNR, SP>(A, offsets, q0, s0, q1, s1, C, L, N, K, by_size != 0, lds);
 }
 
-template <int NMAT, int BNR>
+template <int NMAT, int BNR, int SP>
 moe_status launch_bnr(const char* name, const bf16_t* A, const int32_t* offsets, const void* q0, const void* s0,
                       const void* q1, const void* s1, bf16_t* C, int L, int N, int K, int64_t max_pairs, bool by_size,
                       hipStream_t s) {
-  using S = Shape<NMAT, BNR>;
-  auto kern = kernel<NMAT, BNR>;
+  using S = Shape<NMAT, BNR, SP>;
+  auto kern = kernel<NMAT, BNR, SP>;
   const hipError_t e =
       hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
   if (e != hipSuccess) return set_error(MOE_ERR_HIP, "%s: LDS attribute: %s", name, hipGetErrorString(e));
@@ -363,9 +387,12 @@ moe_status launch(const char* name, const bf16_t* A, const int32_t* offsets, con
                   const void* q1, const void* s1, bf16_t* C, int L, int N, int K, int64_t max_pairs, hipStream_t s) {
   const int64_t m = max_pairs / BM + std::min<int64_t>(L, max_pairs) / 2;
   const int64_t tiles = m * ((N + 256 / NMAT - 1) / (256 / NMAT));
-  if (tiles >= 256)
-    return launch_bnr<NMAT, 256>(name, A, offsets, q0, s0, q1, s1, C, L, N, K, max_pairs, tiles < 1024, s);
-  return launch_bnr<NMAT, 128>(name, A, offsets, q0, s0, q1, s1, C, L, N, K, max_pairs, true, s);
+  const bool pairs = K % 128 == 0;
+#define MOE_PACKED_TILE(BNR_, SP_, BY_SIZE_) \
+  launch_bnr<NMAT, BNR_, SP_>(name, A, offsets, q0, s0, q1, s1, C, L, N, K, max_pairs, BY_SIZE_, s)
+  if (tiles >= 256) return pairs ? MOE_PACKED_TILE(256, 2, tiles < 1024) : MOE_PACKED_TILE(256, 1, tiles < 1024);
+  return pairs ? MOE_PACKED_TILE(128, 2, true) : MOE_PACKED_TILE(128, 1, true);
+#undef MOE_PACKED_TILE
 }
 
 }  // namespace pk
