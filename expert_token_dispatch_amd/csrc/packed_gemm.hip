@@ -8,18 +8,16 @@
 // few for the card, a tile has 128 weight rows.
 //
 // A step is 64 k.  Token rows (128 bytes a step) come by direct global->LDS loads into three
-// slots, two steps ahead.  Codes (32 bytes a step) too, or, where rows begin at multiples of
-// 64 bytes, two steps at a time into two slots, one stage ahead: half as many loads, each of
-// which fetches its lines anew (SP, steps of a stage of codes.  H 4096, I 14336, 8 experts:
-// 512 rows 329 us with one, 299 with two, 16384 rows 4885 and 4809; H = I = 2880, whose rows
-// of 1440 bytes put every other piece of 64 across a boundary, 2047 rows: 189 and 194).  A lane takes 16 bytes of codes, 32 k
-// under one scale, for its weight row; they become four fragments in registers
+// slots, two steps ahead.  Codes (32 bytes a step) too, or two steps at a time into two slots,
+// one stage ahead, half as many loads (SP, steps of a stage of codes).  A lane takes 16 bytes
+// of codes, 32 k under one scale, for its weight row; they become four fragments in registers
 // (v_cvt_scalef32_pk_bf16_fp4, eight a fragment pair, beside eight MFMAs).  The MFMA sums
 // over k in any order: fragment c of lane half g is k = 32 g + 8 c .. of the step in both
 // operands.  The scale bytes come straight to registers, two steps (four bytes) a load.
 //
 // In LDS 16-byte piece c of token row r sits at piece c ^ (r / 2 % 8), piece c of weight row
-// r at c ^ (r / 8 % 2), of two steps' four at c ^ (r / 4 % 4): the reads of 16 rows at one piece cover all banks.
+// r at c ^ (r / 8 % 2), of two steps' four at c ^ (r / 4 % 4): the reads of 16 rows at one
+// piece cover all banks.
 #include <math.h>
 
 #include <algorithm>
@@ -381,17 +379,20 @@ moe_status launch_bnr(const char* name, const bf16_t* A, const int32_t* offsets,
 
 // Tiles of 256 weight rows, 128 where those would not give every CU one; by size while a CU
 // gets fewer than four, in order from there (a prefill of 16384 pairs on 8 experts: in order
-// -2%; 2047 pairs on 16 experts of very different load: by size -6%).
+// -2%; 2047 pairs on 16 experts of very different load: by size -6%).  From there codes go two
+// steps at a time, where rows begin at multiples of 64 bytes (the same prefill 5150 -> 4998
+// us, 8192 pairs on 8 experts of 4096 x 4096 711 -> 696; with fewer tiles, 8192 pairs on 128
+// experts, H 2048, I 768: 141 -> 154).
 template <int NMAT>
 moe_status launch(const char* name, const bf16_t* A, const int32_t* offsets, const void* q0, const void* s0,
                   const void* q1, const void* s1, bf16_t* C, int L, int N, int K, int64_t max_pairs, hipStream_t s) {
   const int64_t m = max_pairs / BM + std::min<int64_t>(L, max_pairs) / 2;
   const int64_t tiles = m * ((N + 256 / NMAT - 1) / (256 / NMAT));
-  const bool pairs = K % 128 == 0;
 #define MOE_PACKED_TILE(BNR_, SP_, BY_SIZE_) \
   launch_bnr<NMAT, BNR_, SP_>(name, A, offsets, q0, s0, q1, s1, C, L, N, K, max_pairs, BY_SIZE_, s)
-  if (tiles >= 256) return pairs ? MOE_PACKED_TILE(256, 2, tiles < 1024) : MOE_PACKED_TILE(256, 1, tiles < 1024);
-  return pairs ? MOE_PACKED_TILE(128, 2, true) : MOE_PACKED_TILE(128, 1, true);
+  if (tiles >= 1024 && K % 128 == 0) return MOE_PACKED_TILE(256, 2, false);
+  if (tiles >= 256) return MOE_PACKED_TILE(256, 1, tiles < 1024);
+  return MOE_PACKED_TILE(128, 1, true);
 #undef MOE_PACKED_TILE
 }
 
