@@ -357,3 +357,25 @@ def test_float32_rows_on_packed_experts(H, I, rows):
             ref, bound = ffn_reference(x[r].double().numpy(), [full[k][2][e] for k in ("gate", "up", "down")], "f32")
             over = np.abs(got[r] - ref) / bound
             assert over.max() <= 1.0, f"expert {e}: {over.max()} of the bound"
+
+
+# products of so many tiles that codes go two steps a load, one stage of K or several
+MANY_TILES = [(256, 2176, (8200, 0, 100)), (4224, 128, (31, 8300)), (4224, 384, (4000, 4301))]
+
+
+@pytest.mark.parametrize("H,I,rows", MANY_TILES)
+def test_products_of_many_tiles(H, I, rows):
+    say(f"[packed ffn] many tiles H={H} I={I} rows={rows}")
+    rng = np.random.default_rng(H + I)
+    L, P = len(rows), sum(rows)
+    full = {k: packed_stack(rng, L, N, K) for k, N, K in (("gate", I, H), ("up", I, H), ("down", H, I))}
+    x = torch.from_numpy(rng.standard_normal((P, H), dtype=np.float32)).bfloat16()
+    y = ffn_packed(x.cuda(), rows, {k: v[:2] for k, v in full.items()})
+    got, off = np_of(y), np.r_[0, np.cumsum(rows)]
+    for e in range(L):
+        if rows[e]:
+            some = np.unique(np.r_[off[e]:min(off[e] + 130, off[e + 1]), max(off[e], off[e + 1] - 130):off[e + 1],
+                                   rng.integers(off[e], off[e + 1], 100)])
+            ref, bound = ffn_reference(x[some].double().numpy(), [full[k][2][e] for k in ("gate", "up", "down")], "bf16")
+            over = np.abs(got[some].astype(np.float64) - ref) / bound
+            assert over.max() <= 1.0, f"expert {e}: {over.max()} of the bound"
