@@ -15,6 +15,9 @@
 // over k in any order: fragment c of lane half g is k = 32 g + 8 c .. of the step in both
 // operands.  The scale bytes come straight to registers, two steps (four bytes) a load.
 //
+// Many rows are bound by the MFMAs (16384 on 8 experts of 4096 x 14336: 5.0 ms, 1150 TFLOP/s),
+// 64 an expert and fewer by the fetching of codes, 32 bytes a row and step (512 rows: 363 us).
+//
 // In LDS 16-byte piece c of token row r sits at piece c ^ (r / 2 % 8), piece c of weight row
 // r at c ^ (r / 8 % 2), of two steps' four at c ^ (r / 4 % 4): the reads of 16 rows at one
 // piece cover all banks.

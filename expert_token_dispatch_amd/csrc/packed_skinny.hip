@@ -12,7 +12,12 @@
 // any order as long as both operands agree, so MFMA j of a step simply takes the lane's
 // codes 8j .. 8j+7 (k = 32 (l / 16) + 8 j ..) and the token row's elements at the same k.
 // The codes turn into bf16 with their scale applied by v_cvt_scalef32_pk_bf16_fp4, two at
-// a time, exactly; a step is 16 of them and four MFMAs 16x16x32 per stream and 16 rows.
+// a time, exactly; a step is 16 of them and four MFMAs 16x16x32 per stream and 16 rows.  In
+// float32 eight codes are eight MFMAs 16x16x4 instead, in the same places of k.
+//
+// Measured: 512 rows on 128 experts of H 2048, I 768 72 us, 4.5 TB/s of codes; one row on 8
+// of them 13 us, two launches of load latency; float32, 64 rows on 8 experts of 512 x 256 12
+// us (34 with the stacks unpacked first).
 //
 // The weights of the next four steps are in flight in registers while a step is
 // multiplied.  One load brings a row's scales of four steps (lane group g holds step g's

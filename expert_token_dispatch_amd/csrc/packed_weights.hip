@@ -15,7 +15,8 @@
 // as the e8m0 byte, so a byte is used as `byte << 23` (0 is 2^-127, 255 gives NaN),
 // rounds to nearest even and saturates at 6 (both checked on the GPU).
 //
-// Both directions are bound by HBM: (dt + 17/32) bytes per weight each.
+// Both directions are bound by HBM: (dt + 17/32) bytes per weight each (16 x 2880 x 2880 in
+// bfloat16, stored [in, out]: packed in 85 us, 4.0 TB/s, unpacked in 71 us, 4.7 TB/s).
 #include <stdint.h>
 
 #include "common.h"
