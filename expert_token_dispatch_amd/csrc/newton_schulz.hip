@@ -772,7 +772,7 @@ __global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, TileMap map) {
     };
     const __amdgpu_buffer_rsrc_t r0 = rsrc(kSym ? p.v : p.x);
     const __amdgpu_buffer_rsrc_t r1 = rsrc(kSym ? p.u : p.x2);
-    const bool two = KIND == kJoin || (KIND == kApply && p.x2 != nullptr);
+    const bool two = KIND == kJoin || (!kSym && p.x2 != nullptr);
     f32x4_t dc4[NB][4];
 #pragma unroll
     for (int j = 0; j < NB; ++j)
