@@ -18,20 +18,22 @@
 //
 // Rounding.  Small singular values are multiplied by up to a^steps (485 for five usual
 // steps) while the large ones stay near 1, and a rounding of X is relative to the large
-// ones.  In bfloat16 that leaves 1 to 5% of error, in float16 0.1 to 0.6%, nearly all of
-// it from the X of the first steps; A and P may be rounded to float16, for p changes
-// little with them.  So a bf16 layer's products run on float16 operands (the same MFMA
-// rate as bfloat16) scaled by powers of two that keep every value in its normal range,
-// and the X of the first two steps are sums of two float16 (22 bits).  In a phase of three
-// steps only X_0 is such an X.  Phases are at most three steps long, since rounding errors
+// ones.  In bfloat16 that leaves 1 to 5% of error; A and P may be rounded to float16, for
+// their errors turn the singular vectors a little but put nothing into directions that X
+// does not have.  So a bf16 layer's products run on float16 operands (the same MFMA rate as
+// bfloat16) scaled by powers of two, and an X that more than two steps follow is the sum of
+// two float16 (22 bits): one float16 would leave 2^-12 in every direction, a^3 = 41 times
+// that after three steps, whole percents of a matrix with few directions (rank 4, one
+// float16 from the third X on: 0.9% at 5 steps, 10% at 7, 330% at 10; so 0.3, 0.3 and 1.0%,
+// where float32 leaves 1.2).  Phases are at most three steps long, since rounding errors
 // of A grow by up to a^2 a step in the directions where A is small; they average out over
 // the shorter side (simulated error of the result, 0.16% of it the bfloat16 result's own:
 // 0.7% at 64, 0.28% at 128, 0.2% at 512, against 0.18% in single steps), so matrices with a
 // shorter side of up to 128 take single steps, and up to 256 those that are less than twice
-// as long: there a phase has no fewer products to do (128 matrices of 256 x 256: 331 us in
-// phases, 295 in single steps; 32 of 256 x 1024: 228 and 259; 256 of 256 x 512: 712 and
-// 1094).  Float32 layers run on float32 operands in single steps (a phase
-// would double the error).
+// as long, at some cost away from the square (128 matrices of 256 x 256: 327 us in phases, 319
+// in single steps; of 256 x 500: 437 and 548), but not longer ones (32 of 256 x 1024: 224 and
+// 282; 256 of 256 x 512: 740 and 1186).  Float32 layers run on float32 operands in single
+// steps (a phase would double the error).
 #include <math.h>
 
 #include <algorithm>
@@ -74,6 +76,15 @@ bool single_steps(int rows, int cols) {
   return shorter <= 128 || (shorter <= 256 && longer < 2 * shorter);
 }
 
+// Steps of the phase that starts after `done` of them.
+int phase_steps(bool single, int done, int steps) { return std::min(steps - done, single ? 1 : (done == 0 ? 3 : 2)); }
+
+// float16: whether X after `done` steps keeps a low half (X_0 always has one): where more than
+// two follow.  In single steps X_1 always does; two steps still multiply its rounding by a^2 = 12.
+bool keeps_low(bool single, int done, int steps) {
+  return done < steps && (steps - done > 2 || (single && done == 1));
+}
+
 // elements of a matrix that one block of the norm kernel adds up
 constexpr int64_t kNormElems = 16384;
 constexpr int kMaxPartials = 256;
@@ -100,10 +111,11 @@ Plan make_plan(const moe_muon_desc* m) {
   };
   p.o_part = take(size_t(p.count) * p.nblk * sizeof(double));
   p.single = m->dtype == MOE_F32 || single_steps(m->rows, m->cols);
-  // X and the X after it, as they are and transposed, and their low halves: of X_0, in single
-  // steps of X_1 too
+  // X and the X after it, as they are and transposed, and their low halves; the X after X_0 is
+  // the first that may keep one
+  const int first = phase_steps(p.single, 0, m->steps);
   for (int i = 0; i < 4; ++i) {
-    const bool used = i < 2 || (m->dtype == MOE_BF16 && (i == 2 || p.single));
+    const bool used = i < 2 || (m->dtype == MOE_BF16 && (i == 2 || keeps_low(p.single, first, m->steps)));
     p.o_x[i] = take(used ? p.x_bytes : 0);
     p.o_t[i] = take(used ? p.x_bytes : 0);
   }
@@ -267,7 +279,7 @@ struct Product {
   const void* b2;
   void* c;
   void* ct;           // C transposed (kApply)
-  void* c2;           // what C's rounding leaves, and that transposed (kApply on small tiles; or NULL)
+  void* c2;           // what C's rounding leaves, and that transposed (kApply; or NULL)
   void* ct2;
   int ldct;
   size_t sa, sb, sc;  // elements from one matrix of the stack to the next
@@ -734,7 +746,9 @@ __device__ __forceinline__ uint2 pack4(const float* f) {
   return __builtin_bit_cast(uint2, h4{f16_t(f[0]), f16_t(f[1]), f16_t(f[2]), f16_t(f[3])});
 }
 
-template <int NW, int KIND>
+// LOW (kApply): what the rounding of C leaves waits in registers and goes out through the same
+// LDS tile.
+template <int NW, int KIND, bool LOW>
 __global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, TileMap map) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   using S = big::Shape<false, NW>;
@@ -773,6 +787,7 @@ __global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, TileMap map) {
     const __amdgpu_buffer_rsrc_t r0 = rsrc(kSym ? p.v : p.x);
     const __amdgpu_buffer_rsrc_t r1 = rsrc(kSym ? p.u : p.x2);
     const bool two = KIND == kJoin || (!kSym && p.x2 != nullptr);
+    uint2 low[LOW ? 4 : 1][NB][4];
     f32x4_t dc4[NB][4];
 #pragma unroll
     for (int j = 0; j < NB; ++j)
@@ -842,6 +857,12 @@ __global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, TileMap map) {
             *reinterpret_cast<uint2*>(lds + rt * kRS + cl * 2) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
           } else {
             *reinterpret_cast<uint2*>(lds + rt * kRS + cl * 2) = pack4(v);
+            if constexpr (LOW) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] -= float(f16_t(v[e]));
+              low[i][j][q] = pack4(v);
+              asm volatile("" : "+v"(low[i][j][q].x), "+v"(low[i][j][q].y));  // here, not where it is stored: registers
+            }
           }
         }
       }
@@ -871,14 +892,33 @@ __global__ __launch_bounds__(NW * 64) void tile_kernel(Product p, TileMap map) {
       if (kSym ? tm != tn : p.ct != nullptr)
         store_tile_turned<f16_t, BM, BNE, kRS, kThr>(lds, kSym ? c : static_cast<f16_t*>(p.ct) + z * p.sc,
                                                      kSym ? p.ldc : p.ldct, p.m, p.n, row0, n0, tid);
+      if constexpr (LOW) {
+        MOE_LGKMCNT0();
+        block_barrier();  // the high halves are read out
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int rt = wm * 128 + i * 32 + fr, cl = wn * NB * 32 + j * 32 + 8 * q + 4 * g4;
+              *reinterpret_cast<uint2*>(lds + rt * kRS + cl * 2) = low[i][j][q];
+            }
+        MOE_LGKMCNT0();
+        block_barrier();
+        store_tile<f16_t, BM, BNE, kRS, kThr>(lds, static_cast<f16_t*>(p.c2) + z * p.sc, p.ldc, p.m, p.n, row0, n0, tid);
+        if (p.ct2 != nullptr)
+          store_tile_turned<f16_t, BM, BNE, kRS, kThr>(lds, static_cast<f16_t*>(p.ct2) + z * p.sc, p.ldct, p.m, p.n, row0,
+                                                       n0, tid);
+      }
     }
   };
   big::tile_loop<1, false, NW, false, false, big::F16, true>(op, p.n, nk, row0, n0, 0, p.a2 != nullptr ? 2 * nk : nk, lds, epi);
 }
 
-template <int NW, int KIND>
+template <int NW, int KIND, bool LOW>
 moe_status launch_nw(const char* name, const Product& p, int count, hipStream_t s) {
-  auto kern = tile_kernel<NW, KIND>;
+  auto kern = tile_kernel<NW, KIND, LOW>;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, int(kLds));
   if (e != hipSuccess) return set_error(MOE_ERR_HIP, "%s: LDS attribute: %s", name, hipGetErrorString(e));
@@ -891,8 +931,12 @@ moe_status launch_nw(const char* name, const Product& p, int count, hipStream_t 
 // 14336: four are 2.7% faster; K = 768: 6% slower).
 template <int KIND>
 moe_status launch(const char* name, const Product& p, int count, hipStream_t s) {
-  if (p.k / BK >= 64) return launch_nw<4, KIND>(name, p, count, s);
-  return launch_nw<8, KIND>(name, p, count, s);
+  const bool four = p.k / BK >= 64;
+  if constexpr (KIND == kApply) {
+    if (p.c2 != nullptr)
+      return four ? launch_nw<4, KIND, true>(name, p, count, s) : launch_nw<8, KIND, true>(name, p, count, s);
+  }
+  return four ? launch_nw<4, KIND, false>(name, p, count, s) : launch_nw<8, KIND, false>(name, p, count, s);
 }
 
 }  // namespace nsbig
@@ -1070,7 +1114,7 @@ struct Run {
     int cur = 0, done = 0;  // X in x(cur), its low half, if it has one, in x(cur + 2)
     bool split = kSplit;
     while (done < a.m->steps) {
-      const int len = std::min(a.m->steps - done, p.single ? 1 : (done == 0 ? 3 : 2));
+      const int len = phase_steps(p.single, done, a.m->steps);
       // A in 0; Q in 1, P in 2 (Q and what it becomes in 1 and 3), and T = P A in 4
       int Q = 1;
       TRY_NS(gram(cur, q(0)));
@@ -1088,7 +1132,7 @@ struct Run {
         }
       }
       done += len;
-      const bool last = done == a.m->steps, keep = kSplit && p.single && done == 1;
+      const bool last = done == a.m->steps, keep = kSplit && keeps_low(p.single, done, a.m->steps);
       TRY_NS(apply(q(Q), cur, split, last ? -1 : cur ^ 1, keep));
       cur ^= 1;
       split = keep;

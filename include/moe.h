@@ -543,8 +543,12 @@ moe_status moe_muon_workspace_size(const moe_muon_desc* m, size_t* bytes);
 
 /* o = the orthogonalised g, matrix by matrix; eps, steps and coefficients from m, the
  * other fields are not used (but checked).  MOE_BF16: the products run on float16
- * operands scaled by powers of two (X_0 as the sum of two) with float32 sums, the
- * result is rounded once.  MOE_F32: float32 throughout.  o may be g.
+ * operands scaled by powers of two (every X that more than two steps follow as the sum
+ * of two, 22 bits) with float32 sums, the result is rounded once.  MOE_F32: float32
+ * throughout.  o may be g.
+ * A singular value near zero grows a-fold a step, and so does what a rounding leaves in
+ * a direction that the matrix does not have: 485-fold in five usual steps, 230000-fold in
+ * ten, where float32 itself is 1 to 4% off on a matrix of few directions.
  *   g   device [count, rows, cols] dtype;  o  device [count, rows, cols] dtype out
  *   ws  device workspace of moe_muon_workspace_size bytes */
 moe_status moe_orthogonalize(const moe_muon_desc* m, const void* g, void* o, void* ws, size_t ws_bytes, void* stream);
