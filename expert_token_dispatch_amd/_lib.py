@@ -427,22 +427,36 @@ def moe_packed_workspace_size(d: LayerDesc, stage: int) -> int:
     return n.value
 
 
-def _packed(v) -> Optional[int]:
-    return None if v is None else ctypes.addressof(v)
+def _packed(d, v) -> Optional[int]:
+    """The struct's address; its tensors have to be the stacks that d describes, since the kernels
+    take every extent from d."""
+    import torch
+    if v is None:
+        return None
+    t = getattr(v, "_tensors", None)  # none: a struct of the caller's own pointers
+    for name, out, in_ in (("gate", d.intermediate, d.hidden), ("up", d.intermediate, d.hidden),
+                           ("down", d.hidden, d.intermediate)):
+        for field, last in ((name + "_codes", in_ // 2), (name + "_scales", in_ // 32)):
+            want = (d.local_count, out, last)
+            if t is not None and (t[field].dtype != torch.uint8 or tuple(t[field].shape) != want):
+                raise ValueError(f"{field} of this layer is a uint8 tensor {want}")
+    return ctypes.addressof(v)
 
 
 def moe_grouped_ffn_packed(d, x_sorted, offsets, packed, y_sorted, ws=None, stream=None) -> None:
+    pk = _packed(d, packed)
     wp, wn = _ws(ws)
-    _check(lib().moe_grouped_ffn_packed(ctypes.byref(d), _p(x_sorted), _p(offsets), _packed(packed), _p(y_sorted),
-                                        wp, wn, _s(stream)))
+    _check(lib().moe_grouped_ffn_packed(ctypes.byref(d), _p(x_sorted), _p(offsets), pk, _p(y_sorted), wp, wn,
+                                        _s(stream)))
 
 
 def moe_layer_forward_packed(d, opts, x, w_router, b_router, packed, y, ws, topk_ids_out=None, topk_w_out=None,
                              counts_out=None, num_dropped_out=None, stream=None) -> None:
+    pk = _packed(d, packed)
     wp, wn = _ws(ws)
-    _check(lib().moe_layer_forward_packed(ctypes.byref(d), _opts(opts), _p(x), _p(w_router), _p(b_router),
-                                          _packed(packed), _p(y), _p(topk_ids_out), _p(topk_w_out), _p(counts_out),
-                                          _p(num_dropped_out), wp, wn, _s(stream)))
+    _check(lib().moe_layer_forward_packed(ctypes.byref(d), _opts(opts), _p(x), _p(w_router), _p(b_router), pk, _p(y),
+                                          _p(topk_ids_out), _p(topk_w_out), _p(counts_out), _p(num_dropped_out), wp, wn,
+                                          _s(stream)))
 
 
 # ---- training: the weight update -----------------------------------------------------------
