@@ -244,13 +244,16 @@ class MoELayer:
         """One Muon step on the expert weights, in place, from backward()'s gradients and muon_state().
         update_scale: factor of the orthogonalised update, by default 0.2 sqrt(longer side), which
         gives its entries the size of an Adam step's."""
+        descs = {}
         for n in self.MUON_WEIGHTS:
-            w = getattr(self, n)
-            scale = 0.2 * max(w.shape[1:]) ** 0.5 if update_scale is None else update_scale
-            m = L.make_muon_desc(*w.shape, dtype=self.dtype, steps=steps, momentum=momentum, nesterov=nesterov, lr=lr,
-                                 update_scale=scale, weight_decay=weight_decay)
-            size = L.moe_muon_workspace_size(m)
-            ws = self._ws.get("muon")
-            if ws is None or ws.numel() < size:  # one workspace for the three stacks, which follow each other
-                ws = self._ws["muon"] = torch.empty(size, dtype=torch.uint8, device=self.device)
-            L.moe_muon_update(m, grads["d" + n], state["momentum"][n], w, ws, master=state["master"].get(n))
+            shape = getattr(self, n).shape
+            scale = 0.2 * max(shape[1:]) ** 0.5 if update_scale is None else update_scale
+            descs[n] = L.make_muon_desc(*shape, dtype=self.dtype, steps=steps, momentum=momentum, nesterov=nesterov, lr=lr,
+                                        update_scale=scale, weight_decay=weight_decay)
+        key = ("muon", steps)  # one workspace for the three stacks, which follow each other; never replaced
+        if key not in self._ws:
+            size = max(L.moe_muon_workspace_size(m) for m in descs.values())
+            self._ws[key] = torch.empty(size, dtype=torch.uint8, device=self.device)
+        ws = self._ws[key]
+        for n, m in descs.items():
+            L.moe_muon_update(m, grads["d" + n], state["momentum"][n], getattr(self, n), ws, master=state["master"].get(n))
