@@ -112,12 +112,13 @@ Plan make_plan(const moe_muon_desc* m) {
   p.o_part = take(size_t(p.count) * p.nblk * sizeof(double));
   p.single = m->dtype == MOE_F32 || single_steps(m->rows, m->cols);
   // X and the X after it, as they are and transposed, and their low halves; the X after X_0 is
-  // the first that may keep one
+  // the first that may keep one.  A low half is read as X is added (as it is) and as the operand
+  // of an application: as it is for a tall matrix, else transposed.
   const int first = phase_steps(p.single, 0, m->steps);
   for (int i = 0; i < 4; ++i) {
     const bool used = i < 2 || (m->dtype == MOE_BF16 && (i == 2 || keeps_low(p.single, first, m->steps)));
     p.o_x[i] = take(used ? p.x_bytes : 0);
-    p.o_t[i] = take(used ? p.x_bytes : 0);
+    p.o_t[i] = take(used && (i < 2 || !p.tall) ? p.x_bytes : 0);
   }
   for (int i = 0; i < (p.single ? 2 : 5); ++i) {
     p.o_q[i] = take(p.q_bytes);
