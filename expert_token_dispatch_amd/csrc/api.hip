@@ -99,7 +99,8 @@ size_t ffn_h_bytes(const moe_layer_desc* d) {
   return align_up(size_t(max_pairs_of(d)) * d->intermediate * dtype_bytes(d->dtype), 256);
 }
 
-// Layout of the moe_layer_forward workspace.
+// Layout of the moe_layer_forward workspace, or of the packed layer's (which brings the scratch of
+// its own feed-forward).
 struct LayerWs {
   int32_t* topk_ids;
   float* topk_w;
@@ -118,7 +119,7 @@ struct LayerWs {
   size_t bytes;
 };
 
-LayerWs layer_layout(const moe_layer_desc* d, void* base) {
+LayerWs layer_layout(const moe_layer_desc* d, void* base, bool packed = false) {
   const int64_t n = d->num_tokens * d->top_k;
   const int64_t pm = max_pairs_of(d);
   const size_t dt = dtype_bytes(d->dtype);
@@ -142,7 +143,7 @@ LayerWs layer_layout(const moe_layer_desc* d, void* base) {
   w.dispatch = take(dispatch_scratch_bytes(d));
   w.x_sorted = take(size_t(pm) * d->hidden * dt);
   w.h = take(size_t(pm) * d->intermediate * dt);
-  const size_t fb = ffn_scratch_bytes(d, pm);
+  const size_t fb = packed ? packed_ffn_scratch_bytes(d, pm) : ffn_scratch_bytes(d, pm);
   w.ffn_scratch = fb ? take(fb) : nullptr;
   w.y_sorted = take(size_t(pm) * d->hidden * dt);
   w.bytes = o;
@@ -182,23 +183,8 @@ LayerBwdWs layer_bwd_layout(const moe_layer_desc* d, void* base) {
   return w;
 }
 
-// The packed layer: the layer's workspace with the packed feed-forward's scratch behind it.
-struct LayerPackedWs {
-  LayerWs w;
-  void* scratch;
-  size_t bytes;
-};
-
-LayerPackedWs layer_packed_layout(const moe_layer_desc* d, void* base) {
-  LayerPackedWs r{};
-  r.w = layer_layout(d, base);
-  r.scratch = base ? static_cast<char*>(base) + r.w.bytes : nullptr;
-  r.bytes = r.w.bytes + align_up(packed_ffn_scratch_bytes(d, max_pairs_of(d)), 256);
-  return r;
-}
-
 size_t packed_stage_bytes(const moe_layer_desc* d, int32_t stage) {
-  if (stage == MOE_STAGE_LAYER) return layer_packed_layout(d, nullptr).bytes;
+  if (stage == MOE_STAGE_LAYER) return layer_layout(d, nullptr, true).bytes;
   return ffn_h_bytes(d) + align_up(packed_ffn_scratch_bytes(d, max_pairs_of(d)), 256);
 }
 
@@ -979,8 +965,7 @@ moe_status moe_layer_forward_packed(const moe_layer_desc* d, const moe_route_opt
   TRY(packed_desc_checks(d));
   if (d->num_tokens == 0) return MOE_OK;
   TRY(check_ws_bytes(packed_stage_bytes(d, MOE_STAGE_LAYER), ws, ws_bytes));
-  const LayerPackedWs lp = layer_packed_layout(d, ws);
-  const LayerWs& w = lp.w;
+  const LayerWs w = layer_layout(d, ws, true);
   int32_t* ids = topk_ids_out ? topk_ids_out : w.topk_ids;
   float* tw = topk_w_out ? topk_w_out : w.topk_w;
   int32_t* counts = counts_out ? counts_out : w.counts;
@@ -1000,7 +985,7 @@ moe_status moe_layer_forward_packed(const moe_layer_desc* d, const moe_route_opt
   DispatchArgs da{d, x, ids, w.topk_logit, counts, w.offsets, w.sorted_pairs, w.pair_row, w.x_sorted, dropped,
                   scr, capacity_of(d), true, s};
   TRY(launch_dispatch(da));
-  PackedFfnArgs fa{d, w.x_sorted, w.offsets, packed, w.y_sorted, w.h, lp.scratch, max_pairs_of(d), s};
+  PackedFfnArgs fa{d, w.x_sorted, w.offsets, packed, w.y_sorted, w.h, w.ffn_scratch, max_pairs_of(d), s};
   TRY(launch_packed_ffn(fa));
   CombineArgs ca{d, w.y_sorted, w.pair_row, tw, y, s};
   return launch_combine(ca);
