@@ -338,7 +338,8 @@ moe_status moe_layer_forward_ex(const moe_layer_desc* d, const moe_route_opts* o
 /*           NaN                                                             */
 /* always by output, whatever layout the weights they come from have.  A     */
 /* weight is value * 2^(b - 127), exact in bfloat16 and in float32 (one       */
-/* below 2^-126 in magnitude may be taken as zero).                           */
+/* below 2^-126 in magnitude may be taken as zero, one from 2^128 on is       */
+/* infinite; packing makes neither infinities nor, of finite weights, NaN).   */
 /* ======================================================================== */
 
 /* Packs a stack of `count` matrices.  Per 32 inputs of one output the scale is
@@ -546,6 +547,11 @@ moe_status moe_muon_workspace_size(const moe_muon_desc* m, size_t* bytes);
  * operands scaled by powers of two (every X that more than two steps follow as the sum
  * of two, 22 bits) with float32 sums, the result is rounded once.  MOE_F32: float32
  * throughout.  o may be g.
+ * MOE_BF16 results are 0.2 to 0.6% of their norm off in five usual steps, 0.16% of it
+ * their own rounding, on gradients of many directions and of few; up to 4% where the
+ * entries take few values (one column repeated, say), so that roundings are alike and
+ * add up.  An entry of X_0 below 2^-38 is lost, and with it a matrix whose norm is less
+ * than about 1e-9 eps.
  * A singular value near zero grows a-fold a step, and so does what a rounding leaves in
  * a direction that the matrix does not have: 485-fold in five usual steps, 230000-fold in
  * ten, where float32 itself is 1 to 4% off on a matrix of few directions.
