@@ -385,7 +385,9 @@ moe_status launch_bnr(const char* name, const bf16_t* A, const int32_t* offsets,
 // -2%; 2047 pairs on 16 experts of very different load: by size -6%).  From there codes go two
 // steps at a time, where rows begin at multiples of 64 bytes (the same prefill 5150 -> 4998
 // us, 8192 pairs on 8 experts of 4096 x 4096 711 -> 696; with fewer tiles, 8192 pairs on 128
-// experts, H 2048, I 768: 141 -> 154).
+// experts, H 2048, I 768: 141 -> 154).  Tiles are counted from the most rows that the
+// descriptor allows; where a rank holds part of the experts fewer arrive, and the choice is the
+// one for more of them.
 template <int NMAT>
 moe_status launch(const char* name, const bf16_t* A, const int32_t* offsets, const void* q0, const void* s0,
                   const void* q1, const void* s1, bf16_t* C, int L, int N, int K, int64_t max_pairs, hipStream_t s) {

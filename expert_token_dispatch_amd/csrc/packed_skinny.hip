@@ -19,11 +19,12 @@
 // of them 13 us, two launches of load latency; float32, 64 rows on 8 experts of 512 x 256 12
 // us (34 with the stacks unpacked first).
 //
-// The weights of the next four steps are in flight in registers while a step is
-// multiplied.  One load brings a row's scales of four steps (lane group g holds step g's
-// four bytes, handed round by a lane permute).  The token rows go through LDS, a chunk of
-// four steps per wave at a time, double buffered: read straight from memory, 64 bytes a
-// lane and step, they would take the address units longer than the weights.
+// A chunk of K is four steps of a wave, two where four waves share K, and half as many in
+// float32.  The weights of so many steps are in flight in registers while one is multiplied.
+// One load brings a row's scales of a chunk (lane group g holds step g's four bytes, handed
+// round by a lane permute).  The token rows go through LDS, a chunk at a time, double
+// buffered: read straight from memory, 64 bytes a lane and step, they would take the address
+// units longer than the weights.
 #include <math.h>
 
 #include <algorithm>
@@ -299,12 +300,8 @@ moe_status launch_wk(const char* name, const T* A, const int32_t* offsets, const
   constexpr int kBuf = 16 * NRB * Chunk<T, WK>::kRowBytes;
   constexpr int kRed = 4 * 2 * NRB * 1024;  // an upper bound of the waves' sums
   static_assert(kRed <= kBuf, "the sums fit in one buffer");
+  static_assert(2 * kBuf <= 64 * 1024, "the dynamic LDS that a launch may have without an attribute");
   const int lds = K > Chunk<T, WK>::kK ? 2 * kBuf : kBuf;
-  if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, 2 * kBuf);
-    if (e != hipSuccess) return set_error(MOE_ERR_HIP, "%s: LDS attribute: %s", name, hipGetErrorString(e));
-  }
   MOE_LAUNCH(name, kern, grid, dim3(kThreads), lds, s, A, offsets, static_cast<const uint8_t*>(q0),
              static_cast<const uint8_t*>(s0), static_cast<const uint8_t*>(q1), static_cast<const uint8_t*>(s1), C, L, N,
              K);
@@ -312,7 +309,9 @@ moe_status launch_wk(const char* name, const T* A, const int32_t* offsets, const
 }
 
 // Waves along K: as many as it takes for two blocks a CU, given the experts that can have
-// rows, while every wave keeps two steps.
+// rows, while every wave keeps two steps.  As in the choice of the kernel, rows are the
+// most that the descriptor allows (T * top_k without a capacity): a rank that holds part of
+// the experts is sent fewer.
 template <typename T, int NMAT>
 moe_status launch(const char* name, const T* A, const int32_t* offsets, const void* q0, const void* s0,
                   const void* q1, const void* s1, T* C, int L, int N, int K, int64_t max_pairs, hipStream_t s) {
@@ -332,7 +331,7 @@ moe_status launch(const char* name, const T* A, const int32_t* offsets, const vo
 }  // namespace
 
 bool packed_skinny_fits(const moe_layer_desc* d, int64_t max_pairs) {
-  // Up to 32 rows an expert, one pass of the kernel: past that the tiles of packed_gemm.hip
+  // Up to 32 rows an expert on average, one pass of the kernel: past that the tiles of packed_gemm.hip
   // win (16 experts, H = I = 2880, 1024 rows: 112 us here, 95 there), in float32 the unpacked
   // products (8 experts, 1024 x 1024, 512 rows: 92 and 89 us; one expert: 686 and 68).
   // An expert's codes and 32 of its rows are addressed with 32-bit byte offsets.
