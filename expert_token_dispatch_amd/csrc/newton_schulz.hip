@@ -25,7 +25,10 @@
 // two float16 (22 bits): one float16 would leave 2^-12 in every direction, a^3 = 41 times
 // that after three steps, whole percents of a matrix with few directions (rank 4, one
 // float16 from the third X on: 0.9% at 5 steps, 10% at 7, 330% at 10; so 0.3, 0.3 and 1.0%,
-// where float32 leaves 1.2).  Phases are at most three steps long, since rounding errors
+// where float32 leaves 1.2).  A is formed from the high half alone: what that leaves out
+// averages out along K, as the roundings of P and Q do over the entries (1.5% in phases for
+// one row of 700 x 520, up to 4% where all entries are alike, 0.3 to 0.6% for random vectors'
+// products).  Phases are at most three steps long, since rounding errors
 // of A grow by up to a^2 a step in the directions where A is small; they average out over
 // the shorter side (simulated error of the result, 0.16% of it the bfloat16 result's own:
 // 0.7% at 64, 0.28% at 128, 0.2% at 512, against 0.18% in single steps), so matrices with a

@@ -549,9 +549,9 @@ moe_status moe_muon_workspace_size(const moe_muon_desc* m, size_t* bytes);
  * throughout.  o may be g.
  * MOE_BF16 results are 0.2 to 0.6% of their norm off in five usual steps, 0.16% of it
  * their own rounding, on gradients of many directions and of few; up to 4% where the
- * entries take few values (one column repeated, say), so that roundings are alike and
- * add up.  An entry of X_0 below 2^-39 is lost, and so is a matrix whose norm is some
- * 1e-8 eps or less.
+ * entries take few values (one column repeated, say) or stand in one row or column, so
+ * that roundings do not average out.  An entry of X_0 below 2^-39 is lost, and so is a
+ * matrix whose norm is some 1e-8 eps or less.
  * A singular value near zero grows a-fold a step, and so does what a rounding leaves in
  * a direction that the matrix does not have: 485-fold in five usual steps, 230000-fold in
  * ten, where float32 itself is 1 to 4% off on a matrix of few directions.
