@@ -12,6 +12,8 @@ lib_path = os.path.join(PKG, "libmoe.so")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = 0, -1, -2, -3, -4
 MOE_F32, MOE_BF16 = 0, 1
 MOE_WEIGHTS_OUT_IN, MOE_WEIGHTS_IN_OUT = 0, 1
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_ELEMENT = 0, 1, 2, 3
+MOE_GATE_LINEAR, MOE_GATE_SIGMOID = 0, 1
 MOE_STAGE_ROUTE, MOE_STAGE_DISPATCH, MOE_STAGE_FFN, MOE_STAGE_COMBINE, MOE_STAGE_LAYER = 0, 1, 2, 3, 4
 MOE_STAGE_FFN_BACKWARD, MOE_STAGE_ROUTE_BACKWARD, MOE_STAGE_LAYER_BACKWARD = 5, 6, 7
 
@@ -81,6 +83,21 @@ class MuonDesc(ctypes.Structure):
     ]
 
 
+class JoinDesc(ctypes.Structure):
+    """moe_join_desc: the join of a block with the residual stream (include/moe.h)."""
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("hidden", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("post_norm", ctypes.c_int32),
+        ("gate_kind", ctypes.c_int32),
+        ("gate_act", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("weight_offset", ctypes.c_float),
+        ("residual_scale", ctypes.c_float),
+    ]
+
+
 def make_saved(t: dict) -> Saved:
     """t: a dict of device tensors under the moe_saved field names.  The struct
     keeps a reference to the dict, so the pointers stay valid while it lives."""
@@ -129,12 +146,27 @@ def make_muon_desc(count: int, rows: int, cols: int, dtype="bf16", steps: int = 
                     weight_decay)
 
 
+def make_join_desc(rows: int, hidden: int, dtype="bf16", post_norm: bool = False, gate="none", gate_act="linear",
+                   eps: float = 1e-6, weight_offset: float = 0.0, residual_scale: float = 1.0) -> JoinDesc:
+    """gate: "none", "channel" [H], "token" [rows] float32 or "element" [rows, H]; gate_act: "linear" or
+    "sigmoid" (or the MOE_GATE_* values)."""
+    if isinstance(dtype, str):
+        dtype = {"bf16": MOE_BF16, "f32": MOE_F32}[dtype]
+    if isinstance(gate, str):
+        gate = {"none": MOE_GATE_NONE, "channel": MOE_GATE_CHANNEL, "token": MOE_GATE_TOKEN,
+                "element": MOE_GATE_ELEMENT}[gate]
+    if isinstance(gate_act, str):
+        gate_act = {"linear": MOE_GATE_LINEAR, "sigmoid": MOE_GATE_SIGMOID}[gate_act]
+    return JoinDesc(rows, hidden, dtype, int(post_norm), gate, gate_act, eps, weight_offset, residual_scale)
+
+
 _LIB = None
 _VP = ctypes.c_void_p
 _DP = ctypes.POINTER(LayerDesc)
 _OP = ctypes.c_void_p  # moe_route_opts*, NULL allowed
 _PP = ctypes.c_void_p  # moe_packed_experts*
 _MP = ctypes.POINTER(MuonDesc)
+_JP = ctypes.POINTER(JoinDesc)
 
 
 def lib() -> ctypes.CDLL:
@@ -189,6 +221,10 @@ def lib() -> ctypes.CDLL:
             "moe_muon_workspace_size": (st, [_MP, ctypes.POINTER(ctypes.c_size_t)]),
             "moe_orthogonalize": (st, [_MP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
             "moe_muon_update": (st, [_MP, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
+            "moe_block_join": (st, [_JP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+            "moe_join_workspace_size": (st, [_JP, ctypes.POINTER(ctypes.c_size_t)]),
+            "moe_block_join_backward": (st, [_JP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
+                                             ctypes.c_size_t, _VP]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -484,3 +520,51 @@ def moe_muon_update(m, grad, momentum, weight, ws, master=None, stream=None) -> 
     _muon_shapes(m, ("momentum", "master"), grad=grad, momentum=momentum, weight=weight, master=master)
     wp, wn = _ws(ws)
     _check(lib().moe_muon_update(ctypes.byref(m), _p(grad), _p(momentum), _p(master), _p(weight), wp, wn, _s(stream)))
+
+
+# ---- the join with the residual stream ------------------------------------------------------
+def _expect(what, name, t, shape, dtype) -> None:
+    """A tensor that a call describes by its descriptor: the kernels take every extent from there."""
+    import torch
+    if t is None:
+        return
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} of this {what} is a {dtype} tensor {shape}")
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _join_shapes(j, rows, weights, gates) -> None:
+    import torch
+    dt = torch.bfloat16 if j.dtype == MOE_BF16 else torch.float32
+    for name, t in rows.items():
+        _expect("join", name, t, (j.rows, j.hidden), dt)
+    for name, t in weights.items():
+        _expect("join", name, t, (j.hidden,), dt)
+    shape, gdt = {MOE_GATE_CHANNEL: ((j.hidden,), dt), MOE_GATE_TOKEN: ((j.rows,), torch.float32),
+                  MOE_GATE_ELEMENT: ((j.rows, j.hidden), dt)}.get(j.gate_kind, (None, None))
+    for name, t in gates.items():
+        if shape is not None:
+            _expect("join", name, t, shape, gdt)
+
+
+def moe_block_join(j, x, y, gate, w_post, w_pre, z, h, stream=None) -> None:
+    _join_shapes(j, {"x": x, "y": y, "z": z, "h": h}, {"w_post": w_post, "w_pre": w_pre}, {"gate": gate})
+    _check(lib().moe_block_join(ctypes.byref(j), _p(x), _p(y), _p(gate), _p(w_post), _p(w_pre), _p(z), _p(h),
+                                _s(stream)))
+
+
+def moe_join_workspace_size(j: JoinDesc) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_join_workspace_size(ctypes.byref(j), ctypes.byref(n)))
+    return n.value
+
+
+def moe_block_join_backward(j, z, y, gate, w_post, w_pre, dz, dh, dx, dy, dgate, dw_post, dw_pre, ws,
+                            stream=None) -> None:
+    _join_shapes(j, {"z": z, "y": y, "dz": dz, "dh": dh, "dx": dx, "dy": dy},
+                 {"w_post": w_post, "w_pre": w_pre, "dw_post": dw_post, "dw_pre": dw_pre}, {"gate": gate, "dgate": dgate})
+    wp, wn = _ws(ws)
+    _check(lib().moe_block_join_backward(ctypes.byref(j), _p(z), _p(y), _p(gate), _p(w_post), _p(w_pre), _p(dz),
+                                         _p(dh), _p(dx), _p(dy), _p(dgate), _p(dw_post), _p(dw_pre), wp, wn,
+                                         _s(stream)))

@@ -417,6 +417,52 @@ MuonArgs muon_args(const moe_muon_desc* m, void* ws, void* stream) {
   return a;
 }
 
+moe_status join_desc_checks(const moe_join_desc* j) {
+  if (j == nullptr) return set_error(MOE_ERR_INVALID_ARG, "descriptor is NULL");
+  if (j->rows < 0) return set_error(MOE_ERR_INVALID_ARG, "rows must be >= 0 (got %lld)", (long long)j->rows);
+  if (j->rows > INT32_MAX) return set_error(MOE_ERR_UNSUPPORTED, "rows must be below 2^31");
+  if (j->hidden <= 0 || j->hidden % 8 != 0)
+    return set_error(MOE_ERR_INVALID_ARG, "hidden must be a positive multiple of 8 (got %d)", j->hidden);
+  if (j->dtype != MOE_F32 && j->dtype != MOE_BF16) return set_error(MOE_ERR_INVALID_ARG, "unknown dtype %d", j->dtype);
+  if (size_t(j->hidden) * dtype_bytes(j->dtype) > size_t(kJoinMaxRowBytes))
+    return set_error(MOE_ERR_UNSUPPORTED, "rows of more than %d bytes are not supported (hidden %d)", kJoinMaxRowBytes,
+                     j->hidden);
+  if (j->post_norm != 0 && j->post_norm != 1)
+    return set_error(MOE_ERR_INVALID_ARG, "post_norm must be 0 or 1 (got %d)", j->post_norm);
+  if (j->gate_kind < MOE_GATE_NONE || j->gate_kind > MOE_GATE_ELEMENT)
+    return set_error(MOE_ERR_INVALID_ARG, "unknown gate_kind %d", j->gate_kind);
+  if (j->gate_act != MOE_GATE_LINEAR && j->gate_act != MOE_GATE_SIGMOID)
+    return set_error(MOE_ERR_INVALID_ARG, "unknown gate_act %d", j->gate_act);
+  if (!(std::isfinite(j->eps) && j->eps > 0.f)) return set_error(MOE_ERR_INVALID_ARG, "eps must be finite and > 0");
+  if (!std::isfinite(j->weight_offset) || !std::isfinite(j->residual_scale))
+    return set_error(MOE_ERR_INVALID_ARG, "weight_offset and residual_scale must be finite");
+  return MOE_OK;
+}
+
+// `out` is given exactly where `in` is
+#define REQUIRE_BOTH(out, in, a)                                                                            \
+  do {                                                                                                      \
+    if (((out) == nullptr) != ((in) == nullptr))                                                            \
+      return set_error(MOE_ERR_INVALID_ARG, "%s and %s: give both or neither", #out, #in);                  \
+    OPTIONAL_PTR(out, a);                                                                                   \
+  } while (0)
+
+// What the forward and the backward take alike.
+moe_status join_operand_checks(const moe_join_desc* j, const void* y, const void* gate, const void* w_post,
+                               const void* w_pre) {
+  if (y == nullptr && (j->post_norm || j->gate_kind != MOE_GATE_NONE))
+    return set_error(MOE_ERR_INVALID_ARG, "without y post_norm has to be 0 and gate_kind MOE_GATE_NONE");
+  OPTIONAL_PTR(y, 16);
+  if ((gate == nullptr) != (j->gate_kind == MOE_GATE_NONE))
+    return set_error(MOE_ERR_INVALID_ARG, "gate is %s and gate_kind %d", gate == nullptr ? "NULL" : "given", j->gate_kind);
+  OPTIONAL_PTR(gate, j->gate_kind == MOE_GATE_TOKEN ? 4 : 16);
+  if (!j->post_norm && w_post != nullptr)
+    return set_error(MOE_ERR_INVALID_ARG, "w_post is given and post_norm is 0");
+  OPTIONAL_PTR(w_post, 16);
+  OPTIONAL_PTR(w_pre, 16);
+  return MOE_OK;
+}
+
 moe_status saved_checks(const moe_saved* v) {
   if (v == nullptr) return set_error(MOE_ERR_INVALID_ARG, "saved is NULL");
   REQUIRE_PTR(v->topk_ids, 4);
@@ -1025,6 +1071,61 @@ moe_status moe_muon_update(const moe_muon_desc* m, const void* grad, float* mome
   a.master = master;
   a.out = weight;
   return launch_muon(a);
+}
+
+moe_status moe_block_join(const moe_join_desc* j, const void* x, const void* y, const void* gate, const void* w_post,
+                          const void* w_pre, void* z, void* h, void* stream) {
+  CallScope scope;
+  TRY(join_desc_checks(j));
+  if (j->rows == 0) return MOE_OK;
+  REQUIRE_PTR(x, 16);
+  TRY(join_operand_checks(j, y, gate, w_post, w_pre));
+  REQUIRE_BOTH(z, y, 16);
+  OPTIONAL_PTR(h, 16);
+  if (h == nullptr && (y == nullptr || w_pre != nullptr))
+    return set_error(MOE_ERR_INVALID_ARG, "h is NULL and %s", y == nullptr ? "y too" : "w_pre is given");
+  JoinArgs a{j, x, y, gate, w_post, w_pre, z, h, static_cast<hipStream_t>(stream)};
+  return launch_join(a);
+}
+
+moe_status moe_join_workspace_size(const moe_join_desc* j, size_t* bytes) {
+  TRY(join_desc_checks(j));
+  if (bytes == nullptr) return set_error(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = join_workspace_bytes(j);
+  return MOE_OK;
+}
+
+moe_status moe_block_join_backward(const moe_join_desc* j, const void* z, const void* y, const void* gate,
+                                   const void* w_post, const void* w_pre, const void* dz, const void* dh, void* dx,
+                                   void* dy, void* dgate, void* dw_post, void* dw_pre, void* ws, size_t ws_bytes,
+                                   void* stream) {
+  CallScope scope;
+  TRY(join_desc_checks(j));
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  REQUIRE_BOTH(dw_post, w_post, 16);
+  REQUIRE_BOTH(dw_pre, w_pre, 16);
+  if (j->rows == 0) {
+    const size_t n = size_t(j->hidden) * dtype_bytes(j->dtype);
+    if (dw_post != nullptr) TRY(launch_zero("block_join_bwd_zero", dw_post, n, s));
+    if (dw_pre != nullptr) TRY(launch_zero("block_join_bwd_zero", dw_pre, n, s));
+    if (j->gate_kind != MOE_GATE_CHANNEL) return MOE_OK;
+    REQUIRE_PTR(dgate, 16);
+    return launch_zero("block_join_bwd_zero", dgate, n, s);
+  }
+  TRY(join_operand_checks(j, y, gate, w_post, w_pre));
+  OPTIONAL_PTR(dz, 16);
+  OPTIONAL_PTR(dh, 16);
+  if (dh != nullptr) {
+    REQUIRE_PTR(z, 16);
+  } else if (dz == nullptr || w_pre != nullptr) {
+    return set_error(MOE_ERR_INVALID_ARG, "dh is NULL and %s", dz == nullptr ? "dz too" : "w_pre is given");
+  }
+  REQUIRE_PTR(dx, 16);
+  REQUIRE_BOTH(dy, y, 16);
+  REQUIRE_BOTH(dgate, gate, j->gate_kind == MOE_GATE_TOKEN ? 4 : 16);
+  TRY(check_ws_bytes(join_workspace_bytes(j), ws, ws_bytes));
+  JoinBwdArgs a{j, z, y, gate, w_post, w_pre, dz, dh, dx, dy, dgate, dw_post, dw_pre, ws, s};
+  return launch_join_backward(a);
 }
 
 }  // extern "C"

@@ -1,0 +1,442 @@
+// The join of a block with the residual stream, and its gradients.
+//
+// Around the layer stand two norms: one of the block's output before it is added to the
+// residual stream, one of the stream before the next block.  With
+// n(v; w) = v / sqrt(mean(v^2) + eps) * (offset + w),
+//   z = x + scale * g * n(y; w_post)          h = n(z; w_pre)
+// where g is a gate per channel, token or element (or its sigmoid), or 1.
+//
+// Both passes do a few operations per element they move, so they are bound by memory: each
+// tensor is read once and written once.  A row's vectors stay in registers from the load to
+// the store (one 16-byte vector of a row belongs to one thread throughout), so the two means
+// of the forward are two reductions over the row's threads, not passes over memory; outputs
+// may overwrite inputs for the same reason.  Every sum is float32, every output is rounded
+// once, and h takes z before its rounding.
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.h"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+struct JoinP {
+  const void* x;
+  const void* y;
+  const void* gate;
+  const void* w_post;
+  const void* w_pre;
+  void* z;
+  void* h;
+  int64_t rows;
+  int H, nvec;  // row length, in elements and in 16-byte vectors
+  int post_norm, gate_kind, gate_act;
+  float eps, offset, scale;
+};
+
+struct JoinBwdP {
+  const void* z;
+  const void* y;
+  const void* gate;
+  const void* w_post;
+  const void* w_pre;
+  const void* dz;
+  const void* dh;
+  void* dx;
+  void* dy;
+  void* dgate;
+  float* part;  // [sums][blocks][H]: column sums of each block's rows
+  int p_pre, p_post, p_gate;  // which of the sums is whose, -1: not asked for
+  int64_t rows;
+  int H, nvec;
+  int post_norm, gate_kind, gate_act;
+  float eps, offset, scale;
+};
+
+// The gate's value; float32 layers take the full exponential.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float v) {
+  return 1.0f / (1.0f + (sizeof(T) == 4 ? expf(-v) : __expf(-v)));
+}
+
+// Sums of N values over the NT threads of a row; every thread gets them.  `buf` alternates
+// between two halves, so one barrier per reduction is enough.
+template <int NT, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float (*buf)[NT / 64]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) v[n] += __shfl_xor(v[n], d, 64);
+  if constexpr (NT > 64) {
+    constexpr int W = NT / 64;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    if (lane == 0)
+#pragma unroll
+      for (int n = 0; n < N; ++n) buf[n][wave] = v[n];
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) s += buf[n][w];
+      v[n] = s;
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 load_vec(const void* p, size_t at) {
+  return reinterpret_cast<const uint4*>(p)[at];
+}
+
+// NT threads and V vectors a thread hold a row.  Rows of one wave (NT = 64) go four to a
+// block, longer ones take a block each.
+template <typename T, int NT, int V>
+__global__ __launch_bounds__(NT == 64 ? 256 : NT) void join_kernel(JoinP p) {
+  constexpr int E = Elem<T>::kPerVec;
+  __shared__ float buf[2][1][NT / 64];
+  const int64_t row = NT == 64 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6) : int64_t(blockIdx.x);
+  if (NT == 64 && row >= p.rows) return;  // whole waves, and no barrier follows
+  const int tid = NT == 64 ? threadIdx.x & 63 : threadIdx.x;
+  const size_t base = size_t(row) * p.nvec;
+  const float inv_h = 1.0f / float(p.H);
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  uint4 xr[V], yr[V], gr[V], wa[V], wb[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = tid + i * NT;
+    const bool in = c < p.nvec;
+    xr[i] = in ? load_vec<T>(p.x, base + c) : none;
+    yr[i] = in && p.y != nullptr ? load_vec<T>(p.y, base + c) : none;
+    gr[i] = none;
+    if (in && p.gate_kind == MOE_GATE_ELEMENT) gr[i] = load_vec<T>(p.gate, base + c);
+    if (in && p.gate_kind == MOE_GATE_CHANNEL) gr[i] = load_vec<T>(p.gate, c);
+    wa[i] = in && p.w_post != nullptr ? load_vec<T>(p.w_post, c) : none;
+    wb[i] = in && p.w_pre != nullptr ? load_vec<T>(p.w_pre, c) : none;
+  }
+  float zv[V][E];
+#pragma unroll
+  for (int i = 0; i < V; ++i) unpack16(xr[i], T(), zv[i]);
+  if (p.y != nullptr) {
+    float g_row = p.scale;
+    if (p.gate_kind == MOE_GATE_TOKEN) {
+      const float g = static_cast<const float*>(p.gate)[row];
+      g_row *= p.gate_act == MOE_GATE_SIGMOID ? sigmoid<T>(g) : g;
+    }
+    float r = 1.0f;
+    if (p.post_norm) {
+      float s[1] = {0.0f};
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float f[E];
+        unpack16(yr[i], T(), f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) s[0] = fmaf(f[e], f[e], s[0]);
+      }
+      row_sum<NT, 1>(s, buf[0]);
+      r = 1.0f / sqrtf(s[0] * inv_h + p.eps);
+    }
+    const bool whole = p.gate_kind == MOE_GATE_ELEMENT || p.gate_kind == MOE_GATE_CHANNEL;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float f[E], w[E], g[E];
+      unpack16(yr[i], T(), f);
+      unpack16(wa[i], T(), w);
+      unpack16(gr[i], T(), g);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        float b = f[e] * r;
+        if (p.w_post != nullptr) b *= p.offset + w[e];
+        float k = g_row;
+        if (whole) k *= p.gate_act == MOE_GATE_SIGMOID ? sigmoid<T>(g[e]) : g[e];
+        zv[i][e] = fmaf(k, b, zv[i][e]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * NT;
+      if (c < p.nvec) reinterpret_cast<uint4*>(p.z)[base + c] = pack16(zv[i], T());
+    }
+  }
+  if (p.h != nullptr) {
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e) s[0] = fmaf(zv[i][e], zv[i][e], s[0]);
+    row_sum<NT, 1>(s, buf[1]);
+    const float r = 1.0f / sqrtf(s[0] * inv_h + p.eps);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * NT;
+      float w[E], o[E];
+      unpack16(wb[i], T(), w);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        o[e] = zv[i][e] * r;
+        if (p.w_pre != nullptr) o[e] *= p.offset + w[e];
+      }
+      if (c < p.nvec) reinterpret_cast<uint4*>(p.h)[base + c] = pack16(o, T());
+    }
+  }
+}
+
+// The gradients.  With zh = z r_z, yh = y r_y (y itself without its norm), b = yh (offset +
+// w_post), a = dh (offset + w_pre):
+//   D  = dz + r_z (a - zh mean(a zh))                       (= dx)
+//   db = scale g D,  c = db (offset + w_post),  dy = r_y (c - yh mean(c yh))
+//   dw_pre = sum dh zh,  dw_post = sum db yh,  dgate = scale D b (s (1 - s) of a sigmoid)
+// r_z, r_y and the first mean are sums over the inputs alone, one reduction; mean(c yh) and a
+// token gate's sum need D, a second one.  A block takes every gridDim.x-th row and keeps its
+// threads' column sums in registers to the end, so the sums over tokens cost blocks * H
+// floats of traffic instead of a pass; join_sum_kernel adds the blocks in order, which makes
+// them the same every time.
+template <typename T, int NT, int V>
+__global__ __launch_bounds__(NT) void join_bwd_kernel(JoinBwdP p) {
+  constexpr int E = Elem<T>::kPerVec;
+  __shared__ float buf[2][3][NT / 64];
+  const int tid = threadIdx.x;
+  const float inv_h = 1.0f / float(p.H);
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  uint4 wa[V], wb[V], gc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = tid + i * NT;
+    const bool in = c < p.nvec;
+    wa[i] = in && p.w_post != nullptr ? load_vec<T>(p.w_post, c) : none;
+    wb[i] = in && p.w_pre != nullptr ? load_vec<T>(p.w_pre, c) : none;
+    gc[i] = in && p.gate_kind == MOE_GATE_CHANNEL ? load_vec<T>(p.gate, c) : none;
+  }
+  float s_pre[V][E], s_post[V][E], s_gate[V][E];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_pre[i][e] = s_post[i][e] = s_gate[i][e] = 0.0f;
+  const bool sig = p.gate_act == MOE_GATE_SIGMOID;
+
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const size_t base = size_t(row) * p.nvec;
+    uint4 zr[V], yr[V], dzr[V], dhr[V], ger[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * NT;
+      const bool in = c < p.nvec;
+      zr[i] = in && p.dh != nullptr ? load_vec<T>(p.z, base + c) : none;
+      dhr[i] = in && p.dh != nullptr ? load_vec<T>(p.dh, base + c) : none;
+      yr[i] = in && p.y != nullptr ? load_vec<T>(p.y, base + c) : none;
+      dzr[i] = in && p.dz != nullptr ? load_vec<T>(p.dz, base + c) : none;
+      ger[i] = in && p.gate_kind == MOE_GATE_ELEMENT ? load_vec<T>(p.gate, base + c) : gc[i];
+    }
+    float g_raw = 0.0f;
+    if (p.gate_kind == MOE_GATE_TOKEN) g_raw = static_cast<const float*>(p.gate)[row];
+
+    float s[3] = {0.0f, 0.0f, 0.0f};  // sum z^2, sum a z, sum y^2
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float zf[E], hf[E], yf[E], w[E];
+      unpack16(zr[i], T(), zf);
+      unpack16(dhr[i], T(), hf);
+      unpack16(yr[i], T(), yf);
+      unpack16(wb[i], T(), w);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float a = p.w_pre != nullptr ? hf[e] * (p.offset + w[e]) : hf[e];
+        s[0] = fmaf(zf[e], zf[e], s[0]);
+        s[1] = fmaf(a, zf[e], s[1]);
+        s[2] = fmaf(yf[e], yf[e], s[2]);
+      }
+    }
+    row_sum<NT, 3>(s, buf[0]);
+    const float rz = p.dh != nullptr ? 1.0f / sqrtf(s[0] * inv_h + p.eps) : 0.0f;
+    const float ry = p.post_norm ? 1.0f / sqrtf(s[2] * inv_h + p.eps) : 1.0f;
+    const float mz = s[1] * rz * inv_h;  // mean(a zh)
+
+    float dv[V][E];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * NT;
+      float zf[E], hf[E], w[E];
+      unpack16(zr[i], T(), zf);
+      unpack16(dhr[i], T(), hf);
+      unpack16(wb[i], T(), w);
+      unpack16(dzr[i], T(), dv[i]);
+      if (p.dh != nullptr) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float zh = zf[e] * rz;
+          const float a = p.w_pre != nullptr ? hf[e] * (p.offset + w[e]) : hf[e];
+          s_pre[i][e] = fmaf(hf[e], zh, s_pre[i][e]);
+          dv[i][e] = fmaf(rz, fmaf(-zh, mz, a), dv[i][e]);
+        }
+      }
+      if (c < p.nvec) reinterpret_cast<uint4*>(p.dx)[base + c] = pack16(dv[i], T());
+    }
+    if (p.y == nullptr) {
+      if (NT > 64) __syncthreads();  // buf[0] is written again
+      continue;
+    }
+
+    float k_row = p.scale;
+    if (p.gate_kind == MOE_GATE_TOKEN) k_row *= sig ? sigmoid<T>(g_raw) : g_raw;
+    const bool whole = p.gate_kind == MOE_GATE_ELEMENT || p.gate_kind == MOE_GATE_CHANNEL;
+    float t[2] = {0.0f, 0.0f};  // sum c yh, sum D b
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float yf[E], w[E], g[E], og[E];
+      unpack16(yr[i], T(), yf);
+      unpack16(wa[i], T(), w);
+      unpack16(ger[i], T(), g);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float yh = yf[e] * ry;
+        const float f = p.w_post != nullptr ? p.offset + w[e] : 1.0f;
+        const float gv = whole ? (sig ? sigmoid<T>(g[e]) : g[e]) : 1.0f;
+        const float db = k_row * gv * dv[i][e];
+        const float dgb = dv[i][e] * (yh * f);
+        t[0] = fmaf(db * f, yh, t[0]);
+        t[1] += dgb;
+        s_post[i][e] = fmaf(db, yh, s_post[i][e]);
+        const float dg = whole ? p.scale * dgb * (sig ? gv * (1.0f - gv) : 1.0f) : 0.0f;
+        s_gate[i][e] += dg;
+        og[e] = dg;
+        dv[i][e] = db * f;  // c
+      }
+      const int c = tid + i * NT;
+      if (p.gate_kind == MOE_GATE_ELEMENT && c < p.nvec) reinterpret_cast<uint4*>(p.dgate)[base + c] = pack16(og, T());
+    }
+    row_sum<NT, 2>(t, buf[1]);
+    const float my = p.post_norm ? t[0] * inv_h : 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * NT;
+      float yf[E], o[E];
+      unpack16(yr[i], T(), yf);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = ry * fmaf(-(yf[e] * ry), my, dv[i][e]);
+      if (c < p.nvec) reinterpret_cast<uint4*>(p.dy)[base + c] = pack16(o, T());
+    }
+    if (p.gate_kind == MOE_GATE_TOKEN && tid == 0) {
+      const float sg = sig ? sigmoid<T>(g_raw) : 0.0f;
+      static_cast<float*>(p.dgate)[row] = p.scale * t[1] * (sig ? sg * (1.0f - sg) : 1.0f);
+    }
+  }
+
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = tid + i * NT;
+    if (c >= p.nvec) continue;
+    auto put = [&](int which, const float (&v)[E]) {
+      if (which < 0) return;
+      float* dst = p.part + (size_t(which) * gridDim.x + blockIdx.x) * p.H + size_t(c) * E;
+#pragma unroll
+      for (int q = 0; q < E; q += 4) *reinterpret_cast<f32x4_t*>(dst + q) = f32x4_t{v[q], v[q + 1], v[q + 2], v[q + 3]};
+    };
+    put(p.p_pre, s_pre[i]);
+    put(p.p_post, s_post[i]);
+    put(p.p_gate, s_gate[i]);
+  }
+}
+
+// Adds the blocks' column sums in a fixed order: 32 columns a block (one 128-byte line of
+// each row of sums), 32 threads down the rows, then the 32 in order.
+struct SumOut {
+  void* out[3];
+};
+template <typename T>
+__global__ __launch_bounds__(256) void join_sum_kernel(const float* __restrict__ part, int blocks, int H, SumOut o) {
+  __shared__ f32x4_t buf[32][8];
+  const int col = blockIdx.x * 32 + (threadIdx.x & 7) * 4, lane = threadIdx.x >> 3;
+  const float* src = part + size_t(blockIdx.y) * blocks * H + col;
+  f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+  if (col < H)
+    for (int b = lane; b < blocks; b += 32) s += *reinterpret_cast<const f32x4_t*>(src + size_t(b) * H);
+  buf[lane][threadIdx.x & 7] = s;
+  __syncthreads();
+  if (threadIdx.x < 8 && col < H) {
+    for (int l = 1; l < 32; ++l) s += buf[l][threadIdx.x];
+    T* dst = static_cast<T*>(o.out[blockIdx.y]) + col;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dst[e] = Elem<T>::from_f32(s[e]);
+  }
+}
+
+int vectors(const moe_join_desc* j) { return int(size_t(j->hidden) * dtype_bytes(j->dtype) / 16); }
+
+template <typename T, int NT, int V>
+moe_status launch_fwd(const JoinP& p, hipStream_t s) {
+  const int64_t blocks = NT == 64 ? (p.rows + 3) / 4 : p.rows;
+  MOE_LAUNCH("block_join", (join_kernel<T, NT, V>), dim3(unsigned(blocks)), dim3(NT == 64 ? 256 : NT), 0, s, p);
+  return MOE_OK;
+}
+
+template <typename T>
+moe_status launch_fwd_t(const JoinP& p, hipStream_t s) {
+  const int n = p.nvec;
+  if (n <= 64) return launch_fwd<T, 64, 1>(p, s);
+  if (n <= 128) return launch_fwd<T, 64, 2>(p, s);
+  if (n <= 256) return launch_fwd<T, 256, 1>(p, s);
+  if (n <= 512) return launch_fwd<T, 256, 2>(p, s);
+  if (n <= 1024) return launch_fwd<T, 256, 4>(p, s);
+  return launch_fwd<T, 1024, 2>(p, s);
+}
+
+// Blocks of the backward: each keeps column sums of its rows.
+constexpr int kBwdBlocks = 512;
+int bwd_blocks(const moe_join_desc* j) { return int(std::min<int64_t>(j->rows, kBwdBlocks)); }
+
+template <typename T, int NT, int V>
+moe_status launch_bwd(const JoinBwdP& p, int blocks, hipStream_t s) {
+  MOE_LAUNCH("block_join_bwd", (join_bwd_kernel<T, NT, V>), dim3(unsigned(blocks)), dim3(NT), 0, s, p);
+  return MOE_OK;
+}
+
+template <typename T>
+moe_status launch_bwd_t(const JoinBwdP& p, int blocks, int sums, const SumOut& o, hipStream_t s) {
+  const int n = p.nvec;
+  const moe_status st = n <= 64     ? launch_bwd<T, 64, 1>(p, blocks, s)
+                        : n <= 128  ? launch_bwd<T, 128, 1>(p, blocks, s)
+                        : n <= 256  ? launch_bwd<T, 256, 1>(p, blocks, s)
+                        : n <= 512  ? launch_bwd<T, 256, 2>(p, blocks, s)
+                        : n <= 1024 ? launch_bwd<T, 512, 2>(p, blocks, s)
+                                    : launch_bwd<T, 1024, 2>(p, blocks, s);
+  if (st != MOE_OK || sums == 0) return st;
+  MOE_LAUNCH("block_join_bwd_sum", (join_sum_kernel<T>), dim3(unsigned((p.H + 31) / 32), unsigned(sums)), dim3(256), 0, s,
+             static_cast<const float*>(p.part), blocks, p.H, o);
+  return MOE_OK;
+}
+
+}  // namespace
+
+size_t join_workspace_bytes(const moe_join_desc* j) {
+  const int sums = 1 + (j->post_norm ? 1 : 0) + (j->gate_kind == MOE_GATE_CHANNEL ? 1 : 0);
+  return align_up(size_t(sums) * bwd_blocks(j) * j->hidden * sizeof(float), 256);
+}
+
+moe_status launch_join(const JoinArgs& a) {
+  const moe_join_desc* j = a.j;
+  const JoinP p{a.x,       a.y,          a.gate,       a.w_post,    a.w_pre, a.z, a.h, j->rows, j->hidden,
+                vectors(j), j->post_norm, j->gate_kind, j->gate_act, j->eps,  j->weight_offset, j->residual_scale};
+  return j->dtype == MOE_BF16 ? launch_fwd_t<bf16_t>(p, a.s) : launch_fwd_t<float>(p, a.s);
+}
+
+moe_status launch_join_backward(const JoinBwdArgs& a) {
+  const moe_join_desc* j = a.j;
+  SumOut o{};
+  int sums = 0;
+  auto ask = [&](void* out) {
+    if (out == nullptr) return -1;
+    o.out[sums] = out;
+    return sums++;
+  };
+  const int p_pre = ask(a.dw_pre), p_post = ask(a.dw_post);
+  const int p_gate = j->gate_kind == MOE_GATE_CHANNEL ? ask(a.dgate) : -1;
+  const JoinBwdP p{a.z,  a.y,  a.gate, a.w_post, a.w_pre, a.dz, a.dh, a.dx, a.dy, a.dgate, static_cast<float*>(a.ws),
+                   p_pre, p_post, p_gate, j->rows, j->hidden, vectors(j), j->post_norm, j->gate_kind, j->gate_act,
+                   j->eps, j->weight_offset, j->residual_scale};
+  return j->dtype == MOE_BF16 ? launch_bwd_t<bf16_t>(p, bwd_blocks(j), sums, o, a.s)
+                              : launch_bwd_t<float>(p, bwd_blocks(j), sums, o, a.s);
+}
+
+}  // namespace moe

@@ -258,4 +258,39 @@ int64_t muon_matrix_bytes(const moe_muon_desc* m);  // one matrix in the working
 size_t muon_workspace_bytes(const moe_muon_desc* m);
 moe_status launch_muon(const MuonArgs& a);
 
+// ---- the join with the residual stream (join.hip) -----------------------------
+constexpr int kJoinMaxRowBytes = 32768;
+struct JoinArgs {
+  const moe_join_desc* j;
+  const void* x;
+  const void* y;       // NULL: h = norm of x alone
+  const void* gate;
+  const void* w_post;
+  const void* w_pre;
+  void* z;
+  void* h;             // NULL: no norm after the join
+  hipStream_t s;
+};
+moe_status launch_join(const JoinArgs& a);
+
+struct JoinBwdArgs {
+  const moe_join_desc* j;
+  const void* z;
+  const void* y;
+  const void* gate;
+  const void* w_post;
+  const void* w_pre;
+  const void* dz;
+  const void* dh;
+  void* dx;
+  void* dy;
+  void* dgate;
+  void* dw_post;
+  void* dw_pre;
+  void* ws;            // join_workspace_bytes
+  hipStream_t s;
+};
+size_t join_workspace_bytes(const moe_join_desc* j);
+moe_status launch_join_backward(const JoinBwdArgs& a);
+
 }  // namespace moe

@@ -1,4 +1,4 @@
-"""Buffer management around the C ABI: one MoE layer's device tensors.
+"""Buffer management around the C ABI: one MoE layer's device tensors, and the join around it.
 
 MoELayer owns the weights (torch device tensors in the library's layout), the
 workspace, and the stage outputs, and calls the libmoe entry points on the
@@ -257,3 +257,58 @@ class MoELayer:
         ws = self._ws[key]
         for n, m in descs.items():
             L.moe_muon_update(m, grads["d" + n], state["momentum"][n], getattr(self, n), ws, master=state["master"].get(n))
+
+
+class BlockJoin:
+    """What stands between a block and the next: the norm of the block's output, its gate and scale, the
+    residual sum, and the next block's norm.  Owns the norm weights and a workspace per number of rows.
+
+    w_post: the norm after the block (post_norm without it: a norm of factor 1); w_pre: the next block's
+    norm (next_norm without it: a norm of factor 1).  gate: "none", "channel", "token" or "element"; the
+    gate itself is an argument of the calls, since all kinds but "channel" depend on the tokens."""
+
+    def __init__(self, hidden: int, dtype: str = "bf16", w_post=None, w_pre=None, post_norm: Optional[bool] = None,
+                 next_norm: Optional[bool] = None, gate="none", gate_act="linear", eps: float = 1e-6,
+                 weight_offset: float = 0.0, residual_scale: float = 1.0, device="cuda"):
+        self.hidden, self.dtype, self.device = hidden, dtype, torch.device(device)
+        self.w_post, self.w_pre = w_post, w_pre
+        self.post_norm = w_post is not None if post_norm is None else post_norm
+        self.next_norm = w_pre is not None if next_norm is None else next_norm
+        self.gate, self.gate_act = gate, gate_act
+        self.eps, self.weight_offset, self.residual_scale = eps, weight_offset, residual_scale
+        self._ws = {}
+
+    def desc(self, rows: int, with_block: bool = True) -> L.JoinDesc:
+        return L.make_join_desc(rows, self.hidden, self.dtype, post_norm=with_block and self.post_norm,
+                                gate=self.gate if with_block else "none", gate_act=self.gate_act, eps=self.eps,
+                                weight_offset=self.weight_offset, residual_scale=self.residual_scale)
+
+    def workspace(self, j: L.JoinDesc) -> torch.Tensor:
+        if j.rows not in self._ws:
+            # the size with a block covers the one without
+            n = L.moe_join_workspace_size(self.desc(j.rows))
+            self._ws[j.rows] = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
+        return self._ws[j.rows]
+
+    def forward(self, x, y=None, gate=None, z=None, h=None):
+        """(z, h) of the stream x and the block's output y; without y, (x, h): the norm before a first block.
+        h is None without a next norm."""
+        j = self.desc(x.shape[0], y is not None)
+        if z is None and y is not None:
+            z = torch.empty_like(x)
+        if h is None and self.next_norm:
+            h = torch.empty_like(x)
+        L.moe_block_join(j, x, y, gate, self.w_post if y is not None else None, self.w_pre, z, h)
+        return (x if y is None else z), h
+
+    def backward(self, z, y=None, gate=None, dz=None, dh=None, grads: Optional[dict] = None) -> dict:
+        """Gradients dx, and with y also dy, dgate, dw_post, and dw_pre, from those of forward()'s results."""
+        j = self.desc(z.shape[0], y is not None)
+        w_post = self.w_post if y is not None else None
+        if grads is None:
+            def like(t):
+                return None if t is None else torch.empty_like(t)
+            grads = {"dx": like(z), "dy": like(y), "dgate": like(gate), "dw_post": like(w_post), "dw_pre": like(self.w_pre)}
+        L.moe_block_join_backward(j, z, y, gate, w_post, self.w_pre, dz, dh, grads["dx"], grads["dy"], grads["dgate"],
+                                  grads["dw_post"], grads["dw_pre"], self.workspace(j))
+        return grads

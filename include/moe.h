@@ -572,6 +572,82 @@ moe_status moe_orthogonalize(const moe_muon_desc* m, const void* g, void* o, voi
 moe_status moe_muon_update(const moe_muon_desc* m, const void* grad, float* momentum, float* master, void* weight,
                            void* ws, size_t ws_bytes, void* stream);
 
+/* ======================================================================== */
+/* The join of a block with the residual stream.                             */
+/*                                                                           */
+/* The layer's output is added to a residual stream, and norms stand around   */
+/* it: one of the block's output y, one of the stream before the next block.  */
+/* With n(v; w) = v / sqrt(mean(v^2) + eps) * (weight_offset + w), the mean   */
+/* over a row,                                                               */
+/*   b = n(y; w_post)  (y itself where post_norm is 0)                        */
+/*   z = x + residual_scale * g * b                                           */
+/*   h = n(z; w_pre)                                                          */
+/* g is 1, or a gate or its sigmoid.  Without y, h = n(x; w_pre): the norm    */
+/* before the first block.  Sums are float32, every output is rounded once,   */
+/* and h takes z before its rounding.                                         */
+/* ======================================================================== */
+
+/* What the gate is given for.  MOE_GATE_CHANNEL [H] dtype, MOE_GATE_TOKEN [rows]
+ * float32, MOE_GATE_ELEMENT [rows, H] dtype. */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_ELEMENT = 3 } moe_gate_kind;
+typedef enum { MOE_GATE_LINEAR = 0, MOE_GATE_SIGMOID = 1 } moe_gate_act;
+
+/*   rows            tokens, >= 0 (at most 2^31 - 1; 0: a successful call that writes no row)
+ *   hidden          H > 0, a multiple of 8; a row takes at most 32 KiB (bf16 16384, f32 8192)
+ *   dtype           moe_dtype of the stream, y, the norm weights and their gradients
+ *   post_norm       0 or 1: y is normed before the gate
+ *   gate_kind, gate_act   moe_gate_kind, moe_gate_act
+ *   eps             > 0, finite;  weight_offset, residual_scale  finite
+ * A norm weight that is NULL stands for a factor of 1 (weight_offset does not count then). */
+typedef struct moe_join_desc {
+  int64_t rows;
+  int32_t hidden;
+  int32_t dtype;
+  int32_t post_norm;
+  int32_t gate_kind;
+  int32_t gate_act;
+  float eps;
+  float weight_offset;
+  float residual_scale;
+} moe_join_desc;
+
+/* The forward.  An output may be the buffer of an input of its shape and type (z may be x,
+ * h may be y); buffers may not overlap in other ways.
+ *   x       device [rows, H] dtype     the stream before the block
+ *   y       device [rows, H] dtype     the block's output, or NULL; then gate, w_post and z have
+ *           to be NULL, post_norm 0 and gate_kind MOE_GATE_NONE
+ *   gate    device, as gate_kind says; NULL exactly for MOE_GATE_NONE
+ *   w_post  device [H] dtype or NULL (has to be NULL where post_norm is 0)
+ *   w_pre   device [H] dtype or NULL (has to be NULL where h is)
+ *   z       device [rows, H] dtype out the stream after the block
+ *   h       device [rows, H] dtype out the next block's input, or NULL (not with y NULL) */
+moe_status moe_block_join(const moe_join_desc* j, const void* x, const void* y, const void* gate, const void* w_post,
+                          const void* w_pre, void* z, void* h, void* stream);
+
+/* Workspace bytes of the backward: the column sums of its blocks of rows. */
+moe_status moe_join_workspace_size(const moe_join_desc* j, size_t* bytes);
+
+/* The gradients, given those of z and h (chain rule through the definition above at the
+ * stored z).  dx is the gradient of x and, with y, of the whole sum before the join.
+ * Sums over rows are float32 in an order that depends on rows alone, rounded once.  With no rows
+ * the weights' (and a channel gate's) gradients are zeros.  Outputs may be the buffers of
+ * inputs as above (dx may be dz or dh, dy may be y).
+ *   z       device [rows, H] dtype: the forward's z (its x without y); not read where dh is NULL
+ *   y, gate, w_post, w_pre   as in the forward
+ *   dz      device [rows, H] dtype, or NULL: none
+ *   dh      device [rows, H] dtype, or NULL where the forward made no h or it has none;
+ *           dz and dh may not both be NULL
+ *   dx      device [rows, H] dtype out
+ *   dy      device [rows, H] dtype out; NULL exactly where y is
+ *   dgate   device out, of the gate's shape and type; NULL exactly where gate is
+ *   dw_post device [H] dtype out; NULL exactly where w_post is
+ *   dw_pre  device [H] dtype out; NULL exactly where w_pre is (w_pre has to be NULL where dh is)
+ *   ws      device workspace of moe_join_workspace_size bytes */
+moe_status moe_block_join_backward(const moe_join_desc* j, const void* z, const void* y, const void* gate,
+                                   const void* w_post, const void* w_pre, const void* dz, const void* dh, void* dx,
+                                   void* dy, void* dgate, void* dw_post, void* dw_pre, void* ws, size_t ws_bytes,
+                                   void* stream);
+
 #ifdef __cplusplus
 }
 #endif
