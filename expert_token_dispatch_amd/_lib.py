@@ -523,33 +523,41 @@ def moe_muon_update(m, grad, momentum, weight, ws, master=None, stream=None) -> 
 
 
 # ---- the join with the residual stream ------------------------------------------------------
-def _expect(what, name, t, shape, dtype) -> None:
-    """A tensor that a call describes by its descriptor: the kernels take every extent from there."""
-    import torch
-    if t is None:
-        return
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{name} of this {what} is a {dtype} tensor {shape}")
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+def _expect(what, items) -> None:
+    """(name, tensor, shape, type) that a call describes by its descriptor: the kernels take every extent
+    from there, and run on the current device."""
+    dev = -1
+    for name, t, shape, dtype in items:
+        if t is None:
+            continue
+        if t.shape != shape or t.dtype is not dtype:
+            raise ValueError(f"{name} of this {what} is a {dtype} tensor {tuple(shape)}")
+        d = t.get_device()
+        if d != dev:  # the first one, or one elsewhere than those before
+            import torch
+            if d >= 0 and (dev >= 0 or d != torch.cuda.current_device()):
+                raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+            dev = d
 
 
-def _join_shapes(j, rows, weights, gates) -> None:
+def _join_items(j, gate):
+    """Shapes and types of a join's rows, weights and gate."""
     import torch
     dt = torch.bfloat16 if j.dtype == MOE_BF16 else torch.float32
-    for name, t in rows.items():
-        _expect("join", name, t, (j.rows, j.hidden), dt)
-    for name, t in weights.items():
-        _expect("join", name, t, (j.hidden,), dt)
-    shape, gdt = {MOE_GATE_CHANNEL: ((j.hidden,), dt), MOE_GATE_TOKEN: ((j.rows,), torch.float32),
-                  MOE_GATE_ELEMENT: ((j.rows, j.hidden), dt)}.get(j.gate_kind, (None, None))
-    for name, t in gates.items():
-        if shape is not None:
-            _expect("join", name, t, shape, gdt)
+    T, H, k = j.rows, j.hidden, j.gate_kind
+    rows, gdt = (T, H), dt
+    shape = (H,) if k == MOE_GATE_CHANNEL else rows
+    if k == MOE_GATE_TOKEN:
+        shape, gdt = (T,), torch.float32
+    elif k == MOE_GATE_NONE and gate is not None:  # the library refuses it
+        shape, gdt = gate.shape, gate.dtype
+    return dt, rows, (H,), shape, gdt
 
 
 def moe_block_join(j, x, y, gate, w_post, w_pre, z, h, stream=None) -> None:
-    _join_shapes(j, {"x": x, "y": y, "z": z, "h": h}, {"w_post": w_post, "w_pre": w_pre}, {"gate": gate})
+    dt, rows, chan, shape, gdt = _join_items(j, gate)
+    _expect("join", (("x", x, rows, dt), ("y", y, rows, dt), ("gate", gate, shape, gdt), ("w_post", w_post, chan, dt),
+                     ("w_pre", w_pre, chan, dt), ("z", z, rows, dt), ("h", h, rows, dt)))
     _check(lib().moe_block_join(ctypes.byref(j), _p(x), _p(y), _p(gate), _p(w_post), _p(w_pre), _p(z), _p(h),
                                 _s(stream)))
 
@@ -562,8 +570,11 @@ def moe_join_workspace_size(j: JoinDesc) -> int:
 
 def moe_block_join_backward(j, z, y, gate, w_post, w_pre, dz, dh, dx, dy, dgate, dw_post, dw_pre, ws,
                             stream=None) -> None:
-    _join_shapes(j, {"z": z, "y": y, "dz": dz, "dh": dh, "dx": dx, "dy": dy},
-                 {"w_post": w_post, "w_pre": w_pre, "dw_post": dw_post, "dw_pre": dw_pre}, {"gate": gate, "dgate": dgate})
+    dt, rows, chan, shape, gdt = _join_items(j, gate)
+    _expect("join", (("z", z, rows, dt), ("y", y, rows, dt), ("gate", gate, shape, gdt), ("w_post", w_post, chan, dt),
+                     ("w_pre", w_pre, chan, dt), ("dz", dz, rows, dt), ("dh", dh, rows, dt), ("dx", dx, rows, dt),
+                     ("dy", dy, rows, dt), ("dgate", dgate, shape, gdt), ("dw_post", dw_post, chan, dt),
+                     ("dw_pre", dw_pre, chan, dt)))
     wp, wn = _ws(ws)
     _check(lib().moe_block_join_backward(ctypes.byref(j), _p(z), _p(y), _p(gate), _p(w_post), _p(w_pre), _p(dz),
                                          _p(dh), _p(dx), _p(dy), _p(dgate), _p(dw_post), _p(dw_pre), wp, wn,

@@ -91,6 +91,8 @@ __device__ __forceinline__ uint4 load_vec(const void* p, size_t at) {
   return reinterpret_cast<const uint4*>(p)[at];
 }
 
+// 8192 x 4096 in bf16 takes 50 us, 5.3 TB/s, as fast as a large copy; 2047 x 2880 with a gate per
+// element 15 us (4 TB/s: the ends of a short kernel).  128 threads of four vectors 53 and 18 us.
 // NT threads and V vectors a thread hold a row.  Rows of one wave (NT = 64) go four to a
 // block, longer ones take a block each.
 template <typename T, int NT, int V>
@@ -188,6 +190,10 @@ __global__ __launch_bounds__(NT == 64 ? 256 : NT) void join_kernel(JoinP p) {
 //   D  = dz + r_z (a - zh mean(a zh))                       (= dx)
 //   db = scale g D,  c = db (offset + w_post),  dy = r_y (c - yh mean(c yh))
 //   dw_pre = sum dh zh,  dw_post = sum db yh,  dgate = scale D b (s (1 - s) of a sigmoid)
+// At 8192 x 4096 in bf16 with a channel gate 91 us with the sums' kernel, 4.4 of the 5.2 TB/s that a
+// large copy reaches: the sums of 512 blocks are another 50 MB, the rest the two waits of a row.
+// (Loading the next row under this one, rows of 1024-thread blocks side by side and barriers
+// that leave loads in flight were all slower, 96 to 150 us: registers, or rows in step.)
 // r_z, r_y and the first mean are sums over the inputs alone, one reduction; mean(c yh) and a
 // token gate's sum need D, a second one.  A block takes every gridDim.x-th row and keeps its
 // threads' column sums in registers to the end, so the sums over tokens cost blocks * H
@@ -339,26 +345,39 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinBwdP p) {
   }
 }
 
-// Adds the blocks' column sums in a fixed order: 32 columns a block (one 128-byte line of
-// each row of sums), 32 threads down the rows, then the 32 in order.
+// Adds the blocks' column sums in a fixed order: 32 columns a block (a 128-byte line of each row
+// of sums; half a line took 9.7 instead of 6 us for 25 MB), 128 threads down the rows with eight
+// loads in flight, then the 128 in order.
 struct SumOut {
   void* out[3];
 };
 template <typename T>
-__global__ __launch_bounds__(256) void join_sum_kernel(const float* __restrict__ part, int blocks, int H, SumOut o) {
-  __shared__ f32x4_t buf[32][8];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 7) * 4, lane = threadIdx.x >> 3;
+__global__ __launch_bounds__(1024) void join_sum_kernel(const float* __restrict__ part, int blocks, int H, SumOut o) {
+  constexpr int kCols = 32, kLanes = 128, kFlight = 8;
+  __shared__ f32x4_t buf[kLanes][kCols / 4];
+  const int sub = threadIdx.x & 7, lane = threadIdx.x >> 3, col = blockIdx.x * kCols + sub * 4;
   const float* src = part + size_t(blockIdx.y) * blocks * H + col;
   f32x4_t s = {0.f, 0.f, 0.f, 0.f};
-  if (col < H)
-    for (int b = lane; b < blocks; b += 32) s += *reinterpret_cast<const f32x4_t*>(src + size_t(b) * H);
-  buf[lane][threadIdx.x & 7] = s;
-  __syncthreads();
-  if (threadIdx.x < 8 && col < H) {
-    for (int l = 1; l < 32; ++l) s += buf[l][threadIdx.x];
-    T* dst = static_cast<T*>(o.out[blockIdx.y]) + col;
+  if (col < H) {
+    for (int b0 = lane; b0 < blocks; b0 += kLanes * kFlight) {
+      f32x4_t v[kFlight];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) dst[e] = Elem<T>::from_f32(s[e]);
+      for (int u = 0; u < kFlight; ++u) {
+        const int b = b0 + kLanes * u;
+        v[u] = b < blocks ? *reinterpret_cast<const f32x4_t*>(src + size_t(b) * H) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) s += v[u];
+    }
+  }
+  buf[lane][sub] = s;
+  __syncthreads();
+  if (threadIdx.x < kCols && blockIdx.x * kCols + threadIdx.x < H) {
+    const float* b = reinterpret_cast<const float*>(buf) + threadIdx.x;
+    float a = 0.0f;
+#pragma unroll
+    for (int l = 0; l < kLanes; ++l) a += b[l * kCols];
+    static_cast<T*>(o.out[blockIdx.y])[blockIdx.x * kCols + threadIdx.x] = Elem<T>::from_f32(a);
   }
 }
 
@@ -382,9 +401,20 @@ moe_status launch_fwd_t(const JoinP& p, hipStream_t s) {
   return launch_fwd<T, 1024, 2>(p, s);
 }
 
-// Blocks of the backward: each keeps column sums of its rows.
-constexpr int kBwdBlocks = 512;
-int bwd_blocks(const moe_join_desc* j) { return int(std::min<int64_t>(j->rows, kBwdBlocks)); }
+// Threads of a row in the backward: one vector each (two past 1024).
+int bwd_threads(const moe_join_desc* j) {
+  for (int t : {64, 128, 192, 256, 384, 512, 768})
+    if (vectors(j) <= t) return t;
+  return 1024;
+}
+// Its blocks: 1024 threads a CU, and rows dealt evenly.  Half as many leave too few loads in
+// flight (8192 x 4096 bf16 91 -> 119 us), twice as many write and read twice the sums (96 us).
+constexpr int kBwdThreads = 262144;
+int bwd_blocks(const moe_join_desc* j) {
+  const int64_t most = kBwdThreads / bwd_threads(j);
+  const int64_t each = std::max<int64_t>(1, (j->rows + most - 1) / most);
+  return int((j->rows + each - 1) / each);
+}
 
 template <typename T, int NT, int V>
 moe_status launch_bwd(const JoinBwdP& p, int blocks, hipStream_t s) {
@@ -393,16 +423,18 @@ moe_status launch_bwd(const JoinBwdP& p, int blocks, hipStream_t s) {
 }
 
 template <typename T>
-moe_status launch_bwd_t(const JoinBwdP& p, int blocks, int sums, const SumOut& o, hipStream_t s) {
-  const int n = p.nvec;
-  const moe_status st = n <= 64     ? launch_bwd<T, 64, 1>(p, blocks, s)
-                        : n <= 128  ? launch_bwd<T, 128, 1>(p, blocks, s)
-                        : n <= 256  ? launch_bwd<T, 256, 1>(p, blocks, s)
-                        : n <= 512  ? launch_bwd<T, 256, 2>(p, blocks, s)
-                        : n <= 1024 ? launch_bwd<T, 512, 2>(p, blocks, s)
-                                    : launch_bwd<T, 1024, 2>(p, blocks, s);
+moe_status launch_bwd_t(const JoinBwdP& p, int nt, int blocks, int sums, const SumOut& o, hipStream_t s) {
+  const moe_status st = nt == 64          ? launch_bwd<T, 64, 1>(p, blocks, s)
+                        : nt == 128       ? launch_bwd<T, 128, 1>(p, blocks, s)
+                        : nt == 192       ? launch_bwd<T, 192, 1>(p, blocks, s)
+                        : nt == 256       ? launch_bwd<T, 256, 1>(p, blocks, s)
+                        : nt == 384       ? launch_bwd<T, 384, 1>(p, blocks, s)
+                        : nt == 512       ? launch_bwd<T, 512, 1>(p, blocks, s)
+                        : nt == 768       ? launch_bwd<T, 768, 1>(p, blocks, s)
+                        : p.nvec <= 1024  ? launch_bwd<T, 1024, 1>(p, blocks, s)
+                                          : launch_bwd<T, 1024, 2>(p, blocks, s);
   if (st != MOE_OK || sums == 0) return st;
-  MOE_LAUNCH("block_join_bwd_sum", (join_sum_kernel<T>), dim3(unsigned((p.H + 31) / 32), unsigned(sums)), dim3(256), 0, s,
+  MOE_LAUNCH("block_join_bwd_sum", (join_sum_kernel<T>), dim3(unsigned((p.H + 31) / 32), unsigned(sums)), dim3(1024), 0, s,
              static_cast<const float*>(p.part), blocks, p.H, o);
   return MOE_OK;
 }
@@ -435,8 +467,8 @@ moe_status launch_join_backward(const JoinBwdArgs& a) {
   const JoinBwdP p{a.z,  a.y,  a.gate, a.w_post, a.w_pre, a.dz, a.dh, a.dx, a.dy, a.dgate, static_cast<float*>(a.ws),
                    p_pre, p_post, p_gate, j->rows, j->hidden, vectors(j), j->post_norm, j->gate_kind, j->gate_act,
                    j->eps, j->weight_offset, j->residual_scale};
-  return j->dtype == MOE_BF16 ? launch_bwd_t<bf16_t>(p, bwd_blocks(j), sums, o, a.s)
-                              : launch_bwd_t<float>(p, bwd_blocks(j), sums, o, a.s);
+  return j->dtype == MOE_BF16 ? launch_bwd_t<bf16_t>(p, bwd_threads(j), bwd_blocks(j), sums, o, a.s)
+                              : launch_bwd_t<float>(p, bwd_threads(j), bwd_blocks(j), sums, o, a.s);
 }
 
 }  // namespace moe

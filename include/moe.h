@@ -629,7 +629,7 @@ moe_status moe_join_workspace_size(const moe_join_desc* j, size_t* bytes);
 
 /* The gradients, given those of z and h (chain rule through the definition above at the
  * stored z).  dx is the gradient of x and, with y, of the whole sum before the join.
- * Sums over rows are float32 in an order that depends on rows alone, rounded once.  With no rows
+ * Sums over rows are float32 in an order that depends on the sizes alone, rounded once.  With no rows
  * the weights' (and a channel gate's) gradients are zeros.  Outputs may be the buffers of
  * inputs as above (dx may be dz or dh, dy may be y).
  *   z       device [rows, H] dtype: the forward's z (its x without y); not read where dh is NULL

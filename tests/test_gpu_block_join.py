@@ -5,8 +5,8 @@ the float32 evaluation.  A row's sum adds at most 16 products in a thread, then 
 waves: 38 roundings, so a mean and its reciprocal root are off by at most 20 + 3 units of 2^-24; a result
 takes at most two of them, a sigmoid (whose exponential is off by 2 + |g| units, |g| < 6 here) and a
 dozen products and sums: under 96 units of 2^-24 of the magnitudes that went into it.  A sum over rows adds
-rows / 512 + 1 rows in a thread (and whatever each is off), 16 blocks in a thread of the second step and 32
-threads.
+at most rows / 256 + 1 rows in a thread (and whatever each is off), up to 4096 / 128 blocks in a thread of
+the second step and 128 threads.
 """
 
 import numpy as np
@@ -83,7 +83,7 @@ def run_both(v, d, dtype, j, jd, form, what):
             continue
         over_rows = name in ("dw_post", "dw_pre") or (name == "dgate" and j.gate == "channel")
         out_dtype = "f32" if t.dtype == torch.float32 else "bf16"
-        units = 96 * 2 + (T // 512 + 1 + 48 if over_rows else 0)
+        units = 96 * 2 + (T // 256 + 1 + 160 if over_rows else 0)
         if name == "dgate" and j.gate == "token":
             units += 38
         check(t, ref[name], ref["mag_" + name], out_dtype, units, f"{what} {name}")
