@@ -83,6 +83,12 @@ class MuonDesc(ctypes.Structure):
     ]
 
 
+class Adapters(ctypes.Structure):
+    """moe_adapters: low-rank pairs of many requests beside the expert weights (include/moe.h)."""
+    _fields_ = [("count", ctypes.c_int32), ("rank", ctypes.c_int32)] + [(n, ctypes.c_void_p) for n in (
+        "scale", "gate_a", "gate_b", "up_a", "up_b", "down_a", "down_b")]
+
+
 class JoinDesc(ctypes.Structure):
     """moe_join_desc: the join of a block with the residual stream (include/moe.h)."""
     _fields_ = [
@@ -146,6 +152,23 @@ def make_muon_desc(count: int, rows: int, cols: int, dtype="bf16", steps: int = 
                     weight_decay)
 
 
+ADAPTED = ("gate", "up", "down")
+
+
+def make_adapters(t: dict) -> Adapters:
+    """t: a dict of device tensors under the moe_adapters field names: "gate_a" [count, L, rank, H],
+    "gate_b" [count, L, I, rank], "up_a", "up_b" alike, "down_a" [count, L, rank, I], "down_b"
+    [count, L, H, rank], and "scale" [count] float32; a projection's pair and the scale may be left
+    out.  The struct keeps a reference to the dict, so the pointers stay valid while it lives."""
+    t = {k: v for k, v in t.items() if v is not None}
+    first = next((t[n + "_a"] for n in ADAPTED if n + "_a" in t), None)
+    if first is None or first.dim() != 4:
+        raise ValueError("adapters have an \"_a\" of at least one projection, of four dimensions")
+    v = Adapters(first.shape[0], first.shape[2], *[_p(t.get(n)) for n, _ in Adapters._fields_[2:]])
+    v._tensors, v._fits = t, None
+    return v
+
+
 def make_join_desc(rows: int, hidden: int, dtype="bf16", post_norm: bool = False, gate="none", gate_act="linear",
                    eps: float = 1e-6, weight_offset: float = 0.0, residual_scale: float = 1.0) -> JoinDesc:
     """gate: "none", "channel" [H], "token" [rows] float32 or "element" [rows, H]; gate_act: "linear" or
@@ -167,6 +190,7 @@ _OP = ctypes.c_void_p  # moe_route_opts*, NULL allowed
 _PP = ctypes.c_void_p  # moe_packed_experts*
 _MP = ctypes.POINTER(MuonDesc)
 _JP = ctypes.POINTER(JoinDesc)
+_AP = ctypes.c_void_p  # moe_adapters*
 
 
 def lib() -> ctypes.CDLL:
@@ -221,6 +245,11 @@ def lib() -> ctypes.CDLL:
             "moe_muon_workspace_size": (st, [_MP, ctypes.POINTER(ctypes.c_size_t)]),
             "moe_orthogonalize": (st, [_MP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
             "moe_muon_update": (st, [_MP, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
+            "moe_adapted_workspace_size": (st, [_DP, _AP, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]),
+            "moe_grouped_ffn_adapted": (st, [_DP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _AP, _VP, _VP, ctypes.c_size_t,
+                                             _VP]),
+            "moe_layer_forward_adapted": (st, [_DP, _OP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _AP, _VP, _VP, _VP, _VP,
+                                               _VP, _VP, ctypes.c_size_t, _VP]),
             "moe_block_join": (st, [_JP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
             "moe_join_workspace_size": (st, [_JP, ctypes.POINTER(ctypes.c_size_t)]),
             "moe_block_join_backward": (st, [_JP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
@@ -522,7 +551,6 @@ def moe_muon_update(m, grad, momentum, weight, ws, master=None, stream=None) -> 
     _check(lib().moe_muon_update(ctypes.byref(m), _p(grad), _p(momentum), _p(master), _p(weight), wp, wn, _s(stream)))
 
 
-# ---- the join with the residual stream ------------------------------------------------------
 def _expect(what, items) -> None:
     """(name, tensor, shape, type) that a call describes by its descriptor: the kernels take every extent
     from there, and run on the current device."""
@@ -540,6 +568,61 @@ def _expect(what, items) -> None:
             dev = d
 
 
+# ---- low-rank adapters beside the experts' weights -------------------------------------------
+def _adapters(d, v) -> Optional[int]:
+    """The struct's address; its tensors have to be the stacks that d describes, since the kernels
+    take every extent from d and the struct."""
+    import torch
+    if v is None:
+        return None
+    t = getattr(v, "_tensors", None)  # none: a struct of the caller's own pointers
+    if t is not None:
+        dt = torch.bfloat16 if d.dtype == MOE_BF16 else torch.float32
+        n, L, R, H, I = v.count, d.local_count, v.rank, d.hidden, d.intermediate
+        key = (dt, L, H, I)
+        if v._fits != key:
+            shapes = {"scale": ((n,), torch.float32)}
+            for name, out, in_ in (("gate", I, H), ("up", I, H), ("down", H, I)):
+                shapes[name + "_a"], shapes[name + "_b"] = ((n, L, R, in_), dt), ((n, L, out, R), dt)
+            if set(t) - set(shapes):
+                raise ValueError(f"adapters have no {sorted(set(t) - set(shapes))}")
+            _expect("layer's adapters", [(k, x, *shapes[k]) for k, x in t.items()])
+            v._fits = key  # the tensors are the struct's own: looked at once for each kind of layer
+    return ctypes.addressof(v)
+
+
+def moe_adapted_workspace_size(d: LayerDesc, adapters, stage: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_adapted_workspace_size(ctypes.byref(d), _adapters(d, adapters), stage, ctypes.byref(n)))
+    return n.value
+
+
+def _ids(d, adapter_ids) -> None:
+    import torch
+    _expect("layer", (("adapter_ids", adapter_ids, (d.num_tokens,), torch.int32),))
+
+
+def moe_grouped_ffn_adapted(d, x_sorted, offsets, sorted_pairs, adapter_ids, w_gate, w_up, w_down, adapters, y_sorted,
+                            ws, stream=None) -> None:
+    ad = _adapters(d, adapters)
+    _ids(d, adapter_ids)
+    wp, wn = _ws(ws)
+    _check(lib().moe_grouped_ffn_adapted(ctypes.byref(d), _p(x_sorted), _p(offsets), _p(sorted_pairs), _p(adapter_ids),
+                                         _p(w_gate), _p(w_up), _p(w_down), ad, _p(y_sorted), wp, wn, _s(stream)))
+
+
+def moe_layer_forward_adapted(d, opts, x, adapter_ids, w_router, b_router, w_gate, w_up, w_down, adapters, y, ws,
+                              topk_ids_out=None, topk_w_out=None, counts_out=None, num_dropped_out=None,
+                              stream=None) -> None:
+    ad = _adapters(d, adapters)
+    _ids(d, adapter_ids)
+    wp, wn = _ws(ws)
+    _check(lib().moe_layer_forward_adapted(ctypes.byref(d), _opts(opts), _p(x), _p(adapter_ids), _p(w_router),
+                                           _p(b_router), _p(w_gate), _p(w_up), _p(w_down), ad, _p(y), _p(topk_ids_out),
+                                           _p(topk_w_out), _p(counts_out), _p(num_dropped_out), wp, wn, _s(stream)))
+
+
+# ---- the join with the residual stream ------------------------------------------------------
 def _join_items(j, gate):
     """Shapes and types of a join's rows, weights and gate."""
     import torch

@@ -417,6 +417,37 @@ MuonArgs muon_args(const moe_muon_desc* m, void* ws, void* stream) {
   return a;
 }
 
+// pointers false: only which of them are NULL counts
+moe_status adapters_checks(const moe_adapters* a, bool pointers = true) {
+  if (a == nullptr) return set_error(MOE_ERR_INVALID_ARG, "adapters are NULL");
+  if (a->count < 1 || a->count > 65535)
+    return set_error(MOE_ERR_INVALID_ARG, "adapters: count must be in [1, 65535] (got %d)", a->count);
+  if (a->rank < 8 || a->rank > 128 || a->rank % 8 != 0)
+    return set_error(MOE_ERR_INVALID_ARG, "adapters: rank must be a multiple of 8 in [8, 128] (got %d)", a->rank);
+  const void* pairs[3][2] = {{a->gate_a, a->gate_b}, {a->up_a, a->up_b}, {a->down_a, a->down_b}};
+  static const char* const names[3] = {"gate", "up", "down"};
+  int given = 0;
+  for (int i = 0; i < 3; ++i) {
+    if ((pairs[i][0] == nullptr) != (pairs[i][1] == nullptr))
+      return set_error(MOE_ERR_INVALID_ARG, "adapters: %s_a and %s_b: give both or neither", names[i], names[i]);
+    if (pointers && (!aligned(pairs[i][0], 16) || !aligned(pairs[i][1], 16)))
+      return set_error(MOE_ERR_INVALID_ARG, "adapters: %s_a or %s_b is not 16-byte aligned", names[i], names[i]);
+    given += pairs[i][0] != nullptr;
+  }
+  if (given == 0) return set_error(MOE_ERR_INVALID_ARG, "adapters: no projection has a pair");
+  if (pointers) OPTIONAL_PTR(a->scale, 4);
+  return MOE_OK;
+}
+
+size_t adapted_stage_bytes(const moe_layer_desc* d, const moe_adapters* a, int32_t stage) {
+  return align_up(stage_bytes(d, stage), 256) + carve_adapter_scratch(d, a, max_pairs_of(d), nullptr).bytes;
+}
+
+// The adapters' part of a workspace: behind what the stage has without them.
+AdapterScratch adapted_scratch(const moe_layer_desc* d, const moe_adapters* a, int32_t stage, void* ws) {
+  return carve_adapter_scratch(d, a, max_pairs_of(d), static_cast<char*>(ws) + align_up(stage_bytes(d, stage), 256));
+}
+
 moe_status join_desc_checks(const moe_join_desc* j) {
   if (j == nullptr) return set_error(MOE_ERR_INVALID_ARG, "descriptor is NULL");
   if (j->rows < 0) return set_error(MOE_ERR_INVALID_ARG, "rows must be >= 0 (got %lld)", (long long)j->rows);
@@ -1071,6 +1102,73 @@ moe_status moe_muon_update(const moe_muon_desc* m, const void* grad, float* mome
   a.master = master;
   a.out = weight;
   return launch_muon(a);
+}
+
+moe_status moe_adapted_workspace_size(const moe_layer_desc* d, const moe_adapters* a, int32_t stage, size_t* bytes) {
+  TRY(check_desc(d));
+  TRY(adapters_checks(a, false));
+  if (bytes == nullptr) return set_error(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  if (stage != MOE_STAGE_FFN && stage != MOE_STAGE_LAYER)
+    return set_error(MOE_ERR_INVALID_ARG, "stage %d has no form with adapters", stage);
+  *bytes = adapted_stage_bytes(d, a, stage);
+  return MOE_OK;
+}
+
+moe_status moe_grouped_ffn_adapted(const moe_layer_desc* d, const void* x_sorted, const int32_t* offsets,
+                                   const int32_t* sorted_pairs, const int32_t* adapter_ids, const void* w_gate,
+                                   const void* w_up, const void* w_down, const moe_adapters* a, void* y_sorted, void* ws,
+                                   size_t ws_bytes, void* stream) {
+  CallScope scope;
+  TRY(check_desc(d));
+  TRY(adapters_checks(a));
+  if (d->num_tokens == 0) return MOE_OK;
+  TRY(ffn_checks(x_sorted, offsets, w_gate, w_up, w_down, y_sorted));
+  REQUIRE_PTR(sorted_pairs, 4);
+  REQUIRE_PTR(adapter_ids, 4);
+  TRY(check_ws_bytes(adapted_stage_bytes(d, a, MOE_STAGE_FFN), ws, ws_bytes));
+  void* scratch = ffn_scratch_bytes(d, max_pairs_of(d)) ? static_cast<char*>(ws) + ffn_h_bytes(d) : nullptr;
+  FfnArgs fa{d, x_sorted, offsets, w_gate, w_up, w_down, y_sorted, ws, scratch, max_pairs_of(d),
+             static_cast<hipStream_t>(stream)};
+  AdaptedFfnArgs aa{fa, sorted_pairs, adapter_ids, a, adapted_scratch(d, a, MOE_STAGE_FFN, ws)};
+  return launch_adapted_ffn(aa);
+}
+
+moe_status moe_layer_forward_adapted(const moe_layer_desc* d, const moe_route_opts* opts, const void* x,
+                                     const int32_t* adapter_ids, const void* w_router, const float* b_router,
+                                     const void* w_gate, const void* w_up, const void* w_down, const moe_adapters* a,
+                                     void* y, int32_t* topk_ids_out, float* topk_w_out, int32_t* counts_out,
+                                     int64_t* num_dropped_out, void* ws, size_t ws_bytes, void* stream) {
+  CallScope scope;
+  TRY(check_desc(d));
+  TRY(adapters_checks(a));
+  if (d->num_tokens == 0) return MOE_OK;
+  TRY(check_ws_bytes(adapted_stage_bytes(d, a, MOE_STAGE_LAYER), ws, ws_bytes));
+  REQUIRE_PTR(adapter_ids, 4);
+  const LayerWs w = layer_layout(d, ws);
+  int32_t* ids = topk_ids_out ? topk_ids_out : w.topk_ids;
+  float* tw = topk_w_out ? topk_w_out : w.topk_w;
+  int32_t* counts = counts_out ? counts_out : w.counts;
+  int64_t* dropped = num_dropped_out ? num_dropped_out : w.num_dropped;
+  const bool cap = capacity_of(d) >= 0;
+  TRY(route_checks(d, x, w_router, b_router, nullptr, nullptr, ids, tw, w.topk_logit));
+  TRY(dispatch_checks(d, x, ids, w.topk_logit, counts, w.offsets, w.sorted_pairs, w.pair_row, w.x_sorted, dropped));
+  TRY(ffn_checks(w.x_sorted, w.offsets, w_gate, w_up, w_down, w.y_sorted));
+  TRY(combine_checks(w.y_sorted, w.pair_row, tw, y));
+  TRY(opts_checks(d, opts));
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const DispatchScratch scr = carve_dispatch_scratch(d, w.dispatch);
+  RouteArgs ra{d, x, w_router, b_router, nullptr, nullptr, ids, tw, cap ? w.topk_logit : nullptr,
+               static_cast<float*>(w.route), scr.blk_all, s};
+  apply_opts(ra, d, opts);
+  TRY(launch_route(ra));
+  DispatchArgs da{d, x, ids, w.topk_logit, counts, w.offsets, w.sorted_pairs, w.pair_row, w.x_sorted, dropped,
+                  scr, capacity_of(d), true, s};
+  TRY(launch_dispatch(da));
+  FfnArgs fa{d, w.x_sorted, w.offsets, w_gate, w_up, w_down, w.y_sorted, w.h, w.ffn_scratch, max_pairs_of(d), s};
+  AdaptedFfnArgs aa{fa, w.sorted_pairs, adapter_ids, a, adapted_scratch(d, a, MOE_STAGE_LAYER, ws)};
+  TRY(launch_adapted_ffn(aa));
+  CombineArgs ca{d, w.y_sorted, w.pair_row, tw, y, s};
+  return launch_combine(ca);
 }
 
 moe_status moe_block_join(const moe_join_desc* j, const void* x, const void* y, const void* gate, const void* w_post,

@@ -26,7 +26,9 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
+#include "adapters.h"
 #include "ffn_common.h"
 #include "kernels.h"
 
@@ -61,18 +63,79 @@ template <> struct Gemm<float> {
 };
 
 
+// Adds the adapters' share to a wave's sums: 32-row blocks i of rows row0 + 32 i (rows_left of
+// them there) and 32-column blocks j of columns col0 + 32 j, in the accumulators' layout (lane ->
+// column, register r -> row 8 (r / 4) + 4 (lane / 32) + r % 4).  One adapter of the rows after
+// another: its products over all rows of a block, added to the rows that are its own.
+template <typename T, int NMAT, int MI, int NJ>
+__device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int row0, int rows_left, int col0, int N,
+                                             f32x16_t (&acc)[NMAT][MI][NJ]) {
+  using G = Gemm<T>;
+  constexpr int FV = G::kFragVec, EPV = 16 / int(sizeof(T));
+  const int lane = threadIdx.x & 63, fr = lane & 31, fk = 8 * (lane >> 5);
+  if (rows_left <= 0) return;
+  int id[MI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) id[i] = i * 32 + fr < rows_left ? ad.rid[row0 + i * 32 + fr] : -1;
+  for (;;) {
+    int cur = -1;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const uint64_t some = __ballot(id[i] >= 0);
+      if (cur < 0 && some != 0) cur = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(some));
+    }
+    if (cur < 0) return;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const uint32_t mine = uint32_t(__ballot(id[i] == cur));
+      if (id[i] == cur) id[i] = -1;
+      if (mine == 0) continue;
+      const int row = row0 + min(i * 32 + fr, rows_left - 1);
+#pragma unroll
+      for (int m = 0; m < NMAT; ++m) {
+        if (ad.u[m] == nullptr) continue;
+        const T* u = adapter_u<T>(ad, m, row) + fk;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const T* b = adapter_b<T>(ad, m, cur, expert, min(col0 + j * 32 + fr, N - 1), N) + fk;
+          f32x16_t t;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) t[r] = 0.0f;
+#pragma unroll 1
+          for (int c = 0; c < ad.rank; c += 16) {
+            uint4 uf[FV], bf[FV];
+#pragma unroll
+            for (int v = 0; v < FV; ++v) {
+              const bool in = c + fk < ad.rank;  // 8 at a time, as the rank is
+              uf[v] = in ? *reinterpret_cast<const uint4*>(u + c + v * EPV) : make_uint4(0, 0, 0, 0);
+              bf[v] = in ? *reinterpret_cast<const uint4*>(b + c + v * EPV) : make_uint4(0, 0, 0, 0);
+            }
+            G::mma(uf, bf, t);
+          }
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int rt = 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+            acc[m][i][j][r] = (mine >> rt) & 1 ? acc[m][i][j][r] + t[r] : acc[m][i][j][r];
+          }
+        }
+      }
+    }
+  }
+}
+
 // NMAT = 2: gate and up products with the SwiGLU epilogue; NMAT = 1: plain product.
 // Tiles of BMT (128 or 64) token rows x BN weight rows; the waves split them 2 x 2,
 // so a wave holds BMT/64 x 2 MFMA 32x32 blocks per matrix.  BKN: the weights are
 // k-major (element (k, n) at B[k * N + n]); thread t then loads k rows 2p and 2p+1
 // (p = t % (BK/2)) of 16-byte column chunk t / (BK/2) and stores them into the
 // [BN][BK] tile as (k, k+1) pairs, so the tile is the one n-major weights give.
-template <typename T, int NMAT, int BMT, bool BKN>
+// AD: Adapters (see adapters.h), whose share is added to the sums, or NoAdapters.
+template <typename T, int NMAT, int BMT, bool BKN, class AD>
 __global__ __launch_bounds__(kThreads) void grouped_gemm_kernel(const T* __restrict__ A,
                                                                 const int32_t* __restrict__ offsets,
                                                                 const T* __restrict__ B0, const T* __restrict__ B1,
                                                                 T* __restrict__ C, int L, int N, int K,
-                                                                T* __restrict__ Gs, T* __restrict__ Us) {
+                                                                T* __restrict__ Gs, T* __restrict__ Us, AD ad) {
   using G = Gemm<T>;
   constexpr int BK = G::BK, kLd = G::kLd, FV = G::kFragVec;
   constexpr int EPV = 16 / int(sizeof(T));     // elements per 16-byte vector
@@ -232,6 +295,9 @@ __global__ __launch_bounds__(kThreads) void grouped_gemm_kernel(const T* __restr
     if (kt + 1 < nk) sstore(buf ^ 1);
     __syncthreads();
   }
+
+  if constexpr (std::is_same<AD, Adapters>::value)
+    add_adapters<T, NMAT, MI, 2>(ad, expert, row0 + wm * (BMT / 2), rows - wm * (BMT / 2), n0 + wn * 64, N, acc);
 
   // ---- epilogue: 32x32 accumulator layout, lane -> column (lane & 31),
   // register r -> row 8*(r/4) + 4*(lane/32) + r%4 ------------------------------
@@ -524,35 +590,44 @@ moe_status launch(const FfnArgs& a) {
 
 }  // namespace ring
 
-template <typename T, int BMT, bool BKN>
-moe_status launch_bm(const FfnArgs& a) {
+// between(): enqueued between the two products
+template <typename T, int BMT, bool BKN, class AD, class Between>
+moe_status launch_bm(const FfnArgs& a, const AD& gu, const AD& dn, const Between& between) {
   const moe_layer_desc* d = a.d;
   const int L = d->local_count, H = d->hidden, I = d->intermediate;
   const unsigned mslots = unsigned((a.max_pairs + BMT - 1) / BMT + L);
-  MOE_LAUNCH("ffn_gate_up", (grouped_gemm_kernel<T, 2, BMT, BKN>), dim3(mslots, (I + BN - 1) / BN), dim3(kThreads), 0,
+  MOE_LAUNCH("ffn_gate_up", (grouped_gemm_kernel<T, 2, BMT, BKN, AD>), dim3(mslots, (I + BN - 1) / BN), dim3(kThreads), 0,
              a.s, static_cast<const T*>(a.x_sorted), a.offsets, static_cast<const T*>(a.w_gate),
              static_cast<const T*>(a.w_up), static_cast<T*>(a.h), L, I, H, static_cast<T*>(a.g_out),
-             static_cast<T*>(a.u_out));
-  MOE_LAUNCH("ffn_down", (grouped_gemm_kernel<T, 1, BMT, BKN>), dim3(mslots, (H + BN - 1) / BN), dim3(kThreads), 0,
+             static_cast<T*>(a.u_out), gu);
+  const moe_status st = between();
+  if (st != MOE_OK) return st;
+  MOE_LAUNCH("ffn_down", (grouped_gemm_kernel<T, 1, BMT, BKN, AD>), dim3(mslots, (H + BN - 1) / BN), dim3(kThreads), 0,
              a.s, static_cast<const T*>(a.h), a.offsets, static_cast<const T*>(a.w_down),
              static_cast<const T*>(a.w_down), static_cast<T*>(a.y_sorted), L, H, I, static_cast<T*>(nullptr),
-             static_cast<T*>(nullptr));
+             static_cast<T*>(nullptr), dn);
   return MOE_OK;
 }
 
-template <typename T, int BMT>
-moe_status launch_bm(const FfnArgs& a) {
-  return a.d->weight_layout == MOE_WEIGHTS_IN_OUT ? launch_bm<T, BMT, true>(a) : launch_bm<T, BMT, false>(a);
+template <typename T, int BMT, class AD, class Between>
+moe_status launch_bm(const FfnArgs& a, const AD& gu, const AD& dn, const Between& between) {
+  return a.d->weight_layout == MOE_WEIGHTS_IN_OUT ? launch_bm<T, BMT, true>(a, gu, dn, between)
+                                                  : launch_bm<T, BMT, false>(a, gu, dn, between);
 }
 
 // 64-row tiles when 128-row tiles would leave fewer than two blocks per CU (the
 // fp32 layer's 8 experts x ~1024 rows x 256 columns: 144 blocks of 128 rows)
-template <typename T>
-moe_status launch_t(const FfnArgs& a) {
+template <typename T, class AD, class Between>
+moe_status launch_t(const FfnArgs& a, const AD& gu, const AD& dn, const Between& between) {
   const moe_layer_desc* d = a.d;
   const int64_t nb = std::min((d->intermediate + BN - 1) / BN, (d->hidden + BN - 1) / BN);
-  if (((a.max_pairs + BM - 1) / BM + d->local_count) * nb < 512) return launch_bm<T, 64>(a);
-  return launch_bm<T, 128>(a);
+  if (((a.max_pairs + BM - 1) / BM + d->local_count) * nb < 512) return launch_bm<T, 64>(a, gu, dn, between);
+  return launch_bm<T, 128>(a, gu, dn, between);
+}
+
+template <typename T>
+moe_status launch_t(const FfnArgs& a) {
+  return launch_t<T>(a, NoAdapters(), NoAdapters(), [] { return MOE_OK; });
 }
 
 }  // namespace
@@ -561,6 +636,12 @@ moe_status launch_general_ffn(const FfnArgs& a) {
   if (a.d->dtype == MOE_BF16) return launch_t<bf16_t>(a);
   if (ring::supported(a.d, a.max_pairs)) return ring::launch(a);
   return launch_t<float>(a);
+}
+
+moe_status launch_general_adapted(const AdaptedFfnArgs& a) {
+  const Adapters gu = gate_up_adapters(a.f.d, a.ad, a.w), dn = down_adapters(a.f.d, a.ad, a.w);
+  const auto between = [&] { return launch_adapter_shrink(a, true); };
+  return a.f.d->dtype == MOE_BF16 ? launch_t<bf16_t>(a.f, gu, dn, between) : launch_t<float>(a.f, gu, dn, between);
 }
 
 }  // namespace moe

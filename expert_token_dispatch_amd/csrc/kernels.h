@@ -113,6 +113,46 @@ bool skinny_ffn_fits(const moe_layer_desc* d, int64_t max_pairs);
 moe_status launch_skinny_ffn(const FfnArgs& a);
 moe_status launch_general_ffn(const FfnArgs& a);
 
+// ---- low-rank adapters beside the experts' products (adapters.hip) -------------
+// The template argument of a product without adapters.
+struct NoAdapters {};
+
+// The adapters of one product (gate and up, or down): sorted row q of expert e has adapter
+// rid[q] = a (-1: none) and adds u[m][q * ldu ..][0 .. rank) . b[m][a, e, column, 0 .. rank) to column
+// `column` of matrix m; u holds s_a (x A^T), rounded once.  A matrix without adapters has
+// u[m] = NULL.
+struct Adapters {
+  const int32_t* rid;
+  const void* u[2];
+  const void* b[2];  // [count, experts, N, rank]
+  int ldu, rank, experts;
+};
+
+// What the first products leave for the second ones, carved from the caller's workspace.
+struct AdapterScratch {
+  int32_t* rid;  // [P_max] adapter of every sorted row, -1: none
+  void* u_gu;    // [P_max, matrices * rank]: gate's columns, then up's
+  void* u_down;  // [P_max, rank]
+  size_t bytes;
+};
+AdapterScratch carve_adapter_scratch(const moe_layer_desc* d, const moe_adapters* a, int64_t max_pairs, void* base);
+Adapters gate_up_adapters(const moe_layer_desc* d, const moe_adapters* a, const AdapterScratch& w);
+Adapters down_adapters(const moe_layer_desc* d, const moe_adapters* a, const AdapterScratch& w);
+
+struct AdaptedFfnArgs {
+  FfnArgs f;
+  const int32_t* sorted_pairs;
+  const int32_t* adapter_ids;
+  const moe_adapters* ad;
+  AdapterScratch w;
+};
+moe_status launch_adapted_ffn(const AdaptedFfnArgs& a);
+// x A^T (down: h A^T) of every row with an adapter; the first also finds the rows' adapters
+moe_status launch_adapter_shrink(const AdaptedFfnArgs& a, bool down);
+// the experts' products with u B^T added, and between them the down product's shrink
+moe_status launch_adapted_products(const AdaptedFfnArgs& a);
+moe_status launch_general_adapted(const AdaptedFfnArgs& a);
+
 // ---- 4-bit expert weights (packed_weights.hip) -------------------------------
 struct PackArgs {
   int count, out, in;

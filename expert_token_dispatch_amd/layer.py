@@ -151,6 +151,34 @@ class MoELayer:
                                    num_dropped_out)
         return y
 
+    # ---- adapters of many requests beside the experts' weights --------------------
+    def adapted_workspace(self, adapters, stage: int) -> torch.Tensor:
+        has = tuple(getattr(adapters, n + "_a") is not None for n in L.ADAPTED)
+        key = ("adapted", stage, adapters.rank, has)
+        if key not in self._ws:
+            n = L.moe_adapted_workspace_size(self.desc, adapters, stage)
+            self._ws[key] = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
+        return self._ws[key]
+
+    def grouped_ffn_adapted(self, x_sorted, offsets, sorted_pairs, adapters, adapter_ids):
+        """grouped_ffn with each token's adapter (L.make_adapters; adapter_ids [T] int32, -1 for none)."""
+        d = self.desc
+        y_sorted = self._empty((max(self.max_pairs, 1), d.hidden), x_sorted.dtype)
+        L.moe_grouped_ffn_adapted(d, x_sorted, offsets, sorted_pairs, adapter_ids, self.w_gate, self.w_up, self.w_down,
+                                  adapters, y_sorted, self.adapted_workspace(adapters, L.MOE_STAGE_FFN))
+        return y_sorted
+
+    def forward_adapted(self, x, adapters, adapter_ids, y=None, topk_ids_out=None, topk_w_out=None, counts_out=None,
+                        num_dropped_out=None, opts=None):
+        """forward with each token's adapter beside the experts' weights."""
+        d = self.desc
+        if y is None:
+            y = self._empty((d.num_tokens, d.hidden), x.dtype)
+        L.moe_layer_forward_adapted(d, opts, x, adapter_ids, self.w_router, self.b_router, self.w_gate, self.w_up,
+                                    self.w_down, adapters, y, self.adapted_workspace(adapters, L.MOE_STAGE_LAYER),
+                                    topk_ids_out, topk_w_out, counts_out, num_dropped_out)
+        return y
+
     def staged(self, x, logits_in=None, opts=None):
         """The four stage calls one after another; returns every intermediate."""
         r = self.route(x, logits_in=logits_in, want_logits=True, want_topk_logit=True, opts=opts)

@@ -573,6 +573,61 @@ moe_status moe_muon_update(const moe_muon_desc* m, const void* grad, float* mome
                            void* ws, size_t ws_bytes, void* stream);
 
 /* ======================================================================== */
+/* Low-rank adapters of many requests beside the expert weights they share.  */
+/*                                                                           */
+/* A serving batch holds tokens of many fine-tunes of one layer, each the     */
+/* shared weights plus a low-rank pair per expert and projection.  Row q of   */
+/* expert e, whose token has adapter a, goes through (math form)             */
+/*   D(v, A, B) = scale[a] (v A[a,e]^T) B[a,e]^T                              */
+/*   g = x Wg + D(x, gate), u = x Wu + D(x, up), h = silu(g) u                */
+/*   y = h Wd + D(h, down)                                                    */
+/* All sums are float32; scale (v A^T), h and y are rounded to dtype once.    */
+/* What one adapter holds reaches the rows of no other.                       */
+/* ======================================================================== */
+
+/* The adapters, device pointers (16-byte aligned).  Both pointers of a projection may be
+ * NULL: no adapter changes it (not all three).
+ *   count   adapters, 1..65535
+ *   rank    R, a multiple of 8, 8..128 (adapters of smaller rank are padded with zeros)
+ *   scale   [count] float32, or NULL: 1
+ *   gate_a, up_a  [count, L, R, H] dtype;  gate_b, up_b  [count, L, I, R] dtype
+ *   down_a        [count, L, R, I] dtype;  down_b        [count, L, H, R] dtype
+ * whatever layout the layer's own weights have. */
+typedef struct moe_adapters {
+  int32_t count;
+  int32_t rank;
+  const float* scale;
+  const void* gate_a;
+  const void* gate_b;
+  const void* up_a;
+  const void* up_b;
+  const void* down_a;
+  const void* down_b;
+} moe_adapters;
+
+/* Workspace bytes of the calls below: stage MOE_STAGE_FFN for moe_grouped_ffn_adapted,
+ * MOE_STAGE_LAYER for moe_layer_forward_adapted.  Of `a` the count, the rank and which
+ * pointers are NULL count. */
+moe_status moe_adapted_workspace_size(const moe_layer_desc* d, const moe_adapters* a, int32_t stage, size_t* bytes);
+
+/* moe_grouped_ffn with adapters.
+ *   sorted_pairs  device [P_max] int32 (from moe_dispatch): row q is a pair of token sorted_pairs[q] / k
+ *   adapter_ids   device [T] int32: each token's adapter; a value outside [0, count) means none
+ * The rest as moe_grouped_ffn.  MOE_ERR_INVALID_ARG also for adapters outside the ranges above, one
+ * pointer of a pair without the other, or no pair. */
+moe_status moe_grouped_ffn_adapted(const moe_layer_desc* d, const void* x_sorted, const int32_t* offsets,
+                                   const int32_t* sorted_pairs, const int32_t* adapter_ids, const void* w_gate,
+                                   const void* w_up, const void* w_down, const moe_adapters* a, void* y_sorted, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/* moe_layer_forward_ex with adapters (the router has none). */
+moe_status moe_layer_forward_adapted(const moe_layer_desc* d, const moe_route_opts* opts, const void* x,
+                                     const int32_t* adapter_ids, const void* w_router, const float* b_router,
+                                     const void* w_gate, const void* w_up, const void* w_down, const moe_adapters* a,
+                                     void* y, int32_t* topk_ids_out, float* topk_w_out, int32_t* counts_out,
+                                     int64_t* num_dropped_out, void* ws, size_t ws_bytes, void* stream);
+
+/* ======================================================================== */
 /* The join of a block with the residual stream.                             */
 /*                                                                           */
 /* The layer's output is added to a residual stream, and norms stand around   */
