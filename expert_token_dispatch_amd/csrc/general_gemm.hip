@@ -375,11 +375,11 @@ bool supported(const moe_layer_desc* d, int64_t max_pairs) {
 #define MOE_VMCNT(n) __builtin_amdgcn_s_waitcnt(((n) & 0xF) | (((n) >> 4) << 14) | (0x7 << 4) | (0xF << 8))
 
 // Tiles of BMT token rows x BNR weight rows (per matrix); the waves split them 2 x 2.
-template <int NMAT, int BMT, int BNR, bool SAVE>
+template <int NMAT, int BMT, int BNR, bool SAVE, class AD>
 __device__ __forceinline__ void ring_body(const float* __restrict__ A, int a_rows, const int32_t* __restrict__ offsets,
                                           const float* __restrict__ B0, const float* __restrict__ B1,
                                           float* __restrict__ C, int L, int N, int K, float* __restrict__ Gs,
-                                          float* __restrict__ Us, char* lds) {
+                                          float* __restrict__ Us, char* lds, const AD& ad) {
   using S = RS<NMAT, BMT, BNR>;
   constexpr int MI = BMT / 64;   // 32-row blocks per wave
   constexpr int NJ = BNR / 64;   // 32-column blocks per wave and matrix
@@ -492,6 +492,8 @@ __device__ __forceinline__ void ring_body(const float* __restrict__ A, int a_row
         for (int j = 0; j < NJ; ++j) Gemm<float>::mma(af[i], bfr[m][j], acc[m][i][j]);
   }
   MOE_VMCNT(0);  // the ring's last (repeated) loads land before the block ends
+  if constexpr (std::is_same<AD, Adapters>::value)
+    add_adapters<float, NMAT, MI, NJ>(ad, expert, row0 + wm * (BMT / 2), rows - wm * (BMT / 2), n0 + wn * (BNR / 2), N, acc);
 
   // ---- epilogue (the general kernel's): lane -> column (lane & 31), register
   // r -> row 8*(r/4) + 4*(lane/32) + r%4 -----------------------------------------
@@ -520,27 +522,27 @@ __device__ __forceinline__ void ring_body(const float* __restrict__ A, int a_row
 }
 #undef MOE_VMCNT
 
-template <int NMAT, int BMT, int BNR, bool SAVE>
+template <int NMAT, int BMT, int BNR, bool SAVE, class AD>
 __global__ __launch_bounds__(kThreads) void ring_kernel(const float* __restrict__ A, int a_rows,
                                                        const int32_t* __restrict__ offsets,
                                                        const float* __restrict__ B0, const float* __restrict__ B1,
                                                        float* __restrict__ C, int L, int N, int K,
-                                                       float* __restrict__ Gs, float* __restrict__ Us) {
+                                                       float* __restrict__ Gs, float* __restrict__ Us, AD ad) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  ring_body<NMAT, BMT, BNR, SAVE>(A, a_rows, offsets, B0, B1, C, L, N, K, Gs, Us, lds);
+  ring_body<NMAT, BMT, BNR, SAVE>(A, a_rows, offsets, B0, B1, C, L, N, K, Gs, Us, lds, ad);
 }
 
-template <int NMAT, int BMT, int BNR, bool SAVE>
+template <int NMAT, int BMT, int BNR, bool SAVE, class AD>
 moe_status launch_one(const char* name, const float* A, int a_rows, const int32_t* offsets, const float* B0,
-                      const float* B1, float* C, int L, int N, int K, float* Gs, float* Us, hipStream_t s) {
-  auto kern = ring_kernel<NMAT, BMT, BNR, SAVE>;
+                      const float* B1, float* C, int L, int N, int K, float* Gs, float* Us, hipStream_t s, const AD& ad) {
+  auto kern = ring_kernel<NMAT, BMT, BNR, SAVE, AD>;
   constexpr size_t lds = RS<NMAT, BMT, BNR>::kLds;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
   if (e != hipSuccess) return set_error(MOE_ERR_HIP, "%s (float32): LDS attribute: %s", name, hipGetErrorString(e));
   const unsigned mslots = unsigned((a_rows + BMT - 1) / BMT + L);
   MOE_LAUNCH(name, kern, dim3(mslots, (N + BNR - 1) / BNR), dim3(kThreads), lds, s, A, a_rows, offsets, B0, B1, C, L,
-             N, K, Gs, Us);
+             N, K, Gs, Us, ad);
   return MOE_OK;
 }
 
@@ -560,15 +562,17 @@ TileShape pick(int64_t max_pairs, int L, int N) {
   return cost(64, 64) * 10 < cost(128, 128) * 9 ? k64x64 : k128x128;
 }
 
-template <int NMAT, bool SAVE>
+template <int NMAT, bool SAVE, class AD>
 moe_status launch_shape(TileShape sh, const char* name, const float* A, int a_rows, const int32_t* offsets,
                         const float* B0, const float* B1, float* C, int L, int N, int K, float* Gs, float* Us,
-                        hipStream_t s) {
-  if (sh == k64x64) return launch_one<NMAT, 64, 64, SAVE>(name, A, a_rows, offsets, B0, B1, C, L, N, K, Gs, Us, s);
-  return launch_one<NMAT, 128, 128, SAVE>(name, A, a_rows, offsets, B0, B1, C, L, N, K, Gs, Us, s);
+                        hipStream_t s, const AD& ad) {
+  if (sh == k64x64) return launch_one<NMAT, 64, 64, SAVE>(name, A, a_rows, offsets, B0, B1, C, L, N, K, Gs, Us, s, ad);
+  return launch_one<NMAT, 128, 128, SAVE>(name, A, a_rows, offsets, B0, B1, C, L, N, K, Gs, Us, s, ad);
 }
 
-moe_status launch(const FfnArgs& a) {
+// between(): enqueued between the two products
+template <class AD, class Between>
+moe_status launch(const FfnArgs& a, const AD& gu, const AD& dn, const Between& between) {
   const moe_layer_desc* d = a.d;
   const int L = d->local_count, H = d->hidden, I = d->intermediate;
   const int arows = int(a.max_pairs);
@@ -578,14 +582,18 @@ moe_status launch(const FfnArgs& a) {
   const float* wd = static_cast<const float*>(a.w_down);
   float* h = static_cast<float*>(a.h);
   const TileShape sgu = pick(a.max_pairs, L, I), sdn = pick(a.max_pairs, L, H);
-  moe_status st = a.g_out != nullptr
-                      ? launch_shape<2, true>(sgu, "ffn_gate_up", x, arows, a.offsets, wg, wu, h, L, I, H,
-                                              static_cast<float*>(a.g_out), static_cast<float*>(a.u_out), a.s)
-                      : launch_shape<2, false>(sgu, "ffn_gate_up", x, arows, a.offsets, wg, wu, h, L, I, H, nullptr,
-                                               nullptr, a.s);
+  moe_status st;
+  if (std::is_same<AD, NoAdapters>::value && a.g_out != nullptr)
+    st = launch_shape<2, std::is_same<AD, NoAdapters>::value>(sgu, "ffn_gate_up", x, arows, a.offsets, wg, wu, h, L, I, H,
+                                                              static_cast<float*>(a.g_out), static_cast<float*>(a.u_out),
+                                                              a.s, gu);
+  else
+    st = launch_shape<2, false>(sgu, "ffn_gate_up", x, arows, a.offsets, wg, wu, h, L, I, H, nullptr, nullptr, a.s, gu);
+  if (st != MOE_OK) return st;
+  st = between();
   if (st != MOE_OK) return st;
   return launch_shape<1, false>(sdn, "ffn_down", h, arows, a.offsets, wd, wd, static_cast<float*>(a.y_sorted), L, H, I,
-                                nullptr, nullptr, a.s);
+                                nullptr, nullptr, a.s, dn);
 }
 
 }  // namespace ring
@@ -634,14 +642,16 @@ moe_status launch_t(const FfnArgs& a) {
 
 moe_status launch_general_ffn(const FfnArgs& a) {
   if (a.d->dtype == MOE_BF16) return launch_t<bf16_t>(a);
-  if (ring::supported(a.d, a.max_pairs)) return ring::launch(a);
+  if (ring::supported(a.d, a.max_pairs)) return ring::launch(a, NoAdapters(), NoAdapters(), [] { return MOE_OK; });
   return launch_t<float>(a);
 }
 
 moe_status launch_general_adapted(const AdaptedFfnArgs& a) {
   const Adapters gu = gate_up_adapters(a.f.d, a.ad, a.w), dn = down_adapters(a.f.d, a.ad, a.w);
   const auto between = [&] { return launch_adapter_shrink(a, true); };
-  return a.f.d->dtype == MOE_BF16 ? launch_t<bf16_t>(a.f, gu, dn, between) : launch_t<float>(a.f, gu, dn, between);
+  if (a.f.d->dtype == MOE_BF16) return launch_t<bf16_t>(a.f, gu, dn, between);
+  if (ring::supported(a.f.d, a.f.max_pairs)) return ring::launch(a.f, gu, dn, between);
+  return launch_t<float>(a.f, gu, dn, between);
 }
 
 }  // namespace moe

@@ -18,7 +18,9 @@
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
+#include "adapters.h"
 #include "big_tile.h"
 #include "kernels.h"
 
@@ -448,16 +450,153 @@ __device__ __forceinline__ f32x4_t* part_ptr(float* __restrict__ parts, int pslo
   return reinterpret_cast<f32x4_t*>(parts + size_t(pslot) * (kPartBytes / sizeof(float)));
 }
 
+// ---- adapters.  A tile's sums get the adapters' share before they are rounded: sixteen to
+// 128 more k of u and of the adapter's B, for one adapter of the tile's rows after another (one or
+// two in a prompt, whose requests follow each other).  Of every rank chunk of up to 64, the tile's rows of u
+// go to LDS once and an adapter's rows of B (the tile's columns) after them, with the next
+// adapter's already in flight; the products of all rows are formed apart and added where the row
+// has the adapter, so that a row's sum, and what a broken adapter spoils, do not depend on the
+// rows beside it.  LDS rows of 64 values and 16 bytes, so that 16 lanes' reads of 16 rows fall
+// in different banks.
+constexpr int kChunkRank = 64, kAdRow = kChunkRank * 2 + 16;
+
+template <int NMAT, bool WIDE, int NW>
+__device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int row0, int rows, int n0, int N, char* lds,
+                                             f32x16_t (&acc)[4][16 / NW]) {
+  using S = Shape<WIDE, NW>;
+  constexpr int NB = S::NB, kThreads = S::kThreads, kIds = S::kA / 64;
+  constexpr int kBLoads = S::kB * (kChunkRank / 8) / kThreads;  // 16-byte pieces of a B chunk a thread
+  char* su = lds;                             // [NMAT][kA] rows of u
+  char* sb = lds + NMAT * S::kA * kAdRow;     // [kB] rows of B
+  static_assert((NMAT * S::kA + S::kB) * kAdRow <= int(kLoopLdsMax), "u and B in the loop's LDS");
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int wm = S::wm(wave), wn = S::wn(wave), fr = lane & 31, g = lane >> 5;
+  int id[kIds];     // rows lane, 64 + lane, ... of the tile: what the block has to do
+  int mine_id[4];   // row fr of the wave's four row blocks
+#pragma unroll
+  for (int v = 0; v < kIds; ++v) id[v] = v * 64 + lane < rows ? ad.rid[row0 + v * 64 + lane] : -1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = wm * 128 + i * 32 + fr;
+    mine_id[i] = r < rows ? ad.rid[row0 + r] : -1;
+  }
+  // the next adapter of the block's rows, in the order of their first rows; -1: none left
+  auto next = [&](int (&left)[kIds]) {
+    int cur = -1;
+#pragma unroll
+    for (int v = 0; v < kIds; ++v) {
+      const uint64_t some = __ballot(left[v] >= 0);
+      if (cur < 0 && some != 0) cur = __builtin_amdgcn_readlane(left[v], __builtin_ctzll(some));
+    }
+#pragma unroll
+    for (int v = 0; v < kIds; ++v)
+      if (left[v] == cur) left[v] = -1;
+    return cur;
+  };
+  MOE_LGKMCNT0();
+  block_barrier();  // every wave is done reading the last stage
+  for (int c0 = 0; c0 < ad.rank; c0 += kChunkRank) {
+    const int cr = min(kChunkRank, ad.rank - c0);  // a multiple of 8
+    const int nkc = (cr + 15) / 16;                // k chunks of 16; the last one's upper half may be zeros
+    const u32x4_t zero = {0, 0, 0, 0};
+    int left[kIds];
+#pragma unroll
+    for (int v = 0; v < kIds; ++v) left[v] = id[v];
+    int cur = next(left);
+    if (cur < 0) return;  // no row of the tile has an adapter
+    // piece p of a thread: row (tid + p * kThreads) / 8 of the tile's B rows, 16-byte piece % 8 of its chunk
+    u32x4_t pb[kBLoads];
+    auto load_b = [&](int a) {
+#pragma unroll
+      for (int p = 0; p < kBLoads; ++p) {
+        const int v = tid + p * kThreads, br = v >> 3, c = (v & 7) * 8;
+        const int m = NMAT == 2 && br >= S::kB / 2 ? 1 : 0;
+        const int col = min(n0 + br - m * (S::kB / 2), N - 1);
+        pb[p] = c < cr && ad.u[m] != nullptr
+                    ? *reinterpret_cast<const u32x4_t*>(adapter_b<bf16_t>(ad, m, a, expert, col, N) + c0 + c)
+                    : zero;
+      }
+    };
+    load_b(cur);
+    if (c0 > 0) {
+      MOE_LGKMCNT0();
+      block_barrier();  // the chunk before has been read
+    }
+    for (int v = tid; v < NMAT * S::kA * (kChunkRank / 8); v += kThreads) {
+      const int c = (v & 7) * 8, r = (v >> 3) & (S::kA - 1), m = (v >> 3) / S::kA;
+      if (c >= nkc * 16 || r >= rows || ad.u[m] == nullptr) continue;
+      const u32x4_t w = c < cr ? *reinterpret_cast<const u32x4_t*>(adapter_u<bf16_t>(ad, m, row0 + r) + c0 + c) : zero;
+      *reinterpret_cast<u32x4_t*>(su + (m * S::kA + r) * kAdRow + c * 2) = w;
+    }
+    for (bool first = true; cur >= 0; first = false) {
+      if (!first) {
+        MOE_LGKMCNT0();
+        block_barrier();  // the adapter before has been read
+      }
+#pragma unroll
+      for (int p = 0; p < kBLoads; ++p) {
+        const int v = tid + p * kThreads;
+        *reinterpret_cast<u32x4_t*>(sb + (v >> 3) * kAdRow + (v & 7) * 16) = pb[p];
+      }
+      const int following = next(left);
+      if (following >= 0) load_b(following);
+      MOE_LGKMCNT0();
+      block_barrier();
+#pragma unroll
+      for (int m = 0; m < NMAT; ++m) {
+        if (ad.u[m] == nullptr) continue;
+        constexpr int NJ = NB / NMAT;
+        bf16x8_t fb[NJ][kChunkRank / 16];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int kc = 0; kc < kChunkRank / 16; ++kc)
+            if (kc < nkc) {
+              const int br = m * (S::kB / 2) + (wn * NJ + j) * 32 + fr;
+              fb[j][kc] = *reinterpret_cast<const bf16x8_t*>(sb + br * kAdRow + (2 * kc + g) * 16);
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool own = mine_id[i] == cur;
+          if (__ballot(own) == 0) continue;
+          const char* ur = su + (m * S::kA + wm * 128 + i * 32 + fr) * kAdRow + g * 16;
+          bf16x8_t fa[kChunkRank / 16];
+#pragma unroll
+          for (int kc = 0; kc < kChunkRank / 16; ++kc)
+            if (kc < nkc) fa[kc] = *reinterpret_cast<const bf16x8_t*>(ur + kc * 32);
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            f32x16_t t;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) t[r] = 0.0f;
+#pragma unroll
+            for (int kc = 0; kc < kChunkRank / 16; ++kc)
+              if (kc < nkc) t = Bf16::mma(fb[j][kc], fa[kc], t);
+            // lane -> token row: the whole column of sums is one row's
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][m * NJ + j][r] = own ? acc[i][m * NJ + j][r] + t[r] : acc[i][m * NJ + j][r];
+          }
+        }
+      }
+      cur = following;
+    }
+  }
+}
+
 // One tile (or one K piece of it): the main loop, then the epilogue or the piece write-out.
-template <int NMAT, bool WIDE, int NW, int EP, bool BKN, bool AKM>
+// AD: Adapters, whose share the tile (its first piece) adds, or NoAdapters.
+template <int NMAT, bool WIDE, int NW, int EP, bool BKN, bool AKM, class AD>
 __device__ __forceinline__ void tile_body(const Operands& op, bf16_t* __restrict__ C, int N, int kcat, const Job& jb,
                                           float* __restrict__ parts, char* lds, bf16_t* __restrict__ Gs,
-                                          bf16_t* __restrict__ Us) {
+                                          bf16_t* __restrict__ Us, const AD& ad) {
   using S = Shape<WIDE, NW>;
   constexpr int NB = S::NB, kThreads = S::kThreads;
   constexpr int ON = NMAT == 2 ? BNE / 2 : BNE;
   const int row0 = jb.row0, rows = jb.rows, n0 = jb.n0 * ON, tid = threadIdx.x;
   const auto epi = [&](f32x16_t (&acc)[4][NB]) {
+    if constexpr (std::is_same<AD, Adapters>::value) {
+      if (jb.part == 0) add_adapters<NMAT, WIDE, NW>(ad, jb.expert, row0, rows, n0, N, lds, acc);
+    }
     if (jb.nparts > 1) {
       // one piece of a split tile: park the accumulators for fixup_kernel
       f32x4_t* dst = part_ptr(parts, jb.pslot);
@@ -519,17 +658,17 @@ __global__ __launch_bounds__(NW * 64) void wgrad_kernel(WgradOps w, const int32_
   op.b_rows = n;
   op.ldb = w.ldb;
   bf16_t* Ce = (z ? w.C1 : w.C0) + size_t(e) * w.M * w.N;
-  tile_body<1, false, NW, kWgrad, true, true>(op, Ce, w.N, 0, jb, nullptr, lds, nullptr, nullptr);
+  tile_body<1, false, NW, kWgrad, true, true>(op, Ce, w.N, 0, jb, nullptr, lds, nullptr, nullptr, NoAdapters());
 }
 
 // BKN, kcat: the weight operand's layout and K split (see tile_body)
-template <int NMAT, int NW, int EP, bool BKN>
+template <int NMAT, int NW, int EP, bool BKN, class AD>
 __global__ __launch_bounds__(NW * 64) void gemm_kernel(const bf16_t* __restrict__ A, const int32_t* __restrict__ offsets,
                                                        const bf16_t* __restrict__ B0, const bf16_t* __restrict__ B1,
                                                        bf16_t* __restrict__ C, int L, int N, int K, int kcat, int a_rows,
                                                         const int32_t* __restrict__ tpre, int cpx, int smax,
                                                         float* __restrict__ parts, bf16_t* __restrict__ Gs,
-                                                        bf16_t* __restrict__ Us) {
+                                                        bf16_t* __restrict__ Us, AD ad) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   static_assert(EP != kWgrad, "the weight-gradient products run wgrad_kernel");
   constexpr int ON = NMAT == 2 ? BNE / 2 : BNE;  // output columns per regular tile
@@ -558,9 +697,9 @@ __global__ __launch_bounds__(NW * 64) void gemm_kernel(const bf16_t* __restrict_
   op.b_rows = BKN ? kw : N;
   op.ldb = BKN ? N : kw;
   if (jb.wide)
-    tile_body<NMAT, true, NW, EP, BKN, false>(op, C, N, kcat, jb, parts, lds, Gs, Us);
+    tile_body<NMAT, true, NW, EP, BKN, false>(op, C, N, kcat, jb, parts, lds, Gs, Us, ad);
   else
-    tile_body<NMAT, false, NW, EP, BKN, false>(op, C, N, kcat, jb, parts, lds, Gs, Us);
+    tile_body<NMAT, false, NW, EP, BKN, false>(op, C, N, kcat, jb, parts, lds, Gs, Us, ad);
 }
 
 
@@ -651,19 +790,21 @@ bool splits(int K) { return K / BK >= kSplitMinSteps; }
 // skewed layer -1.5%); four for longer ones (mixtral-like layer: eight are 1% slower).
 constexpr int kEightWaveSteps = 64;
 
-template <int NMAT, int NW, int EP, bool BKN>
+template <int NMAT, int NW, int EP, bool BKN, class AD>
 moe_status launch_nws(const char* name, const bf16_t* A, const int32_t* offsets, const bf16_t* B0, const bf16_t* B1,
                       bf16_t* C, int L, int N, int K, int kcat, int64_t max_pairs, const int32_t* tpre, float* parts,
-                      hipStream_t s, bf16_t* Gs, bf16_t* Us);
+                      hipStream_t s, bf16_t* Gs, bf16_t* Us, const AD& ad);
 
-template <int NMAT, int NW>
+template <int NMAT, int NW, class AD>
 moe_status launch_nw(const char* name, const bf16_t* A, const int32_t* offsets, const bf16_t* B0, const bf16_t* B1,
                      bf16_t* C, int L, int N, int K, int kcat, bool bkn, int64_t max_pairs, const int32_t* tpre,
-                     float* parts, hipStream_t s, bf16_t* Gs, bf16_t* Us, int ep) {
+                     float* parts, hipStream_t s, bf16_t* Gs, bf16_t* Us, int ep, const AD& ad) {
 #define MOE_NWS(EP_, PARTS_)                                                                                      \
-  (bkn ? launch_nws<NMAT, NW, EP_, true>(name, A, offsets, B0, B1, C, L, N, K, kcat, max_pairs, tpre, PARTS_, s, Gs, Us) \
-       : launch_nws<NMAT, NW, EP_, false>(name, A, offsets, B0, B1, C, L, N, K, kcat, max_pairs, tpre, PARTS_, s, Gs, Us))
-  if constexpr (NMAT == 2) {
+  (bkn ? launch_nws<NMAT, NW, EP_, true>(name, A, offsets, B0, B1, C, L, N, K, kcat, max_pairs, tpre, PARTS_, s, Gs, Us, ad) \
+       : launch_nws<NMAT, NW, EP_, false>(name, A, offsets, B0, B1, C, L, N, K, kcat, max_pairs, tpre, PARTS_, s, Gs, Us, ad))
+  if constexpr (std::is_same<AD, Adapters>::value) {
+    // adapters stand beside the plain products alone
+  } else if constexpr (NMAT == 2) {
     if (ep == kSave) return MOE_NWS(kSave, parts);
   } else {
     if (ep == kSwigluBwd) return MOE_NWS(kSwigluBwd, nullptr);
@@ -674,12 +815,12 @@ moe_status launch_nw(const char* name, const bf16_t* A, const int32_t* offsets, 
 
 // EP: the epilogue (kSave: the training forward's gate/up, which also writes the
 // pre-activations; kSwigluBwd: the backward's down dgrad, never split along K)
-template <int NMAT, int NW, int EP, bool BKN>
+template <int NMAT, int NW, int EP, bool BKN, class AD>
 moe_status launch_nws(const char* name, const bf16_t* A, const int32_t* offsets, const bf16_t* B0, const bf16_t* B1,
                       bf16_t* C, int L, int N, int K, int kcat, int64_t max_pairs, const int32_t* tpre, float* parts,
-                      hipStream_t s, bf16_t* Gs, bf16_t* Us) {
+                      hipStream_t s, bf16_t* Gs, bf16_t* Us, const AD& ad) {
   constexpr int kThreads = NW * 64;
-  auto kern = gemm_kernel<NMAT, NW, EP, BKN>;
+  auto kern = gemm_kernel<NMAT, NW, EP, BKN, AD>;
   constexpr size_t lds = lds_bytes<NMAT>();
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
                                      int(lds));
@@ -693,7 +834,7 @@ moe_status launch_nws(const char* name, const bf16_t* A, const int32_t* offsets,
   const int64_t per_xcd = (tiles + kXcds - 1) / kXcds + (smax > 1 ? kMaxParts - kMaxTail : 0);
   // A holds max_pairs rows (the caller's x_sorted or h)
   MOE_LAUNCH(name, kern, dim3(unsigned(per_xcd * kXcds)), dim3(kThreads), lds, s, A, offsets, B0, B1, C, L, N, K, kcat,
-             int(max_pairs), tpre, cpx, smax, parts, Gs, Us);
+             int(max_pairs), tpre, cpx, smax, parts, Gs, Us, ad);
   if (smax > 1) {
     const char* fname = std::strcmp(name, "ffn_gate_up") == 0         ? "ffn_gate_up_fixup"
                         : std::strcmp(name, "ffn_gate_up_dgrad") == 0 ? "ffn_gate_up_dgrad_fixup"
@@ -720,13 +861,14 @@ moe_status launch_wgrad_nw(const char* name, const moe_layer_desc* d, const int3
 
 // bkn: the weight operand is k-major (element (k, n) at B[k * N + n]); kcat > 0: a
 // one-matrix product over B0 for the first 64 * kcat of K, then B1 (see tile_body)
-template <int NMAT>
+template <int NMAT, class AD = NoAdapters>
 moe_status launch(const char* name, const bf16_t* A, const int32_t* offsets, const bf16_t* B0, const bf16_t* B1,
                   bf16_t* C, int L, int N, int K, int kcat, bool bkn, int64_t max_pairs, const int32_t* tpre,
-                  float* parts, hipStream_t s, bf16_t* Gs = nullptr, bf16_t* Us = nullptr, int ep = kPlain) {
+                  float* parts, hipStream_t s, bf16_t* Gs = nullptr, bf16_t* Us = nullptr, int ep = kPlain,
+                  const AD& ad = AD()) {
   if (K / BK < kEightWaveSteps)
-    return launch_nw<NMAT, 8>(name, A, offsets, B0, B1, C, L, N, K, kcat, bkn, max_pairs, tpre, parts, s, Gs, Us, ep);
-  return launch_nw<NMAT, 4>(name, A, offsets, B0, B1, C, L, N, K, kcat, bkn, max_pairs, tpre, parts, s, Gs, Us, ep);
+    return launch_nw<NMAT, 8>(name, A, offsets, B0, B1, C, L, N, K, kcat, bkn, max_pairs, tpre, parts, s, Gs, Us, ep, ad);
+  return launch_nw<NMAT, 4>(name, A, offsets, B0, B1, C, L, N, K, kcat, bkn, max_pairs, tpre, parts, s, Gs, Us, ep, ad);
 }
 
 }  // namespace big
@@ -806,10 +948,12 @@ moe_status launch_big_backward_wgrad(const char* name, const moe_layer_desc* d, 
   return big::launch_wgrad_nw<4>(name, d, offsets, w, Z, s);
 }
 
-moe_status launch_grouped_ffn(const FfnArgs& a) {
-  if (a.max_pairs <= 0) return MOE_OK;
+namespace {
+
+// Both products on the large tile; between(): enqueued between them.
+template <class AD, class Between>
+moe_status launch_big_ffn(const FfnArgs& a, const AD& gu, const AD& dn, const Between& between) {
   const moe_layer_desc* d = a.d;
-  if (!use_big(d, a.max_pairs)) return launch_small(a);
   const int L = d->local_count, H = d->hidden, I = d->intermediate;
   const bf16_t* x = static_cast<const bf16_t*>(a.x_sorted);
   bf16_t* h = static_cast<bf16_t*>(a.h);
@@ -826,11 +970,29 @@ moe_status launch_grouped_ffn(const FfnArgs& a) {
   moe_status st = big::launch<2>("ffn_gate_up", x, a.offsets, static_cast<const bf16_t*>(a.w_gate),
                                  static_cast<const bf16_t*>(a.w_up), h, L, I, H, 0, kn, a.max_pairs, pre, parts, a.s,
                                  static_cast<bf16_t*>(a.g_out), static_cast<bf16_t*>(a.u_out),
-                                 a.g_out != nullptr ? big::kSave : big::kPlain);
+                                 a.g_out != nullptr ? big::kSave : big::kPlain, gu);
+  if (st != MOE_OK) return st;
+  st = between();
   if (st != MOE_OK) return st;
   return big::launch<1>("ffn_down", h, a.offsets, static_cast<const bf16_t*>(a.w_down),
                         static_cast<const bf16_t*>(a.w_down), static_cast<bf16_t*>(a.y_sorted), L, H, I, 0, kn,
-                        a.max_pairs, pre + L + 1, parts, a.s);
+                        a.max_pairs, pre + L + 1, parts, a.s, nullptr, nullptr, big::kPlain, dn);
+}
+
+}  // namespace
+
+moe_status launch_grouped_ffn(const FfnArgs& a) {
+  if (a.max_pairs <= 0) return MOE_OK;
+  if (!use_big(a.d, a.max_pairs)) return launch_small(a);
+  return launch_big_ffn(a, NoAdapters(), NoAdapters(), [] { return MOE_OK; });
+}
+
+moe_status launch_adapted_products(const AdaptedFfnArgs& a) {
+  const moe_layer_desc* d = a.f.d;
+  if (use_big(d, a.f.max_pairs))
+    return launch_big_ffn(a.f, gate_up_adapters(d, a.ad, a.w), down_adapters(d, a.ad, a.w),
+                          [&] { return launch_adapter_shrink(a, true); });
+  return skinny_ffn_fits(d, a.f.max_pairs) ? launch_skinny_adapted(a) : launch_general_adapted(a);
 }
 
 }  // namespace moe

@@ -151,6 +151,8 @@ moe_status launch_adapted_ffn(const AdaptedFfnArgs& a);
 moe_status launch_adapter_shrink(const AdaptedFfnArgs& a, bool down);
 // the experts' products with u B^T added, and between them the down product's shrink
 moe_status launch_adapted_products(const AdaptedFfnArgs& a);
+// what it picks from, by the sizes as launch_grouped_ffn does
+moe_status launch_skinny_adapted(const AdaptedFfnArgs& a);
 moe_status launch_general_adapted(const AdaptedFfnArgs& a);
 
 // ---- 4-bit expert weights (packed_weights.hip) -------------------------------

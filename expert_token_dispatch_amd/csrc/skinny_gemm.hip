@@ -4,7 +4,9 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
+#include "adapters.h"
 #include "ffn_common.h"
 #include "kernels.h"
 
@@ -37,16 +39,81 @@ bool supported(int K) { return K % 32 == 0; }
 template <int NMAT>
 constexpr int cols_per_block() { return NMAT == 2 ? 64 : 128; }
 
+// Adds the adapters' share to the sums of one row block (16 rows from row0, n of them there) and
+// the wave's two streams of 16 columns; layout of the sums: lane -> column lane & 15, register i ->
+// row 4 (lane / 16) + i.  A decode batch's rows have adapters of their own, so four adapters are
+// in flight together; each one's products take all the rows and are added to its own.
+template <int NMAT>
+__device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int row0, int n, int col0, int N, f32x4_t& acc0,
+                                             f32x4_t& acc1) {
+  constexpr int kFlight = 4;
+  const int lane = threadIdx.x & 63, r16 = lane & 15, kg = (lane >> 4) * 8;
+  const int id = r16 < n ? ad.rid[row0 + r16] : -1;
+  uint32_t todo = uint32_t(__ballot(id >= 0)) & 0xFFFF;
+  const int row = row0 + min(r16, n - 1);
+  const int col[2] = {min(col0 + r16, N - 1), min(NMAT == 2 ? col0 + r16 : col0 + 16 + r16, N - 1)};
+  while (todo != 0) {
+    uint32_t mine[kFlight];
+    const bf16_t* b[kFlight][2];
+    f32x4_t t[kFlight][2];
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      // past the last adapter its products are repeated, for no row
+      const int cur = todo != 0 || f == 0 ? __builtin_amdgcn_readlane(id, __builtin_ctz(todo)) : -1;
+      mine[f] = cur >= 0 ? uint32_t(__ballot(id == cur)) & 0xFFFF : 0;
+      todo &= ~mine[f];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int m = NMAT == 2 ? s : 0;
+        b[f][s] = cur >= 0 && ad.u[m] != nullptr ? adapter_b<bf16_t>(ad, m, cur, expert, col[s], N) : b[0][s];
+        t[f][s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m) {
+      if (ad.u[m] == nullptr) continue;
+      const bf16_t* u = adapter_u<bf16_t>(ad, m, row);
+      for (int c0 = 0; c0 < ad.rank; c0 += 32) {
+        const int c = c0 + kg;
+        const bool in = c < ad.rank;  // eight at a time, as the rank is
+        const u32x4_t zero = {0, 0, 0, 0};
+        const bf16x8_t uf = __builtin_bit_cast(bf16x8_t, in ? *reinterpret_cast<const u32x4_t*>(u + c) : zero);
+        u32x4_t bf[kFlight][2];
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f)
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            if (NMAT == 1 || s == m) bf[f][s] = in ? *reinterpret_cast<const u32x4_t*>(b[f][s] + c) : zero;
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f)
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            if (NMAT == 1 || s == m)
+              t[f][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(uf, __builtin_bit_cast(bf16x8_t, bf[f][s]), t[f][s], 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool own = (mine[f] >> (4 * (lane >> 4) + i)) & 1;
+        acc0[i] = own ? acc0[i] + t[f][0][i] : acc0[i];
+        acc1[i] = own ? acc1[i] + t[f][1][i] : acc1[i];
+      }
+  }
+}
+
 // SAVE (gate/up of the training forward): the gate and up pre-activations go to Gs, Us too.
 // BKN: the weights are k-major (element (k, n) at B[k * N + n]): each lane then loads
 // 16 bytes of one k row (a 32 x 16 block of a stream per step is 32 rows of 32 bytes),
 // the wave parks the block in its own 1 KB of LDS and reads the fragments back with
 // transposing reads, so the MFMAs see the same operands as with n-major weights.
-template <int NMAT, bool SAVE, bool BKN>
+// AD: Adapters, whose share is added to the sums, or NoAdapters.
+template <int NMAT, bool SAVE, bool BKN, class AD>
 __global__ __launch_bounds__(kThreads) void gemm_kernel(const bf16_t* __restrict__ A, const int32_t* __restrict__ offsets,
                                                         const bf16_t* __restrict__ B0, const bf16_t* __restrict__ B1,
                                                         bf16_t* __restrict__ C, int N, int K, bf16_t* __restrict__ Gs,
-                                                        bf16_t* __restrict__ Us) {
+                                                        bf16_t* __restrict__ Us, AD ad) {
   constexpr int kWaveCols = NMAT == 2 ? 16 : 32;
   constexpr int kPipe = 4;
   const int expert = blockIdx.y;
@@ -173,6 +240,12 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(const bf16_t* __restrict
         }
       }
     }
+    if constexpr (std::is_same<AD, Adapters>::value) {
+#pragma unroll
+      for (int rb = 0; rb < kMaxRowBlocks; ++rb)
+        if (rb < nrb)
+          add_adapters<NMAT>(ad, expert, seg0 + m0 + rb * 16, min(16, seg_n - m0 - rb * 16), col0, N, acc[0][rb], acc[1][rb]);
+    }
     // 16x16 layout: lane -> weight row (column of the output) lane & 15,
     // register i -> token row 4*(lane/16) + i of the row block
 #pragma unroll
@@ -205,24 +278,44 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(const bf16_t* __restrict
 }
 
 // bkn: k-major weights (see gemm_kernel)
-template <int NMAT>
+template <int NMAT, class AD>
 moe_status launch(const char* name, const bf16_t* A, const int32_t* offsets, const bf16_t* B0, const bf16_t* B1,
-                  bf16_t* C, int L, int N, int K, bool bkn, hipStream_t s, bf16_t* Gs = nullptr, bf16_t* Us = nullptr) {
+                  bf16_t* C, int L, int N, int K, bool bkn, hipStream_t s, bf16_t* Gs, bf16_t* Us, const AD& ad) {
   const dim3 grid(unsigned((N + cols_per_block<NMAT>() - 1) / cols_per_block<NMAT>()), unsigned(L));
 #define MOE_SKINNY(SAVE_)                                                                                          \
   do {                                                                                                             \
     if (bkn)                                                                                                       \
-      MOE_LAUNCH(name, (gemm_kernel<NMAT, SAVE_, true>), grid, dim3(kThreads), 0, s, A, offsets, B0, B1, C, N, K, Gs, Us); \
+      MOE_LAUNCH(name, (gemm_kernel<NMAT, SAVE_, true, AD>), grid, dim3(kThreads), 0, s, A, offsets, B0, B1, C, N, K, Gs, Us, ad); \
     else                                                                                                           \
-      MOE_LAUNCH(name, (gemm_kernel<NMAT, SAVE_, false>), grid, dim3(kThreads), 0, s, A, offsets, B0, B1, C, N, K, Gs, Us); \
+      MOE_LAUNCH(name, (gemm_kernel<NMAT, SAVE_, false, AD>), grid, dim3(kThreads), 0, s, A, offsets, B0, B1, C, N, K, Gs, Us, ad); \
   } while (0)
-  if (NMAT == 2 && Gs != nullptr) {
-    MOE_SKINNY(true);
-  } else {
-    MOE_SKINNY(false);
+  if constexpr (NMAT == 2 && std::is_same<AD, NoAdapters>::value) {
+    if (Gs != nullptr) {
+      MOE_SKINNY(true);
+      return MOE_OK;
+    }
   }
+  MOE_SKINNY(false);
 #undef MOE_SKINNY
   return MOE_OK;
+}
+
+// between(): enqueued between the two products
+template <class AD, class Between>
+moe_status launch_both(const FfnArgs& a, const AD& gu, const AD& dn, const Between& between) {
+  const moe_layer_desc* d = a.d;
+  const int L = d->local_count, H = d->hidden, I = d->intermediate;
+  bf16_t* h = static_cast<bf16_t*>(a.h);
+  const bool kn = d->weight_layout == MOE_WEIGHTS_IN_OUT;
+  moe_status st = launch<2>("ffn_gate_up", static_cast<const bf16_t*>(a.x_sorted), a.offsets,
+                            static_cast<const bf16_t*>(a.w_gate), static_cast<const bf16_t*>(a.w_up), h, L, I, H, kn, a.s,
+                            static_cast<bf16_t*>(a.g_out), static_cast<bf16_t*>(a.u_out), gu);
+  if (st != MOE_OK) return st;
+  st = between();
+  if (st != MOE_OK) return st;
+  return launch<1>("ffn_down", h, a.offsets, static_cast<const bf16_t*>(a.w_down), static_cast<const bf16_t*>(a.w_down),
+                   static_cast<bf16_t*>(a.y_sorted), L, H, I, kn, a.s, static_cast<bf16_t*>(nullptr),
+                   static_cast<bf16_t*>(nullptr), dn);
 }
 
 }  // namespace skinny
@@ -235,16 +328,12 @@ bool skinny_ffn_fits(const moe_layer_desc* d, int64_t max_pairs) {
 }
 
 moe_status launch_skinny_ffn(const FfnArgs& a) {
-  const moe_layer_desc* d = a.d;
-  const int L = d->local_count, H = d->hidden, I = d->intermediate;
-  bf16_t* h = static_cast<bf16_t*>(a.h);
-  const bool kn = d->weight_layout == MOE_WEIGHTS_IN_OUT;
-  moe_status st = skinny::launch<2>("ffn_gate_up", static_cast<const bf16_t*>(a.x_sorted), a.offsets,
-                                    static_cast<const bf16_t*>(a.w_gate), static_cast<const bf16_t*>(a.w_up), h, L, I,
-                                    H, kn, a.s, static_cast<bf16_t*>(a.g_out), static_cast<bf16_t*>(a.u_out));
-  if (st != MOE_OK) return st;
-  return skinny::launch<1>("ffn_down", h, a.offsets, static_cast<const bf16_t*>(a.w_down),
-                           static_cast<const bf16_t*>(a.w_down), static_cast<bf16_t*>(a.y_sorted), L, H, I, kn, a.s);
+  return skinny::launch_both(a, NoAdapters(), NoAdapters(), [] { return MOE_OK; });
+}
+
+moe_status launch_skinny_adapted(const AdaptedFfnArgs& a) {
+  return skinny::launch_both(a.f, gate_up_adapters(a.f.d, a.ad, a.w), down_adapters(a.f.d, a.ad, a.w),
+                             [&] { return launch_adapter_shrink(a, true); });
 }
 
 }  // namespace moe

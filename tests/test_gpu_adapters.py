@@ -147,7 +147,7 @@ def test_projections_without_adapters(has, P, dtype):
 
 @pytest.mark.parametrize("dtype", ("bf16", "f32"))
 @pytest.mark.parametrize("layout", ("out_in", "in_out"))
-@pytest.mark.parametrize("shape", [(64, 96, 4, 30), (256, 512, 4, 1100), (136, 264, 3, 200), (512, 256, 8, 2000)])
+@pytest.mark.parametrize("shape", [(64, 96, 4, 30), (256, 512, 4, 1100), (136, 264, 3, 200), (4096, 128, 2, 600), (512, 256, 8, 2000)])
 def test_without_an_adapter_a_row_is_the_plain_experts(shape, layout, dtype):
     H, I, Lc, P = shape
     c = Case(H, I, Lc, P, 16, 3, dtype, layout, kind="none")
