@@ -5,14 +5,20 @@
 //
 // A block takes 16 RB rows of one expert and finds the adapters among them (ids come in any
 // order; tokens of one request follow each other in a prompt and are strangers in a decode
-// batch).  For one adapter after another it multiplies all its rows by that adapter's A and
-// keeps the rows that are its own: a row costs no more than its block's adapters, and an
-// adapter's A is read once a block.  A non-finite value in one request's adapter reaches no
-// other request.  The eight waves split K, 16-byte vectors straight from memory into MFMA
-// fragments, and their sums meet in LDS in a fixed order.
+// batch).  For one adapter after another it multiplies the rows that have it by its A; the rows
+// that have not are not loaded.  A non-finite value in one request's adapter reaches no other
+// request, and a row's sums do not depend on its neighbours.
+//
+// What bounds it: in a decode batch reading each adapter's A once, in a prompt reading x (h for
+// the down product) once more than the experts' own products do.  Both operands come by direct
+// global -> LDS loads, whole lines of a row at a time, into a ring of stages: fragments loaded
+// straight from memory have a lane per row, sixteen lines a quarter wave, and kept the
+// texture unit four times as long (16384 pairs, rank 64, 4096 x 14336 experts: 180 and 380 us).
+// The waves split a stage's k (and the rows), and their sums meet in LDS in a fixed order.
 #include <algorithm>
 
 #include "adapters.h"
+#include "ffn_common.h"
 #include "kernels.h"
 
 namespace moe {
@@ -30,18 +36,16 @@ struct ShrinkP {
   int ldu, rank, count, mats, L, K, top_k;
 };
 
-constexpr int kWaves = 8;
+constexpr int kWaves = 4;
 
 template <typename T> struct Mma16;
 template <> struct Mma16<bf16_t> {  // 16 bytes a lane are 32 k of 16 rows
-  static constexpr int kStep = 32;
   __device__ static f32x4_t mma(const u32x4_t& a, const u32x4_t& b, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
                                                    0, 0);
   }
 };
 template <> struct Mma16<float> {  // 16 k, in four products of one k of each lane group
-  static constexpr int kStep = 16;
   __device__ static f32x4_t mma(const u32x4_t& a, const u32x4_t& b, f32x4_t c) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -50,17 +54,36 @@ template <> struct Mma16<float> {  // 16 k, in four products of one k of each la
   }
 };
 
+#define MOE_VMCNT(n) __builtin_amdgcn_s_waitcnt(((n) & 0xF) | (((n) >> 4) << 14) | (0x7 << 4) | (0xF << 8))
+
+// Stages of RB row blocks of x and NG column groups (16 rows of A each), WK x 64 bytes of k a row:
+// one MFMA step for each of the WK waves along k, the others split the rows.
+template <int RB, int NG>
+struct Ring {
+  static constexpr int WK = RB == 1 ? 4 : 2, WM = kWaves / WK, MB = RB / WM;  // MB: row blocks of a wave
+  static constexpr int kRowBytes = WK * 64, kRows = 16 * (RB + NG), kPerLoad = 1024 / kRowBytes;  // rows of a 1 KB load
+  static constexpr int kLoads = (kRows / kPerLoad + kWaves - 1) / kWaves;                         // a wave's, per stage
+  static constexpr int kStage = kLoads * kWaves * 1024;
+  static constexpr int kSums = WK * 16 * RB * 16 * NG * 4;
+  static constexpr int kSlots = kStage <= 12 * 1024 ? 4 : 3;
+  static constexpr int kLds = kSlots * kStage > kSums ? kSlots * kStage : kSums;
+};
+
 // NG groups of 16 of the mats * rank columns a block (blockIdx.z / slots); of its rows' adapters it
 // takes every slots-th (blockIdx.z % slots).
 template <typename T, int RB, int NG>
-__global__ __launch_bounds__(kWaves * 64) void shrink_kernel(ShrinkP p, int slots) {
-  constexpr int E = Elem<T>::kPerVec, kStep = Mma16<T>::kStep;
-  constexpr int kSteps = RB * NG <= 2 ? 4 : 2;  // steps of K loaded together
-  __shared__ float red[kWaves][16][NG * 16];
+__device__ __forceinline__ void shrink_body(const ShrinkP& p, int slots, char* lds) {
+  using S = Ring<RB, NG>;
   const int e = blockIdx.x, seg0 = p.offsets[e], n = p.offsets[e + 1] - seg0;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wk = wave % S::WK, wm = wave / S::WK;
   const int slot = blockIdx.z % slots, c0 = (blockIdx.z / slots) * NG * 16, cols = p.mats * p.rank;
-  const T* x = static_cast<const T*>(p.x);
+  const uint32_t row_bytes = uint32_t(p.K) * sizeof(T);  // a multiple of 16
+  const int nk = int((row_bytes + S::kRowBytes - 1) / S::kRowBytes);
+  constexpr uint32_t kOutside = 0xFFFFFFF0u;  // past every extent below: reads zero, without a memory access
+  constexpr int CPR = S::kRowBytes / 16;      // 16-byte chunks of a stage's row
+  // chunk c of row r sits at chunk c ^ swizzle(r): 16 rows' reads of one chunk fall in different banks
+  auto swizzle = [](int r) { return CPR == 8 ? (r >> 1) & 7 : r & 15; };
   for (int m0 = blockIdx.y * 16 * RB; m0 < n; m0 += gridDim.y * 16 * RB) {
     // the adapters of the rows, one a lane (RB <= 4), the same in every wave
     int id = -1;
@@ -75,67 +98,120 @@ __global__ __launch_bounds__(kWaves * 64) void shrink_kernel(ShrinkP p, int slot
       }
     }
     uint64_t todo = p.mats > 0 ? __ballot(id >= 0) : 0;  // gate and up without adapters: the ids alone
+    const __amdgpu_buffer_rsrc_t x_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<T*>(static_cast<const T*>(p.x) + size_t(seg0 + m0) * p.K), 0, uint32_t(16 * RB) * row_bytes, kRsrcFlags);
     for (int seen = 0; todo != 0; ++seen) {
       const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
       const uint64_t mine = __ballot(id == cur);
       todo &= ~mine;
       if (seen % slots != slot) continue;
-      const T* arow[NG];
+      // this lane's place in each of the wave's loads: row of the stage (x, then A), chunk, byte offset
+      __amdgpu_buffer_rsrc_t rsrc[S::kLoads];
+      uint32_t at[S::kLoads], in_row[S::kLoads];
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const int c = min(c0 + g * 16 + (lane & 15), cols - 1);  // columns past the last repeat it, never stored
-        const int m = c >= p.rank ? 1 : 0;
-        arow[g] = static_cast<const T*>(p.a[m]) + ((size_t(cur) * p.L + e) * p.rank + (c - m * p.rank)) * p.K;
+      for (int j = 0; j < S::kLoads; ++j) {
+        const int b = S::kLoads * wave + j, r0 = b * S::kPerLoad, r = r0 + lane / CPR;
+        in_row[j] = uint32_t((lane % CPR) ^ swizzle(r)) * 16u;
+        if (r0 < 16 * RB) {
+          rsrc[j] = x_rsrc;
+          at[j] = (mine >> r) & 1 ? uint32_t(r) * row_bytes : kOutside;
+        } else {
+          const int col0 = c0 + r0 - 16 * RB, c = col0 + lane / CPR;  // the rank is a multiple of 8: one matrix a load
+          const int m = col0 >= p.rank ? 1 : 0;
+          rsrc[j] = __builtin_amdgcn_make_buffer_rsrc(
+              const_cast<T*>(static_cast<const T*>(p.a[m]) + (size_t(cur) * p.L + e) * p.rank * p.K), 0,
+              uint32_t(p.rank) * row_bytes, kRsrcFlags);
+          at[j] = c < cols && r < S::kRows ? uint32_t(c - m * p.rank) * row_bytes : kOutside;
+        }
       }
-      const T* xrow[RB];
+      auto issue = [&](int s) {  // stage min(s, nk - 1) into slot s
+        char* dst = lds + (s % S::kSlots) * S::kStage + S::kLoads * wave * 1024;
+        const uint32_t k0 = uint32_t(min(s, nk - 1)) * S::kRowBytes;
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb) xrow[rb] = x + size_t(seg0 + min(m0 + rb * 16 + (lane & 15), n - 1)) * p.K;
-      f32x4_t acc[RB][NG];
+        for (int j = 0; j < S::kLoads; ++j) {
+          const uint32_t k = k0 + in_row[j];
+          const uint32_t vo = at[j] != kOutside && k < row_bytes ? at[j] + k : kOutside;
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc[j], (lds_ptr_t)(dst + j * 1024), 16, vo, 0, 0, 0);
+        }
+      };
+      f32x4_t acc[S::MB][NG];
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
+      for (int rb = 0; rb < S::MB; ++rb)
 #pragma unroll
         for (int g = 0; g < NG; ++g) acc[rb][g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      for (int k0 = wave * kSteps * kStep; k0 < p.K; k0 += kWaves * kSteps * kStep) {
-        u32x4_t xv[kSteps][RB], av[kSteps][NG];
+      // fragments: row lane % 16 of a block, chunk 4 wk + lane / 16
+      const int chunk = 4 * wk + (lane >> 4);
+      int xo[S::MB], ao[NG];
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          const int k = k0 + s * kStep + (lane >> 4) * E;  // K is a multiple of 8: a vector is in or out as a whole
-#pragma unroll
-          for (int rb = 0; rb < RB; ++rb)
-            xv[s][rb] = k < p.K ? *reinterpret_cast<const u32x4_t*>(xrow[rb] + k) : u32x4_t{0, 0, 0, 0};
-#pragma unroll
-          for (int g = 0; g < NG; ++g)
-            av[s][g] = k < p.K ? *reinterpret_cast<const u32x4_t*>(arow[g] + k) : u32x4_t{0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-          for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-            for (int g = 0; g < NG; ++g) acc[rb][g] = Mma16<T>::mma(xv[s][rb], av[s][g], acc[rb][g]);
+      for (int rb = 0; rb < S::MB; ++rb) {
+        const int r = (wm * S::MB + rb) * 16 + (lane & 15);
+        xo[rb] = r * S::kRowBytes + (chunk ^ swizzle(r)) * 16;
       }
-      const float sc = p.scale != nullptr ? p.scale[cur] : 1.0f;
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb) {
-        if (((mine >> (16 * rb)) & 0xFFFF) == 0) continue;
-        __syncthreads();  // the sums before these have been read
-        // lane -> column lane % 16 of the group, register i -> row 4 (lane / 16) + i
+      for (int g = 0; g < NG; ++g) {
+        const int r = 16 * RB + g * 16 + (lane & 15);
+        ao[g] = r * S::kRowBytes + (chunk ^ swizzle(r)) * 16;
+      }
+      __syncthreads();  // the sums of the adapter before have been read
+#pragma unroll
+      for (int s = 0; s < S::kSlots - 1; ++s) issue(s);
+      for (int s = 0; s < nk; ++s) {
+        MOE_VMCNT(S::kLoads * (S::kSlots - 2));   // this wave's loads of stage s have landed
+        __builtin_amdgcn_s_waitcnt(0xC07F);       // and its reads of stage s - 1 (lgkmcnt)
+        block_barrier();                          // as every wave's have
+        issue(s + S::kSlots - 1);                 // into the slot of stage s - 1
+        const char* st = lds + (s % S::kSlots) * S::kStage;
+        u32x4_t xv[S::MB], av[NG];
+#pragma unroll
+        for (int rb = 0; rb < S::MB; ++rb) xv[rb] = *reinterpret_cast<const u32x4_t*>(st + xo[rb]);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) av[g] = *reinterpret_cast<const u32x4_t*>(st + ao[g]);
+#pragma unroll
+        for (int rb = 0; rb < S::MB; ++rb)
+#pragma unroll
+          for (int g = 0; g < NG; ++g) acc[rb][g] = Mma16<T>::mma(xv[rb], av[g], acc[rb][g]);
+      }
+      MOE_VMCNT(0);     // the last (repeated) loads land before the sums take their place
+      __syncthreads();  // in every wave
+      // lane -> column lane % 16 of the group, register i -> row 4 (lane / 16) + i
+      float* red = reinterpret_cast<float*>(lds);  // [WK][16 RB][16 NG]
+#pragma unroll
+      for (int rb = 0; rb < S::MB; ++rb)
 #pragma unroll
         for (int g = 0; g < NG; ++g)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) red[wave][4 * (lane >> 4) + i][g * 16 + (lane & 15)] = acc[rb][g][i];
-        __syncthreads();
-        for (int v = threadIdx.x; v < 16 * NG * 16; v += kWaves * 64) {
-          const int r = v / (NG * 16), c = v % (NG * 16);
-          if (!((mine >> (16 * rb + r)) & 1) || c0 + c >= cols) continue;
-          float s = 0.0f;
+          for (int i = 0; i < 4; ++i)
+            red[((wk * RB + wm * S::MB + rb) * 16 + 4 * (lane >> 4) + i) * (NG * 16) + g * 16 + (lane & 15)] = acc[rb][g][i];
+      __syncthreads();
+      const float sc = p.scale != nullptr ? p.scale[cur] : 1.0f;
+      for (int v = threadIdx.x; v < 16 * RB * 16 * NG; v += kWaves * 64) {
+        const int r = v / (NG * 16), c = v % (NG * 16);
+        if (!((mine >> r) & 1) || c0 + c >= cols) continue;
+        float a = red[v];
 #pragma unroll
-          for (int w = 0; w < kWaves; ++w) s += red[w][r][c];
-          static_cast<T*>(p.u)[size_t(seg0 + m0 + rb * 16 + r) * p.ldu + c0 + c] = Elem<T>::from_f32(sc * s);
-        }
+        for (int w = 1; w < S::WK; ++w) a += red[v + w * (16 * RB * 16 * NG)];
+        static_cast<T*>(p.u)[size_t(seg0 + m0 + r) * p.ldu + c0 + c] = Elem<T>::from_f32(sc * a);
       }
     }
   }
+}
+#undef MOE_VMCNT
+
+template <typename T, int RB, int NG>
+__global__ __launch_bounds__(kWaves * 64) void shrink_kernel(ShrinkP p, int slots) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  shrink_body<T, RB, NG>(p, slots, lds);
+}
+
+template <typename T, int RB, int NG>
+moe_status launch_ng(const char* name, const ShrinkP& p, const dim3& grid, int slots, hipStream_t s) {
+  auto kern = shrink_kernel<T, RB, NG>;
+  constexpr int lds = Ring<RB, NG>::kLds;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e != hipSuccess) return set_error(MOE_ERR_HIP, "%s: LDS attribute: %s", name, hipGetErrorString(e));
+  MOE_LAUNCH(name, kern, grid, dim3(kWaves * 64), lds, s, p, slots);
+  return MOE_OK;
 }
 
 template <typename T, int RB>
@@ -144,15 +220,11 @@ moe_status launch_rb(const char* name, const ShrinkP& p, int64_t max_pairs, hipS
   // row blocks of an expert with four times its share; a larger one's blocks take more than one
   const int64_t ny = std::min<int64_t>((max_pairs + 16 * RB - 1) / (16 * RB), 4 * max_pairs / (16 * RB * p.L) + 1);
   const int slots = RB == 1 ? std::min(p.count, 4) : 1;
-#define MOE_SHRINK(NG_)                                                                                          \
-  MOE_LAUNCH(name, (shrink_kernel<T, RB, NG_>), dim3(unsigned(p.L), unsigned(ny), unsigned((groups + NG_ - 1) / NG_ * slots)), \
-             dim3(kWaves * 64), 0, s, p, slots)
-  if (groups <= 1) MOE_SHRINK(1);
-  else if (groups <= 2) MOE_SHRINK(2);
-  else if (groups <= 4) MOE_SHRINK(4);
-  else MOE_SHRINK(8);
-#undef MOE_SHRINK
-  return MOE_OK;
+  const auto grid = [&](int ng) { return dim3(unsigned(p.L), unsigned(ny), unsigned((groups + ng - 1) / ng * slots)); };
+  if (groups <= 1) return launch_ng<T, RB, 1>(name, p, grid(1), slots, s);
+  if (groups <= 2) return launch_ng<T, RB, 2>(name, p, grid(2), slots, s);
+  if (groups <= 4) return launch_ng<T, RB, 4>(name, p, grid(4), slots, s);
+  return launch_ng<T, RB, 8>(name, p, grid(8), slots, s);
 }
 
 // Blocks of 64 rows, which read an adapter's A a quarter as often, where they still fill the card.

@@ -439,6 +439,14 @@ moe_status adapters_checks(const moe_adapters* a, bool pointers = true) {
   return MOE_OK;
 }
 
+// the first products address a row block and an adapter's A with 32-bit offsets
+moe_status adapted_desc_checks(const moe_layer_desc* d) {
+  if (d->hidden > kAdapterMaxK || d->intermediate > kAdapterMaxK)
+    return set_error(MOE_ERR_UNSUPPORTED, "adapters: hidden and intermediate above %d are not supported (got %d, %d)",
+                     kAdapterMaxK, d->hidden, d->intermediate);
+  return MOE_OK;
+}
+
 size_t adapted_stage_bytes(const moe_layer_desc* d, const moe_adapters* a, int32_t stage) {
   return align_up(stage_bytes(d, stage), 256) + carve_adapter_scratch(d, a, max_pairs_of(d), nullptr).bytes;
 }
@@ -1106,6 +1114,7 @@ moe_status moe_muon_update(const moe_muon_desc* m, const void* grad, float* mome
 
 moe_status moe_adapted_workspace_size(const moe_layer_desc* d, const moe_adapters* a, int32_t stage, size_t* bytes) {
   TRY(check_desc(d));
+  TRY(adapted_desc_checks(d));
   TRY(adapters_checks(a, false));
   if (bytes == nullptr) return set_error(MOE_ERR_INVALID_ARG, "bytes is NULL");
   if (stage != MOE_STAGE_FFN && stage != MOE_STAGE_LAYER)
@@ -1120,6 +1129,7 @@ moe_status moe_grouped_ffn_adapted(const moe_layer_desc* d, const void* x_sorted
                                    size_t ws_bytes, void* stream) {
   CallScope scope;
   TRY(check_desc(d));
+  TRY(adapted_desc_checks(d));
   TRY(adapters_checks(a));
   if (d->num_tokens == 0) return MOE_OK;
   TRY(ffn_checks(x_sorted, offsets, w_gate, w_up, w_down, y_sorted));
@@ -1140,6 +1150,7 @@ moe_status moe_layer_forward_adapted(const moe_layer_desc* d, const moe_route_op
                                      int64_t* num_dropped_out, void* ws, size_t ws_bytes, void* stream) {
   CallScope scope;
   TRY(check_desc(d));
+  TRY(adapted_desc_checks(d));
   TRY(adapters_checks(a));
   if (d->num_tokens == 0) return MOE_OK;
   TRY(check_ws_bytes(adapted_stage_bytes(d, a, MOE_STAGE_LAYER), ws, ws_bytes));

@@ -128,6 +128,8 @@ struct Adapters {
   int ldu, rank, experts;
 };
 
+constexpr int kAdapterMaxK = 1 << 22;  // hidden and intermediate
+
 // What the first products leave for the second ones, carved from the caller's workspace.
 struct AdapterScratch {
   int32_t* rid;  // [P_max] adapter of every sorted row, -1: none
