@@ -65,7 +65,7 @@ struct Ring {
   static constexpr int kLoads = (kRows / kPerLoad + kWaves - 1) / kWaves;                         // a wave's, per stage
   static constexpr int kStage = kLoads * kWaves * 1024;
   static constexpr int kSums = WK * 16 * RB * 16 * NG * 4;
-  static constexpr int kSlots = kStage <= 12 * 1024 ? 4 : 3;
+  static constexpr int kSlots = RB == 1 ? (kStage <= 8 * 1024 ? 8 : kStage <= 12 * 1024 ? 6 : kStage <= 20 * 1024 ? 5 : 3) : 3;
   static constexpr int kLds = kSlots * kStage > kSums ? kSlots * kStage : kSums;
 };
 
@@ -252,6 +252,7 @@ AdapterScratch carve_adapter_scratch(const moe_layer_desc* d, const moe_adapters
   w.rid = static_cast<int32_t*>(take(size_t(max_pairs) * 4));
   w.u_gu = take(size_t(max_pairs) * mats_of(a, false) * a->rank * dt);
   w.u_down = take(size_t(max_pairs) * mats_of(a, true) * a->rank * dt);
+  w.ffn = take(adapted_ffn_scratch_bytes(d, max_pairs));
   w.bytes = o;
   return w;
 }

@@ -99,8 +99,8 @@ size_t ffn_h_bytes(const moe_layer_desc* d) {
   return align_up(size_t(max_pairs_of(d)) * d->intermediate * dtype_bytes(d->dtype), 256);
 }
 
-// Layout of the moe_layer_forward workspace, or of the packed layer's (which brings the scratch of
-// its own feed-forward).
+// Layout of the moe_layer_forward workspace, or of another form's of the layer (which brings the
+// scratch of its own feed-forward).
 struct LayerWs {
   int32_t* topk_ids;
   float* topk_w;
@@ -119,7 +119,7 @@ struct LayerWs {
   size_t bytes;
 };
 
-LayerWs layer_layout(const moe_layer_desc* d, void* base, bool packed = false) {
+LayerWs layer_layout(const moe_layer_desc* d, void* base, size_t ffn_scratch) {
   const int64_t n = d->num_tokens * d->top_k;
   const int64_t pm = max_pairs_of(d);
   const size_t dt = dtype_bytes(d->dtype);
@@ -143,11 +143,17 @@ LayerWs layer_layout(const moe_layer_desc* d, void* base, bool packed = false) {
   w.dispatch = take(dispatch_scratch_bytes(d));
   w.x_sorted = take(size_t(pm) * d->hidden * dt);
   w.h = take(size_t(pm) * d->intermediate * dt);
-  const size_t fb = packed ? packed_ffn_scratch_bytes(d, pm) : ffn_scratch_bytes(d, pm);
-  w.ffn_scratch = fb ? take(fb) : nullptr;
+  w.ffn_scratch = ffn_scratch ? take(ffn_scratch) : nullptr;
   w.y_sorted = take(size_t(pm) * d->hidden * dt);
   w.bytes = o;
   return w;
+}
+
+LayerWs layer_layout(const moe_layer_desc* d, void* base) {
+  return layer_layout(d, base, ffn_scratch_bytes(d, max_pairs_of(d)));
+}
+LayerWs packed_layer_layout(const moe_layer_desc* d, void* base) {
+  return layer_layout(d, base, packed_ffn_scratch_bytes(d, max_pairs_of(d)));
 }
 
 // moe_grouped_ffn_backward's workspace: dg | du [P_max, 2I] and the large-tile path's scratch
@@ -184,7 +190,7 @@ LayerBwdWs layer_bwd_layout(const moe_layer_desc* d, void* base) {
 }
 
 size_t packed_stage_bytes(const moe_layer_desc* d, int32_t stage) {
-  if (stage == MOE_STAGE_LAYER) return layer_layout(d, nullptr, true).bytes;
+  if (stage == MOE_STAGE_LAYER) return packed_layer_layout(d, nullptr).bytes;
   return ffn_h_bytes(d) + align_up(packed_ffn_scratch_bytes(d, max_pairs_of(d)), 256);
 }
 
@@ -447,13 +453,16 @@ moe_status adapted_desc_checks(const moe_layer_desc* d) {
   return MOE_OK;
 }
 
-size_t adapted_stage_bytes(const moe_layer_desc* d, const moe_adapters* a, int32_t stage) {
-  return align_up(stage_bytes(d, stage), 256) + carve_adapter_scratch(d, a, max_pairs_of(d), nullptr).bytes;
+// The layer's workspace with adapters: its intermediates, then the adapters' part (with the
+// feed-forward's scratch); the feed-forward's alone: h, then that part.
+size_t adapted_front_bytes(const moe_layer_desc* d, int32_t stage) {
+  return stage == MOE_STAGE_LAYER ? layer_layout(d, nullptr, 0).bytes : ffn_h_bytes(d);
 }
-
-// The adapters' part of a workspace: behind what the stage has without them.
+size_t adapted_stage_bytes(const moe_layer_desc* d, const moe_adapters* a, int32_t stage) {
+  return adapted_front_bytes(d, stage) + carve_adapter_scratch(d, a, max_pairs_of(d), nullptr).bytes;
+}
 AdapterScratch adapted_scratch(const moe_layer_desc* d, const moe_adapters* a, int32_t stage, void* ws) {
-  return carve_adapter_scratch(d, a, max_pairs_of(d), static_cast<char*>(ws) + align_up(stage_bytes(d, stage), 256));
+  return carve_adapter_scratch(d, a, max_pairs_of(d), static_cast<char*>(ws) + adapted_front_bytes(d, stage));
 }
 
 moe_status join_desc_checks(const moe_join_desc* j) {
@@ -1050,7 +1059,7 @@ moe_status moe_layer_forward_packed(const moe_layer_desc* d, const moe_route_opt
   TRY(packed_desc_checks(d));
   if (d->num_tokens == 0) return MOE_OK;
   TRY(check_ws_bytes(packed_stage_bytes(d, MOE_STAGE_LAYER), ws, ws_bytes));
-  const LayerWs w = layer_layout(d, ws, true);
+  const LayerWs w = packed_layer_layout(d, ws);
   int32_t* ids = topk_ids_out ? topk_ids_out : w.topk_ids;
   float* tw = topk_w_out ? topk_w_out : w.topk_w;
   int32_t* counts = counts_out ? counts_out : w.counts;
@@ -1136,10 +1145,10 @@ moe_status moe_grouped_ffn_adapted(const moe_layer_desc* d, const void* x_sorted
   REQUIRE_PTR(sorted_pairs, 4);
   REQUIRE_PTR(adapter_ids, 4);
   TRY(check_ws_bytes(adapted_stage_bytes(d, a, MOE_STAGE_FFN), ws, ws_bytes));
-  void* scratch = ffn_scratch_bytes(d, max_pairs_of(d)) ? static_cast<char*>(ws) + ffn_h_bytes(d) : nullptr;
-  FfnArgs fa{d, x_sorted, offsets, w_gate, w_up, w_down, y_sorted, ws, scratch, max_pairs_of(d),
+  const AdapterScratch as = adapted_scratch(d, a, MOE_STAGE_FFN, ws);
+  FfnArgs fa{d, x_sorted, offsets, w_gate, w_up, w_down, y_sorted, ws, as.ffn, max_pairs_of(d),
              static_cast<hipStream_t>(stream)};
-  AdaptedFfnArgs aa{fa, sorted_pairs, adapter_ids, a, adapted_scratch(d, a, MOE_STAGE_FFN, ws)};
+  AdaptedFfnArgs aa{fa, sorted_pairs, adapter_ids, a, as};
   return launch_adapted_ffn(aa);
 }
 
@@ -1155,7 +1164,8 @@ moe_status moe_layer_forward_adapted(const moe_layer_desc* d, const moe_route_op
   if (d->num_tokens == 0) return MOE_OK;
   TRY(check_ws_bytes(adapted_stage_bytes(d, a, MOE_STAGE_LAYER), ws, ws_bytes));
   REQUIRE_PTR(adapter_ids, 4);
-  const LayerWs w = layer_layout(d, ws);
+  const LayerWs w = layer_layout(d, ws, 0);
+  const AdapterScratch as = adapted_scratch(d, a, MOE_STAGE_LAYER, ws);
   int32_t* ids = topk_ids_out ? topk_ids_out : w.topk_ids;
   float* tw = topk_w_out ? topk_w_out : w.topk_w;
   int32_t* counts = counts_out ? counts_out : w.counts;
@@ -1175,8 +1185,8 @@ moe_status moe_layer_forward_adapted(const moe_layer_desc* d, const moe_route_op
   DispatchArgs da{d, x, ids, w.topk_logit, counts, w.offsets, w.sorted_pairs, w.pair_row, w.x_sorted, dropped,
                   scr, capacity_of(d), true, s};
   TRY(launch_dispatch(da));
-  FfnArgs fa{d, w.x_sorted, w.offsets, w_gate, w_up, w_down, w.y_sorted, w.h, w.ffn_scratch, max_pairs_of(d), s};
-  AdaptedFfnArgs aa{fa, w.sorted_pairs, adapter_ids, a, adapted_scratch(d, a, MOE_STAGE_LAYER, ws)};
+  FfnArgs fa{d, w.x_sorted, w.offsets, w_gate, w_up, w_down, w.y_sorted, w.h, as.ffn, max_pairs_of(d), s};
+  AdaptedFfnArgs aa{fa, w.sorted_pairs, adapter_ids, a, as};
   TRY(launch_adapted_ffn(aa));
   CombineArgs ca{d, w.y_sorted, w.pair_row, tw, y, s};
   return launch_combine(ca);

@@ -871,8 +871,8 @@ moe_status launch(const char* name, const bf16_t* A, const int32_t* offsets, con
 
 // large tiles pay off once segments hold a few hundred rows; decode-sized
 // batches (a handful of rows per expert) take the skinny kernel
-bool use_big(const moe_layer_desc* d, int64_t max_pairs) {
-  return d->dtype == MOE_BF16 && max_pairs >= int64_t(128) * d->local_count && big::supported(d->hidden) &&
+bool use_big(const moe_layer_desc* d, int64_t max_pairs, int rows_each = 128) {
+  return d->dtype == MOE_BF16 && max_pairs >= int64_t(rows_each) * d->local_count && big::supported(d->hidden) &&
          big::supported(d->intermediate) && big::addressable(d->intermediate, d->hidden);
 }
 
@@ -884,11 +884,28 @@ moe_status launch_small(const FfnArgs& a) {
 
 }  // namespace
 
-size_t ffn_scratch_bytes(const moe_layer_desc* d, int64_t max_pairs) {
-  if (!use_big(d, max_pairs)) return 0;
+namespace {
+size_t big_scratch_bytes(const moe_layer_desc* d) {
   const size_t plan = align_up(size_t(2) * (d->local_count + 1) * sizeof(int32_t), 256);
   const bool split = big::splits(d->hidden) || big::splits(d->intermediate);
   return plan + (split ? size_t(big::kXcds) * big::kMaxParts * big::kPartBytes : 0);
+}
+
+// Rows an expert from which adapted products take the large tile (at its end wide tiles of 128 rows).
+// Against the decode kernel, rank 16, even and skewed experts: at 16 rows 258 and 259 us instead of
+// 287 and 363 (16 experts of 2880 x 2880), 344 and 398 instead of 360 and 1016 (128 of 2048 x 768),
+// 641 and 623 instead of 804 and 841 (8 of 4096 x 14336); at 9 rows 248, 335 and 591 instead of 187,
+// 292 and 520 where they are even.
+constexpr int kAdaptedBigRows = 16;
+bool use_big_adapted(const moe_layer_desc* d, int64_t max_pairs) { return use_big(d, max_pairs, kAdaptedBigRows); }
+}  // namespace
+
+size_t ffn_scratch_bytes(const moe_layer_desc* d, int64_t max_pairs) {
+  return use_big(d, max_pairs) ? big_scratch_bytes(d) : 0;
+}
+
+size_t adapted_ffn_scratch_bytes(const moe_layer_desc* d, int64_t max_pairs) {
+  return use_big_adapted(d, max_pairs) ? big_scratch_bytes(d) : 0;
 }
 
 // ---- the backward's dgrad products on the large-tile kernel ---------------------
@@ -985,7 +1002,7 @@ moe_status launch_grouped_ffn(const FfnArgs& a) {
 
 moe_status launch_adapted_products(const AdaptedFfnArgs& a) {
   const moe_layer_desc* d = a.f.d;
-  if (use_big(d, a.f.max_pairs))
+  if (use_big_adapted(d, a.f.max_pairs))
     return launch_big_ffn(a.f, gate_up_adapters(d, a.ad, a.w), down_adapters(d, a.ad, a.w),
                           [&] { return launch_adapter_shrink(a, true); });
   return skinny_ffn_fits(d, a.f.max_pairs) ? launch_skinny_adapted(a) : launch_general_adapted(a);

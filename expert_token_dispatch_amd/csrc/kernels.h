@@ -135,9 +135,11 @@ struct AdapterScratch {
   int32_t* rid;  // [P_max] adapter of every sorted row, -1: none
   void* u_gu;    // [P_max, matrices * rank]: gate's columns, then up's
   void* u_down;  // [P_max, rank]
+  void* ffn;     // adapted_ffn_scratch_bytes: what the products themselves need
   size_t bytes;
 };
 AdapterScratch carve_adapter_scratch(const moe_layer_desc* d, const moe_adapters* a, int64_t max_pairs, void* base);
+size_t adapted_ffn_scratch_bytes(const moe_layer_desc* d, int64_t max_pairs);
 Adapters gate_up_adapters(const moe_layer_desc* d, const moe_adapters* a, const AdapterScratch& w);
 Adapters down_adapters(const moe_layer_desc* d, const moe_adapters* a, const AdapterScratch& w);
 

@@ -31,6 +31,10 @@ constexpr int kThreads = 256, kMaxRowBlocks = 4;
 
 bool supported(int K) { return K % 32 == 0; }
 
+// KS = 4, for a few rows with adapters whose active experts do not fill the card: the waves share
+// their columns and split K, so a block covers a quarter of the columns and there are four times
+// as many; their sums meet in LDS in wave order, and wave w finishes row block w.
+//
 // Each wave streams two sets of 16 weight rows: for gate/up the gate and the
 // up rows of the same 16 output columns, for down two adjacent groups of 16
 // output columns.  So a block (four waves) covers 64 gate/up columns or 128
@@ -109,7 +113,7 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int
 // the wave parks the block in its own 1 KB of LDS and reads the fragments back with
 // transposing reads, so the MFMAs see the same operands as with n-major weights.
 // AD: Adapters, whose share is added to the sums, or NoAdapters.
-template <int NMAT, bool SAVE, bool BKN, class AD>
+template <int NMAT, bool SAVE, bool BKN, class AD, int KS>
 __global__ __launch_bounds__(kThreads) void gemm_kernel(const bf16_t* __restrict__ A, const int32_t* __restrict__ offsets,
                                                         const bf16_t* __restrict__ B0, const bf16_t* __restrict__ B1,
                                                         bf16_t* __restrict__ C, int N, int K, bf16_t* __restrict__ Gs,
@@ -121,8 +125,11 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(const bf16_t* __restrict
   const int seg_n = offsets[expert + 1] - seg0;
   if (seg_n <= 0) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int col0 = blockIdx.x * cols_per_block<NMAT>() + wave * kWaveCols;  // first output column of this wave
+  // first output column of this wave; with KS > 1 the block's waves have the same
+  const int col0 = KS > 1 ? int(blockIdx.x) * kWaveCols : int(blockIdx.x) * cols_per_block<NMAT>() + wave * kWaveCols;
   if (col0 >= N) return;
+  const int kb = KS > 1 ? 32 * ((K / 32) * wave / KS) : 0;              // this wave's k
+  const int ke = KS > 1 ? 32 * ((K / 32) * (wave + 1) / KS) : K;
   const size_t boff = size_t(expert) * N * K;
   const int kg = (lane >> 4) * 8;  // the lane's 8 k values within a step
   const bf16_t* bs0;
@@ -174,7 +181,7 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(const bf16_t* __restrict
     // layer: 0 to -4% per layer against two steps, while capping registers for
     // more waves per SIMD made it 12% slower)
     bf16x8_t w0[2][kPipe], w1[2][kPipe], a0[2][kPipe];
-    const int nset = K / (32 * kPipe);
+    const int nset = (ke - kb) / (32 * kPipe);
     auto load_set = [&](int b, int k0) {
 #pragma unroll
       for (int u = 0; u < kPipe; ++u) {
@@ -212,17 +219,17 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(const bf16_t* __restrict
         }
       }
     };
-    if (nset > 0) load_set(0, 0);
+    if (nset > 0) load_set(0, kb);
     int set = 0;
     for (; set + 2 <= nset; set += 2) {
-      load_set(1, (set + 1) * 32 * kPipe);
-      mma_set(0, set * 32 * kPipe);
-      if (set + 2 < nset) load_set(0, (set + 2) * 32 * kPipe);
-      mma_set(1, (set + 1) * 32 * kPipe);
+      load_set(1, kb + (set + 1) * 32 * kPipe);
+      mma_set(0, kb + set * 32 * kPipe);
+      if (set + 2 < nset) load_set(0, kb + (set + 2) * 32 * kPipe);
+      mma_set(1, kb + (set + 1) * 32 * kPipe);
     }
-    if (set < nset) mma_set(0, set * 32 * kPipe);
-    int k0 = nset * 32 * kPipe;
-    for (; k0 < K; k0 += 32) {
+    if (set < nset) mma_set(0, kb + set * 32 * kPipe);
+    int k0 = kb + nset * 32 * kPipe;
+    for (; k0 < ke; k0 += 32) {
       bf16x8_t v0 = *reinterpret_cast<const bf16x8_t*>(bs0 + size_t(k0) * kstride);
       bf16x8_t v1 = *reinterpret_cast<const bf16x8_t*>(bs1 + size_t(k0) * kstride);
       if constexpr (BKN) {
@@ -240,65 +247,87 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(const bf16_t* __restrict
         }
       }
     }
-    if constexpr (std::is_same<AD, Adapters>::value) {
-#pragma unroll
-      for (int rb = 0; rb < kMaxRowBlocks; ++rb)
-        if (rb < nrb)
-          add_adapters<NMAT>(ad, expert, seg0 + m0 + rb * 16, min(16, seg_n - m0 - rb * 16), col0, N, acc[0][rb], acc[1][rb]);
-    }
-    // 16x16 layout: lane -> weight row (column of the output) lane & 15,
-    // register i -> token row 4*(lane/16) + i of the row block
-#pragma unroll
-    for (int rb = 0; rb < kMaxRowBlocks; ++rb) {
+    // adapters' share, then the stores of one row block.  16x16 layout: lane -> weight row (column of
+    // the output) lane & 15, register i -> token row 4*(lane/16) + i of the row block
+    auto finish = [&](int rb, f32x4_t& s0, f32x4_t& s1) {
+      if constexpr (std::is_same<AD, Adapters>::value)
+        add_adapters<NMAT>(ad, expert, seg0 + m0 + rb * 16, min(16, seg_n - m0 - rb * 16), col0, N, s0, s1);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = m0 + rb * 16 + 4 * (lane >> 4) + i;
-        if (rb < nrb && r < seg_n) {
+        if (r < seg_n) {
           bf16_t* crow = C + size_t(seg0 + r) * N;
           if (NMAT == 2) {
             const int col = col0 + (lane & 15);
             if (col < N) {
-              crow[col] = f32_to_bf16(silu(acc[0][rb][i]) * acc[1][rb][i]);
+              crow[col] = f32_to_bf16(silu(s0[i]) * s1[i]);
               if constexpr (SAVE) {
-                Gs[size_t(seg0 + r) * N + col] = f32_to_bf16(acc[0][rb][i]);
-                Us[size_t(seg0 + r) * N + col] = f32_to_bf16(acc[1][rb][i]);
+                Gs[size_t(seg0 + r) * N + col] = f32_to_bf16(s0[i]);
+                Us[size_t(seg0 + r) * N + col] = f32_to_bf16(s1[i]);
               }
             }
           } else {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              const int col = col0 + 16 * s + (lane & 15);
-              if (col < N) crow[col] = f32_to_bf16(acc[s][rb][i]);
-            }
+            const int c0 = col0 + (lane & 15), c1 = c0 + 16;
+            if (c0 < N) crow[c0] = f32_to_bf16(s0[i]);
+            if (c1 < N) crow[c1] = f32_to_bf16(s1[i]);
           }
         }
+      }
+    };
+    if constexpr (KS == 1) {
+#pragma unroll
+      for (int rb = 0; rb < kMaxRowBlocks; ++rb)
+        if (rb < nrb) finish(rb, acc[0][rb], acc[1][rb]);
+    } else {
+      static_assert(KS == kThreads / 64 && KS == kMaxRowBlocks, "a wave for every row block");
+      __shared__ f32x4_t sums[KS][kMaxRowBlocks][2][64];
+      if (m0 > 0) __syncthreads();  // the sums before these have been read
+#pragma unroll
+      for (int rb = 0; rb < kMaxRowBlocks; ++rb)
+        if (rb < nrb) {
+          sums[wave][rb][0][lane] = acc[0][rb];
+          sums[wave][rb][1][lane] = acc[1][rb];
+        }
+      __syncthreads();
+      if (wave < nrb) {
+        f32x4_t s0 = sums[0][wave][0][lane], s1 = sums[0][wave][1][lane];
+#pragma unroll
+        for (int w = 1; w < KS; ++w) {
+          s0 += sums[w][wave][0][lane];
+          s1 += sums[w][wave][1][lane];
+        }
+        finish(wave, s0, s1);
       }
     }
   }
 }
 
 // bkn: k-major weights (see gemm_kernel)
+// ks: the waves split K (adapters alone)
 template <int NMAT, class AD>
 moe_status launch(const char* name, const bf16_t* A, const int32_t* offsets, const bf16_t* B0, const bf16_t* B1,
-                  bf16_t* C, int L, int N, int K, bool bkn, hipStream_t s, bf16_t* Gs, bf16_t* Us, const AD& ad) {
-  const dim3 grid(unsigned((N + cols_per_block<NMAT>() - 1) / cols_per_block<NMAT>()), unsigned(L));
-#define MOE_SKINNY(SAVE_)                                                                                          \
+                  bf16_t* C, int L, int N, int K, bool bkn, bool ks, hipStream_t s, bf16_t* Gs, bf16_t* Us, const AD& ad) {
+  const int cols = ks ? cols_per_block<NMAT>() / 4 : cols_per_block<NMAT>();
+  const dim3 grid(unsigned((N + cols - 1) / cols), unsigned(L));
+#define MOE_SKINNY(SAVE_, KS_)                                                                                     \
   do {                                                                                                             \
     if (bkn)                                                                                                       \
-      MOE_LAUNCH(name, (gemm_kernel<NMAT, SAVE_, true, AD>), grid, dim3(kThreads), 0, s, A, offsets, B0, B1, C, N, K, Gs, Us, ad); \
+      MOE_LAUNCH(name, (gemm_kernel<NMAT, SAVE_, true, AD, KS_>), grid, dim3(kThreads), 0, s, A, offsets, B0, B1, C, N, K, Gs, Us, ad); \
     else                                                                                                           \
-      MOE_LAUNCH(name, (gemm_kernel<NMAT, SAVE_, false, AD>), grid, dim3(kThreads), 0, s, A, offsets, B0, B1, C, N, K, Gs, Us, ad); \
+      MOE_LAUNCH(name, (gemm_kernel<NMAT, SAVE_, false, AD, KS_>), grid, dim3(kThreads), 0, s, A, offsets, B0, B1, C, N, K, Gs, Us, ad); \
   } while (0)
-  if constexpr (NMAT == 2 && std::is_same<AD, NoAdapters>::value) {
-    if (Gs != nullptr) {
-      MOE_SKINNY(true);
-      return MOE_OK;
-    }
+  if constexpr (std::is_same<AD, Adapters>::value) {
+    if (ks) MOE_SKINNY(false, 4);
+    else MOE_SKINNY(false, 1);
+  } else {
+    if (NMAT == 2 && Gs != nullptr) MOE_SKINNY(NMAT == 2, 1);
+    else MOE_SKINNY(false, 1);
   }
-  MOE_SKINNY(false);
 #undef MOE_SKINNY
   return MOE_OK;
 }
+
+constexpr int kFullBlocks = 1024;
 
 // between(): enqueued between the two products
 template <class AD, class Between>
@@ -307,14 +336,19 @@ moe_status launch_both(const FfnArgs& a, const AD& gu, const AD& dn, const Betwe
   const int L = d->local_count, H = d->hidden, I = d->intermediate;
   bf16_t* h = static_cast<bf16_t*>(a.h);
   const bool kn = d->weight_layout == MOE_WEIGHTS_IN_OUT;
+  // fewer than kFullBlocks blocks, if every row is another expert's, leave the waves waiting for
+  // their own loads
+  const auto ks = [&](int N, int cols) {
+    return std::is_same<AD, Adapters>::value && std::min<int64_t>(a.max_pairs, L) * ((N + cols - 1) / cols) < kFullBlocks;
+  };
   moe_status st = launch<2>("ffn_gate_up", static_cast<const bf16_t*>(a.x_sorted), a.offsets,
-                            static_cast<const bf16_t*>(a.w_gate), static_cast<const bf16_t*>(a.w_up), h, L, I, H, kn, a.s,
+                            static_cast<const bf16_t*>(a.w_gate), static_cast<const bf16_t*>(a.w_up), h, L, I, H, kn, ks(I, cols_per_block<2>()), a.s,
                             static_cast<bf16_t*>(a.g_out), static_cast<bf16_t*>(a.u_out), gu);
   if (st != MOE_OK) return st;
   st = between();
   if (st != MOE_OK) return st;
   return launch<1>("ffn_down", h, a.offsets, static_cast<const bf16_t*>(a.w_down), static_cast<const bf16_t*>(a.w_down),
-                   static_cast<bf16_t*>(a.y_sorted), L, H, I, kn, a.s, static_cast<bf16_t*>(nullptr),
+                   static_cast<bf16_t*>(a.y_sorted), L, H, I, kn, ks(H, cols_per_block<1>()), a.s, static_cast<bf16_t*>(nullptr),
                    static_cast<bf16_t*>(nullptr), dn);
 }
 

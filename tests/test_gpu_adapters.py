@@ -1,6 +1,7 @@
 """The experts with adapters of many requests on the GPU against the float64 oracle, by the framework's
 measures of a row (float32 1e-5 of its largest entry, bf16 2e-2 of its norm), and what has to be equal bit for bit:
-rows without an adapter are the plain experts', and a row does not depend on the other rows' adapters."""
+a row does not depend on the other rows' adapters, and where the plain experts take the same kernels, rows
+without an adapter are theirs."""
 
 import numpy as np
 import pytest
@@ -147,7 +148,7 @@ def test_projections_without_adapters(has, P, dtype):
 
 @pytest.mark.parametrize("dtype", ("bf16", "f32"))
 @pytest.mark.parametrize("layout", ("out_in", "in_out"))
-@pytest.mark.parametrize("shape", [(64, 96, 4, 30), (256, 512, 4, 1100), (136, 264, 3, 200), (4096, 128, 2, 600), (512, 256, 8, 2000)])
+@pytest.mark.parametrize("shape", [(2048, 768, 100, 300), (2048, 768, 128, 512), (256, 512, 4, 1100), (136, 264, 3, 200), (4096, 128, 2, 600), (512, 256, 8, 2000)])
 def test_without_an_adapter_a_row_is_the_plain_experts(shape, layout, dtype):
     H, I, Lc, P = shape
     c = Case(H, I, Lc, P, 16, 3, dtype, layout, kind="none")
