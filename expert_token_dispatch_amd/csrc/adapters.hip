@@ -38,22 +38,6 @@ struct ShrinkP {
 
 constexpr int kWaves = 4;
 
-template <typename T> struct Mma16;
-template <> struct Mma16<bf16_t> {  // 16 bytes a lane are 32 k of 16 rows
-  __device__ static f32x4_t mma(const u32x4_t& a, const u32x4_t& b, f32x4_t c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
-                                                   0, 0);
-  }
-};
-template <> struct Mma16<float> {  // 16 k, in four products of one k of each lane group
-  __device__ static f32x4_t mma(const u32x4_t& a, const u32x4_t& b, f32x4_t c) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c, 0, 0, 0);
-    return c;
-  }
-};
-
 #define MOE_VMCNT(n) __builtin_amdgcn_s_waitcnt(((n) & 0xF) | (((n) >> 4) << 14) | (0x7 << 4) | (0xF << 8))
 
 // Stages of RB row blocks of x and NG column groups (16 rows of A each), WK x 64 bytes of k a row:

@@ -11,6 +11,24 @@ namespace moe {
 // Both ends stay exact: exp(-z) overflowing gives -0, underflowing gives z.
 __device__ __forceinline__ float silu(float z) { return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
+// 16 x 16 products of 64 bytes of k a row: lane l holds row l % 16 of either operand, bytes
+// 16 (l / 16) .. + 15 of them.
+template <typename T> struct Mma16;
+template <> struct Mma16<bf16_t> {  // 16 bytes a lane are 32 k of 16 rows
+  __device__ static f32x4_t mma(const u32x4_t& a, const u32x4_t& b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
+                                                   0, 0);
+  }
+};
+template <> struct Mma16<float> {  // 16 k, in four products of one k of each lane group
+  __device__ static f32x4_t mma(const u32x4_t& a, const u32x4_t& b, f32x4_t c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c, 0, 0, 0);
+    return c;
+  }
+};
+
 // Word 3 of a buffer resource on this family: 32-bit data format, raw byte addressing.
 constexpr int kRsrcFlags = 0x00020000;
 

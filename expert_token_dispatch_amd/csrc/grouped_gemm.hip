@@ -1005,7 +1005,7 @@ moe_status launch_adapted_products(const AdaptedFfnArgs& a) {
   if (use_big_adapted(d, a.f.max_pairs))
     return launch_big_ffn(a.f, gate_up_adapters(d, a.ad, a.w), down_adapters(d, a.ad, a.w),
                           [&] { return launch_adapter_shrink(a, true); });
-  return skinny_ffn_fits(d, a.f.max_pairs) ? launch_skinny_adapted(a) : launch_general_adapted(a);
+  return skinny_adapted_fits(d, a.f.max_pairs) ? launch_skinny_adapted(a) : launch_general_adapted(a);
 }
 
 }  // namespace moe

@@ -28,6 +28,9 @@ namespace {
 namespace skinny {
 
 constexpr int kThreads = 256, kMaxRowBlocks = 4;
+// k of one step: 64 bytes of a row
+template <typename T>
+constexpr int kStep = 64 / int(sizeof(T));
 
 bool supported(int K) { return K % 32 == 0; }
 
@@ -43,22 +46,22 @@ bool supported(int K) { return K % 32 == 0; }
 template <int NMAT>
 constexpr int cols_per_block() { return NMAT == 2 ? 64 : 128; }
 
-// Adds the adapters' share to the sums of one row block (16 rows from row0, n of them there) and
-// the wave's two streams of 16 columns; layout of the sums: lane -> column lane & 15, register i ->
-// row 4 (lane / 16) + i.  A decode batch's rows have adapters of their own, so four adapters are
-// in flight together; each one's products take all the rows and are added to its own.
-template <int NMAT>
-__device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int row0, int n, int col0, int N, f32x4_t& acc0,
-                                             f32x4_t& acc1) {
-  constexpr int kFlight = 4;
-  const int lane = threadIdx.x & 63, r16 = lane & 15, kg = (lane >> 4) * 8;
-  const int id = r16 < n ? ad.rid[row0 + r16] : -1;
+// Adds the adapters' share to the sums of one row block (16 rows from row0, n of them there, id: the
+// adapter of row lane % 16) and the wave's two streams of 16 columns; layout of the sums: lane ->
+// column lane & 15, register i -> row 4 (lane / 16) + i.  A decode batch's rows have adapters of
+// their own, so four adapters are in flight together; each one's products take all the rows and
+// are added to its own.
+template <typename T, int NMAT>
+__device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int row0, int n, int id, int col0, int N,
+                                             f32x4_t& acc0, f32x4_t& acc1) {
+  constexpr int kFlight = 4, E = Elem<T>::kPerVec;
+  const int lane = threadIdx.x & 63, r16 = lane & 15, kg = (lane >> 4) * E;
   uint32_t todo = uint32_t(__ballot(id >= 0)) & 0xFFFF;
   const int row = row0 + min(r16, n - 1);
   const int col[2] = {min(col0 + r16, N - 1), min(NMAT == 2 ? col0 + r16 : col0 + 16 + r16, N - 1)};
   while (todo != 0) {
     uint32_t mine[kFlight];
-    const bf16_t* b[kFlight][2];
+    const T* b[kFlight][2];
     f32x4_t t[kFlight][2];
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
@@ -69,19 +72,19 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int m = NMAT == 2 ? s : 0;
-        b[f][s] = cur >= 0 && ad.u[m] != nullptr ? adapter_b<bf16_t>(ad, m, cur, expert, col[s], N) : b[0][s];
+        b[f][s] = cur >= 0 && ad.u[m] != nullptr ? adapter_b<T>(ad, m, cur, expert, col[s], N) : b[0][s];
         t[f][s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
     }
 #pragma unroll
     for (int m = 0; m < NMAT; ++m) {
       if (ad.u[m] == nullptr) continue;
-      const bf16_t* u = adapter_u<bf16_t>(ad, m, row);
-      for (int c0 = 0; c0 < ad.rank; c0 += 32) {
+      const T* u = adapter_u<T>(ad, m, row);
+      for (int c0 = 0; c0 < ad.rank; c0 += kStep<T>) {
         const int c = c0 + kg;
-        const bool in = c < ad.rank;  // eight at a time, as the rank is
+        const bool in = c < ad.rank;  // a vector at a time, as the rank is
         const u32x4_t zero = {0, 0, 0, 0};
-        const bf16x8_t uf = __builtin_bit_cast(bf16x8_t, in ? *reinterpret_cast<const u32x4_t*>(u + c) : zero);
+        const u32x4_t uf = in ? *reinterpret_cast<const u32x4_t*>(u + c) : zero;
         u32x4_t bf[kFlight][2];
 #pragma unroll
         for (int f = 0; f < kFlight; ++f)
@@ -92,8 +95,7 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int
         for (int f = 0; f < kFlight; ++f)
 #pragma unroll
           for (int s = 0; s < 2; ++s)
-            if (NMAT == 1 || s == m)
-              t[f][s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(uf, __builtin_bit_cast(bf16x8_t, bf[f][s]), t[f][s], 0, 0, 0);
+            if (NMAT == 1 || s == m) t[f][s] = Mma16<T>::mma(uf, bf[f][s], t[f][s]);
       }
     }
 #pragma unroll
@@ -113,13 +115,14 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int
 // the wave parks the block in its own 1 KB of LDS and reads the fragments back with
 // transposing reads, so the MFMAs see the same operands as with n-major weights.
 // AD: Adapters, whose share is added to the sums, or NoAdapters.
-template <int NMAT, bool SAVE, bool BKN, class AD, int KS>
-__global__ __launch_bounds__(kThreads) void gemm_kernel(const bf16_t* __restrict__ A, const int32_t* __restrict__ offsets,
-                                                        const bf16_t* __restrict__ B0, const bf16_t* __restrict__ B1,
-                                                        bf16_t* __restrict__ C, int N, int K, bf16_t* __restrict__ Gs,
-                                                        bf16_t* __restrict__ Us, AD ad) {
+template <typename T, int NMAT, bool SAVE, bool BKN, class AD, int KS>
+__global__ __launch_bounds__(kThreads) void gemm_kernel(const T* __restrict__ A, const int32_t* __restrict__ offsets,
+                                                        const T* __restrict__ B0, const T* __restrict__ B1,
+                                                        T* __restrict__ C, int N, int K, T* __restrict__ Gs,
+                                                        T* __restrict__ Us, AD ad) {
   constexpr int kWaveCols = NMAT == 2 ? 16 : 32;
-  constexpr int kPipe = 4;
+  constexpr int kPipe = 4, KK = kStep<T>, E = Elem<T>::kPerVec;
+  static_assert(!BKN || sizeof(T) == 2, "the transposing reads move 16-bit elements");
   const int expert = blockIdx.y;
   const int seg0 = offsets[expert];
   const int seg_n = offsets[expert + 1] - seg0;
@@ -128,12 +131,12 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(const bf16_t* __restrict
   // first output column of this wave; with KS > 1 the block's waves have the same
   const int col0 = KS > 1 ? int(blockIdx.x) * kWaveCols : int(blockIdx.x) * cols_per_block<NMAT>() + wave * kWaveCols;
   if (col0 >= N) return;
-  const int kb = KS > 1 ? 32 * ((K / 32) * wave / KS) : 0;              // this wave's k
-  const int ke = KS > 1 ? 32 * ((K / 32) * (wave + 1) / KS) : K;
+  const int kb = KS > 1 ? KK * ((K / KK) * wave / KS) : 0;              // this wave's k
+  const int ke = KS > 1 ? KK * ((K / KK) * (wave + 1) / KS) : K;
   const size_t boff = size_t(expert) * N * K;
-  const int kg = (lane >> 4) * 8;  // the lane's 8 k values within a step
-  const bf16_t* bs0;
-  const bf16_t* bs1;
+  const int kg = (lane >> 4) * E;  // the lane's k values within a step (8 in bf16)
+  const T* bs0;
+  const T* bs1;
   size_t kstride;  // elements between consecutive k of a lane's stream
   if constexpr (!BKN) {
     // stream 0 / 1 weight row of this lane (rows past N repeat row N-1; never stored)
@@ -165,10 +168,19 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(const bf16_t* __restrict
   for (int m0 = 0; m0 < seg_n; m0 += 16 * kMaxRowBlocks) {
     const int nrb = min(kMaxRowBlocks, (seg_n - m0 + 15) / 16);
     // token row of each row block for this lane (rows past the segment repeat its last row)
-    const bf16_t* arow[kMaxRowBlocks];
+    const T* arow[kMaxRowBlocks];
 #pragma unroll
     for (int rb = 0; rb < kMaxRowBlocks; ++rb)
       arow[rb] = A + size_t(seg0 + min(m0 + rb * 16 + (lane & 15), seg_n - 1)) * K + kg;
+    // the adapters of the rows that this wave finishes, asked for before the products
+    int ids[KS > 1 ? 1 : kMaxRowBlocks] = {};
+    if constexpr (std::is_same<AD, Adapters>::value) {
+#pragma unroll
+      for (int rb = 0; rb < (KS > 1 ? 1 : kMaxRowBlocks); ++rb) {
+        const int r = m0 + (KS > 1 ? wave : rb) * 16 + (lane & 15);
+        ids[rb] = r < seg_n ? ad.rid[seg0 + r] : -1;
+      }
+    }
     f32x4_t acc[2][kMaxRowBlocks];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -180,14 +192,14 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(const bf16_t* __restrict
     // fit, but each keeps more in flight; same-box A/B on the decode-sized
     // layer: 0 to -4% per layer against two steps, while capping registers for
     // more waves per SIMD made it 12% slower)
-    bf16x8_t w0[2][kPipe], w1[2][kPipe], a0[2][kPipe];
-    const int nset = (ke - kb) / (32 * kPipe);
+    u32x4_t w0[2][kPipe], w1[2][kPipe], a0[2][kPipe];
+    const int nset = (ke - kb) / (KK * kPipe);
     auto load_set = [&](int b, int k0) {
 #pragma unroll
       for (int u = 0; u < kPipe; ++u) {
-        w0[b][u] = *reinterpret_cast<const bf16x8_t*>(bs0 + size_t(k0 + 32 * u) * kstride);
-        w1[b][u] = *reinterpret_cast<const bf16x8_t*>(bs1 + size_t(k0 + 32 * u) * kstride);
-        a0[b][u] = *reinterpret_cast<const bf16x8_t*>(arow[0] + k0 + 32 * u);
+        w0[b][u] = *reinterpret_cast<const u32x4_t*>(bs0 + size_t(k0 + KK * u) * kstride);
+        w1[b][u] = *reinterpret_cast<const u32x4_t*>(bs1 + size_t(k0 + KK * u) * kstride);
+        a0[b][u] = *reinterpret_cast<const u32x4_t*>(arow[0] + k0 + KK * u);
       }
     };
     // k-major weights: park the loaded blocks, then read the fragments back transposed
@@ -195,13 +207,13 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(const bf16_t* __restrict
       if constexpr (BKN) {
 #pragma unroll
         for (int u = 0; u < kPipe; ++u) {
-          *reinterpret_cast<bf16x8_t*>(wpark + u * 1024 + woff) = w0[b][u];
-          *reinterpret_cast<bf16x8_t*>(wpark + (kPipe + u) * 1024 + woff) = w1[b][u];
+          *reinterpret_cast<u32x4_t*>(wpark + u * 1024 + woff) = w0[b][u];
+          *reinterpret_cast<u32x4_t*>(wpark + (kPipe + u) * 1024 + woff) = w1[b][u];
         }
 #pragma unroll
         for (int u = 0; u < kPipe; ++u) {
-          w0[b][u] = read_kn_frag2(wpark + u * 1024 + roff0, wpark + u * 1024 + roff1);
-          w1[b][u] = read_kn_frag2(wpark + (kPipe + u) * 1024 + roff0, wpark + (kPipe + u) * 1024 + roff1);
+          w0[b][u] = __builtin_bit_cast(u32x4_t, read_kn_frag2(wpark + u * 1024 + roff0, wpark + u * 1024 + roff1));
+          w1[b][u] = __builtin_bit_cast(u32x4_t, read_kn_frag2(wpark + (kPipe + u) * 1024 + roff0, wpark + (kPipe + u) * 1024 + roff1));
         }
       }
     };
@@ -212,9 +224,9 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(const bf16_t* __restrict
 #pragma unroll
         for (int rb = 0; rb < kMaxRowBlocks; ++rb) {
           if (rb < nrb) {
-            const bf16x8_t a = rb == 0 ? a0[b][u] : *reinterpret_cast<const bf16x8_t*>(arow[rb] + k0 + 32 * u);
-            acc[0][rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w0[b][u], acc[0][rb], 0, 0, 0);
-            acc[1][rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w1[b][u], acc[1][rb], 0, 0, 0);
+            const u32x4_t a = rb == 0 ? a0[b][u] : *reinterpret_cast<const u32x4_t*>(arow[rb] + k0 + KK * u);
+            acc[0][rb] = Mma16<T>::mma(a, w0[b][u], acc[0][rb]);
+            acc[1][rb] = Mma16<T>::mma(a, w1[b][u], acc[1][rb]);
           }
         }
       }
@@ -222,54 +234,54 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(const bf16_t* __restrict
     if (nset > 0) load_set(0, kb);
     int set = 0;
     for (; set + 2 <= nset; set += 2) {
-      load_set(1, kb + (set + 1) * 32 * kPipe);
-      mma_set(0, kb + set * 32 * kPipe);
-      if (set + 2 < nset) load_set(0, kb + (set + 2) * 32 * kPipe);
-      mma_set(1, kb + (set + 1) * 32 * kPipe);
+      load_set(1, kb + (set + 1) * KK * kPipe);
+      mma_set(0, kb + set * KK * kPipe);
+      if (set + 2 < nset) load_set(0, kb + (set + 2) * KK * kPipe);
+      mma_set(1, kb + (set + 1) * KK * kPipe);
     }
-    if (set < nset) mma_set(0, kb + set * 32 * kPipe);
-    int k0 = kb + nset * 32 * kPipe;
-    for (; k0 < ke; k0 += 32) {
-      bf16x8_t v0 = *reinterpret_cast<const bf16x8_t*>(bs0 + size_t(k0) * kstride);
-      bf16x8_t v1 = *reinterpret_cast<const bf16x8_t*>(bs1 + size_t(k0) * kstride);
+    if (set < nset) mma_set(0, kb + set * KK * kPipe);
+    int k0 = kb + nset * KK * kPipe;
+    for (; k0 < ke; k0 += KK) {
+      u32x4_t v0 = *reinterpret_cast<const u32x4_t*>(bs0 + size_t(k0) * kstride);
+      u32x4_t v1 = *reinterpret_cast<const u32x4_t*>(bs1 + size_t(k0) * kstride);
       if constexpr (BKN) {
-        *reinterpret_cast<bf16x8_t*>(wpark + woff) = v0;
-        *reinterpret_cast<bf16x8_t*>(wpark + kPipe * 1024 + woff) = v1;
-        v0 = read_kn_frag2(wpark + roff0, wpark + roff1);
-        v1 = read_kn_frag2(wpark + kPipe * 1024 + roff0, wpark + kPipe * 1024 + roff1);
+        *reinterpret_cast<u32x4_t*>(wpark + woff) = v0;
+        *reinterpret_cast<u32x4_t*>(wpark + kPipe * 1024 + woff) = v1;
+        v0 = __builtin_bit_cast(u32x4_t, read_kn_frag2(wpark + roff0, wpark + roff1));
+        v1 = __builtin_bit_cast(u32x4_t, read_kn_frag2(wpark + kPipe * 1024 + roff0, wpark + kPipe * 1024 + roff1));
       }
 #pragma unroll
       for (int rb = 0; rb < kMaxRowBlocks; ++rb) {
         if (rb < nrb) {
-          const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(arow[rb] + k0);
-          acc[0][rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, v0, acc[0][rb], 0, 0, 0);
-          acc[1][rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, v1, acc[1][rb], 0, 0, 0);
+          const u32x4_t a = *reinterpret_cast<const u32x4_t*>(arow[rb] + k0);
+          acc[0][rb] = Mma16<T>::mma(a, v0, acc[0][rb]);
+          acc[1][rb] = Mma16<T>::mma(a, v1, acc[1][rb]);
         }
       }
     }
     // adapters' share, then the stores of one row block.  16x16 layout: lane -> weight row (column of
     // the output) lane & 15, register i -> token row 4*(lane/16) + i of the row block
-    auto finish = [&](int rb, f32x4_t& s0, f32x4_t& s1) {
+    auto finish = [&](int rb, int id, f32x4_t& s0, f32x4_t& s1) {
       if constexpr (std::is_same<AD, Adapters>::value)
-        add_adapters<NMAT>(ad, expert, seg0 + m0 + rb * 16, min(16, seg_n - m0 - rb * 16), col0, N, s0, s1);
+        add_adapters<T, NMAT>(ad, expert, seg0 + m0 + rb * 16, min(16, seg_n - m0 - rb * 16), id, col0, N, s0, s1);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = m0 + rb * 16 + 4 * (lane >> 4) + i;
         if (r < seg_n) {
-          bf16_t* crow = C + size_t(seg0 + r) * N;
+          T* crow = C + size_t(seg0 + r) * N;
           if (NMAT == 2) {
             const int col = col0 + (lane & 15);
             if (col < N) {
-              crow[col] = f32_to_bf16(silu(s0[i]) * s1[i]);
+              crow[col] = Elem<T>::from_f32(silu(s0[i]) * s1[i]);
               if constexpr (SAVE) {
-                Gs[size_t(seg0 + r) * N + col] = f32_to_bf16(s0[i]);
-                Us[size_t(seg0 + r) * N + col] = f32_to_bf16(s1[i]);
+                Gs[size_t(seg0 + r) * N + col] = Elem<T>::from_f32(s0[i]);
+                Us[size_t(seg0 + r) * N + col] = Elem<T>::from_f32(s1[i]);
               }
             }
           } else {
             const int c0 = col0 + (lane & 15), c1 = c0 + 16;
-            if (c0 < N) crow[c0] = f32_to_bf16(s0[i]);
-            if (c1 < N) crow[c1] = f32_to_bf16(s1[i]);
+            if (c0 < N) crow[c0] = Elem<T>::from_f32(s0[i]);
+            if (c1 < N) crow[c1] = Elem<T>::from_f32(s1[i]);
           }
         }
       }
@@ -277,7 +289,7 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(const bf16_t* __restrict
     if constexpr (KS == 1) {
 #pragma unroll
       for (int rb = 0; rb < kMaxRowBlocks; ++rb)
-        if (rb < nrb) finish(rb, acc[0][rb], acc[1][rb]);
+        if (rb < nrb) finish(rb, ids[rb], acc[0][rb], acc[1][rb]);
     } else {
       static_assert(KS == kThreads / 64 && KS == kMaxRowBlocks, "a wave for every row block");
       __shared__ f32x4_t sums[KS][kMaxRowBlocks][2][64];
@@ -296,7 +308,7 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(const bf16_t* __restrict
           s0 += sums[w][wave][0][lane];
           s1 += sums[w][wave][1][lane];
         }
-        finish(wave, s0, s1);
+        finish(wave, ids[0], s0, s1);
       }
     }
   }
@@ -304,17 +316,18 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(const bf16_t* __restrict
 
 // bkn: k-major weights (see gemm_kernel)
 // ks: the waves split K (adapters alone)
-template <int NMAT, class AD>
-moe_status launch(const char* name, const bf16_t* A, const int32_t* offsets, const bf16_t* B0, const bf16_t* B1,
-                  bf16_t* C, int L, int N, int K, bool bkn, bool ks, hipStream_t s, bf16_t* Gs, bf16_t* Us, const AD& ad) {
+template <typename T, int NMAT, class AD>
+moe_status launch(const char* name, const T* A, const int32_t* offsets, const T* B0, const T* B1, T* C, int L, int N,
+                  int K, bool bkn, bool ks, hipStream_t s, T* Gs, T* Us, const AD& ad) {
   const int cols = ks ? cols_per_block<NMAT>() / 4 : cols_per_block<NMAT>();
   const dim3 grid(unsigned((N + cols - 1) / cols), unsigned(L));
+  constexpr bool kKn = sizeof(T) == 2;  // float32 layers come n-major alone
 #define MOE_SKINNY(SAVE_, KS_)                                                                                     \
   do {                                                                                                             \
-    if (bkn)                                                                                                       \
-      MOE_LAUNCH(name, (gemm_kernel<NMAT, SAVE_, true, AD, KS_>), grid, dim3(kThreads), 0, s, A, offsets, B0, B1, C, N, K, Gs, Us, ad); \
+    if (kKn && bkn)                                                                                                \
+      MOE_LAUNCH(name, (gemm_kernel<T, NMAT, SAVE_, kKn, AD, KS_>), grid, dim3(kThreads), 0, s, A, offsets, B0, B1, C, N, K, Gs, Us, ad); \
     else                                                                                                           \
-      MOE_LAUNCH(name, (gemm_kernel<NMAT, SAVE_, false, AD, KS_>), grid, dim3(kThreads), 0, s, A, offsets, B0, B1, C, N, K, Gs, Us, ad); \
+      MOE_LAUNCH(name, (gemm_kernel<T, NMAT, SAVE_, false, AD, KS_>), grid, dim3(kThreads), 0, s, A, offsets, B0, B1, C, N, K, Gs, Us, ad); \
   } while (0)
   if constexpr (std::is_same<AD, Adapters>::value) {
     if (ks) MOE_SKINNY(false, 4);
@@ -330,26 +343,26 @@ moe_status launch(const char* name, const bf16_t* A, const int32_t* offsets, con
 constexpr int kFullBlocks = 1024;
 
 // between(): enqueued between the two products
-template <class AD, class Between>
+template <typename T, class AD, class Between>
 moe_status launch_both(const FfnArgs& a, const AD& gu, const AD& dn, const Between& between) {
   const moe_layer_desc* d = a.d;
   const int L = d->local_count, H = d->hidden, I = d->intermediate;
-  bf16_t* h = static_cast<bf16_t*>(a.h);
+  T* h = static_cast<T*>(a.h);
   const bool kn = d->weight_layout == MOE_WEIGHTS_IN_OUT;
   // fewer than kFullBlocks blocks, if every row is another expert's, leave the waves waiting for
   // their own loads
   const auto ks = [&](int N, int cols) {
     return std::is_same<AD, Adapters>::value && std::min<int64_t>(a.max_pairs, L) * ((N + cols - 1) / cols) < kFullBlocks;
   };
-  moe_status st = launch<2>("ffn_gate_up", static_cast<const bf16_t*>(a.x_sorted), a.offsets,
-                            static_cast<const bf16_t*>(a.w_gate), static_cast<const bf16_t*>(a.w_up), h, L, I, H, kn, ks(I, cols_per_block<2>()), a.s,
-                            static_cast<bf16_t*>(a.g_out), static_cast<bf16_t*>(a.u_out), gu);
+  moe_status st = launch<T, 2>("ffn_gate_up", static_cast<const T*>(a.x_sorted), a.offsets,
+                            static_cast<const T*>(a.w_gate), static_cast<const T*>(a.w_up), h, L, I, H, kn, ks(I, cols_per_block<2>()), a.s,
+                            static_cast<T*>(a.g_out), static_cast<T*>(a.u_out), gu);
   if (st != MOE_OK) return st;
   st = between();
   if (st != MOE_OK) return st;
-  return launch<1>("ffn_down", h, a.offsets, static_cast<const bf16_t*>(a.w_down), static_cast<const bf16_t*>(a.w_down),
-                   static_cast<bf16_t*>(a.y_sorted), L, H, I, kn, ks(H, cols_per_block<1>()), a.s, static_cast<bf16_t*>(nullptr),
-                   static_cast<bf16_t*>(nullptr), dn);
+  return launch<T, 1>("ffn_down", h, a.offsets, static_cast<const T*>(a.w_down), static_cast<const T*>(a.w_down),
+                   static_cast<T*>(a.y_sorted), L, H, I, kn, ks(H, cols_per_block<1>()), a.s, static_cast<T*>(nullptr),
+                   static_cast<T*>(nullptr), dn);
 }
 
 }  // namespace skinny
@@ -362,12 +375,21 @@ bool skinny_ffn_fits(const moe_layer_desc* d, int64_t max_pairs) {
 }
 
 moe_status launch_skinny_ffn(const FfnArgs& a) {
-  return skinny::launch_both(a, NoAdapters(), NoAdapters(), [] { return MOE_OK; });
+  return skinny::launch_both<bf16_t>(a, NoAdapters(), NoAdapters(), [] { return MOE_OK; });
+}
+
+// float32 rows too, where the weights lie along k
+bool skinny_adapted_fits(const moe_layer_desc* d, int64_t max_pairs) {
+  if (d->dtype == MOE_BF16) return skinny_ffn_fits(d, max_pairs);
+  return d->weight_layout == MOE_WEIGHTS_OUT_IN && max_pairs <= int64_t(32) * d->local_count &&
+         d->hidden % skinny::kStep<float> == 0 && d->intermediate % skinny::kStep<float> == 0;
 }
 
 moe_status launch_skinny_adapted(const AdaptedFfnArgs& a) {
-  return skinny::launch_both(a.f, gate_up_adapters(a.f.d, a.ad, a.w), down_adapters(a.f.d, a.ad, a.w),
-                             [&] { return launch_adapter_shrink(a, true); });
+  const Adapters gu = gate_up_adapters(a.f.d, a.ad, a.w), dn = down_adapters(a.f.d, a.ad, a.w);
+  const auto between = [&] { return launch_adapter_shrink(a, true); };
+  return a.f.d->dtype == MOE_BF16 ? skinny::launch_both<bf16_t>(a.f, gu, dn, between)
+                                  : skinny::launch_both<float>(a.f, gu, dn, between);
 }
 
 }  // namespace moe

