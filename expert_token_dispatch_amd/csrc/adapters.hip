@@ -49,16 +49,60 @@ struct Ring {
   static constexpr int kLoads = (kRows / kPerLoad + kWaves - 1) / kWaves;                         // a wave's, per stage
   static constexpr int kStage = kLoads * kWaves * 1024;
   static constexpr int kSums = WK * 16 * RB * 16 * NG * 4;
-  static constexpr int kSlots = RB == 1 ? (kStage <= 8 * 1024 ? 8 : kStage <= 12 * 1024 ? 6 : kStage <= 20 * 1024 ? 5 : 3) : 3;
+  static constexpr int kSlots = kStage <= 8 * 1024 ? 8 : kStage <= 12 * 1024 ? 6 : kStage <= 20 * 1024 ? 4 : 3;
   static constexpr int kLds = kSlots * kStage > kSums ? kSlots * kStage : kSums;
 };
+
+// The expert of row block g and the block's first row within it; expert -1 past the last.  The
+// lanes hold four experts each, so 256 experts cost one round of loads.
+struct RowBlock {
+  int expert, m0;
+};
+__device__ __forceinline__ RowBlock find_rows(const int32_t* __restrict__ offsets, int L, int rows, int g) {
+  const int lane = threadIdx.x & 63;
+  for (int i0 = 0; i0 < L; i0 += 256) {
+    int off[5], t[4];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) off[j] = offsets[min(i0 + 4 * lane + j, L)];
+    int own = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) own += t[j] = (off[j + 1] - off[j] + rows - 1) / rows;  // past L: no rows
+    int upto = own;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(upto, d, 64);
+      if (lane >= d) upto += v;
+    }
+    const uint64_t past = __ballot(upto > g);
+    if (past != 0) {
+      const int l = __builtin_ctzll(past);
+      int r = g - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(own, l)), e = i0 + 4 * l;
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        const int tj = __builtin_amdgcn_readlane(t[j], l);
+        if (e == i0 + 4 * l + j && r >= tj) {
+          r -= tj;
+          ++e;
+        }
+      }
+      return {e, r * rows};
+    }
+    g -= __builtin_amdgcn_readlane(upto, 63);
+  }
+  return {-1, 0};
+}
 
 // NG groups of 16 of the mats * rank columns a block (blockIdx.z / slots); of its rows' adapters it
 // takes every slots-th (blockIdx.z % slots).
 template <typename T, int RB, int NG>
 __device__ __forceinline__ void shrink_body(const ShrinkP& p, int slots, char* lds) {
   using S = Ring<RB, NG>;
-  const int e = blockIdx.x, seg0 = p.offsets[e], n = p.offsets[e + 1] - seg0;
+  // in a prompt an XCD's blocks (every eighth) are neighbours, whose adapters are often the same
+  const int per_xcd = (gridDim.x + 7) / 8, b = blockIdx.x;
+  const RowBlock at_rows = find_rows(p.offsets, p.L, 16 * RB, RB > 1 ? b % 8 * per_xcd + b / 8 : b);
+  const int e = at_rows.expert, m0 = at_rows.m0;
+  if (e < 0) return;
+  const int seg0 = p.offsets[e], n = p.offsets[e + 1] - seg0;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wk = wave % S::WK, wm = wave / S::WK;
   const int slot = blockIdx.z % slots, c0 = (blockIdx.z / slots) * NG * 16, cols = p.mats * p.rank;
@@ -68,114 +112,112 @@ __device__ __forceinline__ void shrink_body(const ShrinkP& p, int slots, char* l
   constexpr int CPR = S::kRowBytes / 16;      // 16-byte chunks of a stage's row
   // chunk c of row r sits at chunk c ^ swizzle(r): 16 rows' reads of one chunk fall in different banks
   auto swizzle = [](int r) { return CPR == 8 ? (r >> 1) & 7 : r & 15; };
-  for (int m0 = blockIdx.y * 16 * RB; m0 < n; m0 += gridDim.y * 16 * RB) {
-    // the adapters of the rows, one a lane (RB <= 4), the same in every wave
-    int id = -1;
-    if (lane < 16 * RB && m0 + lane < n) {
-      const int q = seg0 + m0 + lane;
-      if (p.pairs != nullptr) {
-        id = p.ids[p.pairs[q] / p.top_k];
-        if (id < 0 || id >= p.count) id = -1;
-        if (wave == 0 && blockIdx.z == 0) p.rid[q] = id;
+  // the adapters of the rows, one a lane (RB <= 2), the same in every wave
+  int id = -1;
+  if (lane < 16 * RB && m0 + lane < n) {
+    const int q = seg0 + m0 + lane;
+    if (p.pairs != nullptr) {
+      id = p.ids[p.pairs[q] / p.top_k];
+      if (id < 0 || id >= p.count) id = -1;
+      if (wave == 0 && blockIdx.z == 0) p.rid[q] = id;
+    } else {
+      id = p.rid[q];
+    }
+  }
+  uint64_t todo = p.mats > 0 ? __ballot(id >= 0) : 0;  // gate and up without adapters: the ids alone
+  const __amdgpu_buffer_rsrc_t x_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<T*>(static_cast<const T*>(p.x) + size_t(seg0 + m0) * p.K), 0, uint32_t(16 * RB) * row_bytes, kRsrcFlags);
+  for (int seen = 0; todo != 0; ++seen) {
+    const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+    const uint64_t mine = __ballot(id == cur);
+    todo &= ~mine;
+    if (seen % slots != slot) continue;
+    // this lane's place in each of the wave's loads: row of the stage (x, then A), chunk, byte offset
+    __amdgpu_buffer_rsrc_t rsrc[S::kLoads];
+    uint32_t at[S::kLoads], in_row[S::kLoads];
+#pragma unroll
+    for (int j = 0; j < S::kLoads; ++j) {
+      const int b = S::kLoads * wave + j, r0 = b * S::kPerLoad, r = r0 + lane / CPR;
+      in_row[j] = uint32_t((lane % CPR) ^ swizzle(r)) * 16u;
+      if (r0 < 16 * RB) {
+        rsrc[j] = x_rsrc;
+        at[j] = (mine >> r) & 1 ? uint32_t(r) * row_bytes : kOutside;
       } else {
-        id = p.rid[q];
+        const int col0 = c0 + r0 - 16 * RB, c = col0 + lane / CPR;  // the rank is a multiple of 8: one matrix a load
+        const int m = col0 >= p.rank ? 1 : 0;
+        rsrc[j] = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<T*>(static_cast<const T*>(p.a[m]) + (size_t(cur) * p.L + e) * p.rank * p.K), 0,
+            uint32_t(p.rank) * row_bytes, kRsrcFlags);
+        at[j] = c < cols && r < S::kRows ? uint32_t(c - m * p.rank) * row_bytes : kOutside;
       }
     }
-    uint64_t todo = p.mats > 0 ? __ballot(id >= 0) : 0;  // gate and up without adapters: the ids alone
-    const __amdgpu_buffer_rsrc_t x_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<T*>(static_cast<const T*>(p.x) + size_t(seg0 + m0) * p.K), 0, uint32_t(16 * RB) * row_bytes, kRsrcFlags);
-    for (int seen = 0; todo != 0; ++seen) {
-      const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-      const uint64_t mine = __ballot(id == cur);
-      todo &= ~mine;
-      if (seen % slots != slot) continue;
-      // this lane's place in each of the wave's loads: row of the stage (x, then A), chunk, byte offset
-      __amdgpu_buffer_rsrc_t rsrc[S::kLoads];
-      uint32_t at[S::kLoads], in_row[S::kLoads];
+    auto issue = [&](int s) {  // stage min(s, nk - 1) into slot s
+      char* dst = lds + (s % S::kSlots) * S::kStage + S::kLoads * wave * 1024;
+      const uint32_t k0 = uint32_t(min(s, nk - 1)) * S::kRowBytes;
 #pragma unroll
       for (int j = 0; j < S::kLoads; ++j) {
-        const int b = S::kLoads * wave + j, r0 = b * S::kPerLoad, r = r0 + lane / CPR;
-        in_row[j] = uint32_t((lane % CPR) ^ swizzle(r)) * 16u;
-        if (r0 < 16 * RB) {
-          rsrc[j] = x_rsrc;
-          at[j] = (mine >> r) & 1 ? uint32_t(r) * row_bytes : kOutside;
-        } else {
-          const int col0 = c0 + r0 - 16 * RB, c = col0 + lane / CPR;  // the rank is a multiple of 8: one matrix a load
-          const int m = col0 >= p.rank ? 1 : 0;
-          rsrc[j] = __builtin_amdgcn_make_buffer_rsrc(
-              const_cast<T*>(static_cast<const T*>(p.a[m]) + (size_t(cur) * p.L + e) * p.rank * p.K), 0,
-              uint32_t(p.rank) * row_bytes, kRsrcFlags);
-          at[j] = c < cols && r < S::kRows ? uint32_t(c - m * p.rank) * row_bytes : kOutside;
-        }
+        const uint32_t k = k0 + in_row[j];
+        const uint32_t vo = at[j] != kOutside && k < row_bytes ? at[j] + k : kOutside;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc[j], (lds_ptr_t)(dst + j * 1024), 16, vo, 0, 0, 0);
       }
-      auto issue = [&](int s) {  // stage min(s, nk - 1) into slot s
-        char* dst = lds + (s % S::kSlots) * S::kStage + S::kLoads * wave * 1024;
-        const uint32_t k0 = uint32_t(min(s, nk - 1)) * S::kRowBytes;
+    };
+    f32x4_t acc[S::MB][NG];
 #pragma unroll
-        for (int j = 0; j < S::kLoads; ++j) {
-          const uint32_t k = k0 + in_row[j];
-          const uint32_t vo = at[j] != kOutside && k < row_bytes ? at[j] + k : kOutside;
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc[j], (lds_ptr_t)(dst + j * 1024), 16, vo, 0, 0, 0);
-        }
-      };
-      f32x4_t acc[S::MB][NG];
+    for (int rb = 0; rb < S::MB; ++rb)
+#pragma unroll
+      for (int g = 0; g < NG; ++g) acc[rb][g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    // fragments: row lane % 16 of a block, chunk 4 wk + lane / 16
+    const int chunk = 4 * wk + (lane >> 4);
+    int xo[S::MB], ao[NG];
+#pragma unroll
+    for (int rb = 0; rb < S::MB; ++rb) {
+      const int r = (wm * S::MB + rb) * 16 + (lane & 15);
+      xo[rb] = r * S::kRowBytes + (chunk ^ swizzle(r)) * 16;
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int r = 16 * RB + g * 16 + (lane & 15);
+      ao[g] = r * S::kRowBytes + (chunk ^ swizzle(r)) * 16;
+    }
+    __syncthreads();  // the sums of the adapter before have been read
+#pragma unroll
+    for (int s = 0; s < S::kSlots - 1; ++s) issue(s);
+    for (int s = 0; s < nk; ++s) {
+      MOE_VMCNT(S::kLoads * (S::kSlots - 2));   // this wave's loads of stage s have landed
+      __builtin_amdgcn_s_waitcnt(0xC07F);       // and its reads of stage s - 1 (lgkmcnt)
+      block_barrier();                          // as every wave's have
+      issue(s + S::kSlots - 1);                 // into the slot of stage s - 1
+      const char* st = lds + (s % S::kSlots) * S::kStage;
+      u32x4_t xv[S::MB], av[NG];
+#pragma unroll
+      for (int rb = 0; rb < S::MB; ++rb) xv[rb] = *reinterpret_cast<const u32x4_t*>(st + xo[rb]);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) av[g] = *reinterpret_cast<const u32x4_t*>(st + ao[g]);
 #pragma unroll
       for (int rb = 0; rb < S::MB; ++rb)
 #pragma unroll
-        for (int g = 0; g < NG; ++g) acc[rb][g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      // fragments: row lane % 16 of a block, chunk 4 wk + lane / 16
-      const int chunk = 4 * wk + (lane >> 4);
-      int xo[S::MB], ao[NG];
+        for (int g = 0; g < NG; ++g) acc[rb][g] = Mma16<T>::mma(xv[rb], av[g], acc[rb][g]);
+    }
+    MOE_VMCNT(0);     // the last (repeated) loads land before the sums take their place
+    __syncthreads();  // in every wave
+    // lane -> column lane % 16 of the group, register i -> row 4 (lane / 16) + i
+    float* red = reinterpret_cast<float*>(lds);  // [WK][16 RB][16 NG]
 #pragma unroll
-      for (int rb = 0; rb < S::MB; ++rb) {
-        const int r = (wm * S::MB + rb) * 16 + (lane & 15);
-        xo[rb] = r * S::kRowBytes + (chunk ^ swizzle(r)) * 16;
-      }
+    for (int rb = 0; rb < S::MB; ++rb)
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const int r = 16 * RB + g * 16 + (lane & 15);
-        ao[g] = r * S::kRowBytes + (chunk ^ swizzle(r)) * 16;
-      }
-      __syncthreads();  // the sums of the adapter before have been read
+      for (int g = 0; g < NG; ++g)
 #pragma unroll
-      for (int s = 0; s < S::kSlots - 1; ++s) issue(s);
-      for (int s = 0; s < nk; ++s) {
-        MOE_VMCNT(S::kLoads * (S::kSlots - 2));   // this wave's loads of stage s have landed
-        __builtin_amdgcn_s_waitcnt(0xC07F);       // and its reads of stage s - 1 (lgkmcnt)
-        block_barrier();                          // as every wave's have
-        issue(s + S::kSlots - 1);                 // into the slot of stage s - 1
-        const char* st = lds + (s % S::kSlots) * S::kStage;
-        u32x4_t xv[S::MB], av[NG];
+        for (int i = 0; i < 4; ++i)
+          red[((wk * RB + wm * S::MB + rb) * 16 + 4 * (lane >> 4) + i) * (NG * 16) + g * 16 + (lane & 15)] = acc[rb][g][i];
+    __syncthreads();
+    const float sc = p.scale != nullptr ? p.scale[cur] : 1.0f;
+    for (int v = threadIdx.x; v < 16 * RB * 16 * NG; v += kWaves * 64) {
+      const int r = v / (NG * 16), c = v % (NG * 16);
+      if (!((mine >> r) & 1) || c0 + c >= cols) continue;
+      float a = red[v];
 #pragma unroll
-        for (int rb = 0; rb < S::MB; ++rb) xv[rb] = *reinterpret_cast<const u32x4_t*>(st + xo[rb]);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) av[g] = *reinterpret_cast<const u32x4_t*>(st + ao[g]);
-#pragma unroll
-        for (int rb = 0; rb < S::MB; ++rb)
-#pragma unroll
-          for (int g = 0; g < NG; ++g) acc[rb][g] = Mma16<T>::mma(xv[rb], av[g], acc[rb][g]);
-      }
-      MOE_VMCNT(0);     // the last (repeated) loads land before the sums take their place
-      __syncthreads();  // in every wave
-      // lane -> column lane % 16 of the group, register i -> row 4 (lane / 16) + i
-      float* red = reinterpret_cast<float*>(lds);  // [WK][16 RB][16 NG]
-#pragma unroll
-      for (int rb = 0; rb < S::MB; ++rb)
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            red[((wk * RB + wm * S::MB + rb) * 16 + 4 * (lane >> 4) + i) * (NG * 16) + g * 16 + (lane & 15)] = acc[rb][g][i];
-      __syncthreads();
-      const float sc = p.scale != nullptr ? p.scale[cur] : 1.0f;
-      for (int v = threadIdx.x; v < 16 * RB * 16 * NG; v += kWaves * 64) {
-        const int r = v / (NG * 16), c = v % (NG * 16);
-        if (!((mine >> r) & 1) || c0 + c >= cols) continue;
-        float a = red[v];
-#pragma unroll
-        for (int w = 1; w < S::WK; ++w) a += red[v + w * (16 * RB * 16 * NG)];
-        static_cast<T*>(p.u)[size_t(seg0 + m0 + r) * p.ldu + c0 + c] = Elem<T>::from_f32(sc * a);
-      }
+      for (int w = 1; w < S::WK; ++w) a += red[v + w * (16 * RB * 16 * NG)];
+      static_cast<T*>(p.u)[size_t(seg0 + m0 + r) * p.ldu + c0 + c] = Elem<T>::from_f32(sc * a);
     }
   }
 }
@@ -201,20 +243,23 @@ moe_status launch_ng(const char* name, const ShrinkP& p, const dim3& grid, int s
 template <typename T, int RB>
 moe_status launch_rb(const char* name, const ShrinkP& p, int64_t max_pairs, hipStream_t s) {
   const int groups = std::max(1, (p.mats * p.rank + 15) / 16);
-  // row blocks of an expert with four times its share; a larger one's blocks take more than one
-  const int64_t ny = std::min<int64_t>((max_pairs + 16 * RB - 1) / (16 * RB), 4 * max_pairs / (16 * RB * p.L) + 1);
+  const int64_t blocks = (max_pairs + 16 * RB - 1) / (16 * RB) + p.L;  // at most; a multiple of 8 for the XCDs
+  // rows of a decode batch have adapters of their own: four blocks share them
   const int slots = RB == 1 ? std::min(p.count, 4) : 1;
-  const auto grid = [&](int ng) { return dim3(unsigned(p.L), unsigned(ny), unsigned((groups + ng - 1) / ng * slots)); };
+  const auto grid = [&](int ng) {
+    return dim3(unsigned((blocks + 7) / 8 * 8), 1, unsigned((groups + ng - 1) / ng * slots));
+  };
   if (groups <= 1) return launch_ng<T, RB, 1>(name, p, grid(1), slots, s);
   if (groups <= 2) return launch_ng<T, RB, 2>(name, p, grid(2), slots, s);
   if (groups <= 4) return launch_ng<T, RB, 4>(name, p, grid(4), slots, s);
   return launch_ng<T, RB, 8>(name, p, grid(8), slots, s);
 }
 
-// Blocks of 64 rows, which read an adapter's A a quarter as often, where they still fill the card.
+// Blocks of 32 rows, which read an adapter's A half as often, where they fill the card twice (16384
+// pairs, rank 64, 4096 x 14336 experts: 107 and 220 us; 16 rows 146 and 234, 64 rows 119 and 238).
 template <typename T>
 moe_status launch_t(const char* name, const ShrinkP& p, int64_t max_pairs, hipStream_t s) {
-  return max_pairs >= 64 * 128 ? launch_rb<T, 4>(name, p, max_pairs, s) : launch_rb<T, 1>(name, p, max_pairs, s);
+  return max_pairs >= 32 * 256 ? launch_rb<T, 2>(name, p, max_pairs, s) : launch_rb<T, 1>(name, p, max_pairs, s);
 }
 
 int mats_of(const moe_adapters* a, bool down) {
