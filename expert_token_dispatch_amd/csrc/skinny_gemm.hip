@@ -132,7 +132,7 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(const T* __restrict__ A,
   const int col0 = KS > 1 ? int(blockIdx.x) * kWaveCols : int(blockIdx.x) * cols_per_block<NMAT>() + wave * kWaveCols;
   if (col0 >= N) return;
   const int kb = KS > 1 ? KK * ((K / KK) * wave / KS) : 0;              // this wave's k
-  const int ke = KS > 1 ? KK * ((K / KK) * (wave + 1) / KS) : K;
+  const int ke = KS > 1 ? KK * ((K / KK) * (wave + 1) / KS) : KK * (K / KK);
   const size_t boff = size_t(expert) * N * K;
   const int kg = (lane >> 4) * E;  // the lane's k values within a step (8 in bf16)
   const T* bs0;
@@ -259,6 +259,30 @@ __global__ __launch_bounds__(kThreads) void gemm_kernel(const T* __restrict__ A,
         }
       }
     }
+    // with adapters K may end inside a step: its vectors past the end are zeros
+    if constexpr (std::is_same<AD, Adapters>::value) {
+      const int kt = KK * (K / KK);
+      if (kt < K && (KS == 1 || wave == KS - 1)) {
+        const u32x4_t zero = {0, 0, 0, 0};
+        const bool a_in = kt + kg < K, b_in = BKN ? kt + (lane >> 1) < K : a_in;
+        u32x4_t v0 = b_in ? *reinterpret_cast<const u32x4_t*>(bs0 + size_t(kt) * kstride) : zero;
+        u32x4_t v1 = b_in ? *reinterpret_cast<const u32x4_t*>(bs1 + size_t(kt) * kstride) : zero;
+        if constexpr (BKN) {
+          *reinterpret_cast<u32x4_t*>(wpark + woff) = v0;
+          *reinterpret_cast<u32x4_t*>(wpark + kPipe * 1024 + woff) = v1;
+          v0 = __builtin_bit_cast(u32x4_t, read_kn_frag2(wpark + roff0, wpark + roff1));
+          v1 = __builtin_bit_cast(u32x4_t, read_kn_frag2(wpark + kPipe * 1024 + roff0, wpark + kPipe * 1024 + roff1));
+        }
+#pragma unroll
+        for (int rb = 0; rb < kMaxRowBlocks; ++rb) {
+          if (rb < nrb) {
+            const u32x4_t a = a_in ? *reinterpret_cast<const u32x4_t*>(arow[rb] + kt) : zero;
+            acc[0][rb] = Mma16<T>::mma(a, v0, acc[0][rb]);
+            acc[1][rb] = Mma16<T>::mma(a, v1, acc[1][rb]);
+          }
+        }
+      }
+    }
     // adapters' share, then the stores of one row block.  16x16 layout: lane -> weight row (column of
     // the output) lane & 15, register i -> token row 4*(lane/16) + i of the row block
     auto finish = [&](int rb, int id, f32x4_t& s0, f32x4_t& s1) {
@@ -378,11 +402,9 @@ moe_status launch_skinny_ffn(const FfnArgs& a) {
   return skinny::launch_both<bf16_t>(a, NoAdapters(), NoAdapters(), [] { return MOE_OK; });
 }
 
-// float32 rows too, where the weights lie along k
+// With adapters any width, and float32 rows where the weights lie along k.
 bool skinny_adapted_fits(const moe_layer_desc* d, int64_t max_pairs) {
-  if (d->dtype == MOE_BF16) return skinny_ffn_fits(d, max_pairs);
-  return d->weight_layout == MOE_WEIGHTS_OUT_IN && max_pairs <= int64_t(32) * d->local_count &&
-         d->hidden % skinny::kStep<float> == 0 && d->intermediate % skinny::kStep<float> == 0;
+  return max_pairs <= int64_t(32) * d->local_count && (d->dtype == MOE_BF16 || d->weight_layout == MOE_WEIGHTS_OUT_IN);
 }
 
 moe_status launch_skinny_adapted(const AdaptedFfnArgs& a) {
