@@ -15,6 +15,8 @@
 // straight from memory have a lane per row, sixteen lines a quarter wave, and kept the
 // texture unit four times as long (16384 pairs, rank 64, 4096 x 14336 experts: 180 and 380 us).
 // The waves split a stage's k (and the rows), and their sums meet in LDS in a fixed order.
+#include <math.h>
+
 #include <algorithm>
 
 #include "adapters.h"
@@ -32,8 +34,8 @@ struct ShrinkP {
   int32_t* rid;             // [P_max] adapter of every row, -1: none
   const float* scale;       // [count] or NULL
   const void* a[2];         // [count, L, rank, K] of up to two matrices
-  void* u;                  // [P_max, ldu]: matrix m's columns start at m * rank
-  int ldu, rank, count, mats, L, K, top_k;
+  void* u;                  // [P_max, ldu]: matrix m's columns start at m * rank, their low parts lo behind
+  int ldu, lo, rank, count, mats, L, K, top_k;
 };
 
 constexpr int kWaves = 4;
@@ -217,7 +219,14 @@ __device__ __forceinline__ void shrink_body(const ShrinkP& p, int slots, char* l
       float a = red[v];
 #pragma unroll
       for (int w = 1; w < S::WK; ++w) a += red[v + w * (16 * RB * 16 * NG)];
-      static_cast<T*>(p.u)[size_t(seg0 + m0 + r) * p.ldu + c0 + c] = Elem<T>::from_f32(sc * a);
+      T* u = static_cast<T*>(p.u) + size_t(seg0 + m0 + r) * p.ldu + c0 + c;
+      const T hi = Elem<T>::from_f32(sc * a);
+      u[0] = hi;
+      if constexpr (sizeof(T) == 2) {
+        // what hi leaves; nothing behind an infinity, which an inf - inf would make NaN
+        const float left = sc * a - Elem<T>::to_f32(hi);
+        u[p.lo] = Elem<T>::from_f32(fabsf(left) < INFINITY ? left : 0.0f);
+      }
     }
   }
 }
@@ -270,7 +279,6 @@ int mats_of(const moe_adapters* a, bool down) {
 
 AdapterScratch carve_adapter_scratch(const moe_layer_desc* d, const moe_adapters* a, int64_t max_pairs, void* base) {
   AdapterScratch w{};
-  const size_t dt = dtype_bytes(d->dtype);
   char* p = static_cast<char*>(base);
   size_t o = 0;
   auto take = [&](size_t bytes) -> void* {
@@ -279,8 +287,8 @@ AdapterScratch carve_adapter_scratch(const moe_layer_desc* d, const moe_adapters
     return r;
   };
   w.rid = static_cast<int32_t*>(take(size_t(max_pairs) * 4));
-  w.u_gu = take(size_t(max_pairs) * mats_of(a, false) * a->rank * dt);
-  w.u_down = take(size_t(max_pairs) * mats_of(a, true) * a->rank * dt);
+  w.u_gu = take(size_t(max_pairs) * mats_of(a, false) * a->rank * 4);  // float32, or two bfloat16
+  w.u_down = take(size_t(max_pairs) * mats_of(a, true) * a->rank * 4);
   w.ffn = take(adapted_ffn_scratch_bytes(d, max_pairs));
   w.bytes = o;
   return w;
@@ -296,7 +304,8 @@ Adapters gate_up_adapters(const moe_layer_desc* d, const moe_adapters* a, const 
   r.u[1] = a->up_a != nullptr ? u + (mats - 1) * a->rank * dt : nullptr;
   r.b[0] = a->gate_b;
   r.b[1] = a->up_b;
-  r.ldu = mats * a->rank;
+  r.lo = d->dtype == MOE_BF16 ? mats * a->rank : 0;
+  r.ldu = mats * a->rank + r.lo;
   r.rank = a->rank;
   r.experts = d->local_count;
   return r;
@@ -307,7 +316,9 @@ Adapters down_adapters(const moe_layer_desc* d, const moe_adapters* a, const Ada
   r.rid = w.rid;
   r.u[0] = a->down_a != nullptr ? w.u_down : nullptr;
   r.b[0] = a->down_b;
-  r.ldu = r.rank = a->rank;
+  r.rank = a->rank;
+  r.lo = d->dtype == MOE_BF16 ? a->rank : 0;
+  r.ldu = a->rank + r.lo;
   r.experts = d->local_count;
   return r;
 }
@@ -327,7 +338,8 @@ moe_status launch_adapter_shrink(const AdaptedFfnArgs& a, bool down) {
   p.L = d->local_count;
   p.K = down ? d->intermediate : d->hidden;
   p.top_k = d->top_k;
-  p.ldu = p.mats * p.rank;
+  p.lo = d->dtype == MOE_BF16 ? p.mats * p.rank : 0;
+  p.ldu = p.mats * p.rank + p.lo;
   if (down) {
     if (p.mats == 0) return MOE_OK;
     p.a[0] = a.ad->down_a;

@@ -111,6 +111,10 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int
               bf[v] = in ? *reinterpret_cast<const uint4*>(b + c + v * EPV) : make_uint4(0, 0, 0, 0);
             }
             G::mma(uf, bf, t);
+            if constexpr (sizeof(T) == 2) {
+              uf[0] = c + fk < ad.rank ? *reinterpret_cast<const uint4*>(u + ad.lo + c) : make_uint4(0, 0, 0, 0);
+              G::mma(uf, bf, t);
+            }
           }
 #pragma unroll
           for (int r = 0; r < 16; ++r) {

@@ -450,15 +450,15 @@ __device__ __forceinline__ f32x4_t* part_ptr(float* __restrict__ parts, int pslo
   return reinterpret_cast<f32x4_t*>(parts + size_t(pslot) * (kPartBytes / sizeof(float)));
 }
 
-// ---- adapters.  A tile's sums get the adapters' share before they are rounded: sixteen to
-// 128 more k of u and of the adapter's B, for one adapter of the tile's rows after another (one or
-// two in a prompt, whose requests follow each other).  Of every rank chunk of up to 64, the tile's rows of u
+// ---- adapters.  A tile's sums get the adapters' share before they are rounded: u's two parts
+// by the adapter's B, for one adapter of the tile's rows after another (one or two in a prompt,
+// whose requests follow each other).  Of every rank chunk of up to 32, the tile's rows of u
 // go to LDS once and an adapter's rows of B (the tile's columns) after them, with the next
 // adapter's already in flight; the products of all rows are formed apart and added where the row
 // has the adapter, so that a row's sum, and what a broken adapter spoils, do not depend on the
-// rows beside it.  LDS rows of 64 values and 16 bytes, so that 16 lanes' reads of 16 rows fall
+// rows beside it.  LDS rows of 32 values and 16 bytes, so that 16 lanes' reads of 16 rows fall
 // in different banks.
-constexpr int kChunkRank = 64, kAdRow = kChunkRank * 2 + 16;
+constexpr int kChunkRank = 32, kAdRow = kChunkRank * 2 + 16;
 
 template <int NMAT, bool WIDE, int NW>
 __device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int row0, int rows, int n0, int N, char* lds,
@@ -466,9 +466,10 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int
   using S = Shape<WIDE, NW>;
   constexpr int NB = S::NB, kThreads = S::kThreads, kIds = S::kA / 64;
   constexpr int kBLoads = S::kB * (kChunkRank / 8) / kThreads;  // 16-byte pieces of a B chunk a thread
-  char* su = lds;                             // [NMAT][kA] rows of u
-  char* sb = lds + NMAT * S::kA * kAdRow;     // [kB] rows of B
-  static_assert((NMAT * S::kA + S::kB) * kAdRow <= int(kLoopLdsMax), "u and B in the loop's LDS");
+  constexpr int kPieces = kChunkRank / 8;           // of 16 bytes in a row
+  char* su = lds;                                   // [NMAT][2][kA] rows of u and its low part
+  char* sb = lds + NMAT * 2 * S::kA * kAdRow;       // [kB] rows of B
+  static_assert((NMAT * 2 * S::kA + S::kB) * kAdRow <= int(kLoopLdsMax), "u and B in the loop's LDS");
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int wm = S::wm(wave), wn = S::wn(wave), fr = lane & 31, g = lane >> 5;
   int id[kIds];     // rows lane, 64 + lane, ... of the tile: what the block has to do
@@ -504,12 +505,12 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int
     for (int v = 0; v < kIds; ++v) left[v] = id[v];
     int cur = next(left);
     if (cur < 0) return;  // no row of the tile has an adapter
-    // piece p of a thread: row (tid + p * kThreads) / 8 of the tile's B rows, 16-byte piece % 8 of its chunk
+    // load p of a thread: row (tid + p * kThreads) / kPieces of the tile's B rows, piece % kPieces of its chunk
     u32x4_t pb[kBLoads];
     auto load_b = [&](int a) {
 #pragma unroll
       for (int p = 0; p < kBLoads; ++p) {
-        const int v = tid + p * kThreads, br = v >> 3, c = (v & 7) * 8;
+        const int v = tid + p * kThreads, br = v / kPieces, c = (v % kPieces) * 8;
         const int m = NMAT == 2 && br >= S::kB / 2 ? 1 : 0;
         const int col = min(n0 + br - m * (S::kB / 2), N - 1);
         pb[p] = c < cr && ad.u[m] != nullptr
@@ -522,11 +523,12 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int
       MOE_LGKMCNT0();
       block_barrier();  // the chunk before has been read
     }
-    for (int v = tid; v < NMAT * S::kA * (kChunkRank / 8); v += kThreads) {
-      const int c = (v & 7) * 8, r = (v >> 3) & (S::kA - 1), m = (v >> 3) / S::kA;
+    for (int v = tid; v < NMAT * 2 * S::kA * kPieces; v += kThreads) {
+      const int c = (v % kPieces) * 8, r = (v / kPieces) % S::kA, part = v / (kPieces * S::kA), m = part / 2;
       if (c >= nkc * 16 || r >= rows || ad.u[m] == nullptr) continue;
-      const u32x4_t w = c < cr ? *reinterpret_cast<const u32x4_t*>(adapter_u<bf16_t>(ad, m, row0 + r) + c0 + c) : zero;
-      *reinterpret_cast<u32x4_t*>(su + (m * S::kA + r) * kAdRow + c * 2) = w;
+      const bf16_t* u = adapter_u<bf16_t>(ad, m, row0 + r) + (part % 2) * ad.lo + c0 + c;
+      *reinterpret_cast<u32x4_t*>(su + (part * S::kA + r) * kAdRow + c * 2) =
+          c < cr ? *reinterpret_cast<const u32x4_t*>(u) : zero;
     }
     for (bool first = true; cur >= 0; first = false) {
       if (!first) {
@@ -536,7 +538,7 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int
 #pragma unroll
       for (int p = 0; p < kBLoads; ++p) {
         const int v = tid + p * kThreads;
-        *reinterpret_cast<u32x4_t*>(sb + (v >> 3) * kAdRow + (v & 7) * 16) = pb[p];
+        *reinterpret_cast<u32x4_t*>(sb + (v / kPieces) * kAdRow + (v % kPieces) * 16) = pb[p];
       }
       const int following = next(left);
       if (following >= 0) load_b(following);
@@ -557,13 +559,16 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int
           for (int i = 0; i < 4; ++i) {
             const bool own = mine_id[i] == cur;
             if (__ballot(own) == 0) continue;
-            const char* ur = su + (m * S::kA + wm * 128 + i * 32 + fr) * kAdRow + g * 16;
+            const char* ur = su + (2 * m * S::kA + wm * 128 + i * 32 + fr) * kAdRow + g * 16;
             f32x16_t t;
 #pragma unroll
             for (int r = 0; r < 16; ++r) t[r] = 0.0f;
 #pragma unroll
             for (int kc = 0; kc < kChunkRank / 16; ++kc)
-              if (kc < nkc) t = Bf16::mma(fb[kc], *reinterpret_cast<const bf16x8_t*>(ur + kc * 32), t);
+              if (kc < nkc) {
+                t = Bf16::mma(fb[kc], *reinterpret_cast<const bf16x8_t*>(ur + kc * 32), t);
+                t = Bf16::mma(fb[kc], *reinterpret_cast<const bf16x8_t*>(ur + S::kA * kAdRow + kc * 32), t);
+              }
             // lane -> token row: the whole column of sums is one row's
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][m * NJ + j][r] = own ? acc[i][m * NJ + j][r] + t[r] : acc[i][m * NJ + j][r];

@@ -85,6 +85,8 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int
         const bool in = c < ad.rank;  // a vector at a time, as the rank is
         const u32x4_t zero = {0, 0, 0, 0};
         const u32x4_t uf = in ? *reinterpret_cast<const u32x4_t*>(u + c) : zero;
+        u32x4_t ul = zero;
+        if constexpr (sizeof(T) == 2) ul = in ? *reinterpret_cast<const u32x4_t*>(u + ad.lo + c) : zero;
         u32x4_t bf[kFlight][2];
 #pragma unroll
         for (int f = 0; f < kFlight; ++f)
@@ -95,7 +97,10 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int
         for (int f = 0; f < kFlight; ++f)
 #pragma unroll
           for (int s = 0; s < 2; ++s)
-            if (NMAT == 1 || s == m) t[f][s] = Mma16<T>::mma(uf, bf[f][s], t[f][s]);
+            if (NMAT == 1 || s == m) {
+              t[f][s] = Mma16<T>::mma(uf, bf[f][s], t[f][s]);
+              if constexpr (sizeof(T) == 2) t[f][s] = Mma16<T>::mma(ul, bf[f][s], t[f][s]);
+            }
       }
     }
 #pragma unroll

@@ -581,7 +581,8 @@ moe_status moe_muon_update(const moe_muon_desc* m, const void* grad, float* mome
 /*   D(v, A, B) = scale[a] (v A[a,e]^T) B[a,e]^T                              */
 /*   g = x Wg + D(x, gate), u = x Wu + D(x, up), h = silu(g) u                */
 /*   y = h Wd + D(h, down)                                                    */
-/* All sums are float32; scale (v A^T), h and y are rounded to dtype once.    */
+/* All sums are float32; h and y are rounded to dtype once, and scale (v A^T) */
+/* to two bfloat16 (16 bits) where dtype is MOE_BF16.                         */
 /* What one adapter holds reaches the rows of no other.                       */
 /* ======================================================================== */
 

@@ -86,7 +86,7 @@ def test_ffn_arguments_refused(arg, value):
 @pytest.mark.parametrize("dtype", ("bf16", "f32"))
 def test_workspaces(dtype):
     d, lib = etd.make_desc(500, 64, 128, 8, 2, dtype=dtype), L.lib()
-    width = 2 if dtype == "bf16" else 4
+    width = 4   # float32, or two bfloat16
     for stage in (L.MOE_STAGE_FFN, L.MOE_STAGE_LAYER):
         plain = etd.moe_workspace_size(d, stage)
         full = etd.moe_adapted_workspace_size(d, _struct(), stage)
