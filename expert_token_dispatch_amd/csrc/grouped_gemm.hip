@@ -23,6 +23,7 @@
 #include "adapters.h"
 #include "big_tile.h"
 #include "kernels.h"
+#include "tile_adapters.h"
 
 namespace moe {
 namespace {
@@ -450,136 +451,6 @@ __device__ __forceinline__ f32x4_t* part_ptr(float* __restrict__ parts, int pslo
   return reinterpret_cast<f32x4_t*>(parts + size_t(pslot) * (kPartBytes / sizeof(float)));
 }
 
-// ---- adapters.  A tile's sums get the adapters' share before they are rounded: u's two parts
-// by the adapter's B, for one adapter of the tile's rows after another (one or two in a prompt,
-// whose requests follow each other).  Of every rank chunk of up to 32, the tile's rows of u
-// go to LDS once and an adapter's rows of B (the tile's columns) after them, with the next
-// adapter's already in flight; the products of all rows are formed apart and added where the row
-// has the adapter, so that a row's sum, and what a broken adapter spoils, do not depend on the
-// rows beside it.  LDS rows of 32 values and 16 bytes, so that 16 lanes' reads of 16 rows fall
-// in different banks.
-constexpr int kChunkRank = 32, kAdRow = kChunkRank * 2 + 16;
-
-template <int NMAT, bool WIDE, int NW>
-__device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int row0, int rows, int n0, int N, char* lds,
-                                             f32x16_t (&acc)[4][16 / NW]) {
-  using S = Shape<WIDE, NW>;
-  constexpr int NB = S::NB, kThreads = S::kThreads, kIds = S::kA / 64;
-  constexpr int kBLoads = S::kB * (kChunkRank / 8) / kThreads;  // 16-byte pieces of a B chunk a thread
-  constexpr int kPieces = kChunkRank / 8;           // of 16 bytes in a row
-  char* su = lds;                                   // [NMAT][2][kA] rows of u and its low part
-  char* sb = lds + NMAT * 2 * S::kA * kAdRow;       // [kB] rows of B
-  static_assert((NMAT * 2 * S::kA + S::kB) * kAdRow <= int(kLoopLdsMax), "u and B in the loop's LDS");
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int wm = S::wm(wave), wn = S::wn(wave), fr = lane & 31, g = lane >> 5;
-  int id[kIds];     // rows lane, 64 + lane, ... of the tile: what the block has to do
-  int mine_id[4];   // row fr of the wave's four row blocks
-#pragma unroll
-  for (int v = 0; v < kIds; ++v) id[v] = v * 64 + lane < rows ? ad.rid[row0 + v * 64 + lane] : -1;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = wm * 128 + i * 32 + fr;
-    mine_id[i] = r < rows ? ad.rid[row0 + r] : -1;
-  }
-  // the next adapter of the block's rows, in the order of their first rows; -1: none left
-  auto next = [&](int (&left)[kIds]) {
-    int cur = -1;
-#pragma unroll
-    for (int v = 0; v < kIds; ++v) {
-      const uint64_t some = __ballot(left[v] >= 0);
-      if (cur < 0 && some != 0) cur = __builtin_amdgcn_readlane(left[v], __builtin_ctzll(some));
-    }
-#pragma unroll
-    for (int v = 0; v < kIds; ++v)
-      if (left[v] == cur) left[v] = -1;
-    return cur;
-  };
-  MOE_LGKMCNT0();
-  block_barrier();  // every wave is done reading the last stage
-  for (int c0 = 0; c0 < ad.rank; c0 += kChunkRank) {
-    const int cr = min(kChunkRank, ad.rank - c0);  // a multiple of 8
-    const int nkc = (cr + 15) / 16;                // k chunks of 16; the last one's upper half may be zeros
-    const u32x4_t zero = {0, 0, 0, 0};
-    int left[kIds];
-#pragma unroll
-    for (int v = 0; v < kIds; ++v) left[v] = id[v];
-    int cur = next(left);
-    if (cur < 0) return;  // no row of the tile has an adapter
-    // load p of a thread: row (tid + p * kThreads) / kPieces of the tile's B rows, piece % kPieces of its chunk
-    u32x4_t pb[kBLoads];
-    auto load_b = [&](int a) {
-#pragma unroll
-      for (int p = 0; p < kBLoads; ++p) {
-        const int v = tid + p * kThreads, br = v / kPieces, c = (v % kPieces) * 8;
-        const int m = NMAT == 2 && br >= S::kB / 2 ? 1 : 0;
-        const int col = min(n0 + br - m * (S::kB / 2), N - 1);
-        pb[p] = c < cr && ad.u[m] != nullptr
-                    ? *reinterpret_cast<const u32x4_t*>(adapter_b<bf16_t>(ad, m, a, expert, col, N) + c0 + c)
-                    : zero;
-      }
-    };
-    load_b(cur);
-    if (c0 > 0) {
-      MOE_LGKMCNT0();
-      block_barrier();  // the chunk before has been read
-    }
-    for (int v = tid; v < NMAT * 2 * S::kA * kPieces; v += kThreads) {
-      const int c = (v % kPieces) * 8, r = (v / kPieces) % S::kA, part = v / (kPieces * S::kA), m = part / 2;
-      if (c >= nkc * 16 || r >= rows || ad.u[m] == nullptr) continue;
-      const bf16_t* u = adapter_u<bf16_t>(ad, m, row0 + r) + (part % 2) * ad.lo + c0 + c;
-      *reinterpret_cast<u32x4_t*>(su + (part * S::kA + r) * kAdRow + c * 2) =
-          c < cr ? *reinterpret_cast<const u32x4_t*>(u) : zero;
-    }
-    for (bool first = true; cur >= 0; first = false) {
-      if (!first) {
-        MOE_LGKMCNT0();
-        block_barrier();  // the adapter before has been read
-      }
-#pragma unroll
-      for (int p = 0; p < kBLoads; ++p) {
-        const int v = tid + p * kThreads;
-        *reinterpret_cast<u32x4_t*>(sb + (v / kPieces) * kAdRow + (v % kPieces) * 16) = pb[p];
-      }
-      const int following = next(left);
-      if (following >= 0) load_b(following);
-      MOE_LGKMCNT0();
-      block_barrier();
-#pragma unroll
-      for (int m = 0; m < NMAT; ++m) {
-        if (ad.u[m] == nullptr) continue;
-        constexpr int NJ = NB / NMAT;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          bf16x8_t fb[kChunkRank / 16];
-          const char* br = sb + (m * (S::kB / 2) + (wn * NJ + j) * 32 + fr) * kAdRow + g * 16;
-#pragma unroll
-          for (int kc = 0; kc < kChunkRank / 16; ++kc)
-            if (kc < nkc) fb[kc] = *reinterpret_cast<const bf16x8_t*>(br + kc * 32);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool own = mine_id[i] == cur;
-            if (__ballot(own) == 0) continue;
-            const char* ur = su + (2 * m * S::kA + wm * 128 + i * 32 + fr) * kAdRow + g * 16;
-            f32x16_t t;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) t[r] = 0.0f;
-#pragma unroll
-            for (int kc = 0; kc < kChunkRank / 16; ++kc)
-              if (kc < nkc) {
-                t = Bf16::mma(fb[kc], *reinterpret_cast<const bf16x8_t*>(ur + kc * 32), t);
-                t = Bf16::mma(fb[kc], *reinterpret_cast<const bf16x8_t*>(ur + S::kA * kAdRow + kc * 32), t);
-              }
-            // lane -> token row: the whole column of sums is one row's
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][m * NJ + j][r] = own ? acc[i][m * NJ + j][r] + t[r] : acc[i][m * NJ + j][r];
-          }
-        }
-      }
-      cur = following;
-    }
-  }
-}
-
 // One tile (or one K piece of it): the main loop, then the epilogue or the piece write-out.
 // AD: Adapters, whose share the tile (its first piece) adds, or NoAdapters.
 template <int NMAT, bool WIDE, int NW, int EP, bool BKN, bool AKM, class AD>
@@ -592,7 +463,8 @@ __device__ __forceinline__ void tile_body(const Operands& op, bf16_t* __restrict
   const int row0 = jb.row0, rows = jb.rows, n0 = jb.n0 * ON, tid = threadIdx.x;
   const auto epi = [&](f32x16_t (&acc)[4][NB]) {
     if constexpr (std::is_same<AD, Adapters>::value) {
-      if (jb.part == 0) add_adapters<NMAT, WIDE, NW>(ad, jb.expert, row0, rows, n0, N, lds, acc);
+      static_assert(kTileAdapterLds<S, NMAT> <= int(kLoopLdsMax), "u and B in the loop's LDS");
+      if (jb.part == 0) tile_adapters<S, NMAT, 4>(ad, jb.expert, row0, rows, n0, N, lds, acc);
     }
     if (jb.nparts > 1) {
       // one piece of a split tile: park the accumulators for fixup_kernel
@@ -896,13 +768,28 @@ size_t big_scratch_bytes(const moe_layer_desc* d) {
   return plan + (split ? size_t(big::kXcds) * big::kMaxParts * big::kPartBytes : 0);
 }
 
-// Rows an expert from which adapted products take the large tile (at its end wide tiles of 128 rows).
-// Against the decode kernel, rank 16, even and skewed experts: at 16 rows 258 and 259 us instead of
-// 287 and 363 (16 experts of 2880 x 2880), 344 and 398 instead of 360 and 1016 (128 of 2048 x 768),
-// 641 and 623 instead of 804 and 841 (8 of 4096 x 14336); at 9 rows 248, 335 and 591 instead of 187,
-// 292 and 520 where they are even.
-constexpr int kAdaptedBigRows = 16;
-bool use_big_adapted(const moe_layer_desc* d, int64_t max_pairs) { return use_big(d, max_pairs, kAdaptedBigRows); }
+// Which kernels adapted products take, by the most rows an expert that the descriptor allows, P / L
+// (rank 16, even and skewed experts, us; 16 experts of 2880 x 2880, 8 of 4096 x 14336, 128 of 2048 x
+// 768, 4 of 2048 x 4096, 16 of 1024 x 1024):
+//  - the decode kernel to 8 rows (at 9: 197, 536, 292, 69, 39 against 187, 528, 281, 86, 44 in the tiles
+//    of adapted_gemm.hip), to 16 where the experts are small and their weights are not what counts (at
+//    16: 259, 733, 366 against 200, 562, 301, but 81 and 52 against 87 and 51), to 64 of one expert;
+//  - the large tile from 256 rows and a card full of tiles (at 300: 437, 1277, -, 139 against 445, 1283, -,
+//    147; at 600 614, 1743 against 698, 2071; at 127 351, 819, 428 against 314, 720, 426);
+//  - the tiles of adapted_gemm.hip between them and at widths off the large tile's grid.
+// Weights stored along N are read by the large tile from 16 rows on, and by the decode and
+// general kernels elsewhere.
+enum AdaptedPath { kAdaptedSkinny, kAdaptedMid, kAdaptedBig, kAdaptedGeneral };
+AdaptedPath adapted_path(const moe_layer_desc* d, int64_t P) {
+  const int64_t L = d->local_count, H = d->hidden, I = d->intermediate;
+  if (d->dtype == MOE_BF16 && d->weight_layout == MOE_WEIGHTS_OUT_IN && mid_adapted_fits(d, P)) {
+    if (P <= 8 * L || (P <= 16 * L && 3 * L * H * I <= (int64_t(1) << 27)) || (L == 1 && P <= 64)) return kAdaptedSkinny;
+    const bool full = (P / big::BM + L / 2) * ((I + big::BNE / 2 - 1) / (big::BNE / 2)) >= 256;
+    return full && use_big(d, P, 256) ? kAdaptedBig : kAdaptedMid;
+  }
+  if (use_big(d, P, 16)) return kAdaptedBig;
+  return skinny_adapted_fits(d, P) ? kAdaptedSkinny : kAdaptedGeneral;
+}
 }  // namespace
 
 size_t ffn_scratch_bytes(const moe_layer_desc* d, int64_t max_pairs) {
@@ -910,7 +797,7 @@ size_t ffn_scratch_bytes(const moe_layer_desc* d, int64_t max_pairs) {
 }
 
 size_t adapted_ffn_scratch_bytes(const moe_layer_desc* d, int64_t max_pairs) {
-  return use_big_adapted(d, max_pairs) ? big_scratch_bytes(d) : 0;
+  return adapted_path(d, max_pairs) == kAdaptedBig ? big_scratch_bytes(d) : 0;
 }
 
 // ---- the backward's dgrad products on the large-tile kernel ---------------------
@@ -1007,10 +894,15 @@ moe_status launch_grouped_ffn(const FfnArgs& a) {
 
 moe_status launch_adapted_products(const AdaptedFfnArgs& a) {
   const moe_layer_desc* d = a.f.d;
-  if (use_big_adapted(d, a.f.max_pairs))
-    return launch_big_ffn(a.f, gate_up_adapters(d, a.ad, a.w), down_adapters(d, a.ad, a.w),
-                          [&] { return launch_adapter_shrink(a, true); });
-  return skinny_adapted_fits(d, a.f.max_pairs) ? launch_skinny_adapted(a) : launch_general_adapted(a);
+  switch (adapted_path(d, a.f.max_pairs)) {
+    case kAdaptedSkinny: return launch_skinny_adapted(a);
+    case kAdaptedMid: return launch_mid_adapted(a);
+    case kAdaptedBig:
+      return launch_big_ffn(a.f, gate_up_adapters(d, a.ad, a.w), down_adapters(d, a.ad, a.w),
+                            [&] { return launch_adapter_shrink(a, true); });
+    case kAdaptedGeneral: break;
+  }
+  return launch_general_adapted(a);
 }
 
 }  // namespace moe
