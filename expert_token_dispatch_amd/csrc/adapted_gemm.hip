@@ -12,6 +12,7 @@
 // of K, rows past the segment and weight rows past N are not loaded and read as zeros, so any
 // multiple of 8 is a width.
 #include <algorithm>
+#include <atomic>
 
 #include "adapters.h"
 #include "ffn_common.h"
@@ -38,18 +39,42 @@ constexpr int kXcds = 8;
 
 #define MOE_VMCNT(n) __builtin_amdgcn_s_waitcnt(((n) & 0xF) | (((n) >> 4) << 14) | (0x7 << 4) | (0xF << 8))
 
+// ---- which tile, and which part of its K, a block has.  Tiles run over (expert, column tile, row
+// tile), so that the row tiles that read the same weights run together, and each XCD (every
+// eighth block) takes a contiguous share of them in rounds of cpx, its CUs.  The r tiles of a round
+// that does not fill them are cut along K into s pieces, as many as the round has room for; a
+// piece leaves its float32 sums in the workspace and fixup_kernel adds the pieces in order.  (288
+// tiles of 45 stages on 256 CUs: 1.25 instead of 2 rounds.)
+constexpr int kMaxCut = 8, kMinStages = 4;  // pieces of a tile, stages of a piece
+constexpr int kMaxParts = 32;               // pieces of an XCD, a round of its CUs at most
+
+struct Plan {
+  int base, F, r, s, units;
+};
+__device__ __forceinline__ Plan plan_of(int total, int xcd, int cpx, int nk) {
+  Plan p;
+  const int q = total / kXcds, rest = total % kXcds, mine = q + (xcd < rest ? 1 : 0);
+  p.base = xcd * q + min(xcd, rest);
+  p.F = mine / cpx;
+  p.r = mine - p.F * cpx;
+  p.s = p.r == 0 ? 1 : max(1, min(min(cpx / p.r, kMaxCut), nk / kMinStages));
+  p.units = p.F * cpx + p.r * p.s;
+  return p;
+}
+
 struct Tile {
-  int expert, row0, rows, nt;  // nt: which of the product's NT column tiles; expert -1: none
+  int expert, row0, rows, nt;  // nt: which of the product's NT column tiles
 };
 
-// Tile t of the XCD-wise numbering.  Tiles run over (expert, column tile, row tile), so that the row
-// tiles that read the same weights run together, and each XCD takes a contiguous share.  The
-// lanes hold four experts each: 256 experts cost one round of loads.
+// The tiles of the experts, four a lane: 256 experts cost one round of loads.
 template <int KA>
-__device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offsets, int L, int NT, int b) {
-  const int lane = threadIdx.x & 63;
-  int off[5], own = 0, upto = 0, total = 0;
-  auto scan = [&](int i0) {  // lanes' experts from i0 on: their tiles, up to and with this lane's
+struct Tiles {
+  const int32_t* __restrict__ offsets;
+  int L, NT;
+  int off[5], own, upto;  // of the lane's experts of the last scan: tiles, and tiles up to and with them
+
+  __device__ __forceinline__ int scan(int i0) {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int j = 0; j < 5; ++j) off[j] = offsets[min(i0 + 4 * lane + j, L)];
     own = 0;
@@ -62,54 +87,73 @@ __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offsets, i
       if (lane >= d) upto += v;
     }
     return __builtin_amdgcn_readlane(upto, 63);
-  };
-  for (int i0 = 0; i0 < L; i0 += 256) total += scan(i0);
-  const int per_xcd = (total + kXcds - 1) / kXcds, loc = b / kXcds;
-  int t = b % kXcds * per_xcd + loc;
-  if (loc >= per_xcd || t >= total) return {-1, 0, 0, 0};
-  for (int i0 = 0; i0 < L; i0 += 256) {
-    if (L > 256) scan(i0);  // else the lanes hold it
-    const uint64_t past = __ballot(upto > t);
-    if (past != 0) {
-      const int l = __builtin_ctzll(past);
-      int r = t - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(own, l)), e = i0 + 4 * l;
-      int seg0 = 0, n = 0;
-      bool done = false;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int o0 = __builtin_amdgcn_readlane(off[j], l), o1 = __builtin_amdgcn_readlane(off[j + 1], l);
-        const int tj = (o1 - o0 + KA - 1) / KA * NT;
-        if (!done && r < tj) {
-          done = true;
-          e = i0 + 4 * l + j;
-          seg0 = o0;
-          n = o1 - o0;
-        }
-        if (!done) r -= tj;
-      }
-      const int mt = (n + KA - 1) / KA, m = r % mt;
-      return {e, seg0 + m * KA, min(KA, n - m * KA), r / mt};
-    }
-    t -= __builtin_amdgcn_readlane(upto, 63);
   }
-  return {-1, 0, 0, 0};
+  __device__ __forceinline__ int total() {
+    int n = 0;
+    for (int i0 = 0; i0 < L; i0 += 256) n += scan(i0);
+    return n;
+  }
+  // tile t < total(), after it
+  __device__ __forceinline__ Tile find(int t) {
+    for (int i0 = 0; i0 < L; i0 += 256) {
+      if (L > 256) scan(i0);  // else the lanes hold it
+      const uint64_t past = __ballot(upto > t);
+      if (past != 0) {
+        const int l = __builtin_ctzll(past);
+        int r = t - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(own, l)), e = 0, seg0 = 0, n = 1;
+        bool done = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int o0 = __builtin_amdgcn_readlane(off[j], l), o1 = __builtin_amdgcn_readlane(off[j + 1], l);
+          const int tj = (o1 - o0 + KA - 1) / KA * NT;
+          if (!done && r < tj) {
+            done = true;
+            e = i0 + 4 * l + j;
+            seg0 = o0;
+            n = o1 - o0;
+          }
+          if (!done) r -= tj;
+        }
+        const int mt = (n + KA - 1) / KA, m = r % mt;
+        return {e, seg0 + m * KA, min(KA, n - m * KA), r / mt};
+      }
+      t -= __builtin_amdgcn_readlane(upto, 63);
+    }
+    return {0, 0, 0, 0};  // not reached
+  }
+};
+
+// A piece's sums, thread-major: float4 number v of thread t at v * kThreads + t.
+template <int KA>
+__device__ __forceinline__ f32x4_t* part_of(float* parts, int slot) {
+  return reinterpret_cast<f32x4_t*>(parts + size_t(slot) * (Shape<KA>::kA * Shape<KA>::kB));
 }
 
 template <int NMAT, int KA>
 __device__ __forceinline__ void body(const bf16_t* A, const int32_t* __restrict__ offsets, const bf16_t* B0,
-                                     const bf16_t* B1, bf16_t* __restrict__ C, int L, int N, int K, const Adapters& ad,
-                                     char* lds) {
+                                     const bf16_t* B1, bf16_t* __restrict__ C, int L, int N, int K, int cpx, float* parts,
+                                     const Adapters& ad, char* lds) {
   using S = Shape<KA>;
   constexpr int kLoads = S::kLoads, kSlots = S::kSlots, kRowBytes = S::kRowBytes, kStage = S::kStage, NA = S::NA;
   static_assert(kTileAdapterLds<S, NMAT> <= S::kLds, "the adapters' LDS");
   constexpr int ON = S::kB / NMAT;  // columns of the output
-  const Tile tl = find_tile<KA>(offsets, L, (N + ON - 1) / ON, blockIdx.x);
-  if (tl.expert < 0) return;
+  const uint32_t row_bytes = uint32_t(K) * 2u;  // a multiple of 16
+  const int nk = int((row_bytes + kRowBytes - 1) / kRowBytes);
+  Tiles<KA> tiles{offsets, L, (N + ON - 1) / ON};
+  const int xcd = blockIdx.x % kXcds, u = blockIdx.x / kXcds;
+  const Plan plan = plan_of(tiles.total(), xcd, cpx, nk);
+  if (u >= plan.units) return;
+  int t = u, part = 0, nparts = 1;
+  if (u >= plan.F * cpx) {
+    nparts = plan.s;
+    t = plan.F * cpx + (u - plan.F * cpx) / nparts;
+    part = (u - plan.F * cpx) % nparts;
+  }
+  const Tile tl = tiles.find(plan.base + t);
+  const int kb = part * nk / nparts, nks = (part + 1) * nk / nparts - kb;  // the piece's stages
   const int n0 = tl.nt * ON;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int wm = S::wm(wave), wn = S::wn(wave), fr = lane & 31, g = lane >> 5;
-  const uint32_t row_bytes = uint32_t(K) * 2u;  // a multiple of 16
-  const int nk = int((row_bytes + kRowBytes - 1) / kRowBytes);
   constexpr uint32_t kOutside = 0xFFFFFFF0u;  // past every extent below: reads zero, without a memory access
 
   // ---- this lane's place in each of the wave's loads (8 rows of a stage, A's then B's; chunk c of
@@ -132,9 +176,9 @@ __device__ __forceinline__ void body(const bf16_t* A, const int32_t* __restrict_
     at[j] = mrow < (is_a ? tl.rows : cols) ? uint32_t(mrow) * row_bytes : kOutside;
     in_row[j] = uint32_t((lane & 7) ^ ((r >> 1) & 7)) * 16u;
   }
-  auto issue = [&](int s) {  // stage min(s, nk - 1) into slot s
+  auto issue = [&](int s) {  // the piece's stage min(s, nks - 1) into slot s
     char* dst = lds + (s % kSlots) * kStage + kLoads * wave * 1024;
-    const uint32_t k0 = uint32_t(min(s, nk - 1)) * kRowBytes;
+    const uint32_t k0 = uint32_t(kb + min(s, nks - 1)) * kRowBytes;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
       const uint32_t k = k0 + in_row[j];
@@ -162,7 +206,7 @@ __device__ __forceinline__ void body(const bf16_t* A, const int32_t* __restrict_
   }
 #pragma unroll
   for (int s = 0; s < kSlots - 1; ++s) issue(s);
-  for (int s = 0; s < nk; ++s) {
+  for (int s = 0; s < nks; ++s) {
     MOE_VMCNT(kLoads * (kSlots - 2));    // this wave's loads of stage s have landed
     __builtin_amdgcn_s_waitcnt(0xC07F);  // and its reads of stage s - 1 (lgkmcnt)
     block_barrier();                     // as every wave's have
@@ -183,7 +227,19 @@ __device__ __forceinline__ void body(const bf16_t* A, const int32_t* __restrict_
     }
   }
   MOE_VMCNT(0);  // the last (repeated) loads land before the LDS holds anything else
-  tile_adapters<S, NMAT, NA>(ad, tl.expert, tl.row0, tl.rows, n0, N, lds, acc);
+  if (part == 0) tile_adapters<S, NMAT, NA>(ad, tl.expert, tl.row0, tl.rows, n0, N, lds, acc);
+  if (nparts > 1) {
+    f32x4_t* dst = part_of<KA>(parts, xcd * kMaxParts + u - plan.F * cpx);
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          dst[((i * 2 + j) * 4 + q) * S::kThreads + tid] =
+              f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    return;
+  }
   __builtin_amdgcn_s_waitcnt(0xC07F);
   block_barrier();  // every wave is done with the LDS
 
@@ -222,9 +278,69 @@ __device__ __forceinline__ void body(const bf16_t* A, const int32_t* __restrict_
 template <int NMAT, int KA>
 __global__ __launch_bounds__(Shape<KA>::kThreads) void gemm_kernel(const bf16_t* A, const int32_t* offsets,
                                                                    const bf16_t* B0, const bf16_t* B1, bf16_t* C, int L,
-                                                                   int N, int K, Adapters ad) {
+                                                                   int N, int K, int cpx, float* parts, Adapters ad) {
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  body<NMAT, KA>(A, offsets, B0, B1, C, L, N, K, ad, lds);
+  body<NMAT, KA>(A, offsets, B0, B1, C, L, N, K, cpx, parts, ad, lds);
+}
+
+// Adds the pieces of the cut tiles in order and writes the tiles.  A block takes one row block's
+// and, in the plain product, one column block's float4s of a thread: kFixBlocks blocks a tile.
+template <int NMAT, int KA>
+constexpr int kFixBlocks = Shape<KA>::NA * 2 / NMAT;
+
+template <int NMAT, int KA>
+__global__ __launch_bounds__(Shape<KA>::kThreads) void fixup_kernel(const int32_t* offsets, bf16_t* __restrict__ C, int L,
+                                                                    int N, int K, int cpx, const float* parts) {
+  using S = Shape<KA>;
+  constexpr int ON = S::kB / NMAT;
+  const int sub = blockIdx.x % kFixBlocks<NMAT, KA>, cut = blockIdx.x / kFixBlocks<NMAT, KA>;
+  const int xcd = cut % kXcds, w = cut / kXcds;
+  Tiles<KA> tiles{offsets, L, (N + ON - 1) / ON};
+  const Plan plan = plan_of(tiles.total(), xcd, cpx, (K * 2 + S::kRowBytes - 1) / S::kRowBytes);
+  if (w >= plan.r || plan.s == 1) return;
+  const Tile tl = tiles.find(plan.base + plan.F * cpx + w);
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, fr = lane & 31, g = lane >> 5;
+  const int i = sub / (2 / NMAT), j = NMAT == 2 ? 0 : sub % 2;
+  const size_t stride = size_t(S::kA) * S::kB / 4;  // float4s a piece
+  const f32x4_t* src = part_of<KA>(const_cast<float*>(parts), xcd * kMaxParts + w * plan.s) + (i * 2 + j) * 4 * S::kThreads + tid;
+  f32x4_t a[4], b[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    a[q] = src[q * S::kThreads];
+    b[q] = NMAT == 2 ? src[(4 + q) * S::kThreads] : a[q];
+  }
+  for (int p = 1; p < plan.s; ++p)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      a[q] += src[size_t(p) * stride + q * S::kThreads];
+      if (NMAT == 2) b[q] += src[size_t(p) * stride + (4 + q) * S::kThreads];
+    }
+  const int r = (S::wm(wave) * S::NA + i) * 32 + fr;
+  if (r >= tl.rows) return;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int col = tl.nt * ON + S::wn(wave) * (32 * (2 / NMAT)) + j * 32 + 8 * q + 4 * g;
+    float v[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v[x] = NMAT == 2 ? silu(a[q][x]) * b[q][x] : a[q][x];
+    if (col < N)  // N is a multiple of 8
+      *reinterpret_cast<uint2*>(C + size_t(tl.row0 + r) * N + col) =
+          make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  }
+}
+
+// CUs of an XCD, on the current device (32 where they cannot be asked for).
+int cus_per_xcd() {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 32;
+  int n = cached[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < kXcds) n = 256;
+    n = std::min(n / kXcds, kMaxParts);
+    cached[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
 }
 
 // Tiles that max_pairs rows of L experts can have: row tiles at most one an expert more than full ones.
@@ -235,39 +351,53 @@ int64_t most_tiles(int64_t max_pairs, int L, int N) {
 }
 
 template <int NMAT, int KA>
-moe_status launch(const char* name, const void* A, const int32_t* offsets, const void* B0, const void* B1, void* C, int L,
-                  int N, int K, int64_t max_pairs, hipStream_t s, const Adapters& ad) {
+moe_status launch(const char* name, const char* fix_name, const void* A, const int32_t* offsets, const void* B0,
+                  const void* B1, void* C, int L, int N, int K, int64_t max_pairs, float* parts, hipStream_t s,
+                  const Adapters& ad) {
   using S = Shape<KA>;
   auto kern = gemm_kernel<NMAT, KA>;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
   if (e != hipSuccess) return set_error(MOE_ERR_HIP, "%s: LDS attribute: %s", name, hipGetErrorString(e));
-  // an XCD's share of the tiles is rounded up
-  const int64_t blocks = (most_tiles<KA, NMAT>(max_pairs, L, N) + kXcds - 1) / kXcds * kXcds;
-  MOE_LAUNCH(name, kern, dim3(unsigned(blocks)), dim3(S::kThreads), S::kLds, s, static_cast<const bf16_t*>(A), offsets,
-             static_cast<const bf16_t*>(B0), static_cast<const bf16_t*>(B1), static_cast<bf16_t*>(C), L, N, K, ad);
+  const int cpx = cus_per_xcd();
+  // an XCD's share of the tiles is rounded up; pieces add less than a round
+  const int64_t share = (most_tiles<KA, NMAT>(max_pairs, L, N) + kXcds - 1) / kXcds;
+  const int64_t units = share + cpx;
+  MOE_LAUNCH(name, kern, dim3(unsigned(units * kXcds)), dim3(S::kThreads), S::kLds, s, static_cast<const bf16_t*>(A), offsets,
+             static_cast<const bf16_t*>(B0), static_cast<const bf16_t*>(B1), static_cast<bf16_t*>(C), L, N, K, cpx, parts, ad);
+  const int nk = int((int64_t(K) * 2 + S::kRowBytes - 1) / S::kRowBytes);
+  if (nk < 2 * kMinStages) return MOE_OK;  // nothing is cut
+  const int64_t cuts = std::min<int64_t>(share, cpx / 2);  // a round of more than half the CUs is not cut
+  MOE_LAUNCH(fix_name, (fixup_kernel<NMAT, KA>), dim3(unsigned(cuts * kXcds * kFixBlocks<NMAT, KA>)), dim3(S::kThreads), 0, s,
+             offsets, static_cast<bf16_t*>(C), L, N, K, cpx, static_cast<const float*>(parts));
   return MOE_OK;
 }
 
-// 64 x 128 tiles while they take little more than a round of the card (half of the experts' last row
-// tiles counted).  Small against large, rank 16, us: 32 rows on each of 8 experts of 1000 x 2008, 59
-// instead of 78; 300 on one of 4096 x 2048, 70 instead of 112; 600, where they take two rounds, 116
-// instead of 110.
+// 64 x 128 tiles while they take a round of the card (half of the experts' last row tiles counted).
+// Small against large, rank 16, us: 33 rows on each of 8 experts of 1000 x 2008, 60 instead of 74, and on
+// 16 of 1024 x 1024 56 instead of 71; 127 there, 96 instead of 73; 127 on one of 4096 x 2048 57 instead of
+// 70, 600 there 104 instead of 84.
 template <int NMAT>
 bool small_tiles(int64_t max_pairs, int L, int N) {
   constexpr int ON = 128 / NMAT;
-  return (max_pairs / 64 + (L + 1) / 2) * ((N + ON - 1) / ON) <= 400;
+  return (max_pairs / 64 + (L + 1) / 2) * ((N + ON - 1) / ON) <= 300;
 }
 
 template <int NMAT>
-moe_status launch(const char* name, const void* A, const int32_t* offsets, const void* B0, const void* B1, void* C, int L,
-                  int N, int K, int64_t max_pairs, hipStream_t s, const Adapters& ad) {
-  if (small_tiles<NMAT>(max_pairs, L, N)) return launch<NMAT, 64>(name, A, offsets, B0, B1, C, L, N, K, max_pairs, s, ad);
-  return launch<NMAT, 128>(name, A, offsets, B0, B1, C, L, N, K, max_pairs, s, ad);
+moe_status launch(const char* name, const char* fix_name, const void* A, const int32_t* offsets, const void* B0,
+                  const void* B1, void* C, int L, int N, int K, int64_t max_pairs, float* parts, hipStream_t s,
+                  const Adapters& ad) {
+  return small_tiles<NMAT>(max_pairs, L, N)
+             ? launch<NMAT, 64>(name, fix_name, A, offsets, B0, B1, C, L, N, K, max_pairs, parts, s, ad)
+             : launch<NMAT, 128>(name, fix_name, A, offsets, B0, B1, C, L, N, K, max_pairs, parts, s, ad);
 }
 
 }  // namespace mid
 }  // namespace
+
+size_t mid_adapted_scratch_bytes() {
+  return size_t(mid::kXcds) * mid::kMaxParts * mid::Shape<128>::kA * mid::Shape<128>::kB * sizeof(float);
+}
 
 bool mid_adapted_fits(const moe_layer_desc* d, int64_t max_pairs) {
   const int64_t tiles = mid::most_tiles<64, 2>(max_pairs, d->local_count, std::max(d->hidden, d->intermediate));
@@ -278,13 +408,14 @@ moe_status launch_mid_adapted(const AdaptedFfnArgs& a) {
   const FfnArgs& f = a.f;
   const moe_layer_desc* d = f.d;
   const int L = d->local_count, H = d->hidden, I = d->intermediate;
-  moe_status st = mid::launch<2>("ffn_gate_up", f.x_sorted, f.offsets, f.w_gate, f.w_up, f.h, L, I, H, f.max_pairs, f.s,
-                                 gate_up_adapters(d, a.ad, a.w));
+  float* parts = static_cast<float*>(f.scratch);
+  moe_status st = mid::launch<2>("ffn_gate_up", "ffn_gate_up_fixup", f.x_sorted, f.offsets, f.w_gate, f.w_up, f.h, L, I, H,
+                                 f.max_pairs, parts, f.s, gate_up_adapters(d, a.ad, a.w));
   if (st != MOE_OK) return st;
   st = launch_adapter_shrink(a, true);
   if (st != MOE_OK) return st;
-  return mid::launch<1>("ffn_down", f.h, f.offsets, f.w_down, f.w_down, f.y_sorted, L, H, I, f.max_pairs, f.s,
-                        down_adapters(d, a.ad, a.w));
+  return mid::launch<1>("ffn_down", "ffn_down_fixup", f.h, f.offsets, f.w_down, f.w_down, f.y_sorted, L, H, I,
+                        f.max_pairs, parts, f.s, down_adapters(d, a.ad, a.w));
 }
 
 }  // namespace moe

@@ -768,22 +768,25 @@ size_t big_scratch_bytes(const moe_layer_desc* d) {
   return plan + (split ? size_t(big::kXcds) * big::kMaxParts * big::kPartBytes : 0);
 }
 
-// Which kernels adapted products take, by the most rows an expert that the descriptor allows, P / L
-// (rank 16, even and skewed experts, us; 16 experts of 2880 x 2880, 8 of 4096 x 14336, 128 of 2048 x
-// 768, 4 of 2048 x 4096, 16 of 1024 x 1024):
-//  - the decode kernel to 8 rows (at 9: 197, 536, 292, 69, 39 against 187, 528, 281, 86, 44 in the tiles
-//    of adapted_gemm.hip), to 16 where the experts are small and their weights are not what counts (at
-//    16: 259, 733, 366 against 200, 562, 301, but 81 and 52 against 87 and 51), to 64 of one expert;
-//  - the large tile from 256 rows and a card full of tiles (at 300: 437, 1277, -, 139 against 445, 1283, -,
-//    147; at 600 614, 1743 against 698, 2071; at 127 351, 819, 428 against 314, 720, 426);
+// Which kernels adapted products take, by the most rows an expert that the descriptor allows, P / L.
+// Weights along K (rank 16, even experts, us; 16 experts of 2880 x 2880, 8 of 4096 x 14336, 128 of
+// 2048 x 768, 4 of 2048 x 4096, 16 of 1024 x 1024, 8 of 256 x 512):
+//  - the decode kernel to 8 rows (at 9: 197, 535, 291, 70, 39, 20 against 193, 532, 287, 78, 50, 32 in the
+//    tiles of adapted_gemm.hip), to 16 where the weights are under 2^27 (at 16: 259, 734, 366 against
+//    206, 561, 306, but 82 and 51 against 79 and 56), to 32 where they are under 2^22 or one expert's (at 33:
+//    27 against 36; one of 4096 x 2048 60 against 56, one of 512 x 512 23 against 35);
+//  - the large tile from 256 rows and a card full of tiles (at 300: 440, 1282 against 455, 1235; at 600 602,
+//    1734 against 676, 1993; at 127 340, 799, 414 against 277, 712, 428);
 //  - the tiles of adapted_gemm.hip between them and at widths off the large tile's grid.
-// Weights stored along N are read by the large tile from 16 rows on, and by the decode and
-// general kernels elsewhere.
+// Weights along N are read by the large tile from 16 rows on, and by the decode and general
+// kernels elsewhere.
 enum AdaptedPath { kAdaptedSkinny, kAdaptedMid, kAdaptedBig, kAdaptedGeneral };
 AdaptedPath adapted_path(const moe_layer_desc* d, int64_t P) {
   const int64_t L = d->local_count, H = d->hidden, I = d->intermediate;
   if (d->dtype == MOE_BF16 && d->weight_layout == MOE_WEIGHTS_OUT_IN && mid_adapted_fits(d, P)) {
-    if (P <= 8 * L || (P <= 16 * L && 3 * L * H * I <= (int64_t(1) << 27)) || (L == 1 && P <= 64)) return kAdaptedSkinny;
+    const int64_t weights = 3 * L * H * I;
+    const int64_t few = weights <= (int64_t(1) << 22) || L == 1 ? 32 : weights <= (int64_t(1) << 27) ? 16 : 8;
+    if (P <= few * L) return kAdaptedSkinny;
     const bool full = (P / big::BM + L / 2) * ((I + big::BNE / 2 - 1) / (big::BNE / 2)) >= 256;
     return full && use_big(d, P, 256) ? kAdaptedBig : kAdaptedMid;
   }
@@ -797,7 +800,8 @@ size_t ffn_scratch_bytes(const moe_layer_desc* d, int64_t max_pairs) {
 }
 
 size_t adapted_ffn_scratch_bytes(const moe_layer_desc* d, int64_t max_pairs) {
-  return adapted_path(d, max_pairs) == kAdaptedBig ? big_scratch_bytes(d) : 0;
+  const AdaptedPath path = adapted_path(d, max_pairs);
+  return path == kAdaptedBig ? big_scratch_bytes(d) : path == kAdaptedMid ? mid_adapted_scratch_bytes() : 0;
 }
 
 // ---- the backward's dgrad products on the large-tile kernel ---------------------

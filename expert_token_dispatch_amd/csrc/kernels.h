@@ -160,6 +160,7 @@ moe_status launch_adapter_shrink(const AdaptedFfnArgs& a, bool down);
 moe_status launch_adapted_products(const AdaptedFfnArgs& a);
 // what it picks from, by the sizes as launch_grouped_ffn does
 bool mid_adapted_fits(const moe_layer_desc* d, int64_t max_pairs);
+size_t mid_adapted_scratch_bytes();  // pieces of tiles that are cut along K
 moe_status launch_mid_adapted(const AdaptedFfnArgs& a);
 bool skinny_adapted_fits(const moe_layer_desc* d, int64_t max_pairs);
 moe_status launch_skinny_adapted(const AdaptedFfnArgs& a);
