@@ -258,7 +258,8 @@ moe_status launch_rb(const char* name, const ShrinkP& p, int64_t max_pairs, hipS
   const auto grid = [&](int ng) {
     return dim3(unsigned((blocks + 7) / 8 * 8), 1, unsigned((groups + ng - 1) / ng * slots));
   };
-  if (groups <= 1) return launch_ng<T, RB, 1>(name, p, grid(1), slots, s);
+  // a few rows: their columns over more blocks
+  if (groups <= 1 || (RB == 1 && max_pairs <= 64)) return launch_ng<T, RB, 1>(name, p, grid(1), slots, s);
   if (groups <= 2) return launch_ng<T, RB, 2>(name, p, grid(2), slots, s);
   if (groups <= 4) return launch_ng<T, RB, 4>(name, p, grid(4), slots, s);
   return launch_ng<T, RB, 8>(name, p, grid(8), slots, s);
