@@ -401,7 +401,8 @@ size_t mid_adapted_scratch_bytes() {
 
 bool mid_adapted_fits(const moe_layer_desc* d, int64_t max_pairs) {
   const int64_t tiles = mid::most_tiles<64, 2>(max_pairs, d->local_count, std::max(d->hidden, d->intermediate));
-  return d->dtype == MOE_BF16 && d->weight_layout == MOE_WEIGHTS_OUT_IN && tiles < (int64_t(1) << 31) - 8;
+  // fewer than 2^32 threads, whichever tiles they are
+  return d->dtype == MOE_BF16 && d->weight_layout == MOE_WEIGHTS_OUT_IN && tiles < (int64_t(1) << 24) - 1024;
 }
 
 moe_status launch_mid_adapted(const AdaptedFfnArgs& a) {

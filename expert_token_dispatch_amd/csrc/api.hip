@@ -450,6 +450,8 @@ moe_status adapted_desc_checks(const moe_layer_desc* d) {
   if (d->hidden > kAdapterMaxK || d->intermediate > kAdapterMaxK)
     return set_error(MOE_ERR_UNSUPPORTED, "adapters: hidden and intermediate above %d are not supported (got %d, %d)",
                      kAdapterMaxK, d->hidden, d->intermediate);
+  if (max_pairs_of(d) > kAdapterMaxPairs)
+    return set_error(MOE_ERR_UNSUPPORTED, "adapters: more than %d pairs a call are not supported", kAdapterMaxPairs);
   return MOE_OK;
 }
 

@@ -99,8 +99,9 @@ template <typename T, int NT, int V>
 __global__ __launch_bounds__(NT == 64 ? 256 : NT) void join_kernel(JoinP p) {
   constexpr int E = Elem<T>::kPerVec;
   __shared__ float buf[2][1][NT / 64];
-  const int64_t row = NT == 64 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6) : int64_t(blockIdx.x);
-  if (NT == 64 && row >= p.rows) return;  // whole waves, and no barrier follows
+  const int64_t block = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
+  const int64_t row = NT == 64 ? block * 4 + (threadIdx.x >> 6) : block;
+  if (row >= p.rows) return;  // whole blocks, or waves of one that no barrier follows
   const int tid = NT == 64 ? threadIdx.x & 63 : threadIdx.x;
   const size_t base = size_t(row) * p.nvec;
   const float inv_h = 1.0f / float(p.H);
@@ -385,8 +386,10 @@ int vectors(const moe_join_desc* j) { return int(size_t(j->hidden) * dtype_bytes
 
 template <typename T, int NT, int V>
 moe_status launch_fwd(const JoinP& p, hipStream_t s) {
-  const int64_t blocks = NT == 64 ? (p.rows + 3) / 4 : p.rows;
-  MOE_LAUNCH("block_join", (join_kernel<T, NT, V>), dim3(unsigned(blocks)), dim3(NT == 64 ? 256 : NT), 0, s, p);
+  // at most 2^32 threads along x
+  const int64_t blocks = NT == 64 ? (p.rows + 3) / 4 : p.rows, gx = std::min<int64_t>(blocks, 1 << 20);
+  MOE_LAUNCH("block_join", (join_kernel<T, NT, V>), dim3(unsigned(gx), unsigned((blocks + gx - 1) / gx)),
+             dim3(NT == 64 ? 256 : NT), 0, s, p);
   return MOE_OK;
 }
 

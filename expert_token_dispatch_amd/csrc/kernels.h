@@ -131,7 +131,8 @@ struct Adapters {
   int lo;  // 0 in float32: u alone
 };
 
-constexpr int kAdapterMaxK = 1 << 22;  // hidden and intermediate
+constexpr int kAdapterMaxK = 1 << 22;      // hidden and intermediate
+constexpr int kAdapterMaxPairs = 1 << 27;  // pairs that the descriptor allows
 
 // What the first products leave for the second ones, carved from the caller's workspace.
 struct AdapterScratch {

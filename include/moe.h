@@ -616,7 +616,7 @@ moe_status moe_adapted_workspace_size(const moe_layer_desc* d, const moe_adapter
  *   adapter_ids   device [T] int32: each token's adapter; a value outside [0, count) means none
  * The rest as moe_grouped_ffn.  MOE_ERR_INVALID_ARG also for adapters outside the ranges above, one
  * pointer of a pair without the other, or no pair; MOE_ERR_UNSUPPORTED where hidden or
- * intermediate is above 2^22. */
+ * intermediate is above 2^22 or the descriptor allows more than 2^27 pairs. */
 moe_status moe_grouped_ffn_adapted(const moe_layer_desc* d, const void* x_sorted, const int32_t* offsets,
                                    const int32_t* sorted_pairs, const int32_t* adapter_ids, const void* w_gate,
                                    const void* w_up, const void* w_down, const moe_adapters* a, void* y_sorted, void* ws,

@@ -72,6 +72,13 @@ def test_the_widest_rows_are_unsupported(H, I):
     assert L.lib().moe_grouped_ffn_adapted(ctypes.byref(d), *[256] * 7, at, 256, 256, 1 << 60, None) == L.MOE_ERR_UNSUPPORTED
 
 
+def test_more_pairs_than_a_launch_holds_are_unsupported():
+    d, a, n = etd.make_desc((1 << 26) + 1, 64, 64, 8, 2), _struct(), ctypes.c_size_t()
+    at = ctypes.addressof(a)
+    assert L.lib().moe_adapted_workspace_size(ctypes.byref(d), at, L.MOE_STAGE_FFN, ctypes.byref(n)) == L.MOE_ERR_UNSUPPORTED
+    assert L.lib().moe_grouped_ffn_adapted(ctypes.byref(d), *[256] * 7, at, 256, 256, 1 << 60, None) == L.MOE_ERR_UNSUPPORTED
+
+
 # x_sorted, offsets, sorted_pairs, adapter_ids, w_gate, w_up, w_down, (adapters), y_sorted, ws
 @pytest.mark.parametrize("arg", [0, 1, 2, 3, 4, 5, 6, 8])
 @pytest.mark.parametrize("value", [None, 258])

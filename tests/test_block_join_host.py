@@ -136,6 +136,16 @@ def test_backward_workspace():
     assert L.lib().moe_block_join_backward(ctypes.byref(j), *a, need, None) == L.MOE_ERR_WORKSPACE
 
 
+@pytest.mark.parametrize("dtype,H", [("bf16", 8), ("bf16", 2880), ("bf16", 16384), ("f32", 512), ("f32", 8192)])
+def test_a_workspace_for_the_most_rows_is_enough_for_any(dtype, H):
+    def size(rows):
+        return etd.moe_join_workspace_size(etd.make_join_desc(rows, H, dtype, True, "channel"))
+    most = size((1 << 31) - 1)
+    assert 0 < most <= 3 * 4 * 262144 * 16
+    assert all(size(r) <= most for r in [0, 1, 2, 63, 1000, 4095, 4096, 4097, 5000, 10 ** 6, 10 ** 6 + 7])
+    assert size(0) == 0 and size(5) >= 5 * 3 * 4 * H
+
+
 def test_no_rows_is_no_work():
     j = _desc(rows=0, gate="none", post_norm=False)
     assert L.lib().moe_block_join(ctypes.byref(j), *[None] * 7, None) == L.MOE_OK

@@ -122,7 +122,7 @@ SHAPES = [
     (136, 264, 3, 500, 16, 9), (64, 64, 2, 700, 8, 2), (256, 512, 4, 1100, 16, 6), (576, 320, 2, 900, 64, 3),
     (1000, 72, 4, 60, 16, 3), (104, 1096, 5, 9, 8, 2), (2056, 24, 2, 2, 24, 2), (88, 520, 50, 70, 16, 4),
     (192, 448, 3, 1500, 128, 2), (72, 1000, 8, 200, 16, 5), (264, 200, 1, 65, 40, 3), (520, 136, 3, 900, 24, 4),
-    (136, 2056, 2, 1300, 72, 3), (64, 2944, 4, 2100, 16, 6), (40, 8, 300, 6000, 8, 3), (128, 64, 40, 600, 48, 12), (256, 256, 1, 2000, 104, 5),
+    (136, 2056, 2, 1300, 72, 3), (64, 2944, 4, 2100, 16, 6), (40, 8, 300, 6000, 8, 3), (40, 72, 300, 10000, 8, 3), (128, 64, 40, 600, 48, 12), (256, 256, 1, 2000, 104, 5),
 ]
 
 
@@ -173,12 +173,14 @@ def test_without_an_adapter_a_row_is_the_plain_experts(shape, layout, dtype):
 
 
 @pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("layout", ("out_in", "in_out"))
+@pytest.mark.parametrize("I", (192, 200))
 @pytest.mark.parametrize("P", (30, 200, 1200))
-def test_a_row_depends_on_no_other_request(P, dtype):
+def test_a_row_depends_on_no_other_request(P, I, layout, dtype):
     """Other requests' adapters change, and one of them holds NaN and infinities: not a bit of the others' rows."""
-    H, I, Lc, R, n = 128, 192, 2, 24, 6
-    c = Case(H, I, Lc, P, R, n, dtype)
-    say(f"[adapters] isolation P={P} {dtype}")
+    H, Lc, R, n = 128, 2, 24, 6
+    c = Case(H, I, Lc, P, R, n, dtype, layout)
+    say(f"[adapters] isolation P={P} I={I} {layout} {dtype}")
     base = c.run()
     keep = c.ids % 2 == 0                    # adapters 0, 2, 4 stay
     c.set_ids(np.where(keep, c.ids, 5))

@@ -259,3 +259,71 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         for a, b in zip(got, (ze, he, *[t for t in ge.values() if t is not None])):
             assert torch.equal(a, b), f"replay {r}"
+
+
+def test_rows_past_the_first_dimension_of_a_launch():
+    """More than 2^20 rows of a block each: the last ones are the first ones again."""
+    T, H = (1 << 20) + 5, 1032
+    g = torch.Generator(device="cuda").manual_seed(3)
+    head = torch.randn((5, H), generator=g, device="cuda").bfloat16()
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    x[:5], x[-5:] = head, head
+    w = (1 + 0.1 * torch.randn(H, generator=g, device="cuda")).bfloat16()
+    h = torch.full_like(x, 7.0)
+    etd.moe_block_join(etd.make_join_desc(T, H), x, None, None, None, w, None, h)
+    torch.cuda.synchronize()
+    assert torch.equal(h[:5], h[-5:]) and (h[5:-5] == 0).all() and h[:5].abs().min() >= 0
+    ref = oj.forward(oj.Join(), host(head), w_pre=host(w))
+    check(h[-5:], ref["h"], ref["mag_h"], "bf16", 96, "last rows")
+
+
+def test_a_training_step_of_a_block():
+    """norm -> layer -> norm, gate, scale, sum and the next norm, forward and backward, against the gradients that
+    differentiating the whole in 64 bits gives (at the layer's own choice of experts).  Each of the three stages is
+    held to 1e-5 of its rows' largest entries; together they get five times that."""
+    import synth
+    from tests._harness import TOL_F32, layer_of
+    s = synth.spec("tiny_fp32", T=60)
+    layer, x = layer_of(synth.make_layer(s))
+    T, H, k = s.T, s.H, s.k
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=g, device="cuda")
+    w = [1 + 0.1 * rand(H) for _ in range(3)]
+    gate, dz, dh2 = rand(T), rand(T, H), rand(T, H)
+    first = etd.BlockJoin(H, "f32", w_pre=w[0])
+    after = etd.BlockJoin(H, "f32", w_post=w[1], w_pre=w[2], gate="token", gate_act="sigmoid", residual_scale=0.7)
+    _, h = first.forward(x)
+    y, saved = layer.forward_train(h)
+    z, h2 = after.forward(x, y, gate)
+    ga = after.backward(z, y, gate, dz, dh2)
+    gl = layer.backward(h, saved, ga["dy"])
+    gf = first.backward(x, dz=ga["dx"], dh=gl["dx"])
+    torch.cuda.synchronize()
+
+    ids = saved._tensors["topk_ids"].long()
+    P = [t.double().requires_grad_() for t in (x, w[0], w[1], w[2], gate, layer.w_router, layer.w_gate, layer.w_up, layer.w_down)]
+    X, W0, W1, W2, G, WR, WG, WU, WD = P
+
+    def norm(v, f):
+        return v * torch.rsqrt((v * v).mean(-1, keepdim=True) + 1e-6) * f
+    Hn = norm(X, W0)
+    logits = Hn @ WR.T + (0 if layer.b_router is None else layer.b_router.double())
+    wt = torch.softmax(torch.gather(logits, 1, ids), 1)
+    Y = torch.zeros_like(X)
+    for j in range(k):
+        for e in range(s.E):
+            rows = (ids[:, j] == e).nonzero()[:, 0]
+            if len(rows):
+                v = Hn[rows]
+                a, b = (v @ WG[e].T, v @ WU[e].T) if s.weight_layout in ("out_in", 0) else (v @ WG[e], v @ WU[e])
+                o = torch.nn.functional.silu(a) * b
+                o = o @ WD[e].T if s.weight_layout in ("out_in", 0) else o @ WD[e]
+                Y = Y.index_add(0, rows, wt[rows, j, None] * o)
+    Z = X + 0.7 * torch.sigmoid(G)[:, None] * norm(Y, W1)
+    loss = (Z * dz.double()).sum() + (norm(Z, W2) * dh2.double()).sum()
+    ref = torch.autograd.grad(loss, P)
+    got = (gf["dx"], gf["dw_pre"], ga["dw_post"], ga["dw_pre"], ga["dgate"], gl["dw_router"], gl["dw_gate"], gl["dw_up"], gl["dw_down"])
+    for name, a, b in zip(("x", "w0", "w1", "w2", "gate", "router", "gates", "ups", "downs"), got, ref):
+        assert (a.double() - b).abs().max() <= 5 * TOL_F32 * b.abs().max(), name
