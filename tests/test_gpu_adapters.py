@@ -194,6 +194,25 @@ def test_a_row_depends_on_no_other_request(P, I, layout, dtype):
     assert torch.isfinite(base).all()
 
 
+@pytest.mark.parametrize("I", (192, 200))
+@pytest.mark.parametrize("P", (30, 200, 1200))
+@pytest.mark.parametrize("R,n,broken", [(8, 7, 3), (16, 8, 0), (16, 2, 1), (40, 5, 4)])
+def test_a_broken_adapter_beside_each_of_the_others(R, n, broken, P, I):
+    """Every tile has all adapters in changing orders, one of them with NaN in its B alone: the rows of the others
+    are what they are without it."""
+    c = Case(128, I, 2, P, R, n, seed=R)
+    say(f"[adapters] one broken of {n}, rank {R}, P={P} I={I}")
+    c.check("whole")
+    base = c.run()
+    rows = torch.tensor((c.ids != broken)[c.pairs.cpu().numpy()], device="cuda")
+    for k, v in c.t.items():
+        if k.endswith("_b"):
+            v[broken, :, ::3] = float("nan")
+    y = c.run()
+    assert torch.equal(y[rows], base[rows])
+    assert torch.isnan(y[~rows]).any(dim=1).all()
+
+
 def test_the_same_every_time_on_other_streams_and_two_at_once():
     a, b = Case(256, 512, 4, 1100, 16, 6), Case(128, 192, 8, 60, 8, 9, seed=5)
     ya, yb = a.run(), b.run()
