@@ -736,7 +736,7 @@ moe_status launch(const char* name, const bf16_t* A, const int32_t* offsets, con
                   float* parts, hipStream_t s, bf16_t* Gs = nullptr, bf16_t* Us = nullptr, int ep = kPlain,
                   const AD& ad = AD()) {
   // with adapters always eight: beside four waves' 256 sums their loop spills (16384 pairs through
-  // 4096 x 14336 experts: gate/up 5.4 ms)
+  // 4096 x 14336 experts, rank 64: gate/up 5.4 ms, with eight 3.6)
   if (std::is_same<AD, Adapters>::value || K / BK < kEightWaveSteps)
     return launch_nw<NMAT, 8>(name, A, offsets, B0, B1, C, L, N, K, kcat, bkn, max_pairs, tpre, parts, s, Gs, Us, ep, ad);
   if constexpr (std::is_same<AD, NoAdapters>::value)

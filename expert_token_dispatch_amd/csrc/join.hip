@@ -191,7 +191,7 @@ __global__ __launch_bounds__(NT == 64 ? 256 : NT) void join_kernel(JoinP p) {
 //   D  = dz + r_z (a - zh mean(a zh))                       (= dx)
 //   db = scale g D,  c = db (offset + w_post),  dy = r_y (c - yh mean(c yh))
 //   dw_pre = sum dh zh,  dw_post = sum db yh,  dgate = scale D b (s (1 - s) of a sigmoid)
-// At 8192 x 4096 in bf16 with a channel gate 91 us with the sums' kernel, 4.4 of the 5.2 TB/s that a
+// At 8192 x 4096 in bf16 with a channel gate 88 us with the sums' kernel, 4.6 of the 5.2 TB/s that a
 // large copy reaches: the sums of 512 blocks are another 50 MB, the rest the two waits of a row.
 // (Loading the next row under this one, rows of 1024-thread blocks side by side and barriers
 // that leave loads in flight were all slower, 96 to 150 us: registers, or rows in step.)
@@ -411,7 +411,7 @@ int bwd_threads(const moe_join_desc* j) {
   return 1024;
 }
 // Its blocks: 1024 threads a CU, and rows dealt evenly.  Half as many leave too few loads in
-// flight (8192 x 4096 bf16 91 -> 119 us), twice as many write and read twice the sums (96 us).
+// flight (8192 x 4096 bf16 119 us instead of 88), twice as many write and read twice the sums (96 us).
 constexpr int kBwdThreads = 262144;
 int bwd_blocks(const moe_join_desc* j) {
   const int64_t most = kBwdThreads / bwd_threads(j);

@@ -120,9 +120,8 @@ struct NoAdapters {};
 // The adapters of one product (gate and up, or down): sorted row q of expert e has adapter
 // rid[q] = a (-1: none) and adds u[m][q * ldu ..][0 .. rank) . b[m][a, e, column, 0 .. rank) to column
 // `column` of matrix m; u holds s_a (x A^T).  In bfloat16 u is the sum of two, the second one `lo`
-// elements behind the first: rounded to one alone it cost a third more error in y than the rest
-// of the feed-forward has (2.55e-3 of its norm instead of 2.4e-3 at rank 16), for a product that takes
-// a few k.  A matrix without adapters has u[m] = NULL.
+// elements behind the first: rounded to one alone it is the largest rounding on the way to y (error
+// 2.5e-3 of y's norm instead of 2.35e-3 at rank 16), and a second product of the rank's few k mends it.  A matrix without adapters has u[m] = NULL.
 struct Adapters {
   const int32_t* rid;
   const void* u[2];
