@@ -250,26 +250,31 @@ moe_status launch_ng(const char* name, const ShrinkP& p, const dim3& grid, int s
 }
 
 template <typename T, int RB>
-moe_status launch_rb(const char* name, const ShrinkP& p, int64_t max_pairs, hipStream_t s) {
-  const int groups = std::max(1, (p.mats * p.rank + 15) / 16);
+moe_status launch_rb(const char* name, const ShrinkP& p, int64_t max_pairs, int groups, hipStream_t s) {
   const int64_t blocks = (max_pairs + 16 * RB - 1) / (16 * RB) + p.L;  // at most; a multiple of 8 for the XCDs
-  // rows of a decode batch have adapters of their own: four blocks share them
-  const int slots = RB == 1 ? std::min(p.count, 4) : 1;
+  // four blocks share the adapters of their rows, which are many in a decode batch (16384 mixed rows of
+  // 60 adapters, rank 16, gate and up of 4096 x 14336 experts: 601 -> 428 us; eight 410, but one of 512 rows
+  // 19 -> 20), and run side by side in a prompt (one: 114 and 244 us of the case below)
+  const int slots = std::min(p.count, 4);
   const auto grid = [&](int ng) {
     return dim3(unsigned((blocks + 7) / 8 * 8), 1, unsigned((groups + ng - 1) / ng * slots));
   };
   // a few rows: their columns over more blocks
-  if (groups <= 1 || (RB == 1 && max_pairs <= 64)) return launch_ng<T, RB, 1>(name, p, grid(1), slots, s);
+  if constexpr (RB == 1)
+    if (groups <= 1 || max_pairs <= 64) return launch_ng<T, RB, 1>(name, p, grid(1), slots, s);
   if (groups <= 2) return launch_ng<T, RB, 2>(name, p, grid(2), slots, s);
   if (groups <= 4) return launch_ng<T, RB, 4>(name, p, grid(4), slots, s);
   return launch_ng<T, RB, 8>(name, p, grid(8), slots, s);
 }
 
 // Blocks of 32 rows, which read an adapter's A half as often, where they fill the card twice (16384
-// pairs, rank 64, 4096 x 14336 experts: 107 and 220 us; 16 rows 146 and 234, 64 rows 119 and 238).
+// pairs in 8 requests, rank 64, 4096 x 14336 experts: 100 and 195 us; 16 rows 167 and 229) and an
+// adapter has more than 16 columns (with those alone, mixed rows of 60 adapters 1075 us, 16 rows 922).
 template <typename T>
 moe_status launch_t(const char* name, const ShrinkP& p, int64_t max_pairs, hipStream_t s) {
-  return max_pairs >= 32 * 256 ? launch_rb<T, 2>(name, p, max_pairs, s) : launch_rb<T, 1>(name, p, max_pairs, s);
+  const int groups = std::max(1, (p.mats * p.rank + 15) / 16);
+  return groups > 1 && max_pairs >= 32 * 256 ? launch_rb<T, 2>(name, p, max_pairs, groups, s)
+                                             : launch_rb<T, 1>(name, p, max_pairs, groups, s);
 }
 
 int mats_of(const moe_adapters* a, bool down) {
