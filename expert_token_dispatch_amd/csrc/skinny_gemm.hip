@@ -72,36 +72,35 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int m = NMAT == 2 ? s : 0;
-        b[f][s] = cur >= 0 && ad.u[m] != nullptr ? adapter_b<T>(ad, m, cur, expert, col[s], N) : b[0][s];
+        b[f][s] = cur >= 0 && ad.u[m] != nullptr ? adapter_b<T>(ad, m, cur, expert, col[s], N) : f > 0 ? b[0][s] : nullptr;
         t[f][s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
     }
+    for (int c0 = 0; c0 < ad.rank; c0 += kStep<T>) {
+      const int c = c0 + kg;
+      const u32x4_t zero = {0, 0, 0, 0};
+      u32x4_t uf[NMAT], ul[NMAT], bf[kFlight][2];
 #pragma unroll
-    for (int m = 0; m < NMAT; ++m) {
-      if (ad.u[m] == nullptr) continue;
-      const T* u = adapter_u<T>(ad, m, row);
-      for (int c0 = 0; c0 < ad.rank; c0 += kStep<T>) {
-        const int c = c0 + kg;
-        const bool in = c < ad.rank;  // a vector at a time, as the rank is
-        const u32x4_t zero = {0, 0, 0, 0};
-        const u32x4_t uf = in ? *reinterpret_cast<const u32x4_t*>(u + c) : zero;
-        u32x4_t ul = zero;
-        if constexpr (sizeof(T) == 2) ul = in ? *reinterpret_cast<const u32x4_t*>(u + ad.lo + c) : zero;
-        u32x4_t bf[kFlight][2];
+      for (int m = 0; m < NMAT; ++m) {
+        const bool in = c < ad.rank && ad.u[m] != nullptr;  // a vector at a time, as the rank is
+        const T* u = adapter_u<T>(ad, m, row);
+        uf[m] = in ? *reinterpret_cast<const u32x4_t*>(u + c) : zero;
+        ul[m] = zero;
+        if constexpr (sizeof(T) == 2) ul[m] = in ? *reinterpret_cast<const u32x4_t*>(u + ad.lo + c) : zero;
 #pragma unroll
         for (int f = 0; f < kFlight; ++f)
 #pragma unroll
           for (int s = 0; s < 2; ++s)
             if (NMAT == 1 || s == m) bf[f][s] = in ? *reinterpret_cast<const u32x4_t*>(b[f][s] + c) : zero;
-#pragma unroll
-        for (int f = 0; f < kFlight; ++f)
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-            if (NMAT == 1 || s == m) {
-              t[f][s] = Mma16<T>::mma(uf, bf[f][s], t[f][s]);
-              if constexpr (sizeof(T) == 2) t[f][s] = Mma16<T>::mma(ul, bf[f][s], t[f][s]);
-            }
       }
+#pragma unroll
+      for (int f = 0; f < kFlight; ++f)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int m = NMAT == 2 ? s : 0;
+          t[f][s] = Mma16<T>::mma(uf[m], bf[f][s], t[f][s]);
+          if constexpr (sizeof(T) == 2) t[f][s] = Mma16<T>::mma(ul[m], bf[f][s], t[f][s]);
+        }
     }
 #pragma unroll
     for (int f = 0; f < kFlight; ++f)
