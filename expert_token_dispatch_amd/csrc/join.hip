@@ -410,11 +410,12 @@ int bwd_threads(const moe_join_desc* j) {
     if (vectors(j) <= t) return t;
   return 1024;
 }
-// Its blocks: 1024 threads a CU, and rows dealt evenly.  Half as many leave too few loads in
-// flight (8192 x 4096 bf16 119 us instead of 88), twice as many write and read twice the sums (96 us).
-constexpr int kBwdThreads = 262144;
+// Its blocks: as many on each of 256 CUs, up to 1024 threads a CU, and rows dealt evenly.  Half as many leave
+// too few loads in flight (8192 x 4096 bf16 119 us instead of 88), twice as many write and read
+// twice the sums (96 us); some CUs with a block more than others wait for those (262144 / 768 = 341
+// blocks for 5692 x 4672: 118 instead of 85 us; 682 of 384 threads for 4096 x 2880: 52 instead of 39).
 int bwd_blocks(const moe_join_desc* j) {
-  const int64_t most = kBwdThreads / bwd_threads(j);
+  const int64_t most = 256 * (1024 / bwd_threads(j));
   const int64_t each = std::max<int64_t>(1, (j->rows + most - 1) / most);
   return int((j->rows + each - 1) / each);
 }
