@@ -404,18 +404,27 @@ moe_status launch_fwd_t(const JoinP& p, hipStream_t s) {
   return launch_fwd<T, 1024, 2>(p, s);
 }
 
-// Threads of a row in the backward: one vector each (two past 1024).
-int bwd_threads(const moe_join_desc* j) {
+// Threads of a row in the backward and vectors of a thread: one vector each up to 768 threads, and 512
+// threads beyond, which leave each the registers for its sums (4096 x 8192 bf16: 107 us against
+// 174 with 1024 threads, 3591 x 4672 float32 93 against 222; 5461 x 6144 bf16 106 with 768 threads,
+// 114 with 384 of two vectors).  bf16 rows of more than 8192 spill all the same: 2730 x 12288 222 us
+// (1024 threads of two vectors 506), 2048 x 16384 414 (409).
+struct BwdShape {
+  int nt, v;
+};
+BwdShape bwd_shape(const moe_join_desc* j) {
+  const int n = vectors(j);
   for (int t : {64, 128, 192, 256, 384, 512, 768})
-    if (vectors(j) <= t) return t;
-  return 1024;
+    if (n <= t) return {t, 1};
+  return {512, (n + 511) / 512};
 }
-// Its blocks: as many on each of 256 CUs, up to 1024 threads a CU, and rows dealt evenly.  Half as many leave
+// Its blocks: as many on each of 256 CUs, up to 1024 vectors at once, and rows dealt evenly.  Half as many leave
 // too few loads in flight (8192 x 4096 bf16 119 us instead of 88), twice as many write and read
 // twice the sums (96 us); some CUs with a block more than others wait for those (262144 / 768 = 341
 // blocks for 5692 x 4672: 118 instead of 85 us; 682 of 384 threads for 4096 x 2880: 52 instead of 39).
 int bwd_blocks(const moe_join_desc* j) {
-  const int64_t most = 256 * (1024 / bwd_threads(j));
+  const BwdShape w = bwd_shape(j);
+  const int64_t most = 256 * std::max(1, 1024 / (w.nt * w.v));
   const int64_t each = std::max<int64_t>(1, (j->rows + most - 1) / most);
   return int((j->rows + each - 1) / each);
 }
@@ -427,16 +436,17 @@ moe_status launch_bwd(const JoinBwdP& p, int blocks, hipStream_t s) {
 }
 
 template <typename T>
-moe_status launch_bwd_t(const JoinBwdP& p, int nt, int blocks, int sums, const SumOut& o, hipStream_t s) {
-  const moe_status st = nt == 64          ? launch_bwd<T, 64, 1>(p, blocks, s)
-                        : nt == 128       ? launch_bwd<T, 128, 1>(p, blocks, s)
-                        : nt == 192       ? launch_bwd<T, 192, 1>(p, blocks, s)
-                        : nt == 256       ? launch_bwd<T, 256, 1>(p, blocks, s)
-                        : nt == 384       ? launch_bwd<T, 384, 1>(p, blocks, s)
-                        : nt == 512       ? launch_bwd<T, 512, 1>(p, blocks, s)
-                        : nt == 768       ? launch_bwd<T, 768, 1>(p, blocks, s)
-                        : p.nvec <= 1024  ? launch_bwd<T, 1024, 1>(p, blocks, s)
-                                          : launch_bwd<T, 1024, 2>(p, blocks, s);
+moe_status launch_bwd_t(const JoinBwdP& p, const BwdShape& w, int blocks, int sums, const SumOut& o, hipStream_t s) {
+  const moe_status st = w.nt == 64    ? launch_bwd<T, 64, 1>(p, blocks, s)
+                        : w.nt == 128 ? launch_bwd<T, 128, 1>(p, blocks, s)
+                        : w.nt == 192 ? launch_bwd<T, 192, 1>(p, blocks, s)
+                        : w.nt == 256 ? launch_bwd<T, 256, 1>(p, blocks, s)
+                        : w.nt == 384 ? launch_bwd<T, 384, 1>(p, blocks, s)
+                        : w.nt == 768 ? launch_bwd<T, 768, 1>(p, blocks, s)
+                        : w.v == 1    ? launch_bwd<T, 512, 1>(p, blocks, s)
+                        : w.v == 2    ? launch_bwd<T, 512, 2>(p, blocks, s)
+                        : w.v == 3    ? launch_bwd<T, 512, 3>(p, blocks, s)
+                                      : launch_bwd<T, 512, 4>(p, blocks, s);
   if (st != MOE_OK || sums == 0) return st;
   MOE_LAUNCH("block_join_bwd_sum", (join_sum_kernel<T>), dim3(unsigned((p.H + 31) / 32), unsigned(sums)), dim3(1024), 0, s,
              static_cast<const float*>(p.part), blocks, p.H, o);
@@ -471,8 +481,8 @@ moe_status launch_join_backward(const JoinBwdArgs& a) {
   const JoinBwdP p{a.z,  a.y,  a.gate, a.w_post, a.w_pre, a.dz, a.dh, a.dx, a.dy, a.dgate, static_cast<float*>(a.ws),
                    p_pre, p_post, p_gate, j->rows, j->hidden, vectors(j), j->post_norm, j->gate_kind, j->gate_act,
                    j->eps, j->weight_offset, j->residual_scale};
-  return j->dtype == MOE_BF16 ? launch_bwd_t<bf16_t>(p, bwd_threads(j), bwd_blocks(j), sums, o, a.s)
-                              : launch_bwd_t<float>(p, bwd_threads(j), bwd_blocks(j), sums, o, a.s);
+  return j->dtype == MOE_BF16 ? launch_bwd_t<bf16_t>(p, bwd_shape(j), bwd_blocks(j), sums, o, a.s)
+                              : launch_bwd_t<float>(p, bwd_shape(j), bwd_blocks(j), sums, o, a.s);
 }
 
 }  // namespace moe
