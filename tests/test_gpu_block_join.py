@@ -136,6 +136,17 @@ def test_the_norm_before_a_first_block(weighted, dtype):
     run_both(v, d, dtype, oj.Join(eps=1e-5, offset=0.5), jd, "enter", "enter without dz")
 
 
+@pytest.mark.parametrize("gate", GATES)
+@pytest.mark.parametrize("T,H,dtype", [(515, 4104, "f32"), (300, 8192, "f32"), (515, 6152, "bf16"), (259, 12288, "bf16"),
+                                       (513, 4672, "bf16")])
+def test_wide_rows_share_the_blocks(T, H, dtype, gate):
+    """Several rows a block where a thread has several vectors."""
+    say(f"[join] {T} x {H} {gate} {dtype}")
+    v, d = inputs(T, H, dtype, gate, True, "full")
+    jd = etd.make_join_desc(T, H, dtype, True, gate, "sigmoid", 1e-6, 0.0, 0.5)
+    run_both(v, d, dtype, oj.Join(True, gate, True, 1e-6, 0.0, 0.5), jd, "full", f"{T} x {H} {gate} {dtype}")
+
+
 @pytest.mark.parametrize("T", (511, 512, 513, 1700, 5000))
 def test_many_rows_share_the_blocks(T):
     H = 72
