@@ -61,6 +61,17 @@ __device__ __forceinline__ float sigmoid(float v) {
   return 1.0f / (1.0f + (sizeof(T) == 4 ? expf(-v) : __expf(-v)));
 }
 
+// The same and its derivative s (1 - s), which is even in v and would cancel if it were formed from an s
+// near 1: with e = exp(-|v|), s = 1 / (1 + e) or e / (1 + e), s (1 - s) = e / (1 + e)^2.
+struct Sigmoid {
+  float s, slope;
+};
+template <typename T>
+__device__ __forceinline__ Sigmoid sigmoid_and_slope(float v) {
+  const float e = sizeof(T) == 4 ? expf(-fabsf(v)) : __expf(-fabsf(v)), q = 1.0f / (1.0f + e);
+  return {v < 0.0f ? e * q : q, e * q * q};
+}
+
 // Sums of N values over the NT threads of a row; every thread gets them.  `buf` alternates
 // between two halves, so one barrier per reduction is enough.
 template <int NT, int N>
@@ -285,8 +296,9 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinBwdP p) {
       continue;
     }
 
-    float k_row = p.scale;
-    if (p.gate_kind == MOE_GATE_TOKEN) k_row *= sig ? sigmoid<T>(g_raw) : g_raw;
+    Sigmoid g_row = {1.0f, 1.0f};  // a token gate's value and derivative
+    if (p.gate_kind == MOE_GATE_TOKEN) g_row = sig ? sigmoid_and_slope<T>(g_raw) : Sigmoid{g_raw, 1.0f};
+    const float k_row = p.scale * g_row.s;
     const bool whole = p.gate_kind == MOE_GATE_ELEMENT || p.gate_kind == MOE_GATE_CHANNEL;
     float t[2] = {0.0f, 0.0f};  // sum c yh, sum D b
 #pragma unroll
@@ -299,15 +311,15 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinBwdP p) {
       for (int e = 0; e < E; ++e) {
         const float yh = yf[e] * ry;
         const float f = p.w_post != nullptr ? p.offset + w[e] : 1.0f;
-        const float gv = whole ? (sig ? sigmoid<T>(g[e]) : g[e]) : 1.0f;
-        const float db = k_row * gv * dv[i][e];
+        const Sigmoid gv = !whole ? Sigmoid{1.0f, 0.0f} : sig ? sigmoid_and_slope<T>(g[e]) : Sigmoid{g[e], 1.0f};
+        const float db = k_row * gv.s * dv[i][e];
         const float dgb = dv[i][e] * (yh * f);
         t[0] = fmaf(db * f, yh, t[0]);
         t[1] += dgb;
         s_post[i][e] = fmaf(db, yh, s_post[i][e]);
-        const float dg = whole ? p.scale * dgb * (sig ? gv * (1.0f - gv) : 1.0f) : 0.0f;
-        s_gate[i][e] += dg;
-        og[e] = dg;
+        const float dg = whole ? p.scale * dgb : 0.0f;
+        s_gate[i][e] += dg;  // a channel gate's slope is its rows' own factor: once, behind their sum
+        og[e] = dg * gv.slope;
         dv[i][e] = db * f;  // c
       }
       const int c = tid + i * NT;
@@ -324,16 +336,19 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinBwdP p) {
       for (int e = 0; e < E; ++e) o[e] = ry * fmaf(-(yf[e] * ry), my, dv[i][e]);
       if (c < p.nvec) reinterpret_cast<uint4*>(p.dy)[base + c] = pack16(o, T());
     }
-    if (p.gate_kind == MOE_GATE_TOKEN && tid == 0) {
-      const float sg = sig ? sigmoid<T>(g_raw) : 0.0f;
-      static_cast<float*>(p.dgate)[row] = p.scale * t[1] * (sig ? sg * (1.0f - sg) : 1.0f);
-    }
+    if (p.gate_kind == MOE_GATE_TOKEN && tid == 0) static_cast<float*>(p.dgate)[row] = p.scale * t[1] * g_row.slope;
   }
 
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = tid + i * NT;
     if (c >= p.nvec) continue;
+    if (p.gate_kind == MOE_GATE_CHANNEL && sig) {
+      float g[E];
+      unpack16(gc[i], T(), g);
+#pragma unroll
+      for (int e = 0; e < E; ++e) s_gate[i][e] *= sigmoid_and_slope<T>(g[e]).slope;
+    }
     auto put = [&](int which, const float (&v)[E]) {
       if (which < 0) return;
       float* dst = p.part + (size_t(which) * gridDim.x + blockIdx.x) * p.H + size_t(c) * E;

@@ -37,7 +37,7 @@ def _gate(j: Join, gate):
     if not j.sigmoid:
         return g, np.ones_like(g)
     s = 1.0 / (1.0 + np.exp(-g))
-    return s, s * (1.0 - s)
+    return s, s / (1.0 + np.exp(g))  # s (1 - s), without the difference
 
 
 def forward(j: Join, x, y=None, gate=None, w_post=None, w_pre=None, next_norm: bool = True) -> dict:
