@@ -113,6 +113,8 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int
             G::mma(uf, bf, t);
             if constexpr (sizeof(T) == 2) {
               uf[0] = c + fk < ad.rank ? *reinterpret_cast<const uint4*>(u + ad.lo + c) : make_uint4(0, 0, 0, 0);
+              const u32x4_t b0 = __builtin_bit_cast(u32x4_t, bf[0]);
+              if (!all_finite(largest_exponents(u16x2_t{0, 0}, b0))) bf[0] = __builtin_bit_cast(uint4, finite_ones(b0));
               G::mma(uf, bf, t);
             }
           }

@@ -96,11 +96,23 @@ __device__ __forceinline__ void add_adapters(const Adapters& ad, int expert, int
 #pragma unroll
       for (int f = 0; f < kFlight; ++f)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int m = NMAT == 2 ? s : 0;
-          t[f][s] = Mma16<T>::mma(uf[m], bf[f][s], t[f][s]);
-          if constexpr (sizeof(T) == 2) t[f][s] = Mma16<T>::mma(ul[m], bf[f][s], t[f][s]);
-        }
+        for (int s = 0; s < 2; ++s) t[f][s] = Mma16<T>::mma(uf[NMAT == 2 ? s : 0], bf[f][s], t[f][s]);
+      if constexpr (sizeof(T) == 2) {
+        u16x2_t most = {0, 0};
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f)
+#pragma unroll
+          for (int s = 0; s < 2; ++s) most = largest_exponents(most, bf[f][s]);
+        if (!all_finite(most))
+#pragma unroll
+          for (int f = 0; f < kFlight; ++f)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) bf[f][s] = finite_ones(bf[f][s]);
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f)
+#pragma unroll
+          for (int s = 0; s < 2; ++s) t[f][s] = Mma16<T>::mma(ul[NMAT == 2 ? s : 0], bf[f][s], t[f][s]);
+      }
     }
 #pragma unroll
     for (int f = 0; f < kFlight; ++f)

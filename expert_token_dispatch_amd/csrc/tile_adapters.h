@@ -37,7 +37,6 @@ __device__ __forceinline__ f32x16_t mma32(bf16x8_t b, bf16x8_t a, f32x16_t c) {
 template <class S, int NMAT, int NA>
 __device__ __forceinline__ void tile_adapters(const Adapters& ad, int expert, int row0, int rows, int n0, int N,
                                               char* lds, f32x16_t (&acc)[NA][S::NB]) {
-  typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
   constexpr int NB = S::NB, NJ = NB / NMAT, kWaves = S::kThreads / 64, kIds = S::kA / 64, KC = kChunkRank / 16;
   constexpr int kUPlane = S::kA * 32, kBPlane = S::kB * 32, kBSlot = KC * kBPlane;
   constexpr int kULoads = NMAT * 2 * KC * (S::kA / 32) / kWaves, kBLoads = KC * (S::kB / 32) / kWaves;  // a wave's
@@ -138,12 +137,10 @@ __device__ __forceinline__ void tile_adapters(const Adapters& ad, int expert, in
           for (int kc = 0; kc < KC; ++kc) {
             const u32x4_t b =
                 *reinterpret_cast<const u32x4_t*>(sbb + kc * kBPlane + (m * (S::kB / 2) + (wn * NJ + j) * 32) * 32 + at);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2_t, b[r] & 0x7F807F80u));
+            most = largest_exponents(most, b);
             fb[j][kc] = __builtin_bit_cast(bf16x8_t, b);
           }
-        const bool finite = __ballot(most[0] == 0x7F80 || most[1] == 0x7F80) == 0;
+        const bool finite = all_finite(most);
 #pragma unroll
         for (int i = 0; i < NA; ++i) {
 #pragma unroll
@@ -167,7 +164,8 @@ __device__ __forceinline__ void tile_adapters(const Adapters& ad, int expert, in
             } else {
 #pragma unroll
               for (int j = 0; j < NJ; ++j) {
-                const f32x16_t t = mma32(fb[j][kc], ul, mma32(fb[j][kc], uh, acc[i][m * NJ + j]));
+                const bf16x8_t fl = __builtin_bit_cast(bf16x8_t, finite_ones(__builtin_bit_cast(u32x4_t, fb[j][kc])));
+                const f32x16_t t = mma32(fl, ul, mma32(fb[j][kc], uh, acc[i][m * NJ + j]));
                 // lane -> token row: the whole column of sums is one row's
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[i][m * NJ + j][r] = own ? t[r] : acc[i][m * NJ + j][r];
