@@ -326,14 +326,15 @@ __global__ __launch_bounds__(NT) void join_bwd_kernel(JoinBwdP p) {
       if (p.gate_kind == MOE_GATE_ELEMENT && c < p.nvec) reinterpret_cast<uint4*>(p.dgate)[base + c] = pack16(og, T());
     }
     row_sum<NT, 2>(t, buf[1]);
-    const float my = p.post_norm ? t[0] * inv_h : 0.0f;
+    const float my = t[0] * inv_h;  // mean(c yh)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = tid + i * NT;
       float yf[E], o[E];
       unpack16(yr[i], T(), yf);
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = ry * fmaf(-(yf[e] * ry), my, dv[i][e]);
+      for (int e = 0; e < E; ++e)  // without its norm dy is c, whatever y holds: 0 * inf would be NaN
+        o[e] = p.post_norm ? ry * fmaf(-(yf[e] * ry), my, dv[i][e]) : dv[i][e];
       if (c < p.nvec) reinterpret_cast<uint4*>(p.dy)[base + c] = pack16(o, T());
     }
     if (p.gate_kind == MOE_GATE_TOKEN && tid == 0) static_cast<float*>(p.dgate)[row] = p.scale * t[1] * g_row.slope;

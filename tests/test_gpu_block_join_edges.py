@@ -50,3 +50,28 @@ def test_sigmoid_gates_far_from_zero(gate, post, dtype):
         if t is not None:
             units = 192 + 40 + (38 if name == "dgate" and gate == "token" else 0) + (161 if t.dim() == 1 else 0)
             check(t, ref[name], ref["mag_" + name], "f32" if t.dtype == torch.float32 else "bf16", units, f"{gate} {name}")
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("act", ("linear", "sigmoid"))
+@pytest.mark.parametrize("gate", GATES)
+def test_without_a_norm_the_blocks_gradient_does_not_ask_for_its_output(gate, act, dtype):
+    """dy = scale g D: infinities and NaN in y leave it, and dx, as they are; a gate's gradient has them in their row."""
+    T, H = 12, 520
+    say(f"[join] infinite y {gate} {act} {dtype}")
+    v, d = inputs(T, H, dtype, gate, False, "post")
+    jd = etd.make_join_desc(T, H, dtype, False, gate, act, 1e-6, 0.0, 0.5)
+    clean = backward(jd, v, d)
+    y = v["y"].clone()
+    y[3, 7], y[5, 500], y[8, 0] = float("inf"), float("-inf"), float("nan")
+    bad = backward(jd, {**v, "y": y}, d)
+    assert torch.isfinite(clean["dy"]).all()
+    assert torch.equal(bad["dy"], clean["dy"]) and torch.equal(bad["dx"], clean["dx"])
+    if gate in ("token", "element"):
+        keep = [r for r in range(T) if r not in (3, 5, 8)]
+        assert torch.equal(bad["dgate"][keep], clean["dgate"][keep])
+        assert not torch.isfinite(bad["dgate"][[3, 5, 8]].reshape(3, -1)).all(dim=1).any()
+    # and with the next norm's gradient, whose z is another tensor
+    v, d = inputs(T, H, dtype, gate, False, "full")
+    clean, bad = backward(jd, v, d), backward(jd, {**v, "y": y}, d)
+    assert torch.equal(bad["dy"], clean["dy"]) and torch.equal(bad["dw_pre"], clean["dw_pre"])
