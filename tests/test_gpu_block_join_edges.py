@@ -75,3 +75,35 @@ def test_without_a_norm_the_blocks_gradient_does_not_ask_for_its_output(gate, ac
     v, d = inputs(T, H, dtype, gate, False, "full")
     clean, bad = backward(jd, v, d), backward(jd, {**v, "y": y}, d)
     assert torch.equal(bad["dy"], clean["dy"]) and torch.equal(bad["dw_pre"], clean["dw_pre"])
+
+
+@pytest.mark.parametrize("T,H", [(128, 512), (1024, 512), (2048, 512), (4096, 512), (1000, 4096), (4096, 64)])
+def test_sums_over_rows_lose_what_a_tree_loses(T, H):
+    """Rows of ones: zh and yh are 1 to the bit (eps is below a step of 1), so every sum over rows is one of given numbers.
+    They lie less than 2^-17 / 2 past 1, so that adding them one after another drops the same again and again.  A term of
+    the sums passes through a block's rows one by one, the blocks of a thread of the second step eight at a time as a tree
+    (3) and those eights one by one, and 128 threads as a tree (7).  Each of these sums rounds by at most a unit of itself,
+    and all have one sign."""
+    say(f"[join] sums of {T} x {H}")
+    n = H // 4  # vectors of a row
+    most = 256 * max(1, 1024 // next((t for t in (64, 128, 192, 256, 384, 512, 768) if n <= t), 512 * ((n + 511) // 512)))
+    rows = max(1, -(-T // most))
+    blocks = -(-T // rows)
+    units = rows + 3 + -(-blocks // 1024) + 7 + 1
+    rng = np.random.default_rng(T + H)
+    ones = torch.ones((T, H), device="cuda")
+    col = 1.0 + 2.0 ** -17 * (0.45 + 0.04 * rng.random(H))
+    grad = dev(np.broadcast_to(col, (T, H)).copy(), "f32")
+    w = torch.ones(H, device="cuda")
+
+    def off(got, terms):
+        want = host(terms).sum(0)
+        return float((np.abs(host(got) - want) / want).max() / UNIT)
+    # dw_post = sum of dz, dgate the same
+    jd = etd.make_join_desc(T, H, "f32", True, "channel", "linear", 1e-30)
+    out = backward(jd, {"x": ones, "y": ones, "gate": w, "w_post": w, "w_pre": None}, {"dz": grad, "dh": None})
+    assert off(out["dw_post"], grad) <= units and off(out["dgate"], grad) <= units
+    # dw_pre = sum of dh
+    jd = etd.make_join_desc(T, H, "f32", False, "none", "linear", 1e-30)
+    out = backward(jd, {"x": ones, "y": None, "gate": None, "w_post": None, "w_pre": w}, {"dz": grad, "dh": grad})
+    assert off(out["dw_pre"], grad) <= units
