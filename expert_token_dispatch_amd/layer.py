@@ -1,8 +1,10 @@
 """Buffer management around the C ABI: one MoE layer's device tensors, and the join around it.
 
 MoELayer owns the weights (torch device tensors in the library's layout), the
-workspace, and the stage outputs, and calls the libmoe entry points on the
-current torch stream.  It computes nothing itself.
+workspaces, and the stage outputs, and calls the libmoe entry points on the
+current torch stream.  It computes nothing itself.  A layer's calls share its
+workspaces, captured ones too: on several streams each has to wait for the one
+before, or take a MoELayer of its own around the same weights.
 """
 
 from __future__ import annotations
@@ -289,7 +291,8 @@ class MoELayer:
 
 class BlockJoin:
     """What stands between a block and the next: the norm of the block's output, its gate and scale, the
-    residual sum, and the next block's norm.  Owns the norm weights and the backward's workspace.
+    residual sum, and the next block's norm.  Owns the norm weights; its calls share no buffers, so that
+    several may run at once.
 
     w_post: the norm after the block (post_norm without it: a norm of factor 1); w_pre: the next block's
     norm (next_norm without it: a norm of factor 1).  gate: "none", "channel", "token" or "element"; the
@@ -304,19 +307,16 @@ class BlockJoin:
         self.next_norm = w_pre is not None if next_norm is None else next_norm
         self.gate, self.gate_act = gate, gate_act
         self.eps, self.weight_offset, self.residual_scale = eps, weight_offset, residual_scale
-        self._ws = None
 
     def desc(self, rows: int, with_block: bool = True) -> L.JoinDesc:
         return L.make_join_desc(rows, self.hidden, self.dtype, post_norm=with_block and self.post_norm,
                                 gate=self.gate if with_block else "none", gate_act=self.gate_act, eps=self.eps,
                                 weight_offset=self.weight_offset, residual_scale=self.residual_scale)
 
-    def workspace(self) -> torch.Tensor:
-        """The backward's, enough for any number of rows."""
-        if self._ws is None:
-            n = L.moe_join_workspace_size(self.desc((1 << 31) - 1))
-            self._ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-        return self._ws
+    def workspace(self, rows: int = (1 << 31) - 1) -> torch.Tensor:
+        """A new one for the backward of so many rows, by default of any number.  Each call takes its own: torch's
+        allocator keeps what a stream has used for that stream, and a graph's memory for that graph."""
+        return torch.empty(L.moe_join_workspace_size(self.desc(rows)), dtype=torch.uint8, device=self.device)
 
     def forward(self, x, y=None, gate=None, z=None, h=None):
         """(z, h) of the stream x and the block's output y; without y, (x, h): the norm before a first block.
@@ -338,5 +338,5 @@ class BlockJoin:
                 return None if t is None else torch.empty_like(t)
             grads = {"dx": like(z), "dy": like(y), "dgate": like(gate), "dw_post": like(w_post), "dw_pre": like(self.w_pre)}
         L.moe_block_join_backward(j, z, y, gate, w_post, self.w_pre, dz, dh, grads["dx"], grads["dy"], grads["dgate"],
-                                  grads["dw_post"], grads["dw_pre"], self.workspace())
+                                  grads["dw_post"], grads["dw_pre"], self.workspace(z.shape[0]))
         return grads

@@ -107,3 +107,47 @@ def test_sums_over_rows_lose_what_a_tree_loses(T, H):
     jd = etd.make_join_desc(T, H, "f32", False, "none", "linear", 1e-30)
     out = backward(jd, {"x": ones, "y": None, "gate": None, "w_post": None, "w_pre": w}, {"dz": grad, "dh": grad})
     assert off(out["dw_pre"], grad) <= units
+
+
+def test_a_blockjoins_calls_on_two_streams_and_in_two_graphs_share_no_sums(monkeypatch):
+    T, H = 300, 520
+    v, d = inputs(T, H, "bf16", "channel", True, "full")
+    join = etd.BlockJoin(H, "bf16", v["w_post"], v["w_pre"], gate="channel", gate_act="sigmoid")
+    used, real = [], L.moe_block_join_backward
+
+    def recorded(*args):
+        used.append((args[-1].data_ptr(), args[-1].data_ptr() + args[-1].numel()))
+        real(*args)
+    monkeypatch.setattr(L, "moe_block_join_backward", recorded)
+
+    def step(grads=None):
+        return join.backward(v["x"], v["y"], v["gate"], d["dz"], d["dh"], grads=grads)
+    want = step()
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = []
+    for s in sides:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            outs.append(step())
+    graphs = []
+    torch.cuda.synchronize()
+    for _ in sides:
+        outs.append({k: None if t is None else torch.empty_like(t) for k, t in want.items()})
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            step(outs[-1])
+    spans = sorted(used)
+    assert len(used) == 5 and all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+    for _ in range(3):
+        for o in outs[2:]:
+            for t in o.values():
+                t.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, sides):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for o in outs:
+            for k, t in want.items():
+                assert torch.equal(o[k], t), k
