@@ -580,7 +580,8 @@ def _adapters(d, v) -> Optional[int]:
     if t is not None:
         dt = torch.bfloat16 if d.dtype == MOE_BF16 else torch.float32
         n, L, R, H, I = v.count, d.local_count, v.rank, d.hidden, d.intermediate
-        key = (dt, L, H, I)
+        on_gpu = next(iter(t.values())).get_device() >= 0
+        key = (dt, n, L, R, H, I, torch.cuda.current_device() if on_gpu else None)
         if v._fits != key:
             shapes = {"scale": ((n,), torch.float32)}
             for name, out, in_ in (("gate", I, H), ("up", I, H), ("down", H, I)):
@@ -588,7 +589,7 @@ def _adapters(d, v) -> Optional[int]:
             if set(t) - set(shapes):
                 raise ValueError(f"adapters have no {sorted(set(t) - set(shapes))}")
             _expect("layer's adapters", [(k, x, *shapes[k]) for k, x in t.items()])
-            v._fits = key  # the tensors are the struct's own: looked at once for each kind of layer
+            v._fits = key  # the tensors are the struct's own: looked at once for each kind of layer and device
     return ctypes.addressof(v)
 
 

@@ -143,3 +143,34 @@ def test_the_binding_refuses_other_stacks():
         L._ids(d, torch.zeros(5, dtype=torch.int32))
     with pytest.raises(ValueError, match="adapter_ids"):
         L._ids(d, torch.zeros(4, dtype=torch.int64))
+
+
+class _OnGpu0:
+    """What the binding asks of a tensor on the first GPU."""
+
+    def __init__(self, t):
+        self.shape, self.dtype, self.device = t.shape, t.dtype, "cuda:0"
+
+    def get_device(self):
+        return 0
+
+
+def test_the_binding_looks_again_on_another_device_and_after_a_changed_count(monkeypatch):
+    torch = pytest.importorskip("torch")
+    d, bf = etd.make_desc(4, 64, 128, 8, 2), torch.bfloat16
+    v = L.Adapters(3, 16, None, None, None, None, None, 256, 256)
+    v._tensors = {"down_a": _OnGpu0(torch.empty(3, 8, 16, 128, dtype=bf)), "down_b": _OnGpu0(torch.empty(3, 8, 64, 16, dtype=bf))}
+    v._fits = None
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    assert L._adapters(d, v) and L._adapters(d, v)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="current device is cuda:1"):
+        L._adapters(d, v)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    assert L._adapters(d, v)
+    v.count = 4
+    with pytest.raises(ValueError, match="adapters"):
+        L._adapters(d, v)
+    v.count, v.rank = 3, 24
+    with pytest.raises(ValueError, match="adapters"):
+        L._adapters(d, v)
