@@ -1227,11 +1227,10 @@ moe_status moe_block_join_backward(const moe_join_desc* j, const void* z, const 
   REQUIRE_BOTH(dw_pre, w_pre, 16);
   if (j->rows == 0) {
     const size_t n = size_t(j->hidden) * dtype_bytes(j->dtype);
+    if (j->gate_kind == MOE_GATE_CHANNEL) REQUIRE_PTR(dgate, 16);
     if (dw_post != nullptr) TRY(launch_zero("block_join_bwd_zero", dw_post, n, s));
     if (dw_pre != nullptr) TRY(launch_zero("block_join_bwd_zero", dw_pre, n, s));
-    if (j->gate_kind != MOE_GATE_CHANNEL) return MOE_OK;
-    REQUIRE_PTR(dgate, 16);
-    return launch_zero("block_join_bwd_zero", dgate, n, s);
+    return j->gate_kind == MOE_GATE_CHANNEL ? launch_zero("block_join_bwd_zero", dgate, n, s) : MOE_OK;
   }
   TRY(join_operand_checks(j, y, gate, w_post, w_pre));
   OPTIONAL_PTR(dz, 16);

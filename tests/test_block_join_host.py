@@ -163,3 +163,12 @@ def test_the_binding_refuses_other_shapes_and_types():
         a.update(bad)
         with pytest.raises(ValueError, match="of this join is"):
             etd.moe_block_join(j, **a)
+
+
+@pytest.mark.parametrize("dgate", (None, 264))
+def test_no_rows_and_a_refused_gate_gradient_enqueue_nothing(dgate):
+    """The refusal comes before the weights' gradients are cleared (which has no device to run on here)."""
+    a = [256] * 13
+    a[BWD.index("dgate")] = dgate
+    assert L.lib().moe_block_join_backward(ctypes.byref(_desc(rows=0)), *a, 1 << 30, None) == L.MOE_ERR_INVALID_ARG
+    assert "dgate" in L.moe_last_error()
