@@ -330,13 +330,14 @@ class BlockJoin:
         return (x if y is None else z), h
 
     def backward(self, z, y=None, gate=None, dz=None, dh=None, grads: Optional[dict] = None) -> dict:
-        """Gradients dx, and with y also dy, dgate, dw_post, and dw_pre, from those of forward()'s results."""
+        """Gradients dx, and with y also dy, dgate, dw_post, and dw_pre, from those of forward()'s results.
+        grads: tensors for them under these names, for exactly those that there are."""
         j = self.desc(z.shape[0], y is not None)
         w_post = self.w_post if y is not None else None
         if grads is None:
             def like(t):
                 return None if t is None else torch.empty_like(t)
             grads = {"dx": like(z), "dy": like(y), "dgate": like(gate), "dw_post": like(w_post), "dw_pre": like(self.w_pre)}
-        L.moe_block_join_backward(j, z, y, gate, w_post, self.w_pre, dz, dh, grads["dx"], grads["dy"], grads["dgate"],
-                                  grads["dw_post"], grads["dw_pre"], self.workspace(z.shape[0]))
+        out = [grads.get(n) for n in ("dx", "dy", "dgate", "dw_post", "dw_pre")]
+        L.moe_block_join_backward(j, z, y, gate, w_post, self.w_pre, dz, dh, *out, self.workspace(z.shape[0]))
         return grads

@@ -151,3 +151,18 @@ def test_a_blockjoins_calls_on_two_streams_and_in_two_graphs_share_no_sums(monke
         for o in outs:
             for k, t in want.items():
                 assert torch.equal(o[k], t), k
+
+
+def test_gradients_of_the_norm_alone_into_buffers_of_its_own():
+    """Without y the results are dx and dw_pre: the buffers for them are enough."""
+    T, H = 20, 136
+    v, d = inputs(T, H, "f32", "none", False, "enter")
+    join = etd.BlockJoin(H, "f32", w_pre=v["w_pre"])
+    want = join.backward(v["x"], dz=d["dz"], dh=d["dh"])
+    grads = {"dx": torch.empty_like(v["x"]), "dw_pre": torch.empty_like(v["w_pre"])}
+    got = join.backward(v["x"], dz=d["dz"], dh=d["dh"], grads=grads)
+    torch.cuda.synchronize()
+    assert got is grads and torch.equal(got["dx"], want["dx"]) and torch.equal(got["dw_pre"], want["dw_pre"])
+    del grads["dw_pre"]
+    with pytest.raises(L.MoeError, match="dw_pre"):
+        join.backward(v["x"], dz=d["dz"], dh=d["dh"], grads=grads)
