@@ -201,7 +201,7 @@ __global__ __launch_bounds__(NT == 64 ? 256 : NT) void join_kernel(JoinP p) {
 // w_post), a = dh (offset + w_pre):
 //   D  = dz + r_z (a - zh mean(a zh))                       (= dx)
 //   db = scale g D,  c = db (offset + w_post),  dy = r_y (c - yh mean(c yh))
-//   dw_pre = sum dh zh,  dw_post = sum db yh,  dgate = scale D b (s (1 - s) of a sigmoid)
+//   dw_pre = sum dh zh,  dw_post = sum db yh,  dgate = scale D b (times a sigmoid's slope)
 // At 8192 x 4096 in bf16 with a channel gate 88 us with the sums' kernel, 4.6 of the 5.2 TB/s that a
 // large copy reaches: the sums of 512 blocks are another 50 MB, the rest the two waits of a row.
 // (Loading the next row under this one, rows of 1024-thread blocks side by side and barriers
@@ -433,10 +433,10 @@ moe_status launch_fwd_t(const JoinP& p, hipStream_t s) {
 }
 
 // Threads of a row in the backward and vectors of a thread: one vector each up to 768 threads, and 512
-// threads beyond, which leave each the registers for its sums (4096 x 8192 bf16: 107 us against
-// 174 with 1024 threads, 3591 x 4672 float32 93 against 222; 5461 x 6144 bf16 106 with 768 threads,
-// 114 with 384 of two vectors).  bf16 rows of more than 8192 spill all the same: 2730 x 12288 222 us
-// (1024 threads of two vectors 506), 2048 x 16384 414 (409).
+// threads beyond, which leave each the registers for its sums (4096 x 8192 bf16: 106 us against
+// 155 with 1024 threads, 3591 x 4672 float32 93 against 226; 5461 x 6144 bf16 106 with 768 threads,
+// 114 with 384 of two vectors).  bf16 rows of more than 8192 spill all the same: 2730 x 12288 187 us
+// (1024 threads of two vectors 517), 2048 x 16384 412 (418).
 struct BwdShape {
   int nt, v;
 };
@@ -449,7 +449,7 @@ BwdShape bwd_shape(const moe_join_desc* j) {
 // Its blocks: as many on each of 256 CUs, up to 1024 vectors at once, and rows dealt evenly.  Half as many leave
 // too few loads in flight (8192 x 4096 bf16 119 us instead of 88), twice as many write and read
 // twice the sums (96 us); some CUs with a block more than others wait for those (262144 / 768 = 341
-// blocks for 5692 x 4672: 118 instead of 85 us; 682 of 384 threads for 4096 x 2880: 52 instead of 39).
+// blocks for 5692 x 4672: 138 instead of 105 us; 682 of 384 threads for 4096 x 2880: 56 instead of 44).
 int bwd_blocks(const moe_join_desc* j) {
   const BwdShape w = bwd_shape(j);
   const int64_t most = 256 * std::max(1, 1024 / (w.nt * w.v));
