@@ -6,10 +6,12 @@ import pytest
 
 from tests._adapted_paths import CASES, kernel_of
 from tests._harness import say
-from tests.test_gpu_adapters import Case
+from tests.test_gpu_adapters import Case, layer_case
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
+
+import expert_token_dispatch_amd as etd  # noqa: E402
 
 LARGE = [c for c in CASES if c[0] == "large" and c[5] == "out_in"]
 
@@ -153,3 +155,45 @@ def test_infinities_in_an_adapter_give_what_the_sum_gives(kernel, H, I, Lc, P, l
     assert broken.any() and torch.equal(y[~broken], base[~broken])
     want = torch.sign(h[:, p.cols["down"].cuda()]) * float("inf")
     assert torch.equal(y[broken], want[broken])
+
+
+@pytest.mark.parametrize("spread", ("one", "skew"))
+@pytest.mark.parametrize("kernel,H,I,Lc,P,layout,_", CASES)
+def test_uneven_segments_in_every_kernel(kernel, H, I, Lc, P, layout, _, spread):
+    c = Case(H, I, Lc, P, 16, 5, layout=layout, spread=spread)
+    c.check(f"{kernel} {spread}", rows=some_rows(c))
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("kernel,H,I,Lc,P,layout,_", CASES)
+def test_no_row_for_any_of_a_ranks_experts(kernel, H, I, Lc, P, layout, _, dtype):
+    """The descriptor allows P rows, the batch sends none: nothing is read as a row, nothing written."""
+    say(f"[adapters] no rows: {(H, I, Lc, P)} {layout} {dtype}")
+    c = Case(H, I, Lc, P, 16, 5, dtype, layout)
+    c.offsets.zero_()
+    assert (c.run() == 7.0).all()
+
+
+def test_the_most_adapters_and_the_highest_rank():
+    say("[adapters] 65535 adapters; rank 128")
+    c = Case(16, 8, 2, 40, 8, 65535)
+    ids = np.arange(40) * 1679 % 65535
+    ids[::5] = 65534
+    ids[1::5] = 65535  # past the last: none
+    c.set_ids(ids)
+    c.check("65535 adapters")
+    Case(264, 136, 2, 700, 128, 3, kind="mixed").check("rank 128")
+
+
+def test_the_layer_with_route_options_is_its_stages():
+    T, E, k = 300, 16, 4
+    layer, ad, ids, x = layer_case(T, 128, 192, E, k)
+    bias = torch.linspace(-1, 1, E, device="cuda")
+    opts = etd.make_route_opts(bias, 4, 2)
+    y = layer.forward_adapted(x, ad, ids, opts=opts)
+    r = layer.route(x, opts=opts)
+    dd = layer.dispatch(x, r["topk_ids"])
+    ys = layer.grouped_ffn_adapted(dd["x_sorted"], dd["offsets"], dd["sorted_pairs"], ad, ids)
+    z = layer.combine(ys, dd["pair_row"], r["topk_w"])
+    torch.cuda.synchronize()
+    assert torch.equal(y, z) and not torch.equal(y, layer.forward_adapted(x, ad, ids))
